@@ -412,7 +412,7 @@ def _own_commit(s):
     h = s.get("handle")
     if h is None:
         h = s["handle"] = (M.kv_caches(s["k"].unbind(0), s["v"].unbind(0)), M.workspace(M.mtp_tree_workspace_bytes()))
-    M.mtp_tree_accept(s["parents"], s["tokens"], s["verify"], s["path"], s["emitted"], s["count"], h[1])
+    M.mtp_tree_accept(s["parents"], s["tokens"], s["verify"], s["path"], s["emitted"], s["count"])
     M.kv_tree_commit(h[0], s["path"], c["L"], h[1])
     L = c["L"]
     return s["path"], s["emitted"], s["count"], s["k"][:, :, L:L + c["n"]], s["v"][:, :, L:L + c["n"]]
