@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define MTPDRAFT_VERSION 2
+#define MTPDRAFT_VERSION 3
 
 typedef enum {
     MTP_OK = 0,
@@ -85,10 +85,12 @@ mtp_status mtp_workspace_init(void *d_ws, size_t bytes, void *stream);
  *   0 none; 1 a wait for a TMA copy gave up; 2 a token id outside
  *   [0, vocab) (row 0 was used); 3 a wait inside a multi-projection launch
  *   for the previous projection's output gave up; 4 a wait of the attention
- *   splits of a KV head for each other's partials gave up.
+ *   splits of a KV head for each other's partials gave up;
+ *   5 a draft tree's parent, depth or path entry outside its range (see the
+ *   call); 6 a rotary position outside the table (position 0 was used).
  * After code 1, 3 or 4 a launch stopped part-way (its outputs are not
  * valid) and may have left completion counters set: clear the workspace
- * with mtp_workspace_init() before its next use.  Code 2 leaves the
+ * with mtp_workspace_init() before its next use.  Codes 2, 5 and 6 leave the
  * workspace usable.  The waits behind codes 3 and 4 need every CTA of the
  * launch resident at once (the launches size their grids for that); a
  * device shared with other work at the same time can make them give up, so
@@ -513,6 +515,163 @@ mtp_status mtp_mimo_draft_round(const mtp_layer_desc *layers, int32_t n_layers,
                                 int32_t ids_len, float *d_values, void *d_ws, size_t ws_bytes,
                                 void *d_catch_ws, size_t catch_ws_bytes, void *stream,
                                 int32_t *n_drafts);
+
+/* ------------------------------------------------------------------------
+ * Draft trees.  A round over a tree of n <= 64 drafted tokens: node 0 is the
+ * pending token, a node's parent has a lower index.  The target's forward of
+ * the n rows uses rope_axes_rows or attn_tree_sink in every layer, the head
+ * gives logits, logit_rules_argmax each row's greedy token, mtp_tree_accept
+ * the path whose tokens the verifier agrees with, kv_tree_commit moves that
+ * path's K/V rows to the end of the cache.  Everything stays on the device;
+ * the host reads the accepted count when it advances its cache length.
+ * ------------------------------------------------------------------------ */
+
+/* Rotary positions on several axes (text: one; images and video: time, height,
+ * width).  "hf2q 0.1.13 ... mtp.rs", apply_imrope: position ids per axis and
+ * mrope_section.  Pair i of a head (dims i and i + rot_dim/2, rot_dim/2 = the
+ * sum of the sections) turns by the angle of pair i at the position of its
+ * axis.  interleaved = 0: section[0] pairs of axis 0, then section[1] of axis 1,
+ * ...  interleaved = 1: pairs are dealt in turn, pair i to axis a = i mod n_axes
+ * while i < n_axes*section[a], the rest to axis 0 (a section must find its
+ * pairs: a + n_axes*(section[a]-1) < rot_dim/2). */
+typedef struct {
+    const int32_t *d_pos;    /* [n_axes][pos_ld] positions; row r of axis a at d_pos[a*pos_ld + r] */
+    const float *d_rope;     /* table of mtp_rope_table, max_pos rows */
+    int32_t n_axes;          /* 1..4 */
+    int32_t section[4];      /* rotary pairs of each axis, 0..128 */
+    int32_t interleaved;     /* 0/1 */
+    int32_t pos_ld;          /* >= rows */
+    int32_t max_pos;         /* a position outside [0, max_pos) sets device error 6 */
+} mtp_rope_axes;
+
+/* Rows of heads: head h of row r starts at x + r*x_ld + h*x_hs (floats). */
+typedef struct {
+    const float *x;          /* input */
+    float *y;                /* output: x itself with the same strides (in place), or no overlap */
+    const float *norm_w;     /* [head_dim] weight of a per-head RMSNorm before the rotation, or NULL */
+    int64_t x_ld, y_ld;      /* row strides */
+    int32_t x_hs, y_hs;      /* head strides, >= head_dim */
+    int32_t n_heads;
+} mtp_head_rows;
+
+/* rope_axes_rows: per-head RMSNorm (optional) and rotation of the rows of up to
+ * four tensors of heads (q and k, say) in one launch.  Dims past rot_dim are
+ * normalised and copied.  head_dim a multiple of 32, <= 256; strides multiples
+ * of 4; every tensor has `rows` rows.  d_ws holds the error word. */
+size_t rope_axes_rows_workspace_bytes(void);
+mtp_status rope_axes_rows(const mtp_rope_axes *axes, const mtp_head_rows *tensors, int32_t n_tensors,
+                          int32_t rows, int32_t head_dim, float eps, void *d_ws, size_t ws_bytes,
+                          void *stream);
+
+/* mtp_tree_plan: d_mask[i] = bits of node i and its ancestors, d_depth[i] = the
+ * number of its ancestors, from d_parents [n] (-1: no parent, a root; a parent
+ * outside [-1, i) sets device error 5 and counts as -1). */
+size_t mtp_tree_workspace_bytes(void);
+mtp_status mtp_tree_plan(const int32_t *d_parents, int32_t n, uint64_t *d_mask, int32_t *d_depth,
+                         void *d_ws, size_t ws_bytes, void *stream);
+
+/* New rows of a tree. */
+typedef struct {
+    const uint64_t *d_mask;      /* [n]: node i sees new row j when bit j is set (bits >= n are
+                                    ignored; mtp_tree_plan sets a node's own bit too) */
+    const int32_t *d_depth;      /* [n] in [0, n): node i's sequence position is cache_len + depth
+                                    (outside: device error 5, the nearest value is used) */
+    const mtp_rope_axes *axes;   /* rotary positions and table, or NULL: node i rotates at
+                                    pos_base + cache_len + depth in the call's table */
+    int32_t n;                   /* 1..64 */
+    int32_t pos_base;
+    int64_t ld_q, ld_k, ld_v;    /* row strides of d_qp, d_kp, d_vp in floats (multiples of 4),
+                                    0 for contiguous rows */
+} mtp_draft_tree;
+
+/* ------------------------------------------------------------------------
+ * attn_tree_sink: attn_decode_sink for the rows of a tree.  Node i sees the
+ * cached rows j < cache_len (window: j > cache_len + depth_i - window) and the
+ * new rows of its mask (window: depth_j > depth_i - window); a row that a node
+ * does not see has no effect on it, whatever it holds.  A node that sees
+ * nothing gives 0.  Appends the n K/V rows at cache rows cache_len ..
+ * cache_len + n - 1, node i at cache_len + i (kv_tree_commit moves them).
+ *   geometry, norms, sinks, gate, cache layout: as attn_decode_sink; up to 64
+ *   query heads a KV head.  d_rope: table with rope_rows rows,
+ *   pos_base + cache_len + n of them needed (not read when tree->axes is given
+ *   or rot_dim is 0).  d_out [n][n_heads*head_dim_v].
+ *   Accuracy: float32 products and sums throughout.
+ * ------------------------------------------------------------------------ */
+size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n, int32_t cache_len);
+mtp_status attn_tree_sink(const mtp_attn_geom *g, const mtp_draft_tree *tree, const float *d_qp,
+                          const float *d_kp, const float *d_vp, const float *d_q_norm,
+                          const float *d_k_norm, const float *d_rope, int32_t rope_rows,
+                          const float *d_sinks, float *d_k_cache, float *d_v_cache,
+                          int32_t cache_len, int32_t cache_cap, float *d_out, void *d_ws,
+                          size_t ws_bytes, void *stream);
+
+/* Rules of a request on its logits. */
+typedef struct {
+    int32_t vocab;
+    float repetition;              /* > 0; 1: none */
+    float frequency, presence;     /* 0: none */
+    const uint32_t *d_counts;      /* [vocab] count table or NULL: bit 31 set when the token is in
+                                      the prompt, low 31 bits: times it was generated */
+    const int32_t *d_bias_tokens;  /* [n_bias] (ids outside the vocabulary are ignored) */
+    const float *d_bias;           /* [n_bias]: added; entries of one token sum in list order */
+    int32_t n_bias;                /* 0..65536 */
+    const uint32_t *d_allow;       /* mask [rows][allow_ld]: token v allowed when bit v%32 of word
+                                      v/32 is set; NULL: all allowed */
+    int32_t allow_ld;              /* words per row, >= ceil(vocab/32); 0: one row for all */
+    const int32_t *d_path_tokens;  /* [n_path] tokens of a draft tree's nodes */
+    const uint64_t *d_path_mask;   /* [rows]: row r's path holds node j when bit j is set */
+    int32_t n_path;                /* 0..64 */
+} mtp_logit_rules;
+
+/* ------------------------------------------------------------------------
+ * logit_rules_argmax: for each row r and token v, with c = the token's count
+ * plus its occurrences on the row's path, and seen = c > 0 or in the prompt:
+ *   l = seen ? (l > 0 ? l/repetition : l*repetition) : l
+ *   l = l - (frequency*c + presence*[c > 0]);  l = l + bias;
+ *   l = -inf where the mask forbids v;
+ * tokens[r] = the lowest index among the largest values (-1 when no value is
+ * above -inf; NaN never wins), values[r] = its value.
+ * The step after verify_head_argmax's logits when the request has penalties,
+ * biases or a grammar.  Every step rounds to float32.
+ *   d_logits [rows][ld]; d_out [rows][ld_out] receives the final logits (d_logits
+ *   itself: in place), or NULL.  rows in 1..1024.
+ * ------------------------------------------------------------------------ */
+size_t logit_rules_argmax_workspace_bytes(int32_t rows);
+mtp_status logit_rules_argmax(const mtp_logit_rules *rules, const float *d_logits, int64_t ld,
+                              int32_t rows, int32_t *d_tokens, float *d_values, float *d_out,
+                              int64_t ld_out, void *d_ws, size_t ws_bytes, void *stream);
+
+/* mtp_token_counts: adds n token ids to a count table (prompt = 1: sets bit 31;
+ * 0: adds one to the count).  Negative ids are skipped (the unused tail of
+ * mtp_tree_accept's list); an id >= vocab sets device error 2 and is skipped. */
+mtp_status mtp_token_counts(uint32_t *d_counts, int32_t vocab, const int32_t *d_tokens, int32_t n,
+                            int32_t prompt, void *d_ws, size_t ws_bytes, void *stream);
+
+/* mtp_tree_accept: the tree form of mtp_spec_accept.  From node 0, while a child
+ * (a node j > i with parent i) has the verifier's token d_verify[i], goes to the
+ * lowest such child.  d_path [n]: the nodes walked, node 0 first, then -1;
+ * d_emitted [n]: the verifier's token on each of them (the accepted drafts, then
+ * the round's own next token), then -1; d_count: how many (>= 1). */
+mtp_status mtp_tree_accept(const int32_t *d_parents, const int32_t *d_tokens,
+                           const int32_t *d_verify, int32_t n, int32_t *d_path, int32_t *d_emitted,
+                           int32_t *d_count, void *stream);
+
+/* K/V caches of layers with one geometry; cache [n_kv_heads][cache_cap][dim]. */
+typedef struct {
+    float *const *h_k;             /* host array of n_layers device pointers */
+    float *const *h_v;
+    int32_t n_layers;              /* 1..4096 */
+    int32_t n_kv_heads;            /* 1..64 */
+    int32_t head_dim_qk, head_dim_v; /* multiples of 4, <= 256 */
+    int32_t cache_cap;
+} mtp_kv_caches;
+
+/* kv_tree_commit: in every layer and head, cache row cache_len + d_path[j] moves
+ * to row cache_len + j, for j = 0, 1, .. while d_path[j] >= 0 (j < n).  Other
+ * rows stay as they are.  An entry below j or >= n sets device error 5 and ends
+ * the move.  The caller's cache length becomes cache_len + the accepted count. */
+mtp_status kv_tree_commit(const mtp_kv_caches *caches, const int32_t *d_path, int32_t n,
+                          int32_t cache_len, void *d_ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

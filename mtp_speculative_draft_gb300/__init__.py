@@ -11,5 +11,10 @@ from .api import (  # noqa: F401
     mtp_draft_steps, mtp_mimo_commit_layer, mtp_mimo_draft_round, mtp_mimo_plan_layer,
     qmatmul_affine4, rmsnorm_residual, verify_head_argmax, workspace,
 )
+from .tree import (  # noqa: F401
+    attn_tree_sink, attn_tree_sink_workspace_bytes, draft_tree, kv_caches, kv_tree_commit, logit_rules,
+    logit_rules_argmax, logit_rules_argmax_workspace_bytes, mtp_token_counts, mtp_tree_accept,
+    mtp_tree_plan, mtp_tree_workspace_bytes, rope_axes, rope_axes_rows, rope_axes_rows_workspace_bytes,
+)
 from ._lib import MimoLayerState, SpecStats  # noqa: F401
 from .layer import DraftLayer, DraftChain  # noqa: F401

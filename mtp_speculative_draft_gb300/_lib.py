@@ -73,6 +73,33 @@ class SpecStats(C.Structure):
                 ("draft_ns", C.c_uint64), ("verify_ns", C.c_uint64)]
 
 
+class RopeAxes(C.Structure):
+    _fields_ = [("d_pos", vp), ("d_rope", vp), ("n_axes", i32), ("section", i32 * 4),
+                ("interleaved", i32), ("pos_ld", i32), ("max_pos", i32)]
+
+
+class HeadRows(C.Structure):
+    _fields_ = [("x", vp), ("y", vp), ("norm_w", vp), ("x_ld", C.c_int64), ("y_ld", C.c_int64),
+                ("x_hs", i32), ("y_hs", i32), ("n_heads", i32)]
+
+
+class DraftTree(C.Structure):
+    _fields_ = [("d_mask", vp), ("d_depth", vp), ("axes", C.POINTER(RopeAxes)), ("n", i32),
+                ("pos_base", i32), ("ld_q", C.c_int64), ("ld_k", C.c_int64), ("ld_v", C.c_int64)]
+
+
+class LogitRules(C.Structure):
+    _fields_ = [("vocab", i32), ("repetition", f32), ("frequency", f32), ("presence", f32),
+                ("d_counts", vp), ("d_bias_tokens", vp), ("d_bias", vp), ("n_bias", i32),
+                ("d_allow", vp), ("allow_ld", i32), ("d_path_tokens", vp), ("d_path_mask", vp),
+                ("n_path", i32)]
+
+
+class KvCaches(C.Structure):
+    _fields_ = [("h_k", C.POINTER(vp)), ("h_v", C.POINTER(vp)), ("n_layers", i32),
+                ("n_kv_heads", i32), ("head_dim_qk", i32), ("head_dim_v", i32), ("cache_cap", i32)]
+
+
 class StepOut(C.Structure):
     _fields_ = [("d_token", vp), ("d_value", vp), ("d_hidden_out", vp), ("d_u2", vp),
                 ("d_logits", vp)]
@@ -117,6 +144,20 @@ EXPORTS = {
     "mtp_mimo_commit_layer": (C.c_int, [C.POINTER(MimoLayerState), i32, i32, i32]),
     "mtp_mimo_draft_round": (C.c_int, [C.POINTER(LayerDesc), i32, C.POINTER(MimoLayerState), vp, i32,
                                        i32, i32, vp, i32, vp, vp, sz, vp, sz, vp, C.POINTER(i32)]),
+    "rope_axes_rows_workspace_bytes": (sz, []),
+    "rope_axes_rows": (C.c_int, [C.POINTER(RopeAxes), C.POINTER(HeadRows), i32, i32, i32, f32, vp,
+                                 sz, vp]),
+    "mtp_tree_workspace_bytes": (sz, []),
+    "mtp_tree_plan": (C.c_int, [vp, i32, vp, vp, vp, sz, vp]),
+    "attn_tree_sink_workspace_bytes": (sz, [C.POINTER(AttnGeom), i32, i32]),
+    "attn_tree_sink": (C.c_int, [C.POINTER(AttnGeom), C.POINTER(DraftTree), vp, vp, vp, vp, vp, vp,
+                                 i32, vp, vp, vp, i32, i32, vp, vp, sz, vp]),
+    "logit_rules_argmax_workspace_bytes": (sz, [i32]),
+    "logit_rules_argmax": (C.c_int, [C.POINTER(LogitRules), vp, C.c_int64, i32, vp, vp, vp,
+                                     C.c_int64, vp, sz, vp]),
+    "mtp_token_counts": (C.c_int, [vp, i32, vp, i32, i32, vp, sz, vp]),
+    "mtp_tree_accept": (C.c_int, [vp, vp, vp, i32, vp, vp, vp, vp]),
+    "kv_tree_commit": (C.c_int, [C.POINTER(KvCaches), vp, i32, i32, vp, sz, vp]),
     "mtp_kv_catch_up_workspace_bytes": (sz, [C.POINTER(LayerDesc), i32]),
     "mtp_kv_catch_up": (C.c_int, [C.POINTER(LayerDesc), vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
 }
