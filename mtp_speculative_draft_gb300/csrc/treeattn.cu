@@ -9,11 +9,13 @@
 //
 // Three launches:
 //   1. prep:   q heads normalised, rotated and scaled (log2 domain) to the
-//              workspace; k heads normalised and rotated, v heads, appended to
-//              cache rows L .. L + n - 1;
+//              workspace, in float32 and as tensor-core operand tiles; k heads
+//              normalised and rotated, v heads, appended to cache rows
+//              L .. L + n - 1;
 //   2. split:  every query row against the cached keys that all rows see,
 //              [max(0, L + n - W), L) for a window W (a node's depth is below
-//              n), split over CTAs: no mask at all.  Partials (m, l, o);
+//              n), split over CTAs, on tcgen05: no mask at all.  Partials
+//              (m, l, o);
 //   3. finish: one CTA a (node, head) joins the partials, the cached keys at
 //              the window's edge (fewer than n, each row its own) and the
 //              node's ancestors, read key by key, so a row that a mask hides
@@ -21,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "tc5.cuh"
 #include "tree.cuh"
 
 namespace mtp {
@@ -39,15 +42,69 @@ struct TreeAttnArgs {
   const int* depth;
   float* out;
   float* qf;       // [nkv][R][dqk] scaled queries, row r = i * G + g
+  uint8_t* qt;     // [nkv][mt] tiles of 128 rows: f16 hi part, then lo part
+  float* qinv;     // [nkv][mt * 128] power of two that undoes a row's f16 scale
   int* dep;        // [n] depths inside [0, n)
   float* part_o;   // [nkv][ns][R][dv]
   float2* part_ml; // [nkv][ns][R] running maximum and sum
-  int R, ns, kbeg, kper;  // query rows of a KV head, splits, first split key, keys a split
+  int R, mt;              // query rows of a KV head, tiles of 128 of them
+  int ns, kbeg, kper;     // splits, first split key, keys a split
+  int stages;             // K/V tile buffers of the split kernel
   int* err;
 };
 
 // ------------------------------------------------------------------ prep
 constexpr int kPrepThreads = 128;
+
+// Power-of-two scale of a row for its f16 parts: the row's largest |x|, whose
+// float bits are given, lands in [2^14, 2^15), so hi + lo hold 22 bits of every
+// element down to 2^-16 of the largest.  Infinity and NaN keep scale 1; rows
+// below 2^-95 are scaled by at most 2^109.  Returns the inverse, exactly.
+__device__ __forceinline__ float f16_row_scale(uint32_t max_bits, float& scale) {
+  uint32_t e = max_bits >> 23;
+  e = e == 255u ? 141u : max(e, 32u);
+  scale = __uint_as_float((268u - e) << 23);
+  return __uint_as_float((e - 14u) << 23);
+}
+
+// Byte offset of value c of row r in an operand tile of `rows` rows: blocks of
+// 64 values, rows of 128 bytes, 16-byte chunks swizzled by the row (the layout
+// of a K-major operand with c along K, and of an MN-major one with r along K).
+__device__ __forceinline__ uint32_t tile_off(int r, int c, int rows) {
+  return (uint32_t)((c >> 6) * rows * 128 + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2);
+}
+
+// Writes a query row's f16 hi and lo parts into its operand tile.
+__device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVals& v, int kv, int r,
+                                             int half, int lane) {
+  float mx = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(v.a[j]), fabsf(v.b[j])));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v.c[j]));
+  float scale;
+  const float inv = f16_row_scale(__float_as_uint(warp_max(mx * a.qscale)), scale);
+  const int rr = r & 127, tile = r >> 7;
+  const uint32_t part = (uint32_t)((a.dqk + 63) / 64) * 128 * 128;
+  uint8_t* hi = a.qt + ((size_t)kv * a.mt + tile) * 2 * part;
+  if (lane == 0) a.qinv[((size_t)kv * a.mt + tile) * 128 + rr] = inv;
+  auto put = [&](int c, float x) {
+    x = x * a.qscale * scale;
+    const __half h = __float2half_rn(x);
+    const uint32_t off = tile_off(rr, c, 128);
+    *reinterpret_cast<__half*>(hi + off) = h;
+    *reinterpret_cast<__half*>(hi + part + off) = __float2half_rn(x - __half2float(h));
+  };
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (lane + 32 * j < half) {
+      put(lane + 32 * j, v.a[j]);
+      put(lane + 32 * j + half, v.b[j]);
+    }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (2 * half + lane + 32 * j < a.dqk) put(2 * half + lane + 32 * j, v.c[j]);
+}
 
 // One warp an item: n * nh query heads, then n * nkv key heads, then values.
 __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnArgs a) {
@@ -75,6 +132,7 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnA
     head_norm_rope(v, src, a.dqk, a.qn, a.eps, rp, i, a.err, lane);
     const int kv = h / a.G, r = i * a.G + h % a.G;
     head_store(v, a.qf + ((size_t)kv * a.R + r) * a.dqk, a.dqk, rp.half, a.qscale, lane);
+    if (a.ns > 0) store_q_tile(a, v, kv, r, rp.half, lane);
     return;
   }
   it -= a.n * a.nh;
@@ -124,31 +182,404 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 }
 
 // ------------------------------------------------------------------ split
-constexpr int kSplitWarps = 8;
+// One CTA: 128 query rows of a KV head against the keys [k0, k1) in tiles of NK.
+//
+// float32 products on f16 tensor cores: q, K and V rows are scaled by powers of
+// two and split into f16 hi + lo parts (22 bits); q.k and p.v are three products
+// each (lo.hi, hi.lo, hi.hi; lo.lo is below 2^-22).  A tile's small products are
+// accumulated before the large ones, and P V of a tile is added to the running
+// output in float32 registers, so tensor-core accumulation chains stay short.
+//
+// Warps: 8 converters (global float32 rows -> f16 hi/lo operand tiles in shared
+// memory with each row's scale), and two warpgroups that each run softmax on
+// whole rows (thread = row) and issue their own MMAs from one thread.
+//   COL = false (dv <= 128): the warpgroups take alternate tiles, each with its
+//     own (m, l, o), merged at the end: one's softmax overlaps the other's MMAs;
+//   COL = true: both follow every tile (the first one writes P) and keep half
+//     of the output columns each, as 256 do not fit a thread's registers.
+constexpr int kSplitThreads = 512;
+constexpr int kConvWarps = 8;
+constexpr int kScaleRing = 4;  // tiles whose scales are kept: > stages + 1
+// tensor-memory columns
+constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 
-__global__ void __launch_bounds__(kSplitWarps * 32) tree_split_kernel(const TreeAttnArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int sp = blockIdx.x, kv = blockIdx.y, lane = threadIdx.x & 31;
-  const int k0 = a.kbeg + sp * a.kper, k1 = min(a.L, k0 + a.kper);
-  for (int r = threadIdx.x >> 5; r < a.R; r += kSplitWarps) {
-    float q[8];
-    RowState s;
-    s.m = -INFINITY;
-    s.l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q[j] = 32 * j < a.dqk ? a.qf[((size_t)kv * a.R + r) * a.dqk + lane + 32 * j] : 0.f;
-      s.o[j] = 0.f;
+// f16 A and B, f32 accumulator, M = 128; B is MN-major when mn is set (bit 16).
+__device__ __forceinline__ uint32_t idesc_f16(int N, bool mn) {
+  return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+// MN-major operand tile, 128-byte swizzle: 64 values of MN a block, blocks `lead`
+// bytes apart, groups of 8 K rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Two values as packed f16 hi and lo parts.
+__device__ __forceinline__ void split_f16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = half2_bits(h);
+  lo = half2_bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+
+struct SplitSmem {
+  uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
+  uint32_t tmem;
+  float kinv[kScaleRing][64], vinv[kScaleRing][64];
+  float m[128], l[128];
+};
+
+static size_t split_stage_bytes(int NK, int dqk, int dv) {
+  return (size_t)NK * 256 * ((dqk + 63) / 64 + (dv + 63) / 64);
+}
+static size_t split_q_bytes(int dqk) { return (size_t)(dqk + 63) / 64 * 128 * 256; }
+
+// A wait that gives up marks the launch (error 1) and lets every later wait of
+// the thread through, so the barriers below are still met by every thread.
+struct Waiter {
+  int* err;
+  bool dead;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!dead && !mbar_wait_bounded(bar, parity)) {
+      dead = true;
+      set_dev_error(err, kErrMbarTimeout);
     }
-    for (int k = k0; k < k1; ++k)
-      row_step(s, q, a.kc + ((size_t)kv * a.cap + k) * a.dqk, a.vc + ((size_t)kv * a.cap + k) * a.dv,
-               a.dqk, a.dv, lane);
-    const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
-    if (lane == 0) a.part_ml[at] = make_float2(s.m, s.l);
+  }
+};
+
+template <int NK, bool COL>
+__global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const TreeAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smraw[];
+  __shared__ SplitSmem sh;
+  const uint32_t base = (smem_u32(smraw) + 1023u) & ~1023u;
+  uint8_t* sm = smraw + (base - smem_u32(smraw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int sp = blockIdx.x, mt = blockIdx.y, kv = blockIdx.z;
+  const int k0 = a.kbeg + sp * a.kper, k1 = min(a.L, k0 + a.kper);
+  const int nt = (k1 - k0 + NK - 1) / NK;  // >= 1 (host)
+  const int S = a.stages;
+  const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
+  const uint32_t qpart = (uint32_t)qb * 128 * 128, kpart = (uint32_t)qb * NK * 128,
+                 vpart = (uint32_t)vb * NK * 128;
+  const uint32_t koff = 2 * qpart, voff = koff + (uint32_t)S * 2 * kpart;
+
+  if (tid == 0) {
+    mbar_init(&sh.qfull, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.kfull[i], kConvWarps);
+      mbar_init(&sh.kempty[i], 1);
+      mbar_init(&sh.vfull[i], kConvWarps);
+      mbar_init(&sh.vempty[i], 1);
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.ofull[i], 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 0) tc5::alloc(&sh.tmem, 512);
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+  Waiter wait{a.err, false};
+  // every MMA has completed and its operands' memory is free
+  auto block_sync = [&]() { asm volatile("bar.sync 0, 512;" ::: "memory"); };
+
+  if (warp >= 8) {
+    // ---------------- converters
+    const int cw = warp - 8;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    constexpr int RPW = NK / kConvWarps;  // rows a warp of a tile
+    constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
+    const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
+    const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
+    if (cw == 0 && lane == 0) {
+      // the queries come from the previous launch; cached rows were final
+      // before it released this one
+      pdl_wait();
+      fence_proxy_async_global();
+      mbar_arrive_expect_tx(&sh.qfull, 2 * qpart);
+      bulk_load(sm, a.qt + ((size_t)kv * a.mt + mt) * 2 * qpart, 2 * qpart, &sh.qfull,
+                l2_policy_evict_last());
+    }
+    __syncwarp();
+    auto tile = [&](const float* src, int d, int row0, int nv, uint32_t dst, uint32_t part,
+                    float* inv, uint64_t* empty, uint32_t parity, bool first, uint64_t* full) {
+      float4 x[RPW][SL];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (32 * j < a.dv) a.part_o[at * a.dv + lane + 32 * j] = s.o[j];
+      for (int i = 0; i < RPW; ++i)
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          const int r = cw * RPW + i, c = 4 * (lane + 32 * s);
+          x[i][s] = r < nv && c < d
+                        ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)(row0 + r) * d + c))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      if (!first) wait(empty, parity);
+#pragma unroll
+      for (int i = 0; i < RPW; ++i) {
+        const int r = cw * RPW + i;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+          mx = max(max(mx, max(__float_as_uint(x[i][s].x) & 0x7FFFFFFFu,
+                               __float_as_uint(x[i][s].y) & 0x7FFFFFFFu)),
+                   max(__float_as_uint(x[i][s].z) & 0x7FFFFFFFu,
+                       __float_as_uint(x[i][s].w) & 0x7FFFFFFFu));
+        float scale;
+        const float iv = f16_row_scale(__reduce_max_sync(0xffffffffu, mx), scale);
+        if (lane == 0) inv[r] = iv;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          const int c = 4 * (lane + 32 * s);
+          if (c < d) {
+            uint2 hi, lo;
+            split_f16x2(x[i][s].x * scale, x[i][s].y * scale, hi.x, lo.x);
+            split_f16x2(x[i][s].z * scale, x[i][s].w * scale, hi.y, lo.y);
+            uint8_t* p = sm + dst + tile_off(r, c, NK);
+            *reinterpret_cast<uint2*>(p) = hi;
+            *reinterpret_cast<uint2*>(p + part) = lo;
+          }
+        }
+      }
+      tc5::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc5::mbar_arrive(full);
+    };
+    for (int t = 0; t < nt; ++t) {
+      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
+      const int row0 = k0 + t * NK, nv = min(NK, k1 - row0);
+      const uint32_t par = (uint32_t)(use - 1) & 1u;
+      tile(kc, a.dqk, row0, nv, koff + (uint32_t)s * 2 * kpart, kpart, sh.kinv[t % kScaleRing],
+           &sh.kempty[s], par, use == 0, &sh.kfull[s]);
+      tile(vc, a.dv, row0, nv, voff + (uint32_t)s * 2 * vpart, vpart, sh.vinv[t % kScaleRing],
+           &sh.vempty[s], par, use == 0, &sh.vfull[s]);
+    }
+    pdl_launch_dependents();
+    block_sync();
+  } else {
+    // ---------------- softmax and MMA issue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    float o[128];
+    float m = -INFINITY, l = 0.f;
+    const int wg = warp >> 2;
+    const int row = tid & 127, r = mt * 128 + row;
+    const bool issuer = (tid & 127) == 0 && (!COL || wg == 0);
+    const bool active = mt * 128 + (row & ~31) < a.R;  // warps of padding rows only keep step
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int cols = COL ? (wg == 0 ? min(a.dv, 128) : a.dv - 128) : a.dv;  // this warpgroup's
+#pragma unroll
+    for (int c = 0; c < 128; ++c) o[c] = 0.f;
+
+    // S(t) = Q K(t)^T into column block `slot`
+    auto issue_qk = [&](int t, int slot) {
+      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
+      wait(&sh.kfull[s], (uint32_t)use & 1u);
+      tc5::fence_after_sync();
+      const uint32_t id = idesc_f16(NK, false), d = tmem + kColS + 64u * (uint32_t)slot;
+      const uint64_t qh = tc5::desc_k_sw128(base), ql = tc5::desc_k_sw128(base + qpart);
+      const uint32_t kb = base + koff + (uint32_t)s * 2 * kpart;
+      const uint64_t kh = tc5::desc_k_sw128(kb), kl = tc5::desc_k_sw128(kb + kpart);
+      const int ks = a.dqk / 16;
+#pragma unroll 1
+      for (int k = 0; k < ks; ++k) {
+        const uint64_t oq = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                       ok = (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2);
+        tc5::mma_bf16(d, ql + oq, kh + ok, id, k > 0);
+        tc5::mma_bf16(d, qh + oq, kl + ok, id, 1u);
+      }
+#pragma unroll 1
+      for (int k = 0; k < ks; ++k)
+        tc5::mma_bf16(d, qh + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                      kh + (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2), id, 1u);
+      tc5::commit(&sh.sfull[slot]);
+      tc5::commit(&sh.kempty[s]);
+    };
+    // the tile's P V into this warpgroup's output columns
+    auto issue_pv = [&](int t, int slot) {
+      const int s = S == 1 ? 0 : t & 1;
+      const uint32_t id = idesc_f16(a.dv, true);
+      const uint32_t d = tmem + kColO + (COL ? 0u : 128u * (uint32_t)slot),
+                     ph = tmem + kColP + (COL ? 0u : 64u * (uint32_t)slot), pl = ph + NK / 2;
+      const uint32_t v = base + voff + (uint32_t)s * 2 * vpart;
+#pragma unroll
+      for (int k = 0; k < NK / 16; ++k) {
+        const uint64_t vh = desc_mn_sw128(v + k * 2048, NK * 128),
+                       vl = desc_mn_sw128(v + vpart + k * 2048, NK * 128);
+        mma_f16_ta(d, pl + 8 * k, vh, id, k > 0);
+        mma_f16_ta(d, ph + 8 * k, vl, id, 1u);
+      }
+#pragma unroll
+      for (int k = 0; k < NK / 16; ++k)
+        mma_f16_ta(d, ph + 8 * k, desc_mn_sw128(v + k * 2048, NK * 128), id, 1u);
+      tc5::commit(&sh.ofull[slot]);
+      tc5::commit(&sh.vempty[s]);
+    };
+    auto group_sync = [&]() {
+      if (COL)
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      else
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
+    };
+
+    const int step = COL ? 1 : 2;
+    const int first = COL ? 0 : wg;
+    if (issuer && first < nt) {
+      wait(&sh.qfull, 0u);
+      issue_qk(first, first);
+    }
+    __syncwarp();
+    float qinv = 1.f;
+    {
+      pdl_wait();
+      qinv = __ldcg(a.qinv + ((size_t)kv * a.mt + mt) * 128 + row);
+    }
+    for (int t = first, it = 0; t < nt; t += step, ++it) {
+      const int slot = t & 1;
+      const uint32_t ph2 = COL ? (uint32_t)(t >> 1) & 1u : (uint32_t)it & 1u;  // phase of the slot
+      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
+      if (COL) {
+        if (issuer && t + 1 < nt) issue_qk(t + 1, (t + 1) & 1);
+        __syncwarp();
+      }
+      wait(&sh.vfull[s], (uint32_t)use & 1u);  // the tile's scales (and V)
+      wait(&sh.sfull[slot], ph2);
+      tc5::fence_after_sync();
+      const float* kinv = sh.kinv[t % kScaleRing];
+      const float* vinv = sh.vinv[t % kScaleRing];
+      const int nv = min(NK, k1 - (k0 + t * NK));
+      float vmax = lane < NK ? vinv[lane] : 0.f;
+      if (NK == 64) vmax = fmaxf(vmax, vinv[lane + 32]);
+      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+      const float pscale = 16384.f / vmax;   // powers of two: exact
+      const float oscale = vmax * (1.f / 16384.f);
+      float corr = 1.f;
+      if (active) {
+        const uint32_t st = tmem + lanes + kColS + 64u * (uint32_t)slot;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NK; c += 16) {
+          uint32_t x[16];
+          tc5::ld16(st + c, x);
+          tc5::ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < nv) mx = fmaxf(mx, __uint_as_float(x[j]) * kinv[c + j]);
+        }
+        const float mn = fmaxf(m, mx * qinv);
+        corr = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        m = mn;
+        const float mb = mn == -INFINITY ? 0.f : mn;
+        l *= corr;
+        const uint32_t pt = tmem + lanes + kColP + (COL ? 0u : 64u * (uint32_t)slot);
+#pragma unroll
+        for (int c = 0; c < NK; c += 16) {
+          uint32_t x[16], hi[8], lo[8];
+          tc5::ld16(st + c, x);
+          tc5::ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int k = c + j + e;
+              p[e] = k < nv ? exp2f(fmaf(__uint_as_float(x[j + e]) * kinv[k], qinv, -mb)) : 0.f;
+              l += p[e];
+              p[e] *= vinv[k] * pscale;
+            }
+            split_f16x2(p[0], p[1], hi[j / 2], lo[j / 2]);
+          }
+          if (!COL || wg == 0) {
+            tmem_st8(pt + c / 2, hi);
+            tmem_st8(pt + NK / 2 + c / 2, lo);
+          }
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+      tc5::fence_before_sync();
+      group_sync();
+      if (issuer) {
+        tc5::fence_after_sync();
+        issue_pv(t, COL ? 0 : slot);
+        if (!COL && t + 2 < nt) issue_qk(t + 2, slot);
+      }
+      __syncwarp();
+      wait(&sh.ofull[COL ? 0 : slot], COL ? (uint32_t)t & 1u : ph2);
+      tc5::fence_after_sync();
+      if (active) {
+        const uint32_t ot = tmem + lanes + kColO + 128u * (uint32_t)(COL ? wg : slot);
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (c < cols) {
+            uint32_t x[16];
+            tc5::ld16(ot + c, x);
+            tc5::ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[c + j] = fmaf(o[c + j], corr, __uint_as_float(x[j]) * oscale);
+          }
+        }
+      }
+      tc5::fence_before_sync();
+    }
+    pdl_launch_dependents();
+    block_sync();
+    const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
+    if (!COL) {
+      // the second warpgroup hands its state over, columns apart by 128 rows
+      float* xo = reinterpret_cast<float*>(sm);
+      if (wg == 1) {
+        sh.m[row] = m;
+        sh.l[row] = l;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < cols) xo[c * 128 + row] = o[c];
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (wg == 0) {
+        const float m1 = sh.m[row], mn = fmaxf(m, m1);
+        const float c0 = m == -INFINITY ? 0.f : exp2f(m - mn), c1 = m1 == -INFINITY ? 0.f : exp2f(m1 - mn);
+        // a NaN sum has no maximum: it is kept by adding the sums themselves
+        l = (m == -INFINITY ? l : l * c0) + (m1 == -INFINITY ? sh.l[row] : sh.l[row] * c1);
+        m = mn;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c < cols) o[c] = o[c] * c0 + xo[c * 128 + row] * c1;
+      }
+    }
+    if ((COL || wg == 0) && r < a.R) {
+      if (!COL || wg == 0) a.part_ml[at] = make_float2(m, l);
+      float* dst = a.part_o + at * a.dv + (COL ? 128 * wg : 0);
+#pragma unroll
+      for (int c = 0; c < 128; c += 4)
+        if (c < cols) *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+    }
+    if (warp == 0) {
+      tc5::fence_after_sync();
+      tc5::dealloc(tmem, 512);
+    }
   }
 }
 
@@ -194,7 +625,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32) tree_finish_kernel(const Tr
   for (int sp = warp; sp < a.ns; sp += kFinishWarps) {
     const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
     const float2 ml = a.part_ml[at];
-    if (ml.x == -INFINITY) continue;
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;
     const float mn = fmaxf(s.m, ml.x);
     const float c0 = exp2f(s.m - mn), c1 = exp2f(ml.x - mn);
     s.m = mn;
@@ -240,17 +671,23 @@ struct TreePlan {
   int kbeg, ns, kper;
 };
 
+// Keys of a tile of the split kernel: operand tiles of 64 keys fit beside the
+// queries up to 128 dims, 32 above.
+static int split_nk(int dqk, int dv) { return dqk <= 128 && dv <= 128 ? 64 : 32; }
+
 // Splits of the cached keys all rows see: about one CTA per SM.
-static TreePlan tree_plan_splits(int nkv, int L, int window, int n) {
+static TreePlan tree_plan_splits(const mtp_attn_geom* g, int L, int n) {
   TreePlan p;
+  const int window = g->window;
   p.kbeg = window > 0 ? (int)std::min<int64_t>(L, std::max<int64_t>(0, (int64_t)L + n - window)) : 0;
   const int keys = L - p.kbeg;
+  const int mt = (n * (g->n_heads / g->n_kv_heads) + 127) / 128;
   p.ns = 0;
   p.kper = 0;
   if (keys > 0) {
-    int want = std::max(1, sm_count() / nkv);
+    int want = std::max(1, sm_count() / (g->n_kv_heads * mt));
     want = std::min(want, (keys + 31) / 32);
-    p.kper = (keys + want - 1) / want;
+    p.kper = ((keys + want - 1) / want + 15) / 16 * 16;
     p.ns = (keys + p.kper - 1) / p.kper;
   }
   return p;
@@ -258,6 +695,8 @@ static TreePlan tree_plan_splits(int nkv, int L, int window, int n) {
 
 struct TreeWs {
   float* qf;
+  uint8_t* qt;
+  float* qinv;
   int* dep;
   float2* ml;
   float* o;
@@ -276,10 +715,40 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
   const size_t rows = (size_t)n * g->n_heads;
   w.dep = reinterpret_cast<int*>(take(sizeof(int) * kTreeMax));
   w.qf = reinterpret_cast<float*>(take(4 * rows * g->head_dim_qk));
+  const size_t tiles = (size_t)g->n_kv_heads * ((n * (g->n_heads / g->n_kv_heads) + 127) / 128);
+  w.qt = take(tiles * split_q_bytes(g->head_dim_qk));
+  w.qinv = reinterpret_cast<float*>(take(tiles * 128 * 4));
   w.ml = reinterpret_cast<float2*>(take(8 * rows * ns));
   w.o = reinterpret_cast<float*>(take(4 * rows * ns * g->head_dim_v));
   w.bytes = off;
   return w;
+}
+
+template <int NK, bool COL>
+static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
+  static_assert(kScaleRing > 3, "scales outlive their tile's buffers");
+    static_assert(sizeof(SplitSmem) <= 4096, "beside the dynamic shared memory");
+  const size_t q = split_q_bytes(a.dqk), stage = split_stage_bytes(NK, a.dqk, a.dv), limit = 223 * 1024;
+  a.stages = q + 2 * stage + 1024 <= limit ? 2 : 1;
+  size_t smem = q + a.stages * stage;
+  if (!COL) smem = std::max(smem, (size_t)128 * a.dv * 4);  // the merge's buffer
+  smem += 1024;
+  static bool attr[64] = {};  // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr[dev]) {
+    e = cudaFuncSetAttribute(tree_split_kernel<NK, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)limit);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr[dev] = true;
+  }
+  return launch_pdl(tree_split_kernel<NK, COL>, dim3(a.ns, a.mt, a.nkv), kSplitThreads, smem, st, a);
+}
+
+static cudaError_t launch_split(const TreeAttnArgs& a, cudaStream_t st) {
+  if (split_nk(a.dqk, a.dv) == 64) return launch_split_as<64, false>(a, st);
+  return a.dv > 128 ? launch_split_as<32, true>(a, st) : launch_split_as<32, false>(a, st);
 }
 
 static mtp_status check_tree_geom(const mtp_attn_geom* g, int n) {
@@ -314,7 +783,7 @@ size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom* g, int32_t n, int32_t
       g->n_kv_heads > 64 || g->n_heads > 4096 || g->head_dim_qk < 1 || g->head_dim_qk > 256 ||
       g->head_dim_v < 1 || g->head_dim_v > 256)
     return 0;
-  return tree_ws(nullptr, g, n, tree_plan_splits(g->n_kv_heads, cache_len, g->window, n).ns).bytes;
+  return tree_ws(nullptr, g, n, tree_plan_splits(g, cache_len, n).ns).bytes;
 }
 
 mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, const float* d_qp,
@@ -376,7 +845,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
     a.rope.n_axes = 1;
     a.rope.half = g->rot_dim / 2;
   }
-  const TreePlan pl = tree_plan_splits(a.nkv, cache_len, a.window, n);
+  const TreePlan pl = tree_plan_splits(g, cache_len, n);
   const TreeWs w = tree_ws(d_ws, g, n, pl.ns);
   if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
     return fail(MTP_ERR_WORKSPACE, "attn_tree_sink: workspace too small");
@@ -392,10 +861,13 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   a.depth = tree->d_depth;
   a.out = d_out;
   a.qf = w.qf;
+  a.qt = w.qt;
+  a.qinv = w.qinv;
   a.dep = w.dep;
   a.part_o = w.o;
   a.part_ml = w.ml;
   a.R = n * a.G;
+  a.mt = (a.R + 127) / 128;
   a.ns = pl.ns;
   a.kbeg = pl.kbeg;
   a.kper = pl.kper;
@@ -405,7 +877,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   cudaError_t e = launch_pdl(tree_prep_kernel, dim3((items + kPrepThreads / 32 - 1) / (kPrepThreads / 32)),
                              kPrepThreads, 0, st, a);
   if (e == cudaSuccess && a.ns > 0)
-    e = launch_pdl(tree_split_kernel, dim3(a.ns, a.nkv), kSplitWarps * 32, 0, st, a);
+    e = launch_split(a, st);
   if (e == cudaSuccess)
     e = launch_pdl(tree_finish_kernel, dim3(a.nh, n), kFinishWarps * 32, 0, st, a);
   if (e != cudaSuccess) return cuda_fail(e, "attn_tree_sink launch");
