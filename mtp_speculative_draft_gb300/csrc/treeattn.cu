@@ -50,6 +50,7 @@ struct TreeAttnArgs {
   int R, mt;              // query rows of a KV head, tiles of 128 of them
   int ns, kbeg, kper;     // splits, first split key, keys a split
   int stages;             // K/V tile buffers of the split kernel
+  int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
 
@@ -84,16 +85,18 @@ __device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVa
   for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v.c[j]));
   float scale;
   const float inv = f16_row_scale(__float_as_uint(warp_max(mx * a.qscale)), scale);
-  const int rr = r & 127, tile = r >> 7;
+  const int rr = r & 127, tile = r >> 7, rows = 128 / a.rep;
   const uint32_t part = (uint32_t)((a.dqk + 63) / 64) * 128 * 128;
   uint8_t* hi = a.qt + ((size_t)kv * a.mt + tile) * 2 * part;
   if (lane == 0) a.qinv[((size_t)kv * a.mt + tile) * 128 + rr] = inv;
   auto put = [&](int c, float x) {
     x = x * a.qscale * scale;
-    const __half h = __float2half_rn(x);
-    const uint32_t off = tile_off(rr, c, 128);
-    *reinterpret_cast<__half*>(hi + off) = h;
-    *reinterpret_cast<__half*>(hi + part + off) = __float2half_rn(x - __half2float(h));
+    const __half h = __float2half_rn(x), l = __float2half_rn(x - __half2float(h));
+    for (int i = rr; i < 128; i += rows) {
+      const uint32_t off = tile_off(i, c, 128);
+      *reinterpret_cast<__half*>(hi + off) = h;
+      *reinterpret_cast<__half*>(hi + part + off) = l;
+    }
   };
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -197,8 +200,16 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 //     own (m, l, o), merged at the end: one's softmax overlaps the other's MMAs;
 //   COL = true: both follow every tile (the first one writes P) and keep half
 //     of the output columns each, as 256 do not fit a thread's registers.
+// Few query rows (64 or less) are repeated `rep` times in the 128 lanes: each
+// copy takes its own NK / rep keys of a tile (its P is 0 elsewhere), so all four
+// warps of a warpgroup share the exponentials; the copies' states are merged at
+// the end like the warpgroups'.
 constexpr int kSplitThreads = 512;
 constexpr int kConvWarps = 8;
+#ifndef MTP_TREE_AHEAD
+#define MTP_TREE_AHEAD 3
+#endif
+constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
 constexpr int kScaleRing = 4;  // tiles whose scales are kept: > stages + 1
 // tensor-memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
@@ -246,10 +257,38 @@ __device__ __forceinline__ void split_f16x2(float x, float y, uint32_t& hi, uint
   lo = half2_bits(__floats2half2_rn(x - f.x, y - f.y));
 }
 
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void load16(float (&r)[16], const float* p) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + j);
+    r[j] = v.x; r[j + 1] = v.y; r[j + 2] = v.z; r[j + 3] = v.w;
+  }
+}
+__device__ __forceinline__ float max16(const float (&v)[16]) {
+  float t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = fmaxf(v[j], v[j + 8]);
+  return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+}
+__device__ __forceinline__ float sum16(const float (&v)[16]) {
+  float t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) t[j] = v[j] + v[j + 8];
+  return ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+}
+
 struct SplitSmem {
   uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
   uint32_t tmem;
-  float kinv[kScaleRing][64], vinv[kScaleRing][64];
+  alignas(16) float kinv[kScaleRing][64], vinv[kScaleRing][64];
   float m[128], l[128];
 };
 
@@ -369,7 +408,18 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(full);
     };
+    // tiles on their way to L2 while earlier ones are converted
+    auto prefetch = [&](int t) {
+      if (t >= nt) return;
+      const int row0 = k0 + t * NK, nv = min(NK, k1 - row0);
+      l2_prefetch(kc + (size_t)row0 * a.dqk, (uint32_t)nv * a.dqk * 4);
+      l2_prefetch(vc + (size_t)row0 * a.dv, (uint32_t)nv * a.dv * 4);
+    };
+    const bool fetcher = cw == 1 && lane == 0;
+    if (fetcher)
+      for (int t = 0; t < kAhead; ++t) prefetch(t);
     for (int t = 0; t < nt; ++t) {
+      if (fetcher) prefetch(t + kAhead);
       const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
       const int row0 = k0 + t * NK, nv = min(NK, k1 - row0);
       const uint32_t par = (uint32_t)(use - 1) & 1u;
@@ -386,13 +436,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     float o[128];
     float m = -INFINITY, l = 0.f;
     const int wg = warp >> 2;
-    const int row = tid & 127, r = mt * 128 + row;
+    const int row = tid & 127;
     const bool issuer = (tid & 127) == 0 && (!COL || wg == 0);
-    const bool active = mt * 128 + (row & ~31) < a.R;  // warps of padding rows only keep step
+    const int lane_rows = 128 / a.rep;                 // rows of a copy
+    const int qrow = row & (lane_rows - 1);            // this lane's row of the tile
+    const int kw = NK / a.rep, kb = row / lane_rows * kw;  // this copy's keys of a tile
+    // warps of padding rows only keep step
+    const bool active = mt * 128 + (qrow & ~31) < a.R;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int cols = COL ? (wg == 0 ? min(a.dv, 128) : a.dv - 128) : a.dv;  // this warpgroup's
 #pragma unroll
     for (int c = 0; c < 128; ++c) o[c] = 0.f;
+    if (a.rep > 1 && (!COL || wg == 0)) {  // P of other copies' keys
+      const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+      for (int c = 0; c < NK; c += 8) tmem_st8(tmem + lanes + kColP + (COL ? 0u : 64u * wg) + c, z);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
 
     // S(t) = Q K(t)^T into column block `slot`
     auto issue_qk = [&](int t, int slot) {
@@ -455,7 +515,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     float qinv = 1.f;
     {
       pdl_wait();
-      qinv = __ldcg(a.qinv + ((size_t)kv * a.mt + mt) * 128 + row);
+      qinv = __ldcg(a.qinv + ((size_t)kv * a.mt + mt) * 128 + qrow);
     }
     for (int t = first, it = 0; t < nt; t += step, ++it) {
       const int slot = t & 1;
@@ -479,44 +539,51 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       float corr = 1.f;
       if (active) {
         const uint32_t st = tmem + lanes + kColS + 64u * (uint32_t)slot;
+        const bool whole = nv == NK;  // else the tile's last keys are padding
         float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NK; c += 16) {
+#pragma unroll 1
+        for (int c = kb; c < kb + kw; c += 16) {
           uint32_t x[16];
+          float ki[16];
           tc5::ld16(st + c, x);
+          load16(ki, kinv + c);
           tc5::ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < nv) mx = fmaxf(mx, __uint_as_float(x[j]) * kinv[c + j]);
+          for (int j = 0; j < 16; ++j) {
+            const float v = __uint_as_float(x[j]) * ki[j];
+            ki[j] = whole || c + j < nv ? v : -INFINITY;
+          }
+          mx = fmaxf(mx, max16(ki));
         }
         const float mn = fmaxf(m, mx * qinv);
-        corr = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        corr = mn == -INFINITY ? 1.f : ex2(m - mn);
         m = mn;
         const float mb = mn == -INFINITY ? 0.f : mn;
-        l *= corr;
+        float sum = 0.f;
         const uint32_t pt = tmem + lanes + kColP + (COL ? 0u : 64u * (uint32_t)slot);
-#pragma unroll
-        for (int c = 0; c < NK; c += 16) {
+#pragma unroll 1
+        for (int c = kb; c < kb + kw; c += 16) {
           uint32_t x[16], hi[8], lo[8];
+          float p[16], f[16];
           tc5::ld16(st + c, x);
+          load16(p, kinv + c);
+          load16(f, vinv + c);
           tc5::ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float p[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int k = c + j + e;
-              p[e] = k < nv ? exp2f(fmaf(__uint_as_float(x[j + e]) * kinv[k], qinv, -mb)) : 0.f;
-              l += p[e];
-              p[e] *= vinv[k] * pscale;
-            }
-            split_f16x2(p[0], p[1], hi[j / 2], lo[j / 2]);
+          for (int j = 0; j < 16; ++j) {
+            const float e = ex2(fmaf(__uint_as_float(x[j]) * p[j], qinv, -mb));
+            p[j] = whole || c + j < nv ? e : 0.f;
           }
+          sum += sum16(p);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            split_f16x2(p[j] * (f[j] * pscale), p[j + 1] * (f[j + 1] * pscale), hi[j / 2], lo[j / 2]);
           if (!COL || wg == 0) {
             tmem_st8(pt + c / 2, hi);
             tmem_st8(pt + NK / 2 + c / 2, lo);
           }
         }
+        l = fmaf(l, corr, sum);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
       tc5::fence_before_sync();
@@ -531,6 +598,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       tc5::fence_after_sync();
       if (active) {
         const uint32_t ot = tmem + lanes + kColO + 128u * (uint32_t)(COL ? wg : slot);
+        if (!__all_sync(0xffffffffu, corr == 1.f)) {  // some row's maximum rose
+#pragma unroll
+          for (int c = 0; c < 128; ++c) o[c] *= corr;
+        }
 #pragma unroll
         for (int c = 0; c < 128; c += 16) {
           if (c < cols) {
@@ -538,7 +609,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
             tc5::ld16(ot + c, x);
             tc5::ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[c + j] = fmaf(o[c + j], corr, __uint_as_float(x[j]) * oscale);
+            for (int j = 0; j < 16; ++j) o[c + j] = fmaf(__uint_as_float(x[j]), oscale, o[c + j]);
           }
         }
       }
@@ -546,35 +617,63 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     }
     pdl_launch_dependents();
     block_sync();
-    const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
+    // lane states to shared memory (column c of lane i at c * 129 + i): the
+    // warpgroups' states of a lane first, then each row's copies
+    float* xo = reinterpret_cast<float*>(sm) + (COL ? 128 * 129 * wg : 0) + row;
     if (!COL) {
-      // the second warpgroup hands its state over, columns apart by 128 rows
-      float* xo = reinterpret_cast<float*>(sm);
       if (wg == 1) {
         sh.m[row] = m;
         sh.l[row] = l;
 #pragma unroll
         for (int c = 0; c < 128; ++c)
-          if (c < cols) xo[c * 128 + row] = o[c];
+          if (c < cols) xo[c * 129] = o[c];
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (wg == 0) {
         const float m1 = sh.m[row], mn = fmaxf(m, m1);
-        const float c0 = m == -INFINITY ? 0.f : exp2f(m - mn), c1 = m1 == -INFINITY ? 0.f : exp2f(m1 - mn);
-        // a NaN sum has no maximum: it is kept by adding the sums themselves
-        l = (m == -INFINITY ? l : l * c0) + (m1 == -INFINITY ? sh.l[row] : sh.l[row] * c1);
+        // a state without any key, or of NaN logits alone, has no maximum
+        const float c0 = m == -INFINITY ? 1.f : ex2(m - mn), c1 = m1 == -INFINITY ? 1.f : ex2(m1 - mn);
+        l = l * c0 + sh.l[row] * c1;
         m = mn;
 #pragma unroll
         for (int c = 0; c < 128; ++c)
-          if (c < cols) o[c] = o[c] * c0 + xo[c * 128 + row] * c1;
+          if (c < cols) xo[c * 129] = o[c] * c0 + xo[c * 129] * c1;
       }
-    }
-    if ((COL || wg == 0) && r < a.R) {
-      if (!COL || wg == 0) a.part_ml[at] = make_float2(m, l);
-      float* dst = a.part_o + at * a.dv + (COL ? 128 * wg : 0);
+    } else {
 #pragma unroll
-      for (int c = 0; c < 128; c += 4)
-        if (c < cols) *reinterpret_cast<float4*>(dst + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      for (int c = 0; c < 128; ++c)
+        if (c < cols) xo[c * 129] = o[c];
+    }
+    if (wg == 0) {
+      sh.m[row] = m;
+      sh.l[row] = l;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float* xs = reinterpret_cast<const float*>(sm);
+    const int rows = min(lane_rows, a.R - mt * 128);
+    for (int i = warp; i < rows; i += 8) {
+      float w[4], mr = -INFINITY, lr = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        if (g < a.rep) mr = fmaxf(mr, sh.m[g * lane_rows + i]);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (g >= a.rep) break;
+        const float mg = sh.m[g * lane_rows + i];
+        w[g] = mg == -INFINITY ? 1.f : ex2(mg - mr);
+        lr += w[g] * sh.l[g * lane_rows + i];
+      }
+      const size_t at = ((size_t)kv * a.ns + sp) * a.R + mt * 128 + i;
+      if (lane == 0) a.part_ml[at] = make_float2(mr, lr);
+      for (int c = lane; c < a.dv; c += 32) {
+        float v = 0.f;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g >= a.rep) break;
+          v += w[g] * xs[c * 129 + g * lane_rows + i];
+        }
+        a.part_o[at * a.dv + c] = v;
+      }
     }
     if (warp == 0) {
       tc5::fence_after_sync();
@@ -731,7 +830,7 @@ static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   const size_t q = split_q_bytes(a.dqk), stage = split_stage_bytes(NK, a.dqk, a.dv), limit = 223 * 1024;
   a.stages = q + 2 * stage + 1024 <= limit ? 2 : 1;
   size_t smem = q + a.stages * stage;
-  if (!COL) smem = std::max(smem, (size_t)128 * a.dv * 4);  // the merge's buffer
+  smem = std::max(smem, (size_t)129 * (COL ? 256 : a.dv) * 4);  // the merge's buffer
   smem += 1024;
   static bool attr[64] = {};  // per device
   int dev = 0;
@@ -867,7 +966,8 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   a.part_o = w.o;
   a.part_ml = w.ml;
   a.R = n * a.G;
-  a.mt = (a.R + 127) / 128;
+  a.rep = a.R <= 32 && split_nk(a.dqk, a.dv) == 64 ? 4 : a.R <= 64 ? 2 : 1;
+  a.mt = (a.R + 127) / 128;  // 1 where rows are repeated
   a.ns = pl.ns;
   a.kbeg = pl.kbeg;
   a.kper = pl.kper;
