@@ -195,7 +195,7 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 //
 // Warps: 8 converters (global float32 rows -> f16 hi/lo operand tiles in shared
 // memory with each row's scale), and two warpgroups that each run softmax on
-// whole rows (thread = row) and issue their own MMAs from one thread.
+// whole rows (thread = row) and issue their own MMAs from their first warp.
 //   COL = false (dv <= 128): the warpgroups take alternate tiles, each with its
 //     own (m, l, o), merged at the end: one's softmax overlaps the other's MMAs;
 //   COL = true: both follow every tile (the first one writes P) and keep half
@@ -230,13 +230,31 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead)
   return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+// MMAs and commits are issued by a whole warp, of which one elected lane acts:
+// under uniform control flow the descriptors stay in uniform registers.
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 
@@ -316,7 +334,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   __shared__ SplitSmem sh;
   const uint32_t base = (smem_u32(smraw) + 1023u) & ~1023u;
   uint8_t* sm = smraw + (base - smem_u32(smraw));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int sp = blockIdx.x, mt = blockIdx.y, kv = blockIdx.z;
   const int k0 = a.kbeg + sp * a.kper, k1 = min(a.L, k0 + a.kper);
   const int nt = (k1 - k0 + NK - 1) / NK;  // >= 1 (host)
@@ -342,7 +361,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   Waiter wait{a.err, false};
   // every MMA has completed and its operands' memory is free
   auto block_sync = [&]() { asm volatile("bar.sync 0, 512;" ::: "memory"); };
@@ -350,7 +369,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   if (warp >= 8) {
     // ---------------- converters
     const int cw = warp - 8;
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     constexpr int RPW = NK / kConvWarps;  // rows a warp of a tile
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
@@ -365,45 +384,56 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
                 l2_policy_evict_last());
     }
     __syncwarp();
-    auto tile = [&](const float* src, int d, int row0, int nv, uint32_t dst, uint32_t part,
-                    float* inv, uint64_t* empty, uint32_t parity, bool first, uint64_t* full) {
-      float4 x[RPW][SL];
+    // A batch: four 16-byte words a lane, of RB rows of a K or V tile.  Batch b
+    // of the CTA: tile b / 4, K (b & 2 == 0) or V, first or second half of the
+    // warp's rows.
+    constexpr int RB = RPW / 2;
+    static_assert(RB * SL == 4, "a batch is four words a lane");
+    auto load = [&](float4 (&x)[4], int b) {
+      const int t = b >> 2;
+      const bool v = (b & 2) != 0;
+      const int d = v ? a.dv : a.dqk, r0 = cw * RPW + (b & 1) * RB;
+      const int row0 = k0 + t * NK, nv = k1 - row0;  // rows left (<= 0 past the last tile)
+      const float* src = (v ? vc : kc) + (size_t)(row0 + r0) * d;
 #pragma unroll
-      for (int i = 0; i < RPW; ++i)
+      for (int i = 0; i < RB; ++i)
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
-          const int r = cw * RPW + i, c = 4 * (lane + 32 * s);
-          x[i][s] = r < nv && c < d
-                        ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)(row0 + r) * d + c))
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+          const int c = 4 * (lane + 32 * s);
+          x[i * SL + s] = r0 + i < nv && c < d ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)i * d + c))
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-      if (!first) wait(empty, parity);
+    };
+    auto convert = [&](const float4 (&x)[4], int r0, int d, uint32_t dst, uint32_t part, float* inv) {
 #pragma unroll
-      for (int i = 0; i < RPW; ++i) {
-        const int r = cw * RPW + i;
+      for (int i = 0; i < RB; ++i) {
+        const int r = r0 + i;
         uint32_t mx = 0;
 #pragma unroll
-        for (int s = 0; s < SL; ++s)
-          mx = max(max(mx, max(__float_as_uint(x[i][s].x) & 0x7FFFFFFFu,
-                               __float_as_uint(x[i][s].y) & 0x7FFFFFFFu)),
-                   max(__float_as_uint(x[i][s].z) & 0x7FFFFFFFu,
-                       __float_as_uint(x[i][s].w) & 0x7FFFFFFFu));
+        for (int s = 0; s < SL; ++s) {
+          const float4 q = x[i * SL + s];
+          mx = max(max(mx, max(__float_as_uint(q.x) & 0x7FFFFFFFu, __float_as_uint(q.y) & 0x7FFFFFFFu)),
+                   max(__float_as_uint(q.z) & 0x7FFFFFFFu, __float_as_uint(q.w) & 0x7FFFFFFFu));
+        }
         float scale;
         const float iv = f16_row_scale(__reduce_max_sync(0xffffffffu, mx), scale);
         if (lane == 0) inv[r] = iv;
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
+          const float4 q = x[i * SL + s];
           const int c = 4 * (lane + 32 * s);
           if (c < d) {
             uint2 hi, lo;
-            split_f16x2(x[i][s].x * scale, x[i][s].y * scale, hi.x, lo.x);
-            split_f16x2(x[i][s].z * scale, x[i][s].w * scale, hi.y, lo.y);
+            split_f16x2(q.x * scale, q.y * scale, hi.x, lo.x);
+            split_f16x2(q.z * scale, q.w * scale, hi.y, lo.y);
             uint8_t* p = sm + dst + tile_off(r, c, NK);
             *reinterpret_cast<uint2*>(p) = hi;
             *reinterpret_cast<uint2*>(p + part) = lo;
           }
         }
       }
+    };
+    auto publish = [&](uint64_t* full) {
       tc5::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(full);
@@ -418,26 +448,47 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     const bool fetcher = cw == 1 && lane == 0;
     if (fetcher)
       for (int t = 0; t < kAhead; ++t) prefetch(t);
+    // two batches in flight while a third is converted
+    float4 x[4], y[4], z[4];
+    load(x, 0);
+    load(y, 1);
+    auto next = [&](int b) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[i] = x[i];
+        x[i] = y[i];
+      }
+      load(y, b + 2);
+    };
+#pragma unroll 1
     for (int t = 0; t < nt; ++t) {
       if (fetcher) prefetch(t + kAhead);
       const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
-      const int row0 = k0 + t * NK, nv = min(NK, k1 - row0);
       const uint32_t par = (uint32_t)(use - 1) & 1u;
-      tile(kc, a.dqk, row0, nv, koff + (uint32_t)s * 2 * kpart, kpart, sh.kinv[t % kScaleRing],
-           &sh.kempty[s], par, use == 0, &sh.kfull[s]);
-      tile(vc, a.dv, row0, nv, voff + (uint32_t)s * 2 * vpart, vpart, sh.vinv[t % kScaleRing],
-           &sh.vempty[s], par, use == 0, &sh.vfull[s]);
+      const int r0 = cw * RPW;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int d = v ? a.dv : a.dqk;
+        const uint32_t part = v ? vpart : kpart, dst = (v ? voff : koff) + (uint32_t)s * 2 * part;
+        float* inv = v ? sh.vinv[t % kScaleRing] : sh.kinv[t % kScaleRing];
+        next(4 * t + 2 * v);
+        if (use > 0) wait(v ? &sh.vempty[s] : &sh.kempty[s], par);
+        convert(z, r0, d, dst, part, inv);
+        next(4 * t + 2 * v + 1);
+        convert(z, r0 + RB, d, dst, part, inv);
+        publish(v ? &sh.vfull[s] : &sh.kfull[s]);
+      }
     }
     pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     float o[128];
     float m = -INFINITY, l = 0.f;
     const int wg = warp >> 2;
     const int row = tid & 127;
-    const bool issuer = (tid & 127) == 0 && (!COL || wg == 0);
+    const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues MMAs
     const int lane_rows = 128 / a.rep;                 // rows of a copy
     const int qrow = row & (lane_rows - 1);            // this lane's row of the tile
     const int kw = NK / a.rep, kb = row / lane_rows * kw;  // this copy's keys of a tile
@@ -468,15 +519,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       for (int k = 0; k < ks; ++k) {
         const uint64_t oq = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
                        ok = (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2);
-        tc5::mma_bf16(d, ql + oq, kh + ok, id, k > 0);
-        tc5::mma_bf16(d, qh + oq, kl + ok, id, 1u);
+        mma_f16_ss(d, ql + oq, kh + ok, id, k > 0);
+        mma_f16_ss(d, qh + oq, kl + ok, id, 1u);
       }
 #pragma unroll 1
       for (int k = 0; k < ks; ++k)
-        tc5::mma_bf16(d, qh + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+        mma_f16_ss(d, qh + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
                       kh + (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2), id, 1u);
-      tc5::commit(&sh.sfull[slot]);
-      tc5::commit(&sh.kempty[s]);
+      commit_elect(&sh.sfull[slot]);
+      commit_elect(&sh.kempty[s]);
     };
     // the tile's P V into this warpgroup's output columns
     auto issue_pv = [&](int t, int slot) {
@@ -489,14 +540,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       for (int k = 0; k < NK / 16; ++k) {
         const uint64_t vh = desc_mn_sw128(v + k * 2048, NK * 128),
                        vl = desc_mn_sw128(v + vpart + k * 2048, NK * 128);
-        mma_f16_ta(d, pl + 8 * k, vh, id, k > 0);
-        mma_f16_ta(d, ph + 8 * k, vl, id, 1u);
+        mma_f16_ts(d, pl + 8 * k, vh, id, k > 0);
+        mma_f16_ts(d, ph + 8 * k, vl, id, 1u);
       }
 #pragma unroll
       for (int k = 0; k < NK / 16; ++k)
-        mma_f16_ta(d, ph + 8 * k, desc_mn_sw128(v + k * 2048, NK * 128), id, 1u);
-      tc5::commit(&sh.ofull[slot]);
-      tc5::commit(&sh.vempty[s]);
+        mma_f16_ts(d, ph + 8 * k, desc_mn_sw128(v + k * 2048, NK * 128), id, 1u);
+      commit_elect(&sh.ofull[slot]);
+      commit_elect(&sh.vempty[s]);
     };
     auto group_sync = [&]() {
       if (COL)
