@@ -514,18 +514,31 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       const uint64_t qh = tc5::desc_k_sw128(base), ql = tc5::desc_k_sw128(base + qpart);
       const uint32_t kb = base + koff + (uint32_t)s * 2 * kpart;
       const uint64_t kh = tc5::desc_k_sw128(kb), kl = tc5::desc_k_sw128(kb + kpart);
-      const int ks = a.dqk / 16;
+      // blocks of 64 dims; dims come in 32s, so the last block may be half one
 #pragma unroll 1
-      for (int k = 0; k < ks; ++k) {
-        const uint64_t oq = (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
-                       ok = (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2);
-        mma_f16_ss(d, ql + oq, kh + ok, id, k > 0);
-        mma_f16_ss(d, qh + oq, kl + ok, id, 1u);
+      for (int b = 0; b < qb; ++b) {
+        const uint64_t oq = (uint64_t)(b * 1024), ok = (uint64_t)(b * NK * 8);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          mma_f16_ss(d, ql + oq + 2 * k, kh + ok + 2 * k, id, b + k > 0);
+          mma_f16_ss(d, qh + oq + 2 * k, kl + ok + 2 * k, id, 1u);
+        }
+        if (64 * b + 32 < a.dqk)
+#pragma unroll
+          for (int k = 2; k < 4; ++k) {
+            mma_f16_ss(d, ql + oq + 2 * k, kh + ok + 2 * k, id, 1u);
+            mma_f16_ss(d, qh + oq + 2 * k, kl + ok + 2 * k, id, 1u);
+          }
       }
 #pragma unroll 1
-      for (int k = 0; k < ks; ++k)
-        mma_f16_ss(d, qh + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
-                      kh + (uint64_t)((k >> 2) * (NK * 8) + (k & 3) * 2), id, 1u);
+      for (int b = 0; b < qb; ++b) {
+        const uint64_t oq = (uint64_t)(b * 1024), ok = (uint64_t)(b * NK * 8);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) mma_f16_ss(d, qh + oq + 2 * k, kh + ok + 2 * k, id, 1u);
+        if (64 * b + 32 < a.dqk)
+#pragma unroll
+          for (int k = 2; k < 4; ++k) mma_f16_ss(d, qh + oq + 2 * k, kh + ok + 2 * k, id, 1u);
+      }
       commit_elect(&sh.sfull[slot]);
       commit_elect(&sh.kempty[s]);
     };
