@@ -57,12 +57,12 @@ struct TreeAttnArgs {
 // ------------------------------------------------------------------ prep
 constexpr int kPrepThreads = 128;
 
-// Power-of-two scale of a row for its f16 parts: the row's largest |x|, whose
-// float bits are given, lands in [2^14, 2^15), so hi + lo hold 22 bits of every
-// element down to 2^-16 of the largest.  Infinity and NaN keep scale 1; rows
-// below 2^-95 are scaled by at most 2^109.  Returns the inverse, exactly.
-__device__ __forceinline__ float f16_row_scale(uint32_t max_bits, float& scale) {
-  uint32_t e = max_bits >> 23;
+// Power-of-two scale of values for their f16 parts: the largest |x| lands in
+// [2^14, 2^15), so hi + lo hold 22 bits of every element down to 2^-16 of the
+// largest.  Infinity keeps scale 1; values below 2^-95 are scaled by at most
+// 2^109.  Returns the inverse, exactly.
+__device__ __forceinline__ float f16_scale(float largest, float& scale) {
+  uint32_t e = __float_as_uint(largest) >> 23;
   e = e == 255u ? 141u : max(e, 32u);
   scale = __uint_as_float((268u - e) << 23);
   return __uint_as_float((e - 14u) << 23);
@@ -84,7 +84,7 @@ __device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVa
 #pragma unroll
   for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v.c[j]));
   float scale;
-  const float inv = f16_row_scale(__float_as_uint(warp_max(mx * a.qscale)), scale);
+  const float inv = f16_scale(warp_max(mx * a.qscale), scale);
   const int rr = r & 127, tile = r >> 7, rows = 128 / a.rep;
   const uint32_t part = (uint32_t)((a.dqk + 63) / 64) * 128 * 128;
   uint8_t* hi = a.qt + ((size_t)kv * a.mt + tile) * 2 * part;
@@ -187,14 +187,21 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 // ------------------------------------------------------------------ split
 // One CTA: 128 query rows of a KV head against the keys [k0, k1) in tiles of NK.
 //
-// float32 products on f16 tensor cores: q, K and V rows are scaled by powers of
-// two and split into f16 hi + lo parts (22 bits); q.k and p.v are three products
-// each (lo.hi, hi.lo, hi.hi; lo.lo is below 2^-22).  A tile's small products are
-// accumulated before the large ones, and P V of a tile is added to the running
-// output in float32 registers, so tensor-core accumulation chains stay short.
+// float32 products on f16 tensor cores: each query row, K tile and V tile is
+// scaled by a power of two and split into f16 hi + lo parts (22 bits); q.k and
+// p.v are three products each (lo.hi, hi.lo, hi.hi; lo.lo is below 2^-22).  A
+// tile's small products are accumulated before the large ones, and P V of a tile
+// is added to the running output in float32 registers, so tensor-core
+// accumulation chains stay short.  A tile's largest |x| becomes [2^14, 2^15):
+// elements keep 22 bits down to 2^-16 of it and an absolute error of 2^-39 of it
+// below that.
+// Weights are relative to a reference `ref`, set so that the first tile's largest
+// weight is 2^8; it moves only when a weight would pass 2^15.5 (f16 ends at
+// 2^16), so later tiles need no maximum before their exponentials and no
+// rescaling of the output.
 //
 // Warps: 8 converters (global float32 rows -> f16 hi/lo operand tiles in shared
-// memory with each row's scale), and two warpgroups that each run softmax on
+// memory with the tile's scale), and two warpgroups that each run softmax on
 // whole rows (thread = row) and issue their own MMAs from their first warp.
 //   COL = false (dv <= 128): the warpgroups take alternate tiles, each with its
 //     own (m, l, o), merged at the end: one's softmax overlaps the other's MMAs;
@@ -211,6 +218,12 @@ constexpr int kConvWarps = 8;
 #endif
 constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
 constexpr int kScaleRing = 4;  // tiles whose scales are kept: > stages + 1
+constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
+constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
 // tensor-memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 
@@ -267,12 +280,36 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
+// Two floats in one 64-bit register pair (packed float32 arithmetic).
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Two values as packed f16 hi and lo parts.
-__device__ __forceinline__ void split_f16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
+__device__ __forceinline__ void split_f16x2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  const float2 x = unpack2(v);
+  const __half2 h = __floats2half2_rn(x.x, x.y);
   const float2 f = __half22float2(h);
+  const float2 d = unpack2(fma2(pack2(f.x, f.y), pack2(-1.f, -1.f), v));
   hi = half2_bits(h);
-  lo = half2_bits(__floats2half2_rn(x - f.x, y - f.y));
+  lo = half2_bits(__floats2half2_rn(d.x, d.y));
 }
 
 __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
@@ -282,13 +319,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ void load16(float (&r)[16], const float* p) {
-#pragma unroll
-  for (int j = 0; j < 16; j += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + j);
-    r[j] = v.x; r[j + 1] = v.y; r[j + 2] = v.z; r[j + 3] = v.w;
-  }
 }
 __device__ __forceinline__ float max16(const float (&v)[16]) {
   float t[8];
@@ -306,7 +336,8 @@ __device__ __forceinline__ float sum16(const float (&v)[16]) {
 struct SplitSmem {
   uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
   uint32_t tmem;
-  alignas(16) float kinv[kScaleRing][64], vinv[kScaleRing][64];
+  alignas(16) float wmax[2][kConvWarps];          // largest |x| of each converter warp's rows, K and V
+  float kinv[kScaleRing], vinv[kScaleRing];       // a tile's inverse scales
   float m[128], l[128];
 };
 
@@ -369,7 +400,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   if (warp >= 8) {
     // ---------------- converters
     const int cw = warp - 8;
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int RPW = NK / kConvWarps;  // rows a warp of a tile
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
@@ -384,54 +415,63 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
                 l2_policy_evict_last());
     }
     __syncwarp();
-    // A batch: four 16-byte words a lane, of RB rows of a K or V tile.  Batch b
-    // of the CTA: tile b / 4, K (b & 2 == 0) or V, first or second half of the
-    // warp's rows.
-    constexpr int RB = RPW / 2;
-    static_assert(RB * SL == 4, "a batch is four words a lane");
-    auto load = [&](float4 (&x)[4], int b) {
-      const int t = b >> 2;
-      const bool v = (b & 2) != 0;
-      const int d = v ? a.dv : a.dqk, r0 = cw * RPW + (b & 1) * RB;
-      const int row0 = k0 + t * NK, nv = k1 - row0;  // rows left (<= 0 past the last tile)
-      const float* src = (v ? vc : kc) + (size_t)(row0 + r0) * d;
+    // This warp's rows of a K or V tile, eight 16-byte words a lane.
+    static_assert(RPW * SL == 8, "eight words a lane");
+    auto load = [&](float4 (&x)[8], const float* src, int d, int t) {
+      const int nv = k1 - (k0 + t * NK) - cw * RPW;  // rows left (<= 0 past the last tile)
+      src += (size_t)(k0 + t * NK + cw * RPW) * d + 4 * lane;
+      if (nv >= RPW) {
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
+        for (int i = 0; i < RPW; ++i)
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
-          const int c = 4 * (lane + 32 * s);
-          x[i * SL + s] = r0 + i < nv && c < d ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)i * d + c))
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+          for (int s = 0; s < SL; ++s)
+            x[i * SL + s] = 4 * (lane + 32 * s) < d ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < RPW; ++i)
+#pragma unroll
+          for (int s = 0; s < SL; ++s)
+            x[i * SL + s] = i < nv && 4 * (lane + 32 * s) < d
+                                ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     };
-    auto convert = [&](const float4 (&x)[4], int r0, int d, uint32_t dst, uint32_t part, float* inv) {
+    // The tile's scale: the largest |x| of all converter warps' rows.
+    auto scale_of = [&](const float4 (&x)[8], int v, float* inv) {
+      float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const int r = r0 + i;
-        uint32_t mx = 0;
+      for (int i = 0; i < 8; ++i)
+        mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x[i].x)), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+      if (lane == 0) sh.wmax[v][cw] = mx;
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      const float4 a0 = *reinterpret_cast<const float4*>(&sh.wmax[v][0]),
+                   a1 = *reinterpret_cast<const float4*>(&sh.wmax[v][4]);
+      mx = fmaxf(fmaxf(fmaxf(a0.x, a0.y), fmaxf(a0.z, a0.w)), fmaxf(fmaxf(a1.x, a1.y), fmaxf(a1.z, a1.w)));
+      float scale;
+      const float iv = f16_scale(mx, scale);
+      if (cw == 0 && lane == 0) *inv = iv;
+      return scale;
+    };
+    // offset of this lane's words in row r: RPW rows start at a multiple of 4
+    auto convert = [&](const float4 (&x)[8], int d, uint8_t* dst, uint32_t part, float scale) {
+      const uint64_t s2 = pack2(scale, scale);
+#pragma unroll
+      for (int i = 0; i < RPW; ++i)
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
-          const float4 q = x[i * SL + s];
-          mx = max(max(mx, max(__float_as_uint(q.x) & 0x7FFFFFFFu, __float_as_uint(q.y) & 0x7FFFFFFFu)),
-                   max(__float_as_uint(q.z) & 0x7FFFFFFFu, __float_as_uint(q.w) & 0x7FFFFFFFu));
-        }
-        float scale;
-        const float iv = f16_row_scale(__reduce_max_sync(0xffffffffu, mx), scale);
-        if (lane == 0) inv[r] = iv;
-#pragma unroll
-        for (int s = 0; s < SL; ++s) {
-          const float4 q = x[i * SL + s];
           const int c = 4 * (lane + 32 * s);
+          const float4 q = x[i * SL + s];
+          uint2 hi, lo;
+          split_f16x2(mul2(pack2(q.x, q.y), s2), hi.x, lo.x);
+          split_f16x2(mul2(pack2(q.z, q.w), s2), hi.y, lo.y);
+          uint8_t* p = dst + tile_off(cw * RPW + i, c, NK);
           if (c < d) {
-            uint2 hi, lo;
-            split_f16x2(q.x * scale, q.y * scale, hi.x, lo.x);
-            split_f16x2(q.z * scale, q.w * scale, hi.y, lo.y);
-            uint8_t* p = sm + dst + tile_off(r, c, NK);
             *reinterpret_cast<uint2*>(p) = hi;
             *reinterpret_cast<uint2*>(p + part) = lo;
           }
         }
-      }
     };
     auto publish = [&](uint64_t* full) {
       tc5::fence_proxy_async_smem();
@@ -448,44 +488,33 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     const bool fetcher = cw == 1 && lane == 0;
     if (fetcher)
       for (int t = 0; t < kAhead; ++t) prefetch(t);
-    // two batches in flight while a third is converted
-    float4 x[4], y[4], z[4];
-    load(x, 0);
-    load(y, 1);
-    auto next = [&](int b) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[i] = x[i];
-        x[i] = y[i];
-      }
-      load(y, b + 2);
-    };
+    // the next tile's K rows are on their way while this tile's V is converted
+    float4 xk[8], xv[8];
+    load(xk, kc, a.dqk, 0);
+    load(xv, vc, a.dv, 0);
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
       if (fetcher) prefetch(t + kAhead);
       const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
       const uint32_t par = (uint32_t)(use - 1) & 1u;
-      const int r0 = cw * RPW;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int d = v ? a.dv : a.dqk;
-        const uint32_t part = v ? vpart : kpart, dst = (v ? voff : koff) + (uint32_t)s * 2 * part;
-        float* inv = v ? sh.vinv[t % kScaleRing] : sh.kinv[t % kScaleRing];
-        next(4 * t + 2 * v);
-        if (use > 0) wait(v ? &sh.vempty[s] : &sh.kempty[s], par);
-        convert(z, r0, d, dst, part, inv);
-        next(4 * t + 2 * v + 1);
-        convert(z, r0 + RB, d, dst, part, inv);
-        publish(v ? &sh.vfull[s] : &sh.kfull[s]);
-      }
+      float sc = scale_of(xk, 0, &sh.kinv[t % kScaleRing]);
+      if (use > 0) wait(&sh.kempty[s], par);
+      convert(xk, a.dqk, sm + koff + (uint32_t)s * 2 * kpart, kpart, sc);
+      publish(&sh.kfull[s]);
+      load(xk, kc, a.dqk, t + 1);
+      sc = scale_of(xv, 1, &sh.vinv[t % kScaleRing]);
+      if (use > 0) wait(&sh.vempty[s], par);
+      convert(xv, a.dv, sm + voff + (uint32_t)s * 2 * vpart, vpart, sc);
+      publish(&sh.vfull[s]);
+      load(xv, vc, a.dv, t + 1);
     }
     pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     float o[128];
-    float m = -INFINITY, l = 0.f;
+    float ref = 0.f, l = 0.f;
     const int wg = warp >> 2;
     const int row = tid & 127;
     const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues MMAs
@@ -592,62 +621,74 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       wait(&sh.vfull[s], (uint32_t)use & 1u);  // the tile's scales (and V)
       wait(&sh.sfull[slot], ph2);
       tc5::fence_after_sync();
-      const float* kinv = sh.kinv[t % kScaleRing];
-      const float* vinv = sh.vinv[t % kScaleRing];
-      const int nv = min(NK, k1 - (k0 + t * NK));
-      float vmax = lane < NK ? vinv[lane] : 0.f;
-      if (NK == 64) vmax = fmaxf(vmax, vinv[lane + 32]);
-      vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-      const float pscale = 16384.f / vmax;   // powers of two: exact
-      const float oscale = vmax * (1.f / 16384.f);
-      float corr = 1.f;
+      const int nv = min(NK, k1 - (k0 + t * NK)) - kb;  // this copy's keys before the padding
+      const float cs = sh.kinv[t % kScaleRing] * qinv;   // S to logits: a power of two
+      const float oscale = sh.vinv[t % kScaleRing];
       if (active) {
-        const uint32_t st = tmem + lanes + kColS + 64u * (uint32_t)slot;
-        const bool whole = nv == NK;  // else the tile's last keys are padding
-        float mx = -INFINITY;
+        const uint32_t st = tmem + lanes + kColS + 64u * (uint32_t)slot + kb;
+        const uint32_t pt = tmem + lanes + kColP + (COL ? 0u : 64u * (uint32_t)slot) + kb / 2;
+        // largest S of the copy's keys
+        auto scan = [&]() {
+          float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = kb; c < kb + kw; c += 16) {
-          uint32_t x[16];
-          float ki[16];
-          tc5::ld16(st + c, x);
-          load16(ki, kinv + c);
-          tc5::ld_wait();
+          for (int c = 0; c < kw; c += 16) {
+            uint32_t x[16];
+            float f[16];
+            tc5::ld16(st + c, x);
+            tc5::ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float v = __uint_as_float(x[j]) * ki[j];
-            ki[j] = whole || c + j < nv ? v : -INFINITY;
+            for (int j = 0; j < 16; ++j) f[j] = c + j < nv ? __uint_as_float(x[j]) : -INFINITY;
+            mx = fmaxf(mx, max16(f));
           }
-          mx = fmaxf(mx, max16(ki));
-        }
-        const float mn = fmaxf(m, mx * qinv);
-        corr = mn == -INFINITY ? 1.f : ex2(m - mn);
-        m = mn;
-        const float mb = mn == -INFINITY ? 0.f : mn;
-        float sum = 0.f;
-        const uint32_t pt = tmem + lanes + kColP + (COL ? 0u : 64u * (uint32_t)slot);
+          return mx;
+        };
+        // P = 2^(logit - ref) as f16 parts; returns its sum and the largest S
+        float mx;
+        auto weights = [&](auto whole) {
+          float sum = 0.f;
+          mx = -INFINITY;
+          const float nref = -ref;
 #pragma unroll 1
-        for (int c = kb; c < kb + kw; c += 16) {
-          uint32_t x[16], hi[8], lo[8];
-          float p[16], f[16];
-          tc5::ld16(st + c, x);
-          load16(p, kinv + c);
-          load16(f, vinv + c);
-          tc5::ld_wait();
+          for (int c = 0; c < kw; c += 16) {
+            uint32_t x[16], hi[8], lo[8];
+            float p[16];
+            tc5::ld16(st + c, x);
+            tc5::ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float e = ex2(fmaf(__uint_as_float(x[j]) * p[j], qinv, -mb));
-            p[j] = whole || c + j < nv ? e : 0.f;
-          }
-          sum += sum16(p);
+            for (int j = 0; j < 16; ++j) p[j] = whole.value || c + j < nv ? __uint_as_float(x[j]) : -INFINITY;
+            mx = fmaxf(mx, max16(p));
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            split_f16x2(p[j] * (f[j] * pscale), p[j + 1] * (f[j + 1] * pscale), hi[j / 2], lo[j / 2]);
-          if (!COL || wg == 0) {
-            tmem_st8(pt + c / 2, hi);
-            tmem_st8(pt + NK / 2 + c / 2, lo);
+            for (int j = 0; j < 16; ++j) {
+              const float e = ex2(fmaf(__uint_as_float(x[j]), cs, nref));
+              p[j] = whole.value || c + j < nv ? e : 0.f;
+            }
+            sum += sum16(p);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) split_f16x2(pack2(p[j], p[j + 1]), hi[j / 2], lo[j / 2]);
+            if (!COL || wg == 0) {
+              tmem_st8(pt + c / 2, hi);
+              tmem_st8(pt + NK / 2 + c / 2, lo);
+            }
           }
+          return sum;
+        };
+        auto pass = [&]() { return nv >= kw ? weights(Flag<true>{}) : weights(Flag<false>{}); };
+        if (it == 0) {
+          mx = scan();
+          ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
         }
-        l = fmaf(l, corr, sum);
+        float sum = pass();
+        const float top = mx * cs;
+        const bool move = top - ref > kRefMost;
+        if (__any_sync(0xffffffffu, move)) {
+          const float nref = move ? top - kRefBits : ref, corr = ex2(ref - nref);
+          ref = nref;
+          l *= corr;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) o[c] *= corr;
+          sum = pass();
+        }
+        l += sum;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
       tc5::fence_before_sync();
@@ -662,10 +703,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       tc5::fence_after_sync();
       if (active) {
         const uint32_t ot = tmem + lanes + kColO + 128u * (uint32_t)(COL ? wg : slot);
-        if (!__all_sync(0xffffffffu, corr == 1.f)) {  // some row's maximum rose
-#pragma unroll
-          for (int c = 0; c < 128; ++c) o[c] *= corr;
-        }
 #pragma unroll
         for (int c = 0; c < 128; c += 16) {
           if (c < cols) {
@@ -681,6 +718,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     }
     pdl_launch_dependents();
     block_sync();
+    float m = l == 0.f ? -INFINITY : ref;  // the state's reference; none without a key
     // lane states to shared memory (column c of lane i at c * 129 + i): the
     // warpgroups' states of a lane first, then each row's copies
     float* xo = reinterpret_cast<float*>(sm) + (COL ? 128 * 129 * wg : 0) + row;
