@@ -232,35 +232,37 @@ __device__ __forceinline__ uint32_t idesc_f16(int N, bool mn) {
   return (1u << 4) | (mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
 }
 
-// MN-major operand tile, 128-byte swizzle: 64 values of MN a block, blocks `lead`
-// bytes apart, groups of 8 K rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory operand descriptors as two words: the low one holds the address
+// (and the leading offset), the high one is a constant (group offset 1024 bytes,
+// 128-byte swizzle), so a step along an operand is one 32-bit addition.
+// K-major tiles: rows of 128 bytes.  MN-major tiles: 64 values of MN a block,
+// blocks `lead` bytes apart, groups of 8 K rows 1024 bytes apart.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lead) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
 
 // MMAs and commits are issued by a whole warp, of which one elected lane acts:
 // under uniform control flow the descriptors stay in uniform registers.
 // D[tmem] (+)= A[smem] * B[smem]^T
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " mov.b64 b, {%2, %5};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void commit_elect(uint64_t* bar) {
@@ -540,33 +542,27 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       wait(&sh.kfull[s], (uint32_t)use & 1u);
       tc5::fence_after_sync();
       const uint32_t id = idesc_f16(NK, false), d = tmem + kColS + 64u * (uint32_t)slot;
-      const uint64_t qh = tc5::desc_k_sw128(base), ql = tc5::desc_k_sw128(base + qpart);
-      const uint32_t kb = base + koff + (uint32_t)s * 2 * kpart;
-      const uint64_t kh = tc5::desc_k_sw128(kb), kl = tc5::desc_k_sw128(kb + kpart);
-      // blocks of 64 dims; dims come in 32s, so the last block may be half one
+      uint32_t qh = desc_k(base), kh = desc_k(base + koff + (uint32_t)s * 2 * kpart);
+      const uint32_t ql = qpart >> 4, kl = kpart >> 4;  // steps from hi to lo
+      const int n2 = a.dqk / 32;
+      // pairs of 16-dim steps (dims come in 32s): the small products, then the large
+      uint32_t q = qh, k = kh;
 #pragma unroll 1
-      for (int b = 0; b < qb; ++b) {
-        const uint64_t oq = (uint64_t)(b * 1024), ok = (uint64_t)(b * NK * 8);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mma_f16_ss(d, ql + oq + 2 * k, kh + ok + 2 * k, id, b + k > 0);
-          mma_f16_ss(d, qh + oq + 2 * k, kl + ok + 2 * k, id, 1u);
-        }
-        if (64 * b + 32 < a.dqk)
-#pragma unroll
-          for (int k = 2; k < 4; ++k) {
-            mma_f16_ss(d, ql + oq + 2 * k, kh + ok + 2 * k, id, 1u);
-            mma_f16_ss(d, qh + oq + 2 * k, kl + ok + 2 * k, id, 1u);
-          }
+      for (int b = 0; b < n2; ++b) {
+        mma_f16_ss(d, q + ql, k, id, b > 0);
+        mma_f16_ss(d, q, k + kl, id, 1u);
+        mma_f16_ss(d, q + ql + 2, k + 2, id, 1u);
+        mma_f16_ss(d, q + 2, k + kl + 2, id, 1u);
+        q += b & 1 ? 1020 : 4;  // the next half of a 128-byte row, or the next block of 64 dims
+        k += b & 1 ? NK * 8 - 4 : 4;
       }
+      q = qh, k = kh;
 #pragma unroll 1
-      for (int b = 0; b < qb; ++b) {
-        const uint64_t oq = (uint64_t)(b * 1024), ok = (uint64_t)(b * NK * 8);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) mma_f16_ss(d, qh + oq + 2 * k, kh + ok + 2 * k, id, 1u);
-        if (64 * b + 32 < a.dqk)
-#pragma unroll
-          for (int k = 2; k < 4; ++k) mma_f16_ss(d, qh + oq + 2 * k, kh + ok + 2 * k, id, 1u);
+      for (int b = 0; b < n2; ++b) {
+        mma_f16_ss(d, q, k, id, 1u);
+        mma_f16_ss(d, q + 2, k + 2, id, 1u);
+        q += b & 1 ? 1020 : 4;
+        k += b & 1 ? NK * 8 - 4 : 4;
       }
       commit_elect(&sh.sfull[slot]);
       commit_elect(&sh.kempty[s]);
@@ -577,17 +573,14 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       const uint32_t id = idesc_f16(a.dv, true);
       const uint32_t d = tmem + kColO + (COL ? 0u : 128u * (uint32_t)slot),
                      ph = tmem + kColP + (COL ? 0u : 64u * (uint32_t)slot), pl = ph + NK / 2;
-      const uint32_t v = base + voff + (uint32_t)s * 2 * vpart;
+      const uint32_t v = desc_mn(base + voff + (uint32_t)s * 2 * vpart, NK * 128), vl = vpart >> 4;
 #pragma unroll
       for (int k = 0; k < NK / 16; ++k) {
-        const uint64_t vh = desc_mn_sw128(v + k * 2048, NK * 128),
-                       vl = desc_mn_sw128(v + vpart + k * 2048, NK * 128);
-        mma_f16_ts(d, pl + 8 * k, vh, id, k > 0);
-        mma_f16_ts(d, ph + 8 * k, vl, id, 1u);
+        mma_f16_ts(d, pl + 8 * k, v + 128 * k, id, k > 0);
+        mma_f16_ts(d, ph + 8 * k, v + vl + 128 * k, id, 1u);
       }
 #pragma unroll
-      for (int k = 0; k < NK / 16; ++k)
-        mma_f16_ts(d, ph + 8 * k, desc_mn_sw128(v + k * 2048, NK * 128), id, 1u);
+      for (int k = 0; k < NK / 16; ++k) mma_f16_ts(d, ph + 8 * k, v + 128 * k, id, 1u);
       commit_elect(&sh.ofull[slot]);
       commit_elect(&sh.vempty[s]);
     };
