@@ -220,10 +220,7 @@ constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
 constexpr int kScaleRing = 4;  // tiles whose scales are kept: > stages + 1
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
-template <bool V>
-struct Flag {
-  static constexpr bool value = V;
-};
+constexpr int kLaneStride = 132;  // floats of a lane's state: 16-byte accesses without bank conflicts
 // tensor-memory columns
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
 
@@ -273,6 +270,11 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -340,7 +342,7 @@ struct SplitSmem {
   uint32_t tmem;
   alignas(16) float wmax[2][kConvWarps];          // largest |x| of each converter warp's rows, K and V
   float kinv[kScaleRing], vinv[kScaleRing];       // a tile's inverse scales
-  float m[128], l[128];
+  float m[2][128], l[2][128], w[2][128];          // lane states of the warpgroups, their weights
 };
 
 static size_t split_stage_bytes(int NK, int dqk, int dv) {
@@ -378,6 +380,16 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
                  vpart = (uint32_t)vb * NK * 128;
   const uint32_t koff = 2 * qpart, voff = koff + (uint32_t)S * 2 * kpart;
 
+  // tiles on their way to L2 while earlier ones are converted
+  auto prefetch = [&](int t) {
+    if (t >= nt) return;
+    const int row0 = k0 + t * NK, n = min(NK, k1 - row0);
+    l2_prefetch(a.kc + ((size_t)kv * a.cap + row0) * a.dqk, (uint32_t)n * a.dqk * 4);
+    l2_prefetch(a.vc + ((size_t)kv * a.cap + row0) * a.dv, (uint32_t)n * a.dv * 4);
+  };
+  const bool fetcher = tid == 9 * 32;
+  if (fetcher)
+    for (int t = 0; t < kAhead; ++t) prefetch(t);
   if (tid == 0) {
     mbar_init(&sh.qfull, 1);
     for (int i = 0; i < 2; ++i) {
@@ -422,22 +434,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     auto load = [&](float4 (&x)[8], const float* src, int d, int t) {
       const int nv = k1 - (k0 + t * NK) - cw * RPW;  // rows left (<= 0 past the last tile)
       src += (size_t)(k0 + t * NK + cw * RPW) * d + 4 * lane;
-      if (nv >= RPW) {
 #pragma unroll
-        for (int i = 0; i < RPW; ++i)
+      for (int i = 0; i < RPW; ++i)
 #pragma unroll
-          for (int s = 0; s < SL; ++s)
-            x[i * SL + s] = 4 * (lane + 32 * s) < d ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < RPW; ++i)
-#pragma unroll
-          for (int s = 0; s < SL; ++s)
-            x[i * SL + s] = i < nv && 4 * (lane + 32 * s) < d
-                                ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+        for (int s = 0; s < SL; ++s)
+          x[i * SL + s] = i < nv && 4 * (lane + 32 * s) < d
+                              ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
     };
     // The tile's scale: the largest |x| of all converter warps' rows.
     auto scale_of = [&](const float4 (&x)[8], int v, float* inv) {
@@ -480,34 +483,26 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(full);
     };
-    // tiles on their way to L2 while earlier ones are converted
-    auto prefetch = [&](int t) {
-      if (t >= nt) return;
-      const int row0 = k0 + t * NK, nv = min(NK, k1 - row0);
-      l2_prefetch(kc + (size_t)row0 * a.dqk, (uint32_t)nv * a.dqk * 4);
-      l2_prefetch(vc + (size_t)row0 * a.dv, (uint32_t)nv * a.dv * 4);
-    };
-    const bool fetcher = cw == 1 && lane == 0;
-    if (fetcher)
-      for (int t = 0; t < kAhead; ++t) prefetch(t);
     // the next tile's K rows are on their way while this tile's V is converted
     float4 xk[8], xv[8];
-    load(xk, kc, a.dqk, 0);
-    load(xv, vc, a.dv, 0);
 #pragma unroll 1
-    for (int t = 0; t < nt; ++t) {
+    for (int t = -1; t < nt; ++t) {  // -1: the first loads alone
       if (fetcher) prefetch(t + kAhead);
       const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
       const uint32_t par = (uint32_t)(use - 1) & 1u;
-      float sc = scale_of(xk, 0, &sh.kinv[t % kScaleRing]);
-      if (use > 0) wait(&sh.kempty[s], par);
-      convert(xk, a.dqk, sm + koff + (uint32_t)s * 2 * kpart, kpart, sc);
-      publish(&sh.kfull[s]);
+      if (t >= 0) {
+        const float sc = scale_of(xk, 0, &sh.kinv[t % kScaleRing]);
+        if (use > 0) wait(&sh.kempty[s], par);
+        convert(xk, a.dqk, sm + koff + (uint32_t)s * 2 * kpart, kpart, sc);
+        publish(&sh.kfull[s]);
+      }
       load(xk, kc, a.dqk, t + 1);
-      sc = scale_of(xv, 1, &sh.vinv[t % kScaleRing]);
-      if (use > 0) wait(&sh.vempty[s], par);
-      convert(xv, a.dv, sm + voff + (uint32_t)s * 2 * vpart, vpart, sc);
-      publish(&sh.vfull[s]);
+      if (t >= 0) {
+        const float sc = scale_of(xv, 1, &sh.vinv[t % kScaleRing]);
+        if (use > 0) wait(&sh.vempty[s], par);
+        convert(xv, a.dv, sm + voff + (uint32_t)s * 2 * vpart, vpart, sc);
+        publish(&sh.vfull[s]);
+      }
       load(xv, vc, a.dv, t + 1);
     }
     pdl_launch_dependents();
@@ -635,51 +630,59 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
           }
           return mx;
         };
-        // P = 2^(logit - ref) as f16 parts; returns its sum and the largest S
-        float mx;
-        auto weights = [&](auto whole) {
-          float sum = 0.f;
-          mx = -INFINITY;
+        if (it == 0) {
+          const float mx = scan();
+          ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
+        }
+        // P = 2^(logit - ref) as f16 parts, its sum and the largest S
+        float sum;
+#pragma unroll 1
+        while (true) {
+          float mx = -INFINITY;
           const float nref = -ref;
+          sum = 0.f;
 #pragma unroll 1
           for (int c = 0; c < kw; c += 16) {
-            uint32_t x[16], hi[8], lo[8];
+            uint32_t x[16];
             float p[16];
             tc5::ld16(st + c, x);
             tc5::ld_wait();
+            const bool part = c + 16 > nv;  // the tile's last keys are padding
+            if (part) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = whole.value || c + j < nv ? __uint_as_float(x[j]) : -INFINITY;
+              for (int j = 0; j < 16; ++j)
+                if (c + j >= nv) x[j] = 0xFF800000u;  // -inf
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = __uint_as_float(x[j]);
             mx = fmaxf(mx, max16(p));
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float e = ex2(fmaf(__uint_as_float(x[j]), cs, nref));
-              p[j] = whole.value || c + j < nv ? e : 0.f;
+            for (int j = 0; j < 16; ++j) p[j] = ex2(fmaf(__uint_as_float(x[j]), cs, nref));
+            if (part) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c + j >= nv) p[j] = 0.f;
             }
             sum += sum16(p);
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) split_f16x2(pack2(p[j], p[j + 1]), hi[j / 2], lo[j / 2]);
             if (!COL || wg == 0) {
-              tmem_st8(pt + c / 2, hi);
-              tmem_st8(pt + NK / 2 + c / 2, lo);
+#pragma unroll
+              for (int h = 0; h < 16; h += 8) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split_f16x2(pack2(p[h + 2 * j], p[h + 2 * j + 1]), hi[j], lo[j]);
+                tmem_st4(pt + (c + h) / 2, hi);
+                tmem_st4(pt + NK / 2 + (c + h) / 2, lo);
+              }
             }
           }
-          return sum;
-        };
-        auto pass = [&]() { return nv >= kw ? weights(Flag<true>{}) : weights(Flag<false>{}); };
-        if (it == 0) {
-          mx = scan();
-          ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
-        }
-        float sum = pass();
-        const float top = mx * cs;
-        const bool move = top - ref > kRefMost;
-        if (__any_sync(0xffffffffu, move)) {
-          const float nref = move ? top - kRefBits : ref, corr = ex2(ref - nref);
-          ref = nref;
+          const float top = mx * cs;
+          const bool move = top - ref > kRefMost;
+          if (!__any_sync(0xffffffffu, move)) break;
+          const float to = move ? top - kRefBits : ref, corr = ex2(ref - to);
+          ref = to;
           l *= corr;
 #pragma unroll
           for (int c = 0; c < 128; ++c) o[c] *= corr;
-          sum = pass();
         }
         l += sum;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -711,64 +714,51 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     }
     pdl_launch_dependents();
     block_sync();
-    float m = l == 0.f ? -INFINITY : ref;  // the state's reference; none without a key
-    // lane states to shared memory (column c of lane i at c * 129 + i): the
-    // warpgroups' states of a lane first, then each row's copies
-    float* xo = reinterpret_cast<float*>(sm) + (COL ? 128 * 129 * wg : 0) + row;
-    if (!COL) {
-      if (wg == 1) {
-        sh.m[row] = m;
-        sh.l[row] = l;
+    // Lane states to shared memory (lane i of a warpgroup at i * kLaneStride),
+    // then a row's states weighted and summed.  The code that runs once is kept
+    // short: its instructions come from L2 at hundreds of cycles a line.
+    float* xo = reinterpret_cast<float*>(sm) + (wg * 128 + row) * kLaneStride;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < cols) xo[c * 129] = o[c];
+    for (int c = 0; c < 128; c += 4)
+      *reinterpret_cast<float4*>(xo + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+    sh.m[wg][row] = l == 0.f ? -INFINITY : ref;  // no reference without a key
+    sh.l[wg][row] = l;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int rows = min(lane_rows, a.R - mt * 128);
+    const int ng = COL ? 1 : 2;  // warpgroups with states of their own
+    const size_t at0 = ((size_t)kv * a.ns + sp) * a.R + mt * 128;
+    if (tid < rows) {
+      float mr = -INFINITY, lr = 0.f;
+#pragma unroll 1
+      for (int g = 0; g < ng * a.rep; ++g)
+        mr = fmaxf(mr, sh.m[g & (ng - 1)][(g >> (ng - 1)) * lane_rows + tid]);
+#pragma unroll 1
+      for (int g = 0; g < ng * a.rep; ++g) {
+        const int w = g & (ng - 1), i = (g >> (ng - 1)) * lane_rows + tid;
+        const float f = sh.m[w][i] == -INFINITY ? 1.f : ex2(sh.m[w][i] - mr);
+        sh.w[w][i] = f;
+        lr += f * sh.l[w][i];
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (wg == 0) {
-        const float m1 = sh.m[row], mn = fmaxf(m, m1);
-        // a state without any key, or of NaN logits alone, has no maximum
-        const float c0 = m == -INFINITY ? 1.f : ex2(m - mn), c1 = m1 == -INFINITY ? 1.f : ex2(m1 - mn);
-        l = l * c0 + sh.l[row] * c1;
-        m = mn;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c < cols) xo[c * 129] = o[c] * c0 + xo[c * 129] * c1;
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        if (c < cols) xo[c * 129] = o[c];
-    }
-    if (wg == 0) {
-      sh.m[row] = m;
-      sh.l[row] = l;
+      a.part_ml[at0 + tid] = make_float2(mr, lr);
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const float* xs = reinterpret_cast<const float*>(sm);
-    const int rows = min(lane_rows, a.R - mt * 128);
-    for (int i = warp; i < rows; i += 8) {
-      float w[4], mr = -INFINITY, lr = 0.f;
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if (g < a.rep) mr = fmaxf(mr, sh.m[g * lane_rows + i]);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (g >= a.rep) break;
-        const float mg = sh.m[g * lane_rows + i];
-        w[g] = mg == -INFINITY ? 1.f : ex2(mg - mr);
-        lr += w[g] * sh.l[g * lane_rows + i];
+    const int words = a.dv / 4;
+#pragma unroll 1
+    for (int e = tid; e < rows * words; e += 256) {
+      const int i = e / words, c = e % words * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int g = 0; g < ng * a.rep; ++g) {
+        const int w = COL ? c >> 7 : g & 1, ln = (COL ? g : g >> 1) * lane_rows + i;
+        const float f = sh.w[COL ? 0 : w][ln];
+        const float4 x = *reinterpret_cast<const float4*>(xs + (w * 128 + ln) * kLaneStride + (c & 127));
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
       }
-      const size_t at = ((size_t)kv * a.ns + sp) * a.R + mt * 128 + i;
-      if (lane == 0) a.part_ml[at] = make_float2(mr, lr);
-      for (int c = lane; c < a.dv; c += 32) {
-        float v = 0.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (g >= a.rep) break;
-          v += w[g] * xs[c * 129 + g * lane_rows + i];
-        }
-        a.part_o[at * a.dv + c] = v;
-      }
+      *reinterpret_cast<float4*>(a.part_o + (at0 + i) * a.dv + c) = v;
     }
     if (warp == 0) {
       tc5::fence_after_sync();
@@ -925,7 +915,7 @@ static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   const size_t q = split_q_bytes(a.dqk), stage = split_stage_bytes(NK, a.dqk, a.dv), limit = 223 * 1024;
   a.stages = q + 2 * stage + 1024 <= limit ? 2 : 1;
   size_t smem = q + a.stages * stage;
-  smem = std::max(smem, (size_t)129 * (COL ? 256 : a.dv) * 4);  // the merge's buffer
+  smem = std::max(smem, (size_t)256 * kLaneStride * 4);  // the lane states at the end
   smem += 1024;
   static bool attr[64] = {};  // per device
   int dev = 0;
