@@ -21,6 +21,7 @@
 //              node's ancestors, read key by key, so a row that a mask hides
 //              never enters any arithmetic; sink, gate, output.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "tc5.cuh"
@@ -42,14 +43,13 @@ struct TreeAttnArgs {
   const int* depth;
   float* out;
   float* qf;       // [nkv][R][dqk] scaled queries, row r = i * G + g
-  uint8_t* qt;     // [nkv][mt] tiles of 128 rows: f16 hi part, then lo part
+  uint8_t* qt;     // [nkv][mt] tiles of 128 rows: f16 hi parts, then lo parts
   float* qinv;     // [nkv][mt * 128] power of two that undoes a row's f16 scale
   int* dep;        // [n] depths inside [0, n)
   float* part_o;   // [nkv][ns][R][dv]
   float2* part_ml; // [nkv][ns][R] running maximum and sum
   int R, mt;              // query rows of a KV head, tiles of 128 of them
   int ns, kbeg, kper;     // splits, first split key, keys a split
-  int stages;             // K/V tile buffers of the split kernel
   int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
@@ -75,7 +75,8 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c, int rows) {
   return (uint32_t)((c >> 6) * rows * 128 + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2);
 }
 
-// Writes a query row's f16 hi and lo parts into its operand tile.
+// Writes a query row's f16 hi and lo parts for the split kernel: 16-byte chunks
+// of 8 dims, a chunk's 128 rows consecutive, hi chunks then lo chunks.
 __device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVals& v, int kv, int r,
                                              int half, int lane) {
   float mx = 0.f;
@@ -86,16 +87,15 @@ __device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVa
   float scale;
   const float inv = f16_scale(warp_max(mx * a.qscale), scale);
   const int rr = r & 127, tile = r >> 7, rows = 128 / a.rep;
-  const uint32_t part = (uint32_t)((a.dqk + 63) / 64) * 128 * 128;
-  uint8_t* hi = a.qt + ((size_t)kv * a.mt + tile) * 2 * part;
+  __half* hi = reinterpret_cast<__half*>(a.qt + ((size_t)kv * a.mt + tile) * 512 * a.dqk);
   if (lane == 0) a.qinv[((size_t)kv * a.mt + tile) * 128 + rr] = inv;
   auto put = [&](int c, float x) {
     x = x * a.qscale * scale;
     const __half h = __float2half_rn(x), l = __float2half_rn(x - __half2float(h));
     for (int i = rr; i < 128; i += rows) {
-      const uint32_t off = tile_off(i, c, 128);
-      *reinterpret_cast<__half*>(hi + off) = h;
-      *reinterpret_cast<__half*>(hi + part + off) = l;
+      const int at = ((c >> 3) * 128 + i) * 8 + (c & 7);
+      hi[at] = h;
+      hi[128 * a.dqk + at] = l;
     }
   };
 #pragma unroll
@@ -204,25 +204,28 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 // memory with the tile's scale), and two warpgroups that each run softmax on
 // whole rows (thread = row) and issue their own MMAs from their first warp.
 //   COL = false (dv <= 128): the warpgroups take alternate tiles, each with its
-//     own (m, l, o), merged at the end: one's softmax overlaps the other's MMAs;
-//   COL = true: both follow every tile (the first one writes P) and keep half
-//     of the output columns each, as 256 do not fit a thread's registers.
+//     own (ref, l, o), merged at the end: one's softmax overlaps the other's MMAs;
+//   COL = true: they share every tile, each with half of its keys and half of the
+//     output columns, as 256 do not fit a thread's registers.
 // Few query rows (64 or less) are repeated `rep` times in the 128 lanes: each
 // copy takes its own NK / rep keys of a tile (its P is 0 elsewhere), so all four
 // warps of a warpgroup share the exponentials; the copies' states are merged at
 // the end like the warpgroups'.
+// Shared memory feeds the MMAs at 128 bytes a cycle and is what they wait for, so
+// Q and P are operands in tensor memory: P takes the place of S, column by
+// column (16 keys: 8 columns of hi parts, 8 of lo parts), and Q hi and lo lie
+// behind the outputs (Q lo in shared memory where they do not fit).
 constexpr int kSplitThreads = 512;
 constexpr int kConvWarps = 8;
 #ifndef MTP_TREE_AHEAD
 #define MTP_TREE_AHEAD 3
 #endif
 constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
-constexpr int kScaleRing = 4;  // tiles whose scales are kept: > stages + 1
+constexpr int kScaleRing = 4;  // tiles whose scales are kept: > kStages + 1
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
 constexpr int kLaneStride = 132;  // floats of a lane's state: 16-byte accesses without bank conflicts
-// tensor-memory columns
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256;
+constexpr int kStages = 2;        // K and V tile buffers
 
 // f16 A and B, f32 accumulator, M = 128; B is MN-major when mn is set (bit 16).
 __device__ __forceinline__ uint32_t idesc_f16(int N, bool mn) {
@@ -270,11 +273,6 @@ __device__ __forceinline__ void commit_elect(uint64_t* bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
@@ -338,17 +336,22 @@ __device__ __forceinline__ float sum16(const float (&v)[16]) {
 }
 
 struct SplitSmem {
-  uint64_t qfull, kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
   uint32_t tmem;
   alignas(16) float wmax[2][kConvWarps];          // largest |x| of each converter warp's rows, K and V
   float kinv[kScaleRing], vinv[kScaleRing];       // a tile's inverse scales
-  float m[2][128], l[2][128], w[2][128];          // lane states of the warpgroups, their weights
+  float m[2][128], l[2][128], w[2][128];          // lane states of the warpgroups, their weights (COL: m first passes a tile's largest S)
 };
 
 static size_t split_stage_bytes(int NK, int dqk, int dv) {
   return (size_t)NK * 256 * ((dqk + 63) / 64 + (dv + 63) / 64);
 }
-static size_t split_q_bytes(int dqk) { return (size_t)(dqk + 63) / 64 * 128 * 256; }
+// First tensor-memory column of the queries (hi parts, then lo parts) behind two
+// S tiles and the outputs; whether the lo parts fit too.
+__host__ __device__ constexpr int split_q_col(int NK, bool col, int dv) { return 2 * NK + (col ? dv : 2 * dv); }
+__host__ __device__ constexpr bool split_q_lo_fits(int NK, bool col, int dqk, int dv) {
+  return split_q_col(NK, col, dv) + dqk <= 512;
+}
 
 // A wait that gives up marks the launch (error 1) and lets every later wait of
 // the thread through, so the barriers below are still met by every thread.
@@ -374,11 +377,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const int sp = blockIdx.x, mt = blockIdx.y, kv = blockIdx.z;
   const int k0 = a.kbeg + sp * a.kper, k1 = min(a.L, k0 + a.kper);
   const int nt = (k1 - k0 + NK - 1) / NK;  // >= 1 (host)
-  const int S = a.stages;
   const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
-  const uint32_t qpart = (uint32_t)qb * 128 * 128, kpart = (uint32_t)qb * NK * 128,
-                 vpart = (uint32_t)vb * NK * 128;
-  const uint32_t koff = 2 * qpart, voff = koff + (uint32_t)S * 2 * kpart;
+  const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
+  const uint32_t voff = kStages * 2 * kpart, qoff = voff + kStages * 2 * vpart;
+  const bool qlo_tm = split_q_lo_fits(NK, COL, a.dqk, a.dv);
 
   // tiles on their way to L2 while earlier ones are converted
   auto prefetch = [&](int t) {
@@ -391,7 +393,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   if (fetcher)
     for (int t = 0; t < kAhead; ++t) prefetch(t);
   if (tid == 0) {
-    mbar_init(&sh.qfull, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.kfull[i], kConvWarps);
       mbar_init(&sh.kempty[i], 1);
@@ -419,16 +420,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
     const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
-    if (cw == 0 && lane == 0) {
-      // the queries come from the previous launch; cached rows were final
-      // before it released this one
-      pdl_wait();
-      fence_proxy_async_global();
-      mbar_arrive_expect_tx(&sh.qfull, 2 * qpart);
-      bulk_load(sm, a.qt + ((size_t)kv * a.mt + mt) * 2 * qpart, 2 * qpart, &sh.qfull,
-                l2_policy_evict_last());
-    }
-    __syncwarp();
     // This warp's rows of a K or V tile, eight 16-byte words a lane.
     static_assert(RPW * SL == 8, "eight words a lane");
     auto load = [&](float4 (&x)[8], const float* src, int d, int t) {
@@ -488,12 +479,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 #pragma unroll 1
     for (int t = -1; t < nt; ++t) {  // -1: the first loads alone
       if (fetcher) prefetch(t + kAhead);
-      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
+      const int s = t & 1, use = t >> 1;
       const uint32_t par = (uint32_t)(use - 1) & 1u;
       if (t >= 0) {
         const float sc = scale_of(xk, 0, &sh.kinv[t % kScaleRing]);
         if (use > 0) wait(&sh.kempty[s], par);
-        convert(xk, a.dqk, sm + koff + (uint32_t)s * 2 * kpart, kpart, sc);
+        convert(xk, a.dqk, sm + (uint32_t)s * 2 * kpart, kpart, sc);
         publish(&sh.kfull[s]);
       }
       load(xk, kc, a.dqk, t + 1);
@@ -515,48 +506,74 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     const int wg = warp >> 2;
     const int row = tid & 127;
     const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues MMAs
-    const int lane_rows = 128 / a.rep;                 // rows of a copy
-    const int qrow = row & (lane_rows - 1);            // this lane's row of the tile
-    const int kw = NK / a.rep, kb = row / lane_rows * kw;  // this copy's keys of a tile
+    const int lane_rows = 128 / a.rep;       // rows of a copy
+    const int qrow = row & (lane_rows - 1);  // this lane's row of the tile
+    // this lane's keys of a tile
+    const int kw = COL ? 16 : NK / a.rep, kb = COL ? 16 * wg : row / lane_rows * kw;
     // warps of padding rows only keep step
     const bool active = mt * 128 + (qrow & ~31) < a.R;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const int cols = COL ? (wg == 0 ? min(a.dv, 128) : a.dv - 128) : a.dv;  // this warpgroup's
+    const int cols = COL ? (wg == 0 ? 128 : a.dv - 128) : a.dv;  // this warpgroup's
+    const uint32_t ocol = tmem + 2 * NK + (COL ? 0u : (uint32_t)(wg * a.dv));
+    const uint32_t qhi = tmem + split_q_col(NK, COL, a.dv), qlo = qhi + a.dqk / 2;
+
+    // the queries come from the previous launch (cached rows were final before
+    // it released this one): the first warpgroup brings the hi parts, the second
+    // the lo parts
+    pdl_wait();
+    const float qinv = __ldcg(a.qinv + ((size_t)kv * a.mt + mt) * 128 + qrow);
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(a.qt + ((size_t)kv * a.mt + mt) * 512 * a.dqk) +
+                         wg * 16 * a.dqk + row;
+#pragma unroll 4
+      for (int c = 0; c < a.dqk; c += 16) {
+        const uint4 u = __ldcg(src + c * 16), v = __ldcg(src + c * 16 + 128);
+        if (wg == 0 || qlo_tm) {
+          const uint32_t r[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+          tmem_st8((wg == 0 ? qhi : qlo) + lanes + c / 2, r);
+        } else {
+          *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c, 128)) = u;
+          *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c + 8, 128)) = v;
+        }
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc5::fence_proxy_async_smem();
+      tc5::fence_before_sync();
+    }
+    auto pair_sync = [&]() { asm volatile("bar.sync 4, 256;" ::: "memory"); };
+    pair_sync();
 #pragma unroll
     for (int c = 0; c < 128; ++c) o[c] = 0.f;
-    if (a.rep > 1 && (!COL || wg == 0)) {  // P of other copies' keys
-      const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-      for (int c = 0; c < NK; c += 8) tmem_st8(tmem + lanes + kColP + (COL ? 0u : 64u * wg) + c, z);
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-    }
 
-    // S(t) = Q K(t)^T into column block `slot`
+    // S(t) = Q K(t)^T into S tile `slot`
     auto issue_qk = [&](int t, int slot) {
-      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
+      const int s = t & 1, use = t >> 1;
       wait(&sh.kfull[s], (uint32_t)use & 1u);
       tc5::fence_after_sync();
-      const uint32_t id = idesc_f16(NK, false), d = tmem + kColS + 64u * (uint32_t)slot;
-      uint32_t qh = desc_k(base), kh = desc_k(base + koff + (uint32_t)s * 2 * kpart);
-      const uint32_t ql = qpart >> 4, kl = kpart >> 4;  // steps from hi to lo
+      const uint32_t id = idesc_f16(NK, false), d = tmem + NK * (uint32_t)slot;
+      const uint32_t kh = desc_k(base + (uint32_t)s * 2 * kpart), kl = kpart >> 4;
       const int n2 = a.dqk / 32;
       // pairs of 16-dim steps (dims come in 32s): the small products, then the large
-      uint32_t q = qh, k = kh;
+      uint32_t k = kh, q = desc_k(base + qoff);
 #pragma unroll 1
       for (int b = 0; b < n2; ++b) {
-        mma_f16_ss(d, q + ql, k, id, b > 0);
-        mma_f16_ss(d, q, k + kl, id, 1u);
-        mma_f16_ss(d, q + ql + 2, k + 2, id, 1u);
-        mma_f16_ss(d, q + 2, k + kl + 2, id, 1u);
-        q += b & 1 ? 1020 : 4;  // the next half of a 128-byte row, or the next block of 64 dims
+        if (qlo_tm) {
+          mma_f16_ts(d, qlo + 16 * b, k, id, b > 0);
+          mma_f16_ts(d, qlo + 16 * b + 8, k + 2, id, 1u);
+        } else {
+          mma_f16_ss(d, q, k, id, b > 0);
+          mma_f16_ss(d, q + 2, k + 2, id, 1u);
+          q += b & 1 ? 1020 : 4;  // the next half of a 128-byte row, or the next block of 64 dims
+        }
+        mma_f16_ts(d, qhi + 16 * b, k + kl, id, 1u);
+        mma_f16_ts(d, qhi + 16 * b + 8, k + kl + 2, id, 1u);
         k += b & 1 ? NK * 8 - 4 : 4;
       }
-      q = qh, k = kh;
+      k = kh;
 #pragma unroll 1
       for (int b = 0; b < n2; ++b) {
-        mma_f16_ss(d, q, k, id, 1u);
-        mma_f16_ss(d, q + 2, k + 2, id, 1u);
-        q += b & 1 ? 1020 : 4;
+        mma_f16_ts(d, qhi + 16 * b, k, id, 1u);
+        mma_f16_ts(d, qhi + 16 * b + 8, k + 2, id, 1u);
         k += b & 1 ? NK * 8 - 4 : 4;
       }
       commit_elect(&sh.sfull[slot]);
@@ -564,24 +581,22 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     };
     // the tile's P V into this warpgroup's output columns
     auto issue_pv = [&](int t, int slot) {
-      const int s = S == 1 ? 0 : t & 1;
-      const uint32_t id = idesc_f16(a.dv, true);
-      const uint32_t d = tmem + kColO + (COL ? 0u : 128u * (uint32_t)slot),
-                     ph = tmem + kColP + (COL ? 0u : 64u * (uint32_t)slot), pl = ph + NK / 2;
+      const int s = t & 1;
+      const uint32_t id = idesc_f16(a.dv, true), p = tmem + NK * (uint32_t)slot;
       const uint32_t v = desc_mn(base + voff + (uint32_t)s * 2 * vpart, NK * 128), vl = vpart >> 4;
 #pragma unroll
       for (int k = 0; k < NK / 16; ++k) {
-        mma_f16_ts(d, pl + 8 * k, v + 128 * k, id, k > 0);
-        mma_f16_ts(d, ph + 8 * k, v + vl + 128 * k, id, 1u);
+        mma_f16_ts(ocol, p + 16 * k + 8, v + 128 * k, id, k > 0);
+        mma_f16_ts(ocol, p + 16 * k, v + vl + 128 * k, id, 1u);
       }
 #pragma unroll
-      for (int k = 0; k < NK / 16; ++k) mma_f16_ts(d, ph + 8 * k, v + 128 * k, id, 1u);
-      commit_elect(&sh.ofull[slot]);
+      for (int k = 0; k < NK / 16; ++k) mma_f16_ts(ocol, p + 16 * k, v + 128 * k, id, 1u);
+      commit_elect(&sh.ofull[COL ? 0 : slot]);
       commit_elect(&sh.vempty[s]);
     };
     auto group_sync = [&]() {
       if (COL)
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        pair_sync();
       else
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
     };
@@ -589,100 +604,88 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     const int step = COL ? 1 : 2;
     const int first = COL ? 0 : wg;
     if (issuer && first < nt) {
-      wait(&sh.qfull, 0u);
+      tc5::fence_after_sync();
       issue_qk(first, first);
     }
     __syncwarp();
-    float qinv = 1.f;
-    {
-      pdl_wait();
-      qinv = __ldcg(a.qinv + ((size_t)kv * a.mt + mt) * 128 + qrow);
-    }
+#pragma unroll 1
     for (int t = first, it = 0; t < nt; t += step, ++it) {
       const int slot = t & 1;
       const uint32_t ph2 = COL ? (uint32_t)(t >> 1) & 1u : (uint32_t)it & 1u;  // phase of the slot
-      const int s = S == 1 ? 0 : t & 1, use = S == 1 ? t : t >> 1;
-      if (COL) {
-        if (issuer && t + 1 < nt) issue_qk(t + 1, (t + 1) & 1);
-        __syncwarp();
-      }
+      const int s = t & 1, use = t >> 1;
+      // COL: P(t - 1) V has completed, so the other S tile is free
+      if (COL && issuer && t + 1 < nt) issue_qk(t + 1, (t + 1) & 1);
+      __syncwarp();
       wait(&sh.vfull[s], (uint32_t)use & 1u);  // the tile's scales (and V)
       wait(&sh.sfull[slot], ph2);
       tc5::fence_after_sync();
-      const int nv = min(NK, k1 - (k0 + t * NK)) - kb;  // this copy's keys before the padding
+      const int nv = min(NK, k1 - (k0 + t * NK));  // keys before the padding
       const float cs = sh.kinv[t % kScaleRing] * qinv;   // S to logits: a power of two
       const float oscale = sh.vinv[t % kScaleRing];
+      const uint32_t st = tmem + lanes + NK * (uint32_t)slot;
+      float mx = -INFINITY;
       if (active) {
-        const uint32_t st = tmem + lanes + kColS + 64u * (uint32_t)slot + kb;
-        const uint32_t pt = tmem + lanes + kColP + (COL ? 0u : 64u * (uint32_t)slot) + kb / 2;
-        // largest S of the copy's keys
-        auto scan = [&]() {
-          float mx = -INFINITY;
+        // largest S of this lane's keys
 #pragma unroll 1
-          for (int c = 0; c < kw; c += 16) {
-            uint32_t x[16];
-            float f[16];
-            tc5::ld16(st + c, x);
-            tc5::ld_wait();
+        for (int c = kb; c < kb + kw; c += 16) {
+          uint32_t x[16];
+          float f[16];
+          tc5::ld16(st + c, x);
+          tc5::ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = c + j < nv ? __uint_as_float(x[j]) : -INFINITY;
-            mx = fmaxf(mx, max16(f));
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[j]);
+          if (c + 16 > nv) {  // the tile's last keys are padding
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j >= nv) f[j] = -INFINITY;
           }
-          return mx;
-        };
-        if (it == 0) {
-          const float mx = scan();
-          ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
+          mx = fmaxf(mx, max16(f));
         }
-        // P = 2^(logit - ref) as f16 parts, its sum and the largest S
-        float sum;
-#pragma unroll 1
-        while (true) {
-          float mx = -INFINITY;
-          const float nref = -ref;
-          sum = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < kw; c += 16) {
-            uint32_t x[16];
-            float p[16];
-            tc5::ld16(st + c, x);
-            tc5::ld_wait();
-            const bool part = c + 16 > nv;  // the tile's last keys are padding
-            if (part) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j >= nv) x[j] = 0xFF800000u;  // -inf
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = __uint_as_float(x[j]);
-            mx = fmaxf(mx, max16(p));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = ex2(fmaf(__uint_as_float(x[j]), cs, nref));
-            if (part) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j >= nv) p[j] = 0.f;
-            }
-            sum += sum16(p);
-            if (!COL || wg == 0) {
-#pragma unroll
-              for (int h = 0; h < 16; h += 8) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) split_f16x2(pack2(p[h + 2 * j], p[h + 2 * j + 1]), hi[j], lo[j]);
-                tmem_st4(pt + (c + h) / 2, hi);
-                tmem_st4(pt + NK / 2 + (c + h) / 2, lo);
-              }
-            }
-          }
-          const float top = mx * cs;
-          const bool move = top - ref > kRefMost;
-          if (!__any_sync(0xffffffffu, move)) break;
+      }
+      if (COL) {
+        sh.m[wg][row] = mx;
+        pair_sync();
+        mx = fmaxf(mx, sh.m[wg ^ 1][row]);
+      }
+      if (active) {
+        if (it == 0) ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
+        const float top = mx * cs;
+        const bool move = top - ref > kRefMost;
+        if (__any_sync(0xffffffffu, move)) {
           const float to = move ? top - kRefBits : ref, corr = ex2(ref - to);
           ref = to;
           l *= corr;
 #pragma unroll
           for (int c = 0; c < 128; ++c) o[c] *= corr;
+        }
+        // P = 2^(logit - ref) as f16 parts in the place of S
+        const float nref = -ref;
+        float sum = 0.f;
+#pragma unroll 1
+        for (int c = kb; c < kb + kw; c += 16) {
+          uint32_t x[16], hi[8];
+          float p[16];
+          tc5::ld16(st + c, x);
+          tc5::ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) p[j] = ex2(fmaf(__uint_as_float(x[j]), cs, nref));
+          if (c + 16 > nv) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j >= nv) p[j] = 0.f;
+          }
+          sum += sum16(p);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) split_f16x2(pack2(p[2 * j], p[2 * j + 1]), hi[j], x[j]);
+          const uint32_t lo[8] = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+          tmem_st8(st + c, hi);
+          tmem_st8(st + c + 8, lo);
+        }
+        if (!COL && a.rep > 1) {  // the other copies' keys
+          const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+          for (int c = 0; c < NK; c += 8)
+            if ((uint32_t)(c - kb) >= (uint32_t)kw) tmem_st8(st + c, z);
         }
         l += sum;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -691,14 +694,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       group_sync();
       if (issuer) {
         tc5::fence_after_sync();
-        issue_pv(t, COL ? 0 : slot);
-        if (!COL && t + 2 < nt) issue_qk(t + 2, slot);
+        issue_pv(t, slot);
       }
       __syncwarp();
       wait(&sh.ofull[COL ? 0 : slot], COL ? (uint32_t)t & 1u : ph2);
       tc5::fence_after_sync();
+      if (!COL && issuer && t + 2 < nt) issue_qk(t + 2, slot);
+      __syncwarp();
       if (active) {
-        const uint32_t ot = tmem + lanes + kColO + 128u * (uint32_t)(COL ? wg : slot);
+        const uint32_t ot = ocol + lanes + (COL ? 128u * (uint32_t)wg : 0u);
 #pragma unroll
         for (int c = 0; c < 128; c += 16) {
           if (c < cols) {
@@ -723,25 +727,24 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       *reinterpret_cast<float4*>(xo + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
     sh.m[wg][row] = l == 0.f ? -INFINITY : ref;  // no reference without a key
     sh.l[wg][row] = l;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    pair_sync();
     const int rows = min(lane_rows, a.R - mt * 128);
-    const int ng = COL ? 1 : 2;  // warpgroups with states of their own
     const size_t at0 = ((size_t)kv * a.ns + sp) * a.R + mt * 128;
     if (tid < rows) {
       float mr = -INFINITY, lr = 0.f;
 #pragma unroll 1
-      for (int g = 0; g < ng * a.rep; ++g)
-        mr = fmaxf(mr, sh.m[g & (ng - 1)][(g >> (ng - 1)) * lane_rows + tid]);
+      for (int g = 0; g < 2 * a.rep; ++g) mr = fmaxf(mr, sh.m[g & 1][(g >> 1) * lane_rows + tid]);
 #pragma unroll 1
-      for (int g = 0; g < ng * a.rep; ++g) {
-        const int w = g & (ng - 1), i = (g >> (ng - 1)) * lane_rows + tid;
-        const float f = sh.m[w][i] == -INFINITY ? 1.f : ex2(sh.m[w][i] - mr);
+      for (int g = 0; g < 2 * a.rep; ++g) {
+        const int w = g & 1, i = (g >> 1) * lane_rows + tid;
+        // COL: both halves of the columns have one reference
+        const float f = COL || sh.m[w][i] == -INFINITY ? 1.f : ex2(sh.m[w][i] - mr);
         sh.w[w][i] = f;
         lr += f * sh.l[w][i];
       }
       a.part_ml[at0 + tid] = make_float2(mr, lr);
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    pair_sync();
     const float* xs = reinterpret_cast<const float*>(sm);
     const int words = a.dv / 4;
 #pragma unroll 1
@@ -749,9 +752,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       const int i = e / words, c = e % words * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int g = 0; g < ng * a.rep; ++g) {
-        const int w = COL ? c >> 7 : g & 1, ln = (COL ? g : g >> 1) * lane_rows + i;
-        const float f = sh.w[COL ? 0 : w][ln];
+      for (int g = 0; g < (COL ? 1 : 2 * a.rep); ++g) {
+        const int w = COL ? c >> 7 : g & 1, ln = (g >> 1) * lane_rows + i;
+        const float f = sh.w[w][ln];
         const float4 x = *reinterpret_cast<const float4*>(xs + (w * 128 + ln) * kLaneStride + (c & 127));
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
@@ -900,7 +903,7 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
   w.dep = reinterpret_cast<int*>(take(sizeof(int) * kTreeMax));
   w.qf = reinterpret_cast<float*>(take(4 * rows * g->head_dim_qk));
   const size_t tiles = (size_t)g->n_kv_heads * ((n * (g->n_heads / g->n_kv_heads) + 127) / 128);
-  w.qt = take(tiles * split_q_bytes(g->head_dim_qk));
+  w.qt = take(tiles * 512 * g->head_dim_qk);
   w.qinv = reinterpret_cast<float*>(take(tiles * 128 * 4));
   w.ml = reinterpret_cast<float2*>(take(8 * rows * ns));
   w.o = reinterpret_cast<float*>(take(4 * rows * ns * g->head_dim_v));
@@ -910,14 +913,14 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
 
 template <int NK, bool COL>
 static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
-  static_assert(kScaleRing > 3, "scales outlive their tile's buffers");
-    static_assert(sizeof(SplitSmem) <= 4096, "beside the dynamic shared memory");
-  const size_t q = split_q_bytes(a.dqk), stage = split_stage_bytes(NK, a.dqk, a.dv), limit = 223 * 1024;
-  a.stages = q + 2 * stage + 1024 <= limit ? 2 : 1;
-  size_t smem = q + a.stages * stage;
+  static_assert(kScaleRing > kStages + 1, "scales outlive their tile's buffers");
+  static_assert(sizeof(SplitSmem) <= 4096, "beside the dynamic shared memory");
+  const size_t limit = 223 * 1024;
+  size_t smem = kStages * split_stage_bytes(NK, a.dqk, a.dv);
+  if (!split_q_lo_fits(NK, COL, a.dqk, a.dv)) smem += (size_t)(a.dqk + 63) / 64 * 128 * 128;
   smem = std::max(smem, (size_t)256 * kLaneStride * 4);  // the lane states at the end
   smem += 1024;
-  static bool attr[64] = {};  // per device
+  static std::atomic<bool> attr[64];  // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1051,7 +1054,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   a.part_o = w.o;
   a.part_ml = w.ml;
   a.R = n * a.G;
-  a.rep = a.R <= 32 && split_nk(a.dqk, a.dv) == 64 ? 4 : a.R <= 64 ? 2 : 1;
+  a.rep = a.dv > 128 || a.R > 64 ? 1 : a.R <= 32 && split_nk(a.dqk, a.dv) == 64 ? 4 : 2;
   a.mt = (a.R + 127) / 128;  // 1 where rows are repeated
   a.ns = pl.ns;
   a.kbeg = pl.kbeg;
