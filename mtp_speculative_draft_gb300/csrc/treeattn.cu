@@ -50,6 +50,7 @@ struct TreeAttnArgs {
   float2* part_ml; // [nkv][ns][R] running maximum and sum
   int R, mt;              // query rows of a KV head, tiles of 128 of them
   int ns, kbeg, kper;     // splits, first split key, keys a split
+  int raw;                // raw K/V row buffers of a converter warp (1 or 2)
   int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
@@ -218,7 +219,7 @@ __device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const
 constexpr int kSplitThreads = 512;
 constexpr int kConvWarps = 8;
 #ifndef MTP_TREE_AHEAD
-#define MTP_TREE_AHEAD 3
+#define MTP_TREE_AHEAD 2
 #endif
 constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
 constexpr int kScaleRing = 4;  // tiles whose scales are kept: > kStages + 1
@@ -337,10 +338,16 @@ __device__ __forceinline__ float sum16(const float (&v)[16]) {
 
 struct SplitSmem {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
+  uint64_t raw[kConvWarps][2], top[2];       // a warp's rows have arrived; every warp's largest |x| is there
   uint32_t tmem;
-  alignas(16) float wmax[2][kConvWarps];          // largest |x| of each converter warp's rows, K and V
-  float kinv[kScaleRing], vinv[kScaleRing];       // a tile's inverse scales
-  float m[2][128], l[2][128], w[2][128];          // lane states of the warpgroups, their weights (COL: m first passes a tile's largest S)
+  float kinv[kScaleRing], vinv[kScaleRing];  // a tile's inverse scales
+  alignas(16) float wmax[4][kConvWarps];     // largest |x| of each converter warp's rows
+  float smax[2][128];                        // COL: largest S of each warpgroup's keys
+};
+// At the end, behind the lane states: m, l and weight of each lane of both
+// warpgroups.
+struct SplitStates {
+  float m[2][128], l[2][128], w[2][128];
 };
 
 static size_t split_stage_bytes(int NK, int dqk, int dv) {
@@ -381,6 +388,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
   const uint32_t voff = kStages * 2 * kpart, qoff = voff + kStages * 2 * vpart;
   const bool qlo_tm = split_q_lo_fits(NK, COL, a.dqk, a.dv);
+  const uint32_t roff = qoff + (qlo_tm ? 0u : (uint32_t)qb * 128 * 128);  // raw rows
 
   // tiles on their way to L2 while earlier ones are converted
   auto prefetch = [&](int t) {
@@ -400,6 +408,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       mbar_init(&sh.vempty[i], 1);
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.ofull[i], 1);
+      mbar_init(&sh.top[i], kConvWarps);
+      for (int w = 0; w < kConvWarps; ++w) mbar_init(&sh.raw[w][i], 1);
     }
     mbar_fence_init();
   }
@@ -415,36 +425,56 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   if (warp >= 8) {
     // ---------------- converters
     const int cw = warp - 8;
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     constexpr int RPW = NK / kConvWarps;  // rows a warp of a tile
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
     const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
-    // This warp's rows of a K or V tile, eight 16-byte words a lane.
+    const uint64_t pol = l2_policy_evict_first();
+    // Phase p of the loop: tile p / 2, K (even) or V.  A warp's rows of a phase
+    // come by bulk copy into one of its RS raw buffers, which is filled anew
+    // as soon as the rows are in registers (eight 16-byte words a lane).
     static_assert(RPW * SL == 8, "eight words a lane");
-    auto load = [&](float4 (&x)[8], const float* src, int d, int t) {
-      const int nv = k1 - (k0 + t * NK) - cw * RPW;  // rows left (<= 0 past the last tile)
-      src += (size_t)(k0 + t * NK + cw * RPW) * d + 4 * lane;
+    const int np = 2 * nt, RS = a.raw;
+    uint8_t* raw = sm + roff + (size_t)cw * RS * 4096;
+    auto rows_of = [&](int p) { return min(RPW, k1 - (k0 + (p >> 1) * NK) - cw * RPW); };
+    auto fetch = [&](int p) {
+      if (p >= np || lane != 0) return;
+      const int n = rows_of(p), d = p & 1 ? a.dv : a.dqk;
+      if (n <= 0) return;
+      uint64_t* bar = &sh.raw[cw][p & (RS - 1)];
+      mbar_arrive_expect_tx(bar, (uint32_t)n * d * 4);
+      bulk_load(raw + (p & (RS - 1)) * 4096,
+                (p & 1 ? vc : kc) + (size_t)(k0 + (p >> 1) * NK + cw * RPW) * d, (uint32_t)n * d * 4, bar, pol);
+    };
+    // the rows of phase p, and their largest |x| for the tile's scale
+    auto take = [&](float4 (&x)[8], int p) {
+      const int n = rows_of(p), d = p & 1 ? a.dv : a.dqk;
+      if (n > 0) wait(&sh.raw[cw][p & (RS - 1)], (uint32_t)(RS == 2 ? p >> 1 : p) & 1u);
+      const float* src = reinterpret_cast<const float*>(raw + (p & (RS - 1)) * 4096) + 4 * lane;
+      float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < RPW; ++i)
 #pragma unroll
-        for (int s = 0; s < SL; ++s)
-          x[i * SL + s] = i < nv && 4 * (lane + 32 * s) < d
-                              ? __ldcg(reinterpret_cast<const float4*>(src + i * d + 128 * s))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    // The tile's scale: the largest |x| of all converter warps' rows.
-    auto scale_of = [&](const float4 (&x)[8], int v, float* inv) {
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x[i].x)), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
+        for (int s = 0; s < SL; ++s) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n && 4 * (lane + 32 * s) < d) v = *reinterpret_cast<const float4*>(src + i * d + 128 * s);
+          x[i * SL + s] = v;
+          mx = fmaxf(fmaxf(fmaxf(mx, fabsf(v.x)), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+        }
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-      if (lane == 0) sh.wmax[v][cw] = mx;
-      asm volatile("bar.sync 3, 256;" ::: "memory");
-      const float4 a0 = *reinterpret_cast<const float4*>(&sh.wmax[v][0]),
-                   a1 = *reinterpret_cast<const float4*>(&sh.wmax[v][4]);
-      mx = fmaxf(fmaxf(fmaxf(a0.x, a0.y), fmaxf(a0.z, a0.w)), fmaxf(fmaxf(a1.x, a1.y), fmaxf(a1.z, a1.w)));
+      if (lane == 0) {
+        sh.wmax[p & 3][cw] = mx;
+        tc5::mbar_arrive(&sh.top[p & 1]);
+        fence_proxy_async_shared_cta();
+      }
+      fetch(p + RS);
+    };
+    auto scale_of = [&](int p, float* inv) {
+      wait(&sh.top[p & 1], (uint32_t)(p >> 1) & 1u);
+      const float4 a0 = *reinterpret_cast<const float4*>(&sh.wmax[p & 3][0]),
+                   a1 = *reinterpret_cast<const float4*>(&sh.wmax[p & 3][4]);
+      const float mx = fmaxf(fmaxf(fmaxf(a0.x, a0.y), fmaxf(a0.z, a0.w)), fmaxf(fmaxf(a1.x, a1.y), fmaxf(a1.z, a1.w)));
       float scale;
       const float iv = f16_scale(mx, scale);
       if (cw == 0 && lane == 0) *inv = iv;
@@ -474,35 +504,27 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(full);
     };
-    // the next tile's K rows are on their way while this tile's V is converted
-    float4 xk[8], xv[8];
+    for (int p = 0; p < RS; ++p) fetch(p);
+    float4 x[8];
 #pragma unroll 1
-    for (int t = -1; t < nt; ++t) {  // -1: the first loads alone
-      if (fetcher) prefetch(t + kAhead);
-      const int s = t & 1, use = t >> 1;
-      const uint32_t par = (uint32_t)(use - 1) & 1u;
-      if (t >= 0) {
-        const float sc = scale_of(xk, 0, &sh.kinv[t % kScaleRing]);
-        if (use > 0) wait(&sh.kempty[s], par);
-        convert(xk, a.dqk, sm + (uint32_t)s * 2 * kpart, kpart, sc);
-        publish(&sh.kfull[s]);
-      }
-      load(xk, kc, a.dqk, t + 1);
-      if (t >= 0) {
-        const float sc = scale_of(xv, 1, &sh.vinv[t % kScaleRing]);
-        if (use > 0) wait(&sh.vempty[s], par);
-        convert(xv, a.dv, sm + voff + (uint32_t)s * 2 * vpart, vpart, sc);
-        publish(&sh.vfull[s]);
-      }
-      load(xv, vc, a.dv, t + 1);
+    for (int p = 0; p < np; ++p) {
+      const int t = p >> 1, v = p & 1, s = t & 1, use = t >> 1;
+      if (fetcher && v == 0) prefetch(t + kAhead);
+      take(x, p);
+      const float sc = scale_of(p, v ? &sh.vinv[t % kScaleRing] : &sh.kinv[t % kScaleRing]);
+      if (use > 0) wait(v ? &sh.vempty[s] : &sh.kempty[s], (uint32_t)(use - 1) & 1u);
+      const uint32_t part = v ? vpart : kpart;
+      convert(x, v ? a.dv : a.dqk, sm + (v ? voff : 0u) + (uint32_t)s * 2 * part, part, sc);
+      publish(v ? &sh.vfull[s] : &sh.kfull[s]);
     }
     pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     float o[128];
     float ref = 0.f, l = 0.f;
+    SplitStates* states = reinterpret_cast<SplitStates*>(sm + 256 * kLaneStride * 4);
     const int wg = warp >> 2;
     const int row = tid & 127;
     const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues MMAs
@@ -553,28 +575,30 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       const uint32_t id = idesc_f16(NK, false), d = tmem + NK * (uint32_t)slot;
       const uint32_t kh = desc_k(base + (uint32_t)s * 2 * kpart), kl = kpart >> 4;
       const int n2 = a.dqk / 32;
-      // pairs of 16-dim steps (dims come in 32s): the small products, then the large
-      uint32_t k = kh, q = desc_k(base + qoff);
-#pragma unroll 1
-      for (int b = 0; b < n2; ++b) {
+      // pairs of 16-dim steps (dims come in 32s): the small products, then the
+      // large
+      const uint32_t q = desc_k(base + qoff);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b >= n2) break;
+        // byte offsets / 16: half of a 128-byte row, or a block of 64 dims
+        const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4, ql = q + (b >> 1) * 1024 + (b & 1) * 4;
         if (qlo_tm) {
           mma_f16_ts(d, qlo + 16 * b, k, id, b > 0);
           mma_f16_ts(d, qlo + 16 * b + 8, k + 2, id, 1u);
         } else {
-          mma_f16_ss(d, q, k, id, b > 0);
-          mma_f16_ss(d, q + 2, k + 2, id, 1u);
-          q += b & 1 ? 1020 : 4;  // the next half of a 128-byte row, or the next block of 64 dims
+          mma_f16_ss(d, ql, k, id, b > 0);
+          mma_f16_ss(d, ql + 2, k + 2, id, 1u);
         }
         mma_f16_ts(d, qhi + 16 * b, k + kl, id, 1u);
         mma_f16_ts(d, qhi + 16 * b + 8, k + kl + 2, id, 1u);
-        k += b & 1 ? NK * 8 - 4 : 4;
       }
-      k = kh;
-#pragma unroll 1
-      for (int b = 0; b < n2; ++b) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b >= n2) break;
+        const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4;
         mma_f16_ts(d, qhi + 16 * b, k, id, 1u);
         mma_f16_ts(d, qhi + 16 * b + 8, k + 2, id, 1u);
-        k += b & 1 ? NK * 8 - 4 : 4;
       }
       commit_elect(&sh.sfull[slot]);
       commit_elect(&sh.kempty[s]);
@@ -643,9 +667,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
         }
       }
       if (COL) {
-        sh.m[wg][row] = mx;
+        sh.smax[wg][row] = mx;
         pair_sync();
-        mx = fmaxf(mx, sh.m[wg ^ 1][row]);
+        mx = fmaxf(mx, sh.smax[wg ^ 1][row]);
       }
       if (active) {
         if (it == 0) ref = mx == -INFINITY ? 0.f : mx * cs - kRefBits;  // no key, or NaN logits alone: any
@@ -725,22 +749,22 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 #pragma unroll
     for (int c = 0; c < 128; c += 4)
       *reinterpret_cast<float4*>(xo + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-    sh.m[wg][row] = l == 0.f ? -INFINITY : ref;  // no reference without a key
-    sh.l[wg][row] = l;
+    states->m[wg][row] = l == 0.f ? -INFINITY : ref;  // no reference without a key
+    states->l[wg][row] = l;
     pair_sync();
     const int rows = min(lane_rows, a.R - mt * 128);
     const size_t at0 = ((size_t)kv * a.ns + sp) * a.R + mt * 128;
     if (tid < rows) {
       float mr = -INFINITY, lr = 0.f;
 #pragma unroll 1
-      for (int g = 0; g < 2 * a.rep; ++g) mr = fmaxf(mr, sh.m[g & 1][(g >> 1) * lane_rows + tid]);
+      for (int g = 0; g < 2 * a.rep; ++g) mr = fmaxf(mr, states->m[g & 1][(g >> 1) * lane_rows + tid]);
 #pragma unroll 1
       for (int g = 0; g < 2 * a.rep; ++g) {
         const int w = g & 1, i = (g >> 1) * lane_rows + tid;
         // COL: both halves of the columns have one reference
-        const float f = COL || sh.m[w][i] == -INFINITY ? 1.f : ex2(sh.m[w][i] - mr);
-        sh.w[w][i] = f;
-        lr += f * sh.l[w][i];
+        const float f = COL || states->m[w][i] == -INFINITY ? 1.f : ex2(states->m[w][i] - mr);
+        states->w[w][i] = f;
+        lr += f * states->l[w][i];
       }
       a.part_ml[at0 + tid] = make_float2(mr, lr);
     }
@@ -754,7 +778,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 #pragma unroll 1
       for (int g = 0; g < (COL ? 1 : 2 * a.rep); ++g) {
         const int w = COL ? c >> 7 : g & 1, ln = (g >> 1) * lane_rows + i;
-        const float f = sh.w[w][ln];
+        const float f = states->w[w][ln];
         const float4 x = *reinterpret_cast<const float4*>(xs + (w * 128 + ln) * kLaneStride + (c & 127));
         v.x = fmaf(f, x.x, v.x);
         v.y = fmaf(f, x.y, v.y);
@@ -914,12 +938,14 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
 template <int NK, bool COL>
 static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   static_assert(kScaleRing > kStages + 1, "scales outlive their tile's buffers");
-  static_assert(sizeof(SplitSmem) <= 4096, "beside the dynamic shared memory");
-  const size_t limit = 223 * 1024;
-  size_t smem = kStages * split_stage_bytes(NK, a.dqk, a.dv);
+  static_assert(sizeof(SplitSmem) <= 2048, "beside the dynamic shared memory");
+  constexpr size_t limit = 227 * 1024 - 2048;  // beside SplitSmem
+  size_t smem = 1024 + kStages * split_stage_bytes(NK, a.dqk, a.dv);  // 1024: the buffers' alignment
   if (!split_q_lo_fits(NK, COL, a.dqk, a.dv)) smem += (size_t)(a.dqk + 63) / 64 * 128 * 128;
-  smem = std::max(smem, (size_t)256 * kLaneStride * 4);  // the lane states at the end
-  smem += 1024;
+  const size_t raw = kConvWarps * 4096;
+  a.raw = smem + 2 * raw <= limit ? 2 : 1;
+  smem = std::max(smem + a.raw * raw, 1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
+  if (smem > limit) return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr[64];  // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
