@@ -11,6 +11,7 @@
 // Every step rounds once to float32, so equal inputs give equal outputs bit
 // for bit; the argmax takes the lowest index among equal values and -1 where
 // nothing is above -inf (NaN never wins).
+#include <algorithm>
 #include <cmath>
 
 #include "tree.cuh"
@@ -20,6 +21,8 @@ namespace mtp {
 constexpr int kRuleThreads = 256;
 constexpr int kRulePer = 8;                          // tokens a thread of a chunk
 constexpr int kRuleChunk = kRuleThreads * kRulePer;  // tokens a CTA
+constexpr int kRuleHits = 128;                       // bias entries of a chunk kept at hand
+constexpr int kRuleRows = 16;                        // rows a CTA, at most
 
 struct RuleArgs {
   const float* x;
@@ -44,110 +47,201 @@ struct RuleArgs {
   unsigned* cnt;             // [rows], zero at rest
 };
 
-// grid (chunks, row groups).  The CTA's chunk of the biases and of the count
-// table is gathered once for its rows.
-__global__ void __launch_bounds__(kRuleThreads) logit_rules_kernel(const RuleArgs a) {
+// grid (chunks, row groups).  Few tokens have a count, a bias or a place on a
+// path.  A CTA lists its chunk's once for all its rows; a row's listed tokens go
+// to as many threads as there are (a division for one lane holds up its warp),
+// the rest need the mask and the maximum alone.  The rows' argmax joins the other
+// chunks' at the end, a thread a row.  Bound by HBM on many rows (the logits read
+// and written once) and by a few dependent reads on few; the code before the row
+// loop is rolled up, as a CTA runs it once and fetches its instructions from L2.
+__global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __grid_constant__ RuleArgs a) {
+  constexpr int kWarps = kRuleThreads / 32;
+  __shared__ uint32_t marked[kRuleChunk / 32];        // tokens with a bias or on a path
+  __shared__ uint16_t list[kRuleChunk];               // the listed tokens, their count words, summed
+  __shared__ uint32_t cnt[kRuleChunk];                // biases and path nodes
   __shared__ float adj[kRuleChunk];
-  __shared__ unsigned long long extra[kRuleChunk];  // which path nodes hold the token
-  __shared__ unsigned long long red[kRuleThreads / 32];
-  __shared__ int any_path;
-  pdl_wait();
-  pdl_launch_dependents();
+  __shared__ uint8_t slot[kRuleChunk];                // first path node of the token, or kTreeMax
+  __shared__ unsigned long long nodes[kTreeMax + 1];  // the nodes of a slot's token
+  __shared__ float hand[2][kRuleChunk];               // their logits of a row and the next
+  __shared__ int ptok[kTreeMax];
+  __shared__ int hit_i[kRuleHits], hit_t[kRuleHits];  // bias entries of the chunk, in any order
+  __shared__ unsigned long long best[kRuleRows][kWarps];
+  __shared__ int nlist, nhits, npath;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = blockIdx.x * kRuleChunk;
-  for (int i = tid; i < kRuleChunk; i += kRuleThreads) {
-    adj[i] = 0.f;
-    extra[i] = 0ull;
+  const int row0 = blockIdx.y * a.rows_per_cta, nrows = min(a.rows - row0, a.rows_per_cta);
+  if (tid < kRuleChunk / 32) marked[tid] = 0u;
+  if (tid == 0) {
+    nlist = nhits = npath = 0;
+    nodes[kTreeMax] = 0ull;
   }
-  if (tid == 0) any_path = 0;
-  __syncthreads();
-  // path tokens of the chunk: node j sets bit j of its token's word
-  if (tid < a.n_path) {
-    const int t = a.path_tok[tid] - v0;
-    if (t >= 0 && t < kRuleChunk) {
-      atomicOr(&extra[t], 1ull << tid);
-      any_path = 1;
-    }
-  }
-  // biases of the chunk in list order: hits are added one after another
-  if (warp == kRuleThreads / 32 - 1) {
-    for (int i0 = 0; i0 < a.n_bias; i0 += 32) {
-      const int i = i0 + lane;
-      const int t = i < a.n_bias ? a.bias_tok[i] - v0 : -1;
-      unsigned hit = __ballot_sync(0xffffffffu, t >= 0 && t < kRuleChunk);
-      const float b = t >= 0 && t < kRuleChunk ? a.bias[i] : 0.f;
-      while (hit) {
-        const int l = __ffs(hit) - 1;
-        hit &= hit - 1;
-        if (lane == l) adj[t] += b;
-        __syncwarp();
-      }
-    }
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   uint32_t cw[kRulePer];
 #pragma unroll
   for (int k = 0; k < kRulePer; ++k) {
     const int v = v0 + tid + k * kRuleThreads;
     cw[k] = a.counts && v < a.V ? a.counts[v] : 0u;
   }
-  __syncthreads();
-  const bool path = any_path != 0;
-  const int r1 = min(a.rows, ((int)blockIdx.y + 1) * a.rows_per_cta);
-  for (int r = blockIdx.y * a.rows_per_cta; r < r1; ++r) {
-    const float* x = a.x + (size_t)r * a.ld;
-    float l[kRulePer];
+  float l[kRulePer];
+  uint32_t w[kRulePer];
+  unsigned long long pm = 0ull;
+  // a row's logits, mask words (one a warp and word) and path
+  auto load = [&](int r) {
+    const float* src = a.x + (size_t)r * a.ld + v0 + tid;
+    const uint32_t* ok = a.allow + (size_t)r * a.allow_ld + ((v0 + tid) >> 5);
 #pragma unroll
     for (int k = 0; k < kRulePer; ++k) {
-      const int v = v0 + tid + k * kRuleThreads;
-      l[k] = v < a.V ? x[v] : -INFINITY;
+      const bool in = v0 + tid + k * kRuleThreads < a.V;
+      l[k] = in ? src[k * kRuleThreads] : 0.f;
+      w[k] = a.allow && in ? ok[k * kWarps] : 0xFFFFFFFFu;
     }
-    const unsigned long long pm = path ? a.path_mask[r] : 0ull;
-    float best = -INFINITY;
-    int at = -1;
+    pm = a.n_path ? a.path_mask[r] : 0ull;
+  };
+  load(row0);
+  __syncthreads();
+  if (tid < a.n_path) {
+    const int t = a.path_tok[tid] - v0;
+    ptok[tid] = t;
+    if (t >= 0 && t < kRuleChunk) {
+      atomicOr(&marked[t >> 5], 1u << (t & 31));
+      npath = 1;
+    }
+  }
+#pragma unroll 1
+  for (int i = tid; i < a.n_bias; i += kRuleThreads) {
+    const int t = a.bias_tok[i] - v0;
+    if (t >= 0 && t < kRuleChunk) {
+      atomicOr(&marked[t >> 5], 1u << (t & 31));
+      const int at = atomicAdd(&nhits, 1);
+      if (at < kRuleHits) {
+        hit_i[at] = i;
+        hit_t[at] = t;
+      }
+    }
+  }
+  __syncthreads();
+  unsigned listed = 0;  // bit k: this thread's token k is listed (or past the vocabulary)
+#pragma unroll
+  for (int k = 0; k < kRulePer; ++k) {
+    const int i = tid + k * kRuleThreads;
+    const bool is = cw[k] || (marked[i >> 5] >> lane) & 1u;
+    if (is) {
+      const int at = atomicAdd(&nlist, 1);
+      list[at] = (uint16_t)i;
+      cnt[at] = cw[k];
+    }
+    if (is || v0 + i >= a.V) listed |= 1u << k;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int e = tid; e < nlist; e += kRuleThreads) {
+    const int t = list[e];
+    int first = kTreeMax;
+    if (npath) {
+      unsigned long long m = 0ull;
+#pragma unroll 1
+      for (int x = a.n_path - 1; x >= 0; --x)
+        if (ptok[x] == t) {
+          m |= 1ull << x;
+          first = x;
+        }
+      if (m) nodes[first] = m;
+    }
+    slot[e] = (uint8_t)first;
+    // the token's biases in list order: the next entry after the last one taken
+    float sum = 0.f;
+    if (nhits <= kRuleHits) {
+#pragma unroll 1
+      for (int last = -1, next; last < a.n_bias; last = next) {
+        next = a.n_bias;
+#pragma unroll 1
+        for (int x = 0; x < nhits; ++x)
+          if (hit_t[x] == t && hit_i[x] > last && hit_i[x] < next) next = hit_i[x];
+        if (next < a.n_bias) sum += a.bias[next];
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < a.n_bias; ++i)
+        if (a.bias_tok[i] - v0 == t) sum += a.bias[i];
+    }
+    adj[e] = sum;
+  }
+  __syncthreads();
+  const int nl = nlist;
+  const uint32_t bit = 1u << lane;  // a word holds the 32 tokens of a warp
+  float* y = a.y ? a.y + (size_t)row0 * a.ldy + v0 : nullptr;
+#pragma unroll 1
+  for (int q = 0; q < nrows; ++q) {
+    const int r = row0 + q;
+    if (q > 0) load(r);
+    float top = -INFINITY;
+    int at = 0x7FFFFFFF;
+    // listed tokens to the threads that serve them, the others here
+    float* xs = hand[q & 1];
 #pragma unroll
     for (int k = 0; k < kRulePer; ++k) {
-      const int i = tid + k * kRuleThreads, v = v0 + i;
+      const int i = tid + k * kRuleThreads;
+      if ((listed >> k) & 1u) {
+        xs[i] = l[k];
+        continue;
+      }
+      const float t = w[k] & bit ? l[k] : -INFINITY;
+      if (y) y[i] = t;
+      if (t > top) {
+        top = t;
+        at = v0 + i;
+      }
+    }
+    if (nl > 0) __syncthreads();
+#pragma unroll 1
+    for (int e = tid; e < nl; e += kRuleThreads) {
+      const int i = list[e], v = v0 + i;
       if (v >= a.V) continue;
-      float t = l[k];
-      uint32_t w = cw[k];
-      if (path) w += __popcll(extra[i] & pm);
-      if (w) {
-        const uint32_t c = w & 0x7FFFFFFFu;
+      float t = xs[i];
+      const uint32_t ok = a.allow ? a.allow[(size_t)r * a.allow_ld + (v >> 5)] >> (v & 31) : 1u;
+      uint32_t c = cnt[e] + __popcll(nodes[slot[e]] & pm);
+      if (c) {  // seen
+        c &= 0x7FFFFFFFu;
         t = t > 0.f ? __fdiv_rn(t, a.rep) : __fmul_rn(t, a.rep);
         t = __fsub_rn(t, __fadd_rn(__fmul_rn((float)c, a.freq), c ? a.pres : 0.f));
       }
-      const float b = adj[i];
+      const float b = adj[e];
       if (b != 0.f) t = __fadd_rn(t, b);
-      if (a.allow && !((a.allow[(size_t)r * a.allow_ld + (v >> 5)] >> (v & 31)) & 1u)) t = -INFINITY;
-      if (a.y) a.y[(size_t)r * a.ldy + v] = t;
-      if (t > best) {
-        best = t;
+      if (!(ok & 1u)) t = -INFINITY;
+      if (y) y[i] = t;
+      if (t > top || (t == top && t > -INFINITY && v < at)) {
+        top = t;
         at = v;
       }
     }
-    // a zero's sign does not order it; v + 0 makes -0 equal +0
-    unsigned long long key = at < 0 ? 0ull : argmax_key(best + 0.f, at);
+    if (y) y += a.ldy;
+    // the warp's largest value, then the lowest index that has it; + 0 makes -0
+    // equal +0 (a zero's sign does not order it)
+    const uint32_t u = (uint32_t)(argmax_key(top + 0.f, 0) >> 32);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, u);
+    const int lowest = __reduce_min_sync(0xffffffffu, u == most ? at : 0x7FFFFFFF);
+    if (lane == 0)
+      best[q][warp] = lowest == 0x7FFFFFFF ? 0ull
+                                           : (unsigned long long)most << 32 | (0xFFFFFFFFu - (uint32_t)lowest);
+  }
+  __syncthreads();
+  if (tid < nrows) {
+    const int r = row0 + tid;
+    unsigned long long key = best[tid][0];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other > key ? other : key;
-    }
-    if (lane == 0) red[warp] = key;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 1; w < kRuleThreads / 32; ++w) key = red[w] > key ? red[w] : key;
+    for (int x = 1; x < kWarps; ++x) key = best[tid][x] > key ? best[tid][x] : key;
+    if (gridDim.x > 1) {
       if (key) atomicMax(a.keys + r, key);
       __threadfence();
-      if (atomicAdd(a.cnt + r, 1u) == gridDim.x - 1) {  // every chunk of the row has merged
-        __threadfence();
-        const unsigned long long best_key = atomicMax(a.keys + r, 0ull);
-        a.tok[r] = best_key ? argmax_key_index(best_key) : -1;
-        a.val[r] = best_key ? argmax_key_value(best_key) : -INFINITY;
-        a.keys[r] = 0ull;  // leave the workspace cleared for the next call
-        a.cnt[r] = 0u;
-      }
+      if (atomicAdd(a.cnt + r, 1u) != gridDim.x - 1) return;
+      __threadfence();  // every chunk of the row has merged
+      key = atomicMax(a.keys + r, 0ull);
+      a.keys[r] = 0ull;  // leave the workspace cleared for the next call
+      a.cnt[r] = 0u;
     }
-    __syncthreads();
+    a.tok[r] = key ? argmax_key_index(key) : -1;
+    a.val[r] = key ? argmax_key_value(key) : -INFINITY;
   }
 }
 
@@ -237,9 +331,12 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
   uint8_t* body = static_cast<uint8_t*>(d_ws) + sizeof(WsHeader);
   a.keys = reinterpret_cast<unsigned long long*>(body);
   a.cnt = reinterpret_cast<unsigned*>(body + (size_t)rows * 8);
-  a.rows_per_cta = 1;
   const int chunks = (R->vocab + kRuleChunk - 1) / kRuleChunk;
-  cudaError_t e = launch_pdl(logit_rules_kernel, dim3(chunks, rows), kRuleThreads, 0,
+#ifndef MTP_RULE_CTAS
+#define MTP_RULE_CTAS 8
+#endif
+  a.rows_per_cta = std::min(kRuleRows, std::max(1, (int)((long long)chunks * rows / (sm_count() * MTP_RULE_CTAS))));
+  cudaError_t e = launch_pdl(logit_rules_kernel, dim3(chunks, (rows + a.rows_per_cta - 1) / a.rows_per_cta), kRuleThreads, 0,
                              static_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return cuda_fail(e, "logit_rules_argmax launch");
   return MTP_OK;

@@ -13,9 +13,9 @@
 //              normalised and rotated, v heads, appended to cache rows
 //              L .. L + n - 1;
 //   2. split:  every query row against the cached keys that all rows see,
-//              [max(0, L + n - W), L) for a window W (a node's depth is below
-//              n), split over CTAs, on tcgen05: no mask at all.  Partials
-//              (m, l, o);
+//              [max(0, L + D + 1 - W), L) for a window W and the tree's
+//              largest depth D, split over CTAs, on tcgen05: no mask at all.
+//              Partials (m, l, o);
 //   3. finish: one CTA a (node, head) joins the partials, the cached keys at
 //              the window's edge (fewer than n, each row its own) and the
 //              node's ancestors, read key by key, so a row that a mask hides
@@ -45,15 +45,22 @@ struct TreeAttnArgs {
   float* qf;       // [nkv][R][dqk] scaled queries, row r = i * G + g
   uint8_t* qt;     // [nkv][mt] tiles of 128 rows: f16 hi parts, then lo parts
   float* qinv;     // [nkv][mt * 128] power of two that undoes a row's f16 scale
-  int* dep;        // [n] depths inside [0, n)
+  int* dep;        // [n] depths inside [0, n), then at kTreeMax the largest
   float* part_o;   // [nkv][ns][R][dv]
   float2* part_ml; // [nkv][ns][R] running maximum and sum
   int R, mt;              // query rows of a KV head, tiles of 128 of them
-  int ns, kbeg, kper;     // splits, first split key, keys a split
+  int ns, kper;           // splits, keys a split
   int raw;                // raw K/V row buffers of a converter warp (1 or 2)
   int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
+
+// First cached key that every row sees (the prep launch has left the depths).
+__device__ __forceinline__ int first_common_key(const TreeAttnArgs& a) {
+  if (a.window <= 0) return 0;
+  const long long k = (long long)a.L + __ldcg(a.dep + kTreeMax) + 1 - a.window;
+  return k <= 0 ? 0 : k < a.L ? (int)k : a.L;
+}
 
 // ------------------------------------------------------------------ prep
 constexpr int kPrepThreads = 128;
@@ -125,6 +132,11 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnA
     if (blockIdx.x == 0) a.dep[threadIdx.x] = d;
   }
   __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    int d = max(threadIdx.x < a.n ? dep[threadIdx.x] : 0, threadIdx.x + 32 < a.n ? dep[threadIdx.x + 32] : 0);
+    d = __reduce_max_sync(0xffffffffu, d);
+    if (threadIdx.x == 0) a.dep[kTreeMax] = d;
+  }
   RopePos rp = a.rope;
   rp.depth = dep;
   const int lane = threadIdx.x & 31;
@@ -154,35 +166,6 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnA
     float* dst = a.vc + ((size_t)kv * a.cap + a.L + i) * a.dv;
     for (int c = lane; c < a.dv; c += 32) dst[c] = src[c];
   }
-}
-
-// A warp's running softmax state over up to 256 output dims: lane l holds dims
-// l + 32 j.
-struct RowState {
-  float m, l;
-  float o[8];
-};
-
-// One key against a warp's query row (dims lane + 32 j in q).
-__device__ __forceinline__ void row_step(RowState& s, const float (&q)[8], const float* k,
-                                         const float* v, int dqk, int dv, int lane) {
-  float dot = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (32 * j < dqk) dot += q[j] * k[lane + 32 * j];
-  dot = warp_sum(dot);
-  if (!(dot <= s.m)) {  // a larger logit, or NaN, which then stays
-    const float c = exp2f(s.m - dot);  // 0 at the first key (m = -inf)
-    s.m = dot;
-    s.l *= c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s.o[j] *= c;
-  }
-  const float p = dot == -INFINITY ? 0.f : exp2f(dot - s.m);
-  s.l += p;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (32 * j < dv) s.o[j] += p * v[lane + 32 * j];
 }
 
 // ------------------------------------------------------------------ split
@@ -382,8 +365,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int sp = blockIdx.x, mt = blockIdx.y, kv = blockIdx.z;
-  const int k0 = a.kbeg + sp * a.kper, k1 = min(a.L, k0 + a.kper);
-  const int nt = (k1 - k0 + NK - 1) / NK;  // >= 1 (host)
+  if (a.window > 0) pdl_wait();  // the first key comes from the depths
+  const int k0 = first_common_key(a) + sp * a.kper, k1 = min(a.L, k0 + a.kper);
+  const int nt = max(0, (k1 - k0 + NK - 1) / NK);  // 0 at a window's end: an empty partial
   const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
   const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
   const uint32_t voff = kStages * 2 * kpart, qoff = voff + kStages * 2 * vpart;
@@ -795,91 +779,195 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 }
 
 // ------------------------------------------------------------------ finish
+// One CTA a (node, head), its four warps sharing the splits and the keys read one
+// by one; lane l holds dims 4 l .. 4 l + 3 and, past 128 dims, 128 + 4 l ...
+// Bound by the latency of a few dependent reads from L2, so keys go four at a
+// time (a chain of 64 nodes: 27 -> 10 us).
+// H: 128-dim halves of the wider of the two head sizes.
 constexpr int kFinishWarps = 4;
+constexpr int kFinishKeys = 4;  // keys of a step
 
-__global__ void __launch_bounds__(kFinishWarps * 32) tree_finish_kernel(const TreeAttnArgs a) {
+template <int H>
+struct RowState {
+  float m, l;
+  float4 o[H];
+};
+
+__device__ __forceinline__ float4 dims4(const float* row, int d, int lane, int h) {
+  const int c = 128 * h + 4 * lane;
+  return c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+__device__ __forceinline__ void scale4(float4& v, float f) {
+  v.x *= f;
+  v.y *= f;
+  v.z *= f;
+  v.w *= f;
+}
+
+__device__ __forceinline__ void add4(float4& v, float f, const float4& x) {
+  v.x = fmaf(f, x.x, v.x);
+  v.y = fmaf(f, x.y, v.y);
+  v.z = fmaf(f, x.z, v.z);
+  v.w = fmaf(f, x.w, v.w);
+}
+
+// Cache rows at[0 .. n) (n <= kFinishKeys) against a warp's query row.
+template <int H>
+__device__ __forceinline__ void keys_step(RowState<H>& s, const float4 (&q)[H], const float* kc,
+                                          const float* vc, const int (&at)[kFinishKeys], int n, int dqk,
+                                          int dv, int lane) {
+  float dot[kFinishKeys];
+  float4 v[kFinishKeys][H];
+#pragma unroll
+  for (int i = 0; i < kFinishKeys; ++i) {
+    dot[i] = 0.f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      v[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float4 k = dims4(kc + (size_t)at[i] * dqk, dqk, lane, h);
+        v[i][h] = dims4(vc + (size_t)at[i] * dv, dv, lane, h);
+        dot[i] += q[h].x * k.x + q[h].y * k.y + q[h].z * k.z + q[h].w * k.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+    for (int i = 0; i < kFinishKeys; ++i) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], x);
+  float mn = s.m;
+#pragma unroll
+  for (int i = 0; i < kFinishKeys; ++i)
+    if (i < n) mn = fmaxf(mn, dot[i]);
+  const float c = mn == -INFINITY ? 1.f : exp2f(s.m - mn);  // 0 at the first keys
+  s.m = mn;
+  s.l *= c;
+#pragma unroll
+  for (int h = 0; h < H; ++h) scale4(s.o[h], c);
+#pragma unroll
+  for (int i = 0; i < kFinishKeys; ++i)
+    if (i < n) {
+      const float p = dot[i] == -INFINITY ? 0.f : exp2f(dot[i] - mn);  // NaN stays
+      s.l += p;
+#pragma unroll
+      for (int h = 0; h < H; ++h) add4(s.o[h], p, v[i][h]);
+    }
+}
+
+template <int H>
+__global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish_kernel(const TreeAttnArgs a) {
   __shared__ float sm_m[kFinishWarps], sm_l[kFinishWarps];
-  __shared__ float sm_o[kFinishWarps][256];
+  __shared__ float4 sm_o[kFinishWarps][32 * H];
   pdl_wait();
   pdl_launch_dependents();
   const int h = blockIdx.x, i = blockIdx.y, kv = h / a.G, r = i * a.G + h % a.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float q[8];
-  RowState s;
+  const float* qrow = a.qf + ((size_t)kv * a.R + r) * a.dqk;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 q[H];
+  RowState<H> s;
   s.m = -INFINITY;
   s.l = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    q[j] = 32 * j < a.dqk ? a.qf[((size_t)kv * a.R + r) * a.dqk + lane + 32 * j] : 0.f;
-    s.o[j] = 0.f;
+  for (int x = 0; x < H; ++x) {
+    q[x] = dims4(qrow, a.dqk, lane, x);
+    s.o[x] = zero;
+  }
+  // the splits' partials: warp w takes splits w, w + 4, ...; lane l has the
+  // weight of the l-th of them
+#pragma unroll 1
+  for (int s0 = warp; s0 < a.ns; s0 += 32 * kFinishWarps) {
+    const int sp = s0 + lane * kFinishWarps;
+    const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
+    const float2 ml = sp < a.ns ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
+    const float mn = fmaxf(s.m, warp_max(ml.x));
+    const float c = s.m == -INFINITY ? 1.f : exp2f(s.m - mn);
+    // a partial of NaN logits alone has no maximum, and its sum is NaN
+    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - mn);
+    s.m = mn;
+    s.l = s.l * c + warp_sum(f * ml.y);
+#pragma unroll
+    for (int x = 0; x < H; ++x) scale4(s.o[x], c);
+    const int n = min(32, (a.ns - s0 + kFinishWarps - 1) / kFinishWarps);
+    const float* po = a.part_o + (((size_t)kv * a.ns + s0) * a.R + r) * a.dv;
+    const size_t step = (size_t)kFinishWarps * a.R * a.dv;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float w = __shfl_sync(0xffffffffu, f, j);
+#pragma unroll
+      for (int x = 0; x < H; ++x) add4(s.o[x], w, dims4(po + j * step, a.dv, lane, x));
+    }
   }
   const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
   const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
   const int dep = a.dep[i];
+  int at[kFinishKeys];
   // cached keys at the window's edge: seen by this row, not by every row
   if (a.window > 0) {
-    const int e0 = max(0, a.L + dep - a.window + 1), e1 = min(a.L, a.kbeg);
-    for (int k = e0 + warp; k < e1; k += kFinishWarps)
-      row_step(s, q, kc + (size_t)k * a.dqk, vc + (size_t)k * a.dv, a.dqk, a.dv, lane);
+    const int e0 = max(0, a.L + dep - a.window + 1), e1 = first_common_key(a);
+#pragma unroll 1
+    for (int k = e0 + warp * kFinishKeys; k < e1; k += kFinishWarps * kFinishKeys) {
+#pragma unroll
+      for (int j = 0; j < kFinishKeys; ++j) at[j] = k + j;
+      keys_step(s, q, kc, vc, at, min(kFinishKeys, e1 - k), a.dqk, a.dv, lane);
+    }
   }
-  // the node's ancestors
+  // the node's ancestors inside the window
   unsigned long long m = a.mask[i];
   if (a.n < 64) m &= (1ull << a.n) - 1;
-  for (int c = 0; m; ++c) {
-    const int j = __ffsll(m) - 1;
-    m &= m - 1;
-    if (c % kFinishWarps != warp) continue;
-    if (a.window > 0 && a.dep[j] <= dep - a.window) continue;
-    row_step(s, q, kc + (size_t)(a.L + j) * a.dqk, vc + (size_t)(a.L + j) * a.dv, a.dqk, a.dv, lane);
+  if (a.window > 0) {
+    const bool in0 = lane < a.n && a.dep[lane] > dep - a.window,
+               in1 = lane + 32 < a.n && a.dep[lane + 32] > dep - a.window;
+    m &= __ballot_sync(0xffffffffu, in0) | (unsigned long long)__ballot_sync(0xffffffffu, in1) << 32;
   }
-  // the splits' partials
-  for (int sp = warp; sp < a.ns; sp += kFinishWarps) {
-    const size_t at = ((size_t)kv * a.ns + sp) * a.R + r;
-    const float2 ml = a.part_ml[at];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;
-    const float mn = fmaxf(s.m, ml.x);
-    const float c0 = exp2f(s.m - mn), c1 = exp2f(ml.x - mn);
-    s.m = mn;
-    s.l = s.l * c0 + ml.y * c1;
+#pragma unroll 1
+  for (int b = 0; m; ++b) {
+    int n = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (32 * j < a.dv) s.o[j] = s.o[j] * c0 + a.part_o[at * a.dv + lane + 32 * j] * c1;
+    for (int j = 0; j < kFinishKeys; ++j)
+      if (m) {
+        at[j] = a.L + __ffsll(m) - 1;
+        m &= m - 1;
+        n = j + 1;
+      }
+    if (b % kFinishWarps == warp) keys_step(s, q, kc, vc, at, n, a.dqk, a.dv, lane);
   }
   if (lane == 0) {
     sm_m[warp] = s.m;
     sm_l[warp] = s.l;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (32 * j < a.dv) sm_o[warp][lane + 32 * j] = s.o[j];
+  for (int x = 0; x < H; ++x) sm_o[warp][lane + 32 * x] = s.o[x];
   __syncthreads();
+  const int c = threadIdx.x;  // four dims a thread
+  if (4 * c >= a.dv) return;
   const float sink = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
   float M = sink;
+#pragma unroll
   for (int w = 0; w < kFinishWarps; ++w) M = fmaxf(M, sm_m[w]);
   float den = sink == -INFINITY ? 0.f : exp2f(sink - M);
-  float wt[kFinishWarps];
+  float4 o = zero;
 #pragma unroll
   for (int w = 0; w < kFinishWarps; ++w) {
-    wt[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - M);
-    den += wt[w] * sm_l[w];
+    const float f = sm_m[w] == -INFINITY ? 1.f : exp2f(sm_m[w] - M);  // none or NaN: 0 or NaN stays
+    den += f * sm_l[w];
+    add4(o, f, sm_o[w][c]);
   }
-  const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // empty row: 0; NaN stays
-  for (int c = threadIdx.x; c < a.dv; c += kFinishWarps * 32) {
-    float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kFinishWarps; ++w) o += wt[w] * sm_o[w][c];
-    o *= inv;
-    if (a.gated) {
-      const float g = a.qp[(size_t)i * a.ldq + ((size_t)2 * h + 1) * a.dqk + c];
-      o *= 1.f / (1.f + expf(-g));
-    }
-    a.out[((size_t)i * a.nh + h) * a.dv + c] = o;
+  scale4(o, den == 0.f ? 0.f : 1.f / den);  // a row that sees nothing: 0
+  if (a.gated) {
+    const float4 g = *reinterpret_cast<const float4*>(a.qp + (size_t)i * a.ldq + ((size_t)2 * h + 1) * a.dqk + 4 * c);
+    o.x /= 1.f + expf(-g.x);
+    o.y /= 1.f + expf(-g.y);
+    o.z /= 1.f + expf(-g.z);
+    o.w /= 1.f + expf(-g.w);
   }
+  *reinterpret_cast<float4*>(a.out + ((size_t)i * a.nh + h) * a.dv + 4 * c) = o;
 }
 
 // ------------------------------------------------------------------ host
 struct TreePlan {
-  int kbeg, ns, kper;
+  int ns, kper;
 };
 
 // Keys of a tile of the split kernel: operand tiles of 64 keys fit beside the
@@ -889,9 +977,8 @@ static int split_nk(int dqk, int dv) { return dqk <= 128 && dv <= 128 ? 64 : 32;
 // Splits of the cached keys all rows see: about one CTA per SM.
 static TreePlan tree_plan_splits(const mtp_attn_geom* g, int L, int n) {
   TreePlan p;
-  const int window = g->window;
-  p.kbeg = window > 0 ? (int)std::min<int64_t>(L, std::max<int64_t>(0, (int64_t)L + n - window)) : 0;
-  const int keys = L - p.kbeg;
+  // a window's rows have at most window - 1 cached keys in common (depth 0 alone)
+  const int keys = g->window > 0 ? std::min(L, g->window - 1) : L;
   const int mt = (n * (g->n_heads / g->n_kv_heads) + 127) / 128;
   p.ns = 0;
   p.kper = 0;
@@ -924,7 +1011,7 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
     return p;
   };
   const size_t rows = (size_t)n * g->n_heads;
-  w.dep = reinterpret_cast<int*>(take(sizeof(int) * kTreeMax));
+  w.dep = reinterpret_cast<int*>(take(sizeof(int) * (kTreeMax + 1)));
   w.qf = reinterpret_cast<float*>(take(4 * rows * g->head_dim_qk));
   const size_t tiles = (size_t)g->n_kv_heads * ((n * (g->n_heads / g->n_kv_heads) + 127) / 128);
   w.qt = take(tiles * 512 * g->head_dim_qk);
@@ -1083,7 +1170,6 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   a.rep = a.dv > 128 || a.R > 64 ? 1 : a.R <= 32 && split_nk(a.dqk, a.dv) == 64 ? 4 : 2;
   a.mt = (a.R + 127) / 128;  // 1 where rows are repeated
   a.ns = pl.ns;
-  a.kbeg = pl.kbeg;
   a.kper = pl.kper;
   a.err = &static_cast<WsHeader*>(d_ws)->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1093,7 +1179,8 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   if (e == cudaSuccess && a.ns > 0)
     e = launch_split(a, st);
   if (e == cudaSuccess)
-    e = launch_pdl(tree_finish_kernel, dim3(a.nh, n), kFinishWarps * 32, 0, st, a);
+    e = launch_pdl(std::max(a.dqk, a.dv) > 128 ? tree_finish_kernel<2> : tree_finish_kernel<1>, dim3(a.nh, n),
+                   kFinishWarps * 32, 0, st, a);
   if (e != cudaSuccess) return cuda_fail(e, "attn_tree_sink launch");
   return MTP_OK;
 }
