@@ -56,7 +56,7 @@ struct RuleArgs {
 // loop is rolled up, as a CTA runs it once and fetches its instructions from L2.
 __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __grid_constant__ RuleArgs a) {
   constexpr int kWarps = kRuleThreads / 32;
-  __shared__ uint32_t marked[kRuleChunk / 32];        // tokens with a bias or on a path
+  __shared__ uint32_t biased[kRuleChunk / 32], on_path[kRuleChunk / 32];  // a bit a token
   __shared__ uint16_t list[kRuleChunk];               // the listed tokens, their count words, summed
   __shared__ uint32_t cnt[kRuleChunk];                // biases and path nodes
   __shared__ float adj[kRuleChunk];
@@ -65,14 +65,15 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
   __shared__ float hand[2][kRuleChunk];               // their logits of a row and the next
   __shared__ int ptok[kTreeMax];
   __shared__ int hit_i[kRuleHits], hit_t[kRuleHits];  // bias entries of the chunk, in any order
+  __shared__ float hit_b[kRuleHits];
   __shared__ unsigned long long best[kRuleRows][kWarps];
-  __shared__ int nlist, nhits, npath;
+  __shared__ int nlist, nhits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int v0 = blockIdx.x * kRuleChunk;
   const int row0 = blockIdx.y * a.rows_per_cta, nrows = min(a.rows - row0, a.rows_per_cta);
-  if (tid < kRuleChunk / 32) marked[tid] = 0u;
+  if (tid < kRuleChunk / 32) biased[tid] = on_path[tid] = 0u;
   if (tid == 0) {
-    nlist = nhits = npath = 0;
+    nlist = nhits = 0;
     nodes[kTreeMax] = 0ull;
   }
   pdl_wait();
@@ -99,46 +100,68 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
     pm = a.n_path ? a.path_mask[r] : 0ull;
   };
   load(row0);
+  const int pt = tid < a.n_path ? a.path_tok[tid] : 0;
+  int bt = tid < a.n_bias ? a.bias_tok[tid] : 0;
+  float bv = tid < a.n_bias ? a.bias[tid] : 0.f;
   __syncthreads();
   if (tid < a.n_path) {
-    const int t = a.path_tok[tid] - v0;
+    const int t = pt - v0;
     ptok[tid] = t;
-    if (t >= 0 && t < kRuleChunk) {
-      atomicOr(&marked[t >> 5], 1u << (t & 31));
-      npath = 1;
-    }
+    if (t >= 0 && t < kRuleChunk) atomicOr(&on_path[t >> 5], 1u << (t & 31));
   }
 #pragma unroll 1
   for (int i = tid; i < a.n_bias; i += kRuleThreads) {
-    const int t = a.bias_tok[i] - v0;
+    const int t = bt - v0;
+    const float b = bv;
+    if (i + kRuleThreads < a.n_bias) {
+      bt = a.bias_tok[i + kRuleThreads];
+      bv = a.bias[i + kRuleThreads];
+    }
     if (t >= 0 && t < kRuleChunk) {
-      atomicOr(&marked[t >> 5], 1u << (t & 31));
+      atomicOr(&biased[t >> 5], 1u << (t & 31));
       const int at = atomicAdd(&nhits, 1);
       if (at < kRuleHits) {
         hit_i[at] = i;
         hit_t[at] = t;
+        hit_b[at] = b;
       }
     }
   }
   __syncthreads();
+  const uint32_t bit = 1u << lane;  // a word holds the 32 tokens of a warp
   unsigned listed = 0;  // bit k: this thread's token k is listed (or past the vocabulary)
+  unsigned marks = 0;
 #pragma unroll
   for (int k = 0; k < kRulePer; ++k) {
     const int i = tid + k * kRuleThreads;
-    const bool is = cw[k] || (marked[i >> 5] >> lane) & 1u;
-    if (is) {
-      const int at = atomicAdd(&nlist, 1);
-      list[at] = (uint16_t)i;
-      cnt[at] = cw[k];
+    if (cw[k] || (biased[i >> 5] | on_path[i >> 5]) & bit) marks |= 1u << k;
+    if (v0 + i >= a.V) listed |= 1u << k;
+  }
+  listed |= marks;
+  {
+    const int mine = __popc(marks);
+    int at = mine;  // inclusive sum over the warp's lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += x;
     }
-    if (is || v0 + i >= a.V) listed |= 1u << k;
+    int base = 0;
+    if (lane == 31 && at > 0) base = atomicAdd(&nlist, at);
+    at += __shfl_sync(0xffffffffu, base, 31) - mine;
+#pragma unroll
+    for (int k = 0; k < kRulePer; ++k)
+      if ((marks >> k) & 1u) {
+        list[at] = (uint16_t)(tid + k * kRuleThreads);
+        cnt[at++] = cw[k];
+      }
   }
   __syncthreads();
 #pragma unroll 1
   for (int e = tid; e < nlist; e += kRuleThreads) {
     const int t = list[e];
     int first = kTreeMax;
-    if (npath) {
+    if ((on_path[t >> 5] >> (t & 31)) & 1u) {
       unsigned long long m = 0ull;
 #pragma unroll 1
       for (int x = a.n_path - 1; x >= 0; --x)
@@ -146,19 +169,25 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
           m |= 1ull << x;
           first = x;
         }
-      if (m) nodes[first] = m;
+      nodes[first] = m;
     }
     slot[e] = (uint8_t)first;
     // the token's biases in list order: the next entry after the last one taken
     float sum = 0.f;
-    if (nhits <= kRuleHits) {
+    if (!((biased[t >> 5] >> (t & 31)) & 1u)) {
+    } else if (nhits <= kRuleHits) {
 #pragma unroll 1
-      for (int last = -1, next; last < a.n_bias; last = next) {
-        next = a.n_bias;
+      for (int last = -1;;) {
+        int next = a.n_bias, at = 0;
 #pragma unroll 1
         for (int x = 0; x < nhits; ++x)
-          if (hit_t[x] == t && hit_i[x] > last && hit_i[x] < next) next = hit_i[x];
-        if (next < a.n_bias) sum += a.bias[next];
+          if (hit_t[x] == t && hit_i[x] > last && hit_i[x] < next) {
+            next = hit_i[x];
+            at = x;
+          }
+        if (next == a.n_bias) break;
+        sum += hit_b[at];
+        last = next;
       }
     } else {
 #pragma unroll 1
@@ -169,12 +198,10 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
   }
   __syncthreads();
   const int nl = nlist;
-  const uint32_t bit = 1u << lane;  // a word holds the 32 tokens of a warp
   float* y = a.y ? a.y + (size_t)row0 * a.ldy + v0 : nullptr;
 #pragma unroll 1
   for (int q = 0; q < nrows; ++q) {
     const int r = row0 + q;
-    if (q > 0) load(r);
     float top = -INFINITY;
     int at = 0x7FFFFFFF;
     // listed tokens to the threads that serve them, the others here
@@ -193,6 +220,8 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
         at = v0 + i;
       }
     }
+    const unsigned long long path = pm;
+    if (q + 1 < nrows) load(r + 1);  // on its way while the listed tokens are served
     if (nl > 0) __syncthreads();
 #pragma unroll 1
     for (int e = tid; e < nl; e += kRuleThreads) {
@@ -200,7 +229,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       if (v >= a.V) continue;
       float t = xs[i];
       const uint32_t ok = a.allow ? a.allow[(size_t)r * a.allow_ld + (v >> 5)] >> (v & 31) : 1u;
-      uint32_t c = cnt[e] + __popcll(nodes[slot[e]] & pm);
+      uint32_t c = cnt[e] + __popcll(nodes[slot[e]] & path);
       if (c) {  // seen
         c &= 0x7FFFFFFFu;
         t = t > 0.f ? __fdiv_rn(t, a.rep) : __fmul_rn(t, a.rep);
@@ -333,7 +362,7 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
   a.cnt = reinterpret_cast<unsigned*>(body + (size_t)rows * 8);
   const int chunks = (R->vocab + kRuleChunk - 1) / kRuleChunk;
 #ifndef MTP_RULE_CTAS
-#define MTP_RULE_CTAS 8
+#define MTP_RULE_CTAS 3
 #endif
   a.rows_per_cta = std::min(kRuleRows, std::max(1, (int)((long long)chunks * rows / (sm_count() * MTP_RULE_CTAS))));
   cudaError_t e = launch_pdl(logit_rules_kernel, dim3(chunks, (rows + a.rows_per_cta - 1) / a.rows_per_cta), kRuleThreads, 0,
