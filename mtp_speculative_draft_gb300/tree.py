@@ -13,41 +13,57 @@ import torch
 
 from . import _lib as L
 from ._lib import AttnGeom, DraftTree, HeadRows, KvCaches, LogitRules, RopeAxes, check
-from .api import _stream, workspace
+from .api import workspace
 
 _I32, _F32 = torch.int32, torch.float32
+
+
+def _refuse(t, dtype, numel, name):
+    if not t.is_cuda or t.get_device() != _device():
+        raise ValueError(f"{name}: a tensor on the current CUDA device is required")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} is required, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is required")
+    raise ValueError(f"{name}: {numel} values are needed, got {t.numel()}")
 
 
 def _ptr(t, dtype, numel, name, device):
     """Device pointer of a contiguous tensor of ``dtype`` with at least ``numel`` values."""
     if t is None:
         return None
-    if not t.is_cuda or t.get_device() != device:
-        raise ValueError(f"{name}: a tensor on the current CUDA device is required")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: {dtype} is required, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is required")
-    if t.numel() < numel:
-        raise ValueError(f"{name}: {numel} values are needed, got {t.numel()}")
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.numel() < numel:
+        _refuse(t, dtype, numel, name)
     return t.data_ptr()
 
 
 def _device():
-    if not torch.cuda.is_available():
-        raise ValueError("a CUDA device is required")
-    return torch.cuda.current_device()
+    """The current CUDA device."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        raise ValueError("a CUDA device is required") from None
+
+
+def _on(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _rows(t, rows, width, name, device):
-    """Pointer and row stride of a float32 ``[rows, width]`` matrix whose rows are contiguous."""
-    if t is None or not t.is_cuda or t.get_device() != device:
+    """Pointer and row stride (0: contiguous rows) of a float32 ``[rows, width]`` matrix whose rows are
+    contiguous."""
+    if t is None or t.get_device() != device:
         raise ValueError(f"{name}: a tensor on the current CUDA device is required")
     if t.dtype is not _F32:
         raise TypeError(f"{name}: torch.float32 is required, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: [{rows}, {width}] with contiguous rows is required, got {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] != width:
+        raise ValueError(f"{name}: [{rows}, {width}] with contiguous rows is required, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    if (width > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{name}: [{rows}, {width}] with contiguous rows is required, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
 
 
 def _ws(ws):
@@ -84,22 +100,26 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
     dev = _device()
     lib = L.load()
     rows, _, d = tensors[0][0].shape
-    arr = (HeadRows * len(tensors))()
-    for a, (x, y, w) in zip(arr, tensors):
-        for t in (x, y):
-            if not t.is_cuda or t.get_device() != dev:
-                raise ValueError("rope_axes_rows: tensors on the current CUDA device are required")
-            if t.dtype is not _F32 or t.dim() != 3 or t.stride(2) != 1:
-                raise TypeError("rope_axes_rows: float32 [rows, heads, head_dim] with contiguous head rows")
-        if x.shape[0] != rows or x.shape[2] != d or y.shape != x.shape:
-            raise ValueError("rope_axes_rows: x and y of one shape, one row count and head_dim are required")
-        n = x.shape[1]
-        a.x, a.y, a.norm_w, a.n_heads = x.data_ptr(), y.data_ptr(), _ptr(w, _F32, d, "norm_w", dev), n
-        a.x_hs, a.y_hs = (x.stride(1), y.stride(1)) if n > 1 else (d, d)
-        a.x_ld, a.y_ld = (x.stride(0), y.stride(0)) if rows > 1 else (n * a.x_hs, n * a.y_hs)
+    descs = []
+    for x, y, w in tensors:
+        shape = x.shape
+        if x.get_device() != dev or y.get_device() != dev:
+            raise ValueError("rope_axes_rows: tensors on the current CUDA device are required")
+        if len(shape) != 3 or shape[0] != rows or shape[2] != d or y.shape != shape:
+            raise ValueError("rope_axes_rows: x and y [rows, heads, head_dim] of one row count and head_dim are required")
+        n = shape[1]
+        (xr, xh, x1), (yr, yh, y1) = x.stride(), y.stride()
+        if x.dtype is not _F32 or y.dtype is not _F32 or x1 != 1 or y1 != 1:
+            raise TypeError("rope_axes_rows: float32 with contiguous head rows is required")
+        if n == 1:  # a stride that is never stepped may be anything
+            xh = yh = d
+        if rows == 1:
+            xr, yr = n * xh, n * yh
+        descs.append(HeadRows(x.data_ptr(), y.data_ptr(), _ptr(w, _F32, d, "norm_w", dev), xr, yr, xh, yh, n))
+    arr = (HeadRows * len(descs))(*descs)
     if ws is None:
         ws = workspace(lib.rope_axes_rows_workspace_bytes(), stream=stream)
-    check(lib.rope_axes_rows(C.byref(axes), arr, len(arr), rows, d, eps, *_ws(ws), _stream(stream)),
+    check(lib.rope_axes_rows(C.byref(axes), arr, len(arr), rows, d, eps, *_ws(ws), _on(stream, dev)),
           "rope_axes_rows")
     return ws
 
@@ -131,7 +151,7 @@ def mtp_tree_plan(parents, mask, depth, ws=None, stream=None):
         raise TypeError("mtp_tree_plan: mask holds 64-bit words")
     check(L.load().mtp_tree_plan(_ptr(parents, _I32, n, "parents", dev), n,
                                  _ptr(mask, mask.dtype, n, "mask", dev),
-                                 _ptr(depth, _I32, n, "depth", dev), *_ws(ws), _stream(stream)),
+                                 _ptr(depth, _I32, n, "depth", dev), *_ws(ws), _on(stream, dev)),
           "mtp_tree_plan")
     return ws
 
@@ -150,19 +170,20 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
     pq, ldq = _rows(qp, n, nh * dqk * (2 if g.gated_q else 1), "qp", dev)
     pk, ldk = _rows(kp, n, nkv * dqk, "kp", dev)
     pv, ldv = _rows(vp, n, nkv * dv, "vp", dev)
-    t = DraftTree(tree.d_mask, tree.d_depth, tree.axes, n, tree.pos_base, ldq, ldk, ldv)
+    if ldq or ldk or ldv:  # a call's own strides: the descriptor stays as it is
+        tree = DraftTree(tree.d_mask, tree.d_depth, tree.axes, n, tree.pos_base, ldq, ldk, ldv)
     cap = k_cache.shape[1] if k_cache.dim() == 3 else 0
-    if tuple(k_cache.shape) != (nkv, cap, dqk) or tuple(v_cache.shape) != (nkv, cap, dv):
+    if k_cache.shape != (nkv, cap, dqk) or v_cache.shape != (nkv, cap, dv):
         raise ValueError("attn_tree_sink: caches [n_kv, cap, dim] of the geometry are required")
     if ws is None:
         ws = workspace(lib.attn_tree_sink_workspace_bytes(C.byref(g), n, cache_len), stream=stream)
     check(lib.attn_tree_sink(
-        C.byref(g), C.byref(t), pq, pk, pv, _ptr(q_norm, _F32, dqk, "q_norm", dev),
+        C.byref(g), C.byref(tree), pq, pk, pv, _ptr(q_norm, _F32, dqk, "q_norm", dev),
         _ptr(k_norm, _F32, dqk, "k_norm", dev), _ptr(rope, _F32, 0, "rope", dev),
         rope.numel() // g.rot_dim if rope is not None and g.rot_dim > 0 else 0,
         _ptr(sinks, _F32, nh, "sinks", dev), _ptr(k_cache, _F32, 0, "k_cache", dev),
         _ptr(v_cache, _F32, 0, "v_cache", dev), int(cache_len), cap,
-        _ptr(out, _F32, n * nh * dv, "out", dev), *_ws(ws), _stream(stream)), "attn_tree_sink")
+        _ptr(out, _F32, n * nh * dv, "out", dev), *_ws(ws), _on(stream, dev)), "attn_tree_sink")
     return ws
 
 
@@ -208,13 +229,14 @@ def logit_rules_argmax(rules: LogitRules, logits, tokens, values, out=None, ws=N
     rows = logits.shape[0]
     if rows > rules.rows:
         raise ValueError(f"logit_rules_argmax: the rules' mask has {rules.rows} rows, the logits {rows}")
-    px, ld = _rows(logits, rows, rules.vocab, "logits", dev)
-    py, ldy = (None, 0) if out is None else _rows(out, rows, rules.vocab, "out", dev)
+    vocab = rules.vocab
+    px, ld = _rows(logits, rows, vocab, "logits", dev)
+    py, ldy = (None, 0) if out is None else _rows(out, rows, vocab, "out", dev)
     if ws is None:
         ws = workspace(lib.logit_rules_argmax_workspace_bytes(rows), stream=stream)
-    check(lib.logit_rules_argmax(C.byref(rules), px, ld, rows, _ptr(tokens, _I32, rows, "tokens", dev),
-                                 _ptr(values, _F32, rows, "values", dev), py, ldy, *_ws(ws),
-                                 _stream(stream)), "logit_rules_argmax")
+    check(lib.logit_rules_argmax(C.byref(rules), px, ld or vocab, rows, _ptr(tokens, _I32, rows, "tokens", dev),
+                                 _ptr(values, _F32, rows, "values", dev), py, ldy or vocab, *_ws(ws),
+                                 _on(stream, dev)), "logit_rules_argmax")
     return ws
 
 
@@ -228,7 +250,7 @@ def mtp_token_counts(counts, tokens, prompt=False, ws=None, stream=None):
     n = tokens.numel()
     check(L.load().mtp_token_counts(_ptr(counts, counts.dtype, 1, "counts", dev), counts.numel(),
                                     _ptr(tokens, _I32, n, "tokens", dev), n, int(bool(prompt)), *_ws(ws),
-                                    _stream(stream)), "mtp_token_counts")
+                                    _on(stream, dev)), "mtp_token_counts")
     return ws
 
 
@@ -241,7 +263,7 @@ def mtp_tree_accept(parents, tokens, verify, path, emitted, count, stream=None):
     check(L.load().mtp_tree_accept(
         _ptr(parents, _I32, n, "parents", dev), _ptr(tokens, _I32, n, "tokens", dev),
         _ptr(verify, _I32, n, "verify", dev), n, _ptr(path, _I32, n, "path", dev),
-        _ptr(emitted, _I32, n, "emitted", dev), _ptr(count, _I32, 1, "count", dev), _stream(stream)),
+        _ptr(emitted, _I32, n, "emitted", dev), _ptr(count, _I32, 1, "count", dev), _on(stream, dev)),
         "mtp_tree_accept")
 
 
@@ -271,5 +293,5 @@ def kv_tree_commit(caches: KvCaches, path, cache_len, ws=None, stream=None):
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     n = path.numel()
     check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, int(cache_len),
-                                  *_ws(ws), _stream(stream)), "kv_tree_commit")
+                                  *_ws(ws), _on(stream, dev)), "kv_tree_commit")
     return ws

@@ -355,6 +355,38 @@ def test_attn_tree_graphs_streams_and_a_shared_workspace(dev):
     b.check("second graph")
 
 
+def test_wrappers_refuse_what_the_kernels_cannot_read(dev):
+    """Broadcast rows, wrong types, short or non-contiguous tensors: refused before any launch."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    call = Call(_attn_case(11, nh=4, nkv=2, dqk=64, dv=64, L=10, n=3), dev)
+    good = dict(qp=call.qp, kp=call.kp, out=call.out, k=call.k)
+    for name, bad, error in (
+            ("qp", call.qp[:1].expand(3, -1), ValueError),      # one row seen three times
+            ("qp", call.qp.double(), TypeError), ("qp", call.qp[:, ::2], ValueError),
+            ("kp", call.kp[:2], ValueError), ("kp", call.kp.cpu(), ValueError),
+            ("out", call.out[:2], ValueError), ("out", call.out.t(), ValueError), ("out", call.out.half(), TypeError),
+            ("k", call.k[:1], ValueError)):
+        for key, value in {**good, name: bad}.items():
+            setattr(call, key, value)
+        with pytest.raises(error):
+            call()
+    for key, value in good.items():
+        setattr(call, key, value)
+    call()
+    call.check()
+    x = torch.zeros(1, 100, device=dev)
+    tok, val = torch.zeros(4, dtype=torch.int32, device=dev), torch.zeros(4, device=dev)
+    with pytest.raises(ValueError):
+        M.logit_rules_argmax(M.logit_rules(100), x.expand(4, 100), tok, val)
+    with pytest.raises(ValueError):  # the mask has fewer rows than the logits
+        M.logit_rules_argmax(M.logit_rules(100, allow=torch.zeros(3, 4, dtype=torch.int32, device=dev)),
+                             torch.zeros(4, 100, device=dev), tok, val)
+    with pytest.raises(M._lib.MtpError):  # rows that overlap
+        ax = M.rope_axes((16,), torch.zeros(1, 4, dtype=torch.int32, device=dev), torch.zeros(64, device=dev))
+        M.rope_axes_rows(ax, [(torch.zeros(1, 2, 32, device=dev).expand(4, 2, 32), torch.zeros(4, 2, 32, device=dev), None)])
+
+
 # ------------------------------------------------------------------ logit rules
 def _rules_case(seed, rows, V, n_path=0, n_bias=0, allow=None, counts=True, rep=1.3, freq=0.4, pres=0.3):
     rng = np.random.default_rng(seed)
