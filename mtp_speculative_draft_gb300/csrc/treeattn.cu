@@ -50,7 +50,7 @@ struct TreeAttnArgs {
   float2* part_ml; // [nkv][ns][R] running maximum and sum
   int R, mt;              // query rows of a KV head, tiles of 128 of them
   int ns, kper;           // splits, keys a split
-  int raw;                // raw K/V row buffers of a converter warp (1 or 2)
+  int vstages;            // V tile buffers of the split kernel (1 or 2)
   int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
@@ -209,7 +209,8 @@ constexpr int kScaleRing = 4;  // tiles whose scales are kept: > kStages + 1
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
 constexpr int kLaneStride = 132;  // floats of a lane's state: 16-byte accesses without bank conflicts
-constexpr int kStages = 2;        // K and V tile buffers
+constexpr int kStages = 2;        // K tile buffers (V: two, or one where they do not fit)
+constexpr int kRawBytes = 8192;   // a converter warp's rows of a tile: NK / 4 rows of up to 128 or 256 floats
 
 // f16 A and B, f32 accumulator, M = 128; B is MN-major when mn is set (bit 16).
 __device__ __forceinline__ uint32_t idesc_f16(int N, bool mn) {
@@ -321,10 +322,10 @@ __device__ __forceinline__ float sum16(const float (&v)[16]) {
 
 struct SplitSmem {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
-  uint64_t raw[kConvWarps][2], top[2];       // a warp's rows have arrived; every warp's largest |x| is there
+  uint64_t raw[kConvWarps], top[2];          // a warp's rows have arrived; the K or V warps' largest |x| are there
   uint32_t tmem;
   float kinv[kScaleRing], vinv[kScaleRing];  // a tile's inverse scales
-  alignas(16) float wmax[4][kConvWarps];     // largest |x| of each converter warp's rows
+  alignas(16) float wmax[2][2][4];           // largest |x| of each converter warp's rows: K or V, odd or even tile
   float smax[2][128];                        // COL: largest S of each warpgroup's keys
 };
 // At the end, behind the lane states: m, l and weight of each lane of both
@@ -333,9 +334,6 @@ struct SplitStates {
   float m[2][128], l[2][128], w[2][128];
 };
 
-static size_t split_stage_bytes(int NK, int dqk, int dv) {
-  return (size_t)NK * 256 * ((dqk + 63) / 64 + (dv + 63) / 64);
-}
 // First tensor-memory column of the queries (hi parts, then lo parts) behind two
 // S tiles and the outputs; whether the lo parts fit too.
 __host__ __device__ constexpr int split_q_col(int NK, bool col, int dv) { return 2 * NK + (col ? dv : 2 * dv); }
@@ -370,7 +368,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const int nt = max(0, (k1 - k0 + NK - 1) / NK);  // 0 at a window's end: an empty partial
   const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
   const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
-  const uint32_t voff = kStages * 2 * kpart, qoff = voff + kStages * 2 * vpart;
+  const int VS = a.vstages;
+  const uint32_t voff = kStages * 2 * kpart, qoff = voff + (uint32_t)VS * 2 * vpart;
   const bool qlo_tm = split_q_lo_fits(NK, COL, a.dqk, a.dv);
   const uint32_t roff = qoff + (qlo_tm ? 0u : (uint32_t)qb * 128 * 128);  // raw rows
 
@@ -386,15 +385,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     for (int t = 0; t < kAhead; ++t) prefetch(t);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kfull[i], kConvWarps);
+      mbar_init(&sh.kfull[i], kConvWarps / 2);
       mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.vfull[i], kConvWarps);
+      mbar_init(&sh.vfull[i], kConvWarps / 2);
       mbar_init(&sh.vempty[i], 1);
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.ofull[i], 1);
-      mbar_init(&sh.top[i], kConvWarps);
-      for (int w = 0; w < kConvWarps; ++w) mbar_init(&sh.raw[w][i], 1);
+      mbar_init(&sh.top[i], kConvWarps / 2);
     }
+    for (int w = 0; w < kConvWarps; ++w) mbar_init(&sh.raw[w], 1);
     mbar_fence_init();
   }
   if (warp == 0) tc5::alloc(&sh.tmem, 512);
@@ -407,105 +406,92 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   auto block_sync = [&]() { asm volatile("bar.sync 0, 512;" ::: "memory"); };
 
   if (warp >= 8) {
-    // ---------------- converters
-    const int cw = warp - 8;
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    constexpr int RPW = NK / kConvWarps;  // rows a warp of a tile
+    // ---------------- converters: four warps for K, four for V
+    const int cw = warp - 8, v = cw >> 2, w4 = cw & 3;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    constexpr int RPW = NK / 4;           // rows a warp of a tile
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
-    const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
-    const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
+    static_assert(RPW * SL == 16, "sixteen words a lane");
+    const int d = v ? a.dv : a.dqk, r0 = w4 * RPW;
+    const float* src = v ? a.vc + (size_t)kv * a.cap * a.dv : a.kc + (size_t)kv * a.cap * a.dqk;
+    const uint32_t part = v ? vpart : kpart, off = v ? voff : 0u;
+    uint64_t* full = v ? sh.vfull : sh.kfull;
+    uint64_t* empty = v ? sh.vempty : sh.kempty;
+    float* inv = v ? sh.vinv : sh.kinv;
+    const int ns = v ? VS : kStages;
+    uint8_t* raw = sm + roff + (size_t)cw * kRawBytes;
     const uint64_t pol = l2_policy_evict_first();
-    // Phase p of the loop: tile p / 2, K (even) or V.  A warp's rows of a phase
-    // come by bulk copy into one of its RS raw buffers, which is filled anew
-    // as soon as the rows are in registers (eight 16-byte words a lane).
-    static_assert(RPW * SL == 8, "eight words a lane");
-    const int np = 2 * nt, RS = a.raw;
-    uint8_t* raw = sm + roff + (size_t)cw * RS * 4096;
-    auto rows_of = [&](int p) { return min(RPW, k1 - (k0 + (p >> 1) * NK) - cw * RPW); };
-    auto fetch = [&](int p) {
-      if (p >= np || lane != 0) return;
-      const int n = rows_of(p), d = p & 1 ? a.dv : a.dqk;
-      if (n <= 0) return;
-      uint64_t* bar = &sh.raw[cw][p & (RS - 1)];
-      mbar_arrive_expect_tx(bar, (uint32_t)n * d * 4);
-      bulk_load(raw + (p & (RS - 1)) * 4096,
-                (p & 1 ? vc : kc) + (size_t)(k0 + (p >> 1) * NK + cw * RPW) * d, (uint32_t)n * d * 4, bar, pol);
+    auto rows_of = [&](int t) { return min(RPW, k1 - (k0 + t * NK) - r0); };
+    // A warp's rows of a tile come by bulk copy into its raw buffer, which is
+    // filled anew as soon as the rows are in registers.
+    auto fetch = [&](int t) {
+      const int n = rows_of(t);
+      if (t >= nt || n <= 0 || lane != 0) return;
+      mbar_arrive_expect_tx(&sh.raw[cw], (uint32_t)n * d * 4);
+      bulk_load(raw, src + (size_t)(k0 + t * NK + r0) * d, (uint32_t)n * d * 4, &sh.raw[cw], pol);
     };
-    // the rows of phase p, and their largest |x| for the tile's scale
-    auto take = [&](float4 (&x)[8], int p) {
-      const int n = rows_of(p), d = p & 1 ? a.dv : a.dqk;
-      if (n > 0) wait(&sh.raw[cw][p & (RS - 1)], (uint32_t)(RS == 2 ? p >> 1 : p) & 1u);
-      const float* src = reinterpret_cast<const float*>(raw + (p & (RS - 1)) * 4096) + 4 * lane;
+    fetch(0);
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      if (fetcher) prefetch(t + kAhead);
+      const int n = rows_of(t);
+      if (n > 0) wait(&sh.raw[cw], (uint32_t)t & 1u);
+      float4 x[16];
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < RPW; ++i)
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i < n && 4 * (lane + 32 * s) < d) v = *reinterpret_cast<const float4*>(src + i * d + 128 * s);
-          x[i * SL + s] = v;
-          mx = fmaxf(fmaxf(fmaxf(mx, fabsf(v.x)), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+          float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n && 4 * (lane + 32 * s) < d)
+            q = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(raw) + i * d + 4 * lane + 128 * s);
+          x[i * SL + s] = q;
         }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x[i].x)), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w)));
       mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
       if (lane == 0) {
-        sh.wmax[p & 3][cw] = mx;
-        tc5::mbar_arrive(&sh.top[p & 1]);
+        sh.wmax[v][t & 1][w4] = mx;
+        tc5::mbar_arrive(&sh.top[v]);
         fence_proxy_async_shared_cta();
       }
-      fetch(p + RS);
-    };
-    auto scale_of = [&](int p, float* inv) {
-      wait(&sh.top[p & 1], (uint32_t)(p >> 1) & 1u);
-      const float4 a0 = *reinterpret_cast<const float4*>(&sh.wmax[p & 3][0]),
-                   a1 = *reinterpret_cast<const float4*>(&sh.wmax[p & 3][4]);
-      const float mx = fmaxf(fmaxf(fmaxf(a0.x, a0.y), fmaxf(a0.z, a0.w)), fmaxf(fmaxf(a1.x, a1.y), fmaxf(a1.z, a1.w)));
+      fetch(t + 1);
+      // the tile's scale: the largest |x| of the four warps' rows
+      __syncwarp();
+      wait(&sh.top[v], (uint32_t)t & 1u);
+      const float4 m4 = *reinterpret_cast<const float4*>(sh.wmax[v][t & 1]);
       float scale;
-      const float iv = f16_scale(mx, scale);
-      if (cw == 0 && lane == 0) *inv = iv;
-      return scale;
-    };
-    // offset of this lane's words in row r: RPW rows start at a multiple of 4
-    auto convert = [&](const float4 (&x)[8], int d, uint8_t* dst, uint32_t part, float scale) {
+      const float iv = f16_scale(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), scale);
+      if (w4 == 0 && lane == 0) inv[t % kScaleRing] = iv;
+      const int s = ns == 1 ? 0 : t & 1, use = ns == 1 ? t : t >> 1;
+      if (use > 0) wait(&empty[s], (uint32_t)(use - 1) & 1u);
+      uint8_t* dst = sm + off + (uint32_t)s * 2 * part;
       const uint64_t s2 = pack2(scale, scale);
 #pragma unroll
       for (int i = 0; i < RPW; ++i)
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
-          const int c = 4 * (lane + 32 * s);
-          const float4 q = x[i * SL + s];
+        for (int k = 0; k < SL; ++k) {
+          const int c = 4 * (lane + 32 * k);
+          const float4 q = x[i * SL + k];
           uint2 hi, lo;
           split_f16x2(mul2(pack2(q.x, q.y), s2), hi.x, lo.x);
           split_f16x2(mul2(pack2(q.z, q.w), s2), hi.y, lo.y);
-          uint8_t* p = dst + tile_off(cw * RPW + i, c, NK);
+          uint8_t* p = dst + tile_off(r0 + i, c, NK);
           if (c < d) {
             *reinterpret_cast<uint2*>(p) = hi;
             *reinterpret_cast<uint2*>(p + part) = lo;
           }
         }
-    };
-    auto publish = [&](uint64_t* full) {
       tc5::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) tc5::mbar_arrive(full);
-    };
-    for (int p = 0; p < RS; ++p) fetch(p);
-    float4 x[8];
-#pragma unroll 1
-    for (int p = 0; p < np; ++p) {
-      const int t = p >> 1, v = p & 1, s = t & 1, use = t >> 1;
-      if (fetcher && v == 0) prefetch(t + kAhead);
-      take(x, p);
-      const float sc = scale_of(p, v ? &sh.vinv[t % kScaleRing] : &sh.kinv[t % kScaleRing]);
-      if (use > 0) wait(v ? &sh.vempty[s] : &sh.kempty[s], (uint32_t)(use - 1) & 1u);
-      const uint32_t part = v ? vpart : kpart;
-      convert(x, v ? a.dv : a.dqk, sm + (v ? voff : 0u) + (uint32_t)s * 2 * part, part, sc);
-      publish(v ? &sh.vfull[s] : &sh.kfull[s]);
+      if (lane == 0) tc5::mbar_arrive(&full[s]);
     }
     pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     float o[128];
     float ref = 0.f, l = 0.f;
     SplitStates* states = reinterpret_cast<SplitStates*>(sm + 256 * kLaneStride * 4);
@@ -531,7 +517,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     {
       const uint4* src = reinterpret_cast<const uint4*>(a.qt + ((size_t)kv * a.mt + mt) * 512 * a.dqk) +
                          wg * 16 * a.dqk + row;
-#pragma unroll 4
+#pragma unroll 8
       for (int c = 0; c < a.dqk; c += 16) {
         const uint4 u = __ldcg(src + c * 16), v = __ldcg(src + c * 16 + 128);
         if (wg == 0 || qlo_tm) {
@@ -589,7 +575,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     };
     // the tile's P V into this warpgroup's output columns
     auto issue_pv = [&](int t, int slot) {
-      const int s = t & 1;
+      const int s = VS == 1 ? 0 : t & 1;
       const uint32_t id = idesc_f16(a.dv, true), p = tmem + NK * (uint32_t)slot;
       const uint32_t v = desc_mn(base + voff + (uint32_t)s * 2 * vpart, NK * 128), vl = vpart >> 4;
 #pragma unroll
@@ -620,7 +606,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     for (int t = first, it = 0; t < nt; t += step, ++it) {
       const int slot = t & 1;
       const uint32_t ph2 = COL ? (uint32_t)(t >> 1) & 1u : (uint32_t)it & 1u;  // phase of the slot
-      const int s = t & 1, use = t >> 1;
+      const int s = VS == 1 ? 0 : t & 1, use = VS == 1 ? t : t >> 1;  // of V
       // COL: P(t - 1) V has completed, so the other S tile is free
       if (COL && issuer && t + 1 < nt) issue_qk(t + 1, (t + 1) & 1);
       __syncwarp();
@@ -735,46 +721,47 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       *reinterpret_cast<float4*>(xo + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
     states->m[wg][row] = l == 0.f ? -INFINITY : ref;  // no reference without a key
     states->l[wg][row] = l;
-    pair_sync();
-    const int rows = min(lane_rows, a.R - mt * 128);
-    const size_t at0 = ((size_t)kv * a.ns + sp) * a.R + mt * 128;
-    if (tid < rows) {
-      float mr = -INFINITY, lr = 0.f;
+  }
+  block_sync();
+  const int lane_rows = 128 / a.rep, rows = min(lane_rows, a.R - mt * 128);
+  const size_t at0 = ((size_t)kv * a.ns + sp) * a.R + mt * 128;
+  SplitStates* states = reinterpret_cast<SplitStates*>(sm + 256 * kLaneStride * 4);
+  if (tid < rows) {
+    float mr = -INFINITY, lr = 0.f;
 #pragma unroll 1
-      for (int g = 0; g < 2 * a.rep; ++g) mr = fmaxf(mr, states->m[g & 1][(g >> 1) * lane_rows + tid]);
+    for (int g = 0; g < 2 * a.rep; ++g) mr = fmaxf(mr, states->m[g & 1][(g >> 1) * lane_rows + tid]);
 #pragma unroll 1
-      for (int g = 0; g < 2 * a.rep; ++g) {
-        const int w = g & 1, i = (g >> 1) * lane_rows + tid;
-        // COL: both halves of the columns have one reference
-        const float f = COL || states->m[w][i] == -INFINITY ? 1.f : ex2(states->m[w][i] - mr);
-        states->w[w][i] = f;
-        lr += f * states->l[w][i];
-      }
-      a.part_ml[at0 + tid] = make_float2(mr, lr);
+    for (int g = 0; g < 2 * a.rep; ++g) {
+      const int w = g & 1, i = (g >> 1) * lane_rows + tid;
+      // COL: both halves of the columns have one reference
+      const float f = COL || states->m[w][i] == -INFINITY ? 1.f : ex2(states->m[w][i] - mr);
+      states->w[w][i] = f;
+      lr += f * states->l[w][i];
     }
-    pair_sync();
-    const float* xs = reinterpret_cast<const float*>(sm);
-    const int words = a.dv / 4;
+    a.part_ml[at0 + tid] = make_float2(mr, lr);
+  }
+  block_sync();
+  const float* xs = reinterpret_cast<const float*>(sm);
+  const int words = a.dv / 4;
+#pragma unroll 2
+  for (int e = tid; e < rows * words; e += kSplitThreads) {
+    const int i = e / words, c = e % words * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int e = tid; e < rows * words; e += 256) {
-      const int i = e / words, c = e % words * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int g = 0; g < (COL ? 1 : 2 * a.rep); ++g) {
-        const int w = COL ? c >> 7 : g & 1, ln = (g >> 1) * lane_rows + i;
-        const float f = states->w[w][ln];
-        const float4 x = *reinterpret_cast<const float4*>(xs + (w * 128 + ln) * kLaneStride + (c & 127));
-        v.x = fmaf(f, x.x, v.x);
-        v.y = fmaf(f, x.y, v.y);
-        v.z = fmaf(f, x.z, v.z);
-        v.w = fmaf(f, x.w, v.w);
-      }
-      *reinterpret_cast<float4*>(a.part_o + (at0 + i) * a.dv + c) = v;
+    for (int g = 0; g < (COL ? 1 : 2 * a.rep); ++g) {
+      const int w = COL ? c >> 7 : g & 1, ln = (g >> 1) * lane_rows + i;
+      const float f = states->w[w][ln];
+      const float4 x = *reinterpret_cast<const float4*>(xs + (w * 128 + ln) * kLaneStride + (c & 127));
+      v.x = fmaf(f, x.x, v.x);
+      v.y = fmaf(f, x.y, v.y);
+      v.z = fmaf(f, x.z, v.z);
+      v.w = fmaf(f, x.w, v.w);
     }
-    if (warp == 0) {
-      tc5::fence_after_sync();
-      tc5::dealloc(tmem, 512);
-    }
+    *reinterpret_cast<float4*>(a.part_o + (at0 + i) * a.dv + c) = v;
+  }
+  if (warp == 0) {
+    tc5::fence_after_sync();
+    tc5::dealloc(tmem, 512);
   }
 }
 
@@ -1027,11 +1014,11 @@ static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   static_assert(kScaleRing > kStages + 1, "scales outlive their tile's buffers");
   static_assert(sizeof(SplitSmem) <= 2048, "beside the dynamic shared memory");
   constexpr size_t limit = 227 * 1024 - 2048;  // beside SplitSmem
-  size_t smem = 1024 + kStages * split_stage_bytes(NK, a.dqk, a.dv);  // 1024: the buffers' alignment
+  const size_t kstage = (size_t)NK * 256 * ((a.dqk + 63) / 64), vstage = (size_t)NK * 256 * ((a.dv + 63) / 64);
+  size_t smem = 1024 + kStages * kstage + kConvWarps * kRawBytes;  // 1024: the buffers' alignment
   if (!split_q_lo_fits(NK, COL, a.dqk, a.dv)) smem += (size_t)(a.dqk + 63) / 64 * 128 * 128;
-  const size_t raw = kConvWarps * 4096;
-  a.raw = smem + 2 * raw <= limit ? 2 : 1;
-  smem = std::max(smem + a.raw * raw, 1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
+  a.vstages = smem + 2 * vstage <= limit ? 2 : 1;
+  smem = std::max(smem + a.vstages * vstage, 1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
   if (smem > limit) return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr[64];  // per device
   int dev = 0;
