@@ -228,15 +228,20 @@ __device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t lead) {
   return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
 
-// MMAs and commits are issued by a whole warp, of which one elected lane acts:
-// under uniform control flow the descriptors stay in uniform registers.
-// D[tmem] (+)= A[smem] * B[smem]^T
+// One lane of a converged warp, chosen by the hardware: the compiler knows that
+// the branch on it is taken by one lane and keeps operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T, by one thread
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n"
       " mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
@@ -244,17 +249,10 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, u
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n"
       " mov.b64 b, {%2, %5};\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_u32(bar))
       : "memory");
 }
 
@@ -322,7 +320,7 @@ __device__ __forceinline__ float sum16(const float (&v)[16]) {
 
 struct SplitSmem {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], ofull[2];
-  uint64_t raw[kConvWarps], top[2];          // a warp's rows have arrived; the K or V warps' largest |x| are there
+  uint64_t qready, raw[kConvWarps], top[2];          // a warp's rows have arrived; the K or V warps' largest |x| are there
   uint32_t tmem;
   float kinv[kScaleRing], vinv[kScaleRing];  // a tile's inverse scales
   alignas(16) float wmax[2][2][4];           // largest |x| of each converter warp's rows: K or V, odd or even tile
@@ -393,6 +391,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       mbar_init(&sh.ofull[i], 1);
       mbar_init(&sh.top[i], kConvWarps / 2);
     }
+    mbar_init(&sh.qready, 8);
     for (int w = 0; w < kConvWarps; ++w) mbar_init(&sh.raw[w], 1);
     mbar_fence_init();
   }
@@ -404,6 +403,42 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   Waiter wait{a.err, false};
   // every MMA has completed and its operands' memory is free
   auto block_sync = [&]() { asm volatile("bar.sync 0, 512;" ::: "memory"); };
+
+  const uint32_t qhi = tmem + split_q_col(NK, COL, a.dv), qlo = qhi + a.dqk / 2;
+  // S(t) = Q K(t)^T into S tile `slot`
+  auto issue_qk = [&](int t, int slot) {
+    const int s = t & 1;
+    const uint32_t id = idesc_f16(NK, false), d = tmem + NK * (uint32_t)slot;
+    const uint32_t kh = desc_k(base + (uint32_t)s * 2 * kpart), kl = kpart >> 4;
+    const int n2 = a.dqk / 32;
+    // pairs of 16-dim steps (dims come in 32s): the small products, then the
+    // large
+    const uint32_t q = desc_k(base + qoff);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b >= n2) break;
+      // byte offsets / 16: half of a 128-byte row, or a block of 64 dims
+      const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4, ql = q + (b >> 1) * 1024 + (b & 1) * 4;
+      if (qlo_tm) {
+        mma_f16_ts(d, qlo + 16 * b, k, id, b > 0);
+        mma_f16_ts(d, qlo + 16 * b + 8, k + 2, id, 1u);
+      } else {
+        mma_f16_ss(d, ql, k, id, b > 0);
+        mma_f16_ss(d, ql + 2, k + 2, id, 1u);
+      }
+      mma_f16_ts(d, qhi + 16 * b, k + kl, id, 1u);
+      mma_f16_ts(d, qhi + 16 * b + 8, k + kl + 2, id, 1u);
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b >= n2) break;
+      const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4;
+      mma_f16_ts(d, qhi + 16 * b, k, id, 1u);
+      mma_f16_ts(d, qhi + 16 * b + 8, k + 2, id, 1u);
+    }
+    tc5::commit(&sh.sfull[slot]);
+    tc5::commit(&sh.kempty[s]);
+  };
 
   if (warp >= 8) {
     // ---------------- converters: four warps for K, four for V
@@ -497,7 +532,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     SplitStates* states = reinterpret_cast<SplitStates*>(sm + 256 * kLaneStride * 4);
     const int wg = warp >> 2;
     const int row = tid & 127;
-    const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues MMAs
+    const bool issuer = (warp & 3) == 0 && (!COL || wg == 0);  // the warp that issues P V
     const int lane_rows = 128 / a.rep;       // rows of a copy
     const int qrow = row & (lane_rows - 1);  // this lane's row of the tile
     // this lane's keys of a tile
@@ -507,7 +542,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int cols = COL ? (wg == 0 ? 128 : a.dv - 128) : a.dv;  // this warpgroup's
     const uint32_t ocol = tmem + 2 * NK + (COL ? 0u : (uint32_t)(wg * a.dv));
-    const uint32_t qhi = tmem + split_q_col(NK, COL, a.dv), qlo = qhi + a.dqk / 2;
 
     // the queries come from the previous launch (cached rows were final before
     // it released this one): the first warpgroup brings the hi parts, the second
@@ -533,46 +567,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       tc5::fence_before_sync();
     }
     auto pair_sync = [&]() { asm volatile("bar.sync 4, 256;" ::: "memory"); };
-    pair_sync();
+    __syncwarp();
+    if (lane == 0) tc5::mbar_arrive(&sh.qready);
 #pragma unroll
     for (int c = 0; c < 128; ++c) o[c] = 0.f;
 
-    // S(t) = Q K(t)^T into S tile `slot`
-    auto issue_qk = [&](int t, int slot) {
-      const int s = t & 1, use = t >> 1;
-      wait(&sh.kfull[s], (uint32_t)use & 1u);
-      tc5::fence_after_sync();
-      const uint32_t id = idesc_f16(NK, false), d = tmem + NK * (uint32_t)slot;
-      const uint32_t kh = desc_k(base + (uint32_t)s * 2 * kpart), kl = kpart >> 4;
-      const int n2 = a.dqk / 32;
-      // pairs of 16-dim steps (dims come in 32s): the small products, then the
-      // large
-      const uint32_t q = desc_k(base + qoff);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (b >= n2) break;
-        // byte offsets / 16: half of a 128-byte row, or a block of 64 dims
-        const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4, ql = q + (b >> 1) * 1024 + (b & 1) * 4;
-        if (qlo_tm) {
-          mma_f16_ts(d, qlo + 16 * b, k, id, b > 0);
-          mma_f16_ts(d, qlo + 16 * b + 8, k + 2, id, 1u);
-        } else {
-          mma_f16_ss(d, ql, k, id, b > 0);
-          mma_f16_ss(d, ql + 2, k + 2, id, 1u);
-        }
-        mma_f16_ts(d, qhi + 16 * b, k + kl, id, 1u);
-        mma_f16_ts(d, qhi + 16 * b + 8, k + kl + 2, id, 1u);
-      }
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        if (b >= n2) break;
-        const uint32_t k = kh + (b >> 1) * (NK * 8) + (b & 1) * 4;
-        mma_f16_ts(d, qhi + 16 * b, k, id, 1u);
-        mma_f16_ts(d, qhi + 16 * b + 8, k + 2, id, 1u);
-      }
-      commit_elect(&sh.sfull[slot]);
-      commit_elect(&sh.kempty[s]);
-    };
     // the tile's P V into this warpgroup's output columns
     auto issue_pv = [&](int t, int slot) {
       const int s = VS == 1 ? 0 : t & 1;
@@ -585,8 +584,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       }
 #pragma unroll
       for (int k = 0; k < NK / 16; ++k) mma_f16_ts(ocol, p + 16 * k, v + 128 * k, id, 1u);
-      commit_elect(&sh.ofull[COL ? 0 : slot]);
-      commit_elect(&sh.vempty[s]);
+      tc5::commit(&sh.ofull[slot]);
+      tc5::commit(&sh.vempty[s]);
     };
     auto group_sync = [&]() {
       if (COL)
@@ -597,19 +596,21 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 
     const int step = COL ? 1 : 2;
     const int first = COL ? 0 : wg;
-    if (issuer && first < nt) {
+    auto scores = [&](int t) {
+      if (!issuer || t >= nt) return;
+      wait(&sh.kfull[t & 1], (uint32_t)(t >> 1) & 1u);
       tc5::fence_after_sync();
-      issue_qk(first, first);
-    }
-    __syncwarp();
+      if (elect_one()) issue_qk(t, t & 1);
+      __syncwarp();
+    };
+    if (issuer) wait(&sh.qready, 0u);
+    scores(first);
 #pragma unroll 1
     for (int t = first, it = 0; t < nt; t += step, ++it) {
       const int slot = t & 1;
       const uint32_t ph2 = COL ? (uint32_t)(t >> 1) & 1u : (uint32_t)it & 1u;  // phase of the slot
       const int s = VS == 1 ? 0 : t & 1, use = VS == 1 ? t : t >> 1;  // of V
-      // COL: P(t - 1) V has completed, so the other S tile is free
-      if (COL && issuer && t + 1 < nt) issue_qk(t + 1, (t + 1) & 1);
-      __syncwarp();
+      if (COL) scores(t + 1);  // its S tile is free: P(t - 1) V has completed
       wait(&sh.vfull[s], (uint32_t)use & 1u);  // the tile's scales (and V)
       wait(&sh.sfull[slot], ph2);
       tc5::fence_after_sync();
@@ -688,13 +689,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       group_sync();
       if (issuer) {
         tc5::fence_after_sync();
-        issue_pv(t, slot);
+        if (elect_one()) issue_pv(t, slot);
       }
       __syncwarp();
-      wait(&sh.ofull[COL ? 0 : slot], COL ? (uint32_t)t & 1u : ph2);
+      wait(&sh.ofull[slot], ph2);
       tc5::fence_after_sync();
-      if (!COL && issuer && t + 2 < nt) issue_qk(t + 2, slot);
-      __syncwarp();
+      if (!COL) scores(t + 2);
       if (active) {
         const uint32_t ot = ocol + lanes + (COL ? 128u * (uint32_t)wg : 0u);
 #pragma unroll
