@@ -38,9 +38,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_any_kernel(const __gri
   const mtp_head_rows& t = a.t[ti];
   const int hh = h - (ti ? a.head_end[ti - 1] : 0);
   for (int row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    HeadVals v;
-    head_norm_rope(v, t.x + (size_t)row * t.x_ld + (size_t)hh * t.x_hs, a.d, t.norm_w, a.eps, a.r,
-                   row, a.err, lane);
+    HeadVals v, w;
+    head_load(v, t.x + (size_t)row * t.x_ld + (size_t)hh * t.x_hs, a.d, a.r.half, lane);
+    head_load(w, t.norm_w, a.d, a.r.half, lane);
+    head_norm_rope(v, w, t.norm_w != nullptr, a.d, a.eps, a.r, row, a.err, lane);
     head_store(v, t.y + (size_t)row * t.y_ld + (size_t)hh * t.y_hs, a.d, a.r.half, 1.f, lane);
   }
 }

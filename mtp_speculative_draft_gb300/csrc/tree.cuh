@@ -60,26 +60,31 @@ struct HeadVals {
   float a[4], b[4], c[8];
 };
 
-// Loads a head row, RMS-normalises it (w given) and rotates its pairs.
-__device__ __forceinline__ void head_norm_rope(HeadVals& h, const float* src, int d,
-                                               const float* w, float eps, const RopePos& r,
-                                               int row, int* err, int lane) {
-  const int half = r.half, rot = 2 * half;
-  float2 cs[4];
+// The values of a head row, or of a norm weight (1 when null), in that layout.
+__device__ __forceinline__ void head_load(HeadVals& h, const float* src, int d, int half, int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = lane + 32 * j;
     const bool in = i < half;
-    h.a[j] = in ? src[i] : 0.f;
-    h.b[j] = in ? src[i + half] : 0.f;
-    cs[j] = in ? rope_entry(r, row, i, err) : make_float2(1.f, 0.f);
+    h.a[j] = src ? (in ? src[i] : 0.f) : 1.f;
+    h.b[j] = src ? (in ? src[i + half] : 0.f) : 1.f;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int i = rot + lane + 32 * j;
-    h.c[j] = i < d ? src[i] : 0.f;
+    const int i = 2 * half + lane + 32 * j;
+    h.c[j] = src ? (i < d ? src[i] : 0.f) : 1.f;
   }
-  if (w) {
+}
+
+// RMS-normalises a loaded head row (with its loaded weight, when norm) and
+// rotates its pairs.
+__device__ __forceinline__ void head_norm_rope(HeadVals& h, const HeadVals& w, bool norm, int d, float eps,
+                                               const RopePos& r, int row, int* err, int lane) {
+  float2 cs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    cs[j] = lane + 32 * j < r.half ? rope_entry(r, row, lane + 32 * j, err) : make_float2(1.f, 0.f);
+  if (norm) {
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) ss += h.a[j] * h.a[j] + h.b[j] * h.b[j];
@@ -88,17 +93,11 @@ __device__ __forceinline__ void head_norm_rope(HeadVals& h, const float* src, in
     const float inv = rsqrtf(warp_sum(ss) / (float)d + eps);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = lane + 32 * j;
-      if (i < half) {
-        h.a[j] = h.a[j] * inv * w[i];
-        h.b[j] = h.b[j] * inv * w[i + half];
-      }
+      h.a[j] = h.a[j] * inv * w.a[j];
+      h.b[j] = h.b[j] * inv * w.b[j];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = rot + lane + 32 * j;
-      if (i < d) h.c[j] = h.c[j] * inv * w[i];
-    }
+    for (int j = 0; j < 8; ++j) h.c[j] = h.c[j] * inv * w.c[j];
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

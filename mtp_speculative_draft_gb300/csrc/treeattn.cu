@@ -118,10 +118,25 @@ __device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVa
 }
 
 // One warp an item: n * nh query heads, then n * nkv key heads, then values.
-__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnArgs a) {
+// Bound by its dependent reads; a row's values are on their way before the
+// depths, which the rotary positions need, are waited for.
+__global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_constant__ TreeAttnArgs a) {
+  __shared__ int dep[kTreeMax];
+  const int lane = threadIdx.x & 31, half = a.rope.half;
+  const int it = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  const int nq = a.n * a.nh, nk = a.n * a.nkv;
+  const bool is_q = it < nq, is_k = !is_q && it < nq + nk;
+  const int h = is_q ? it % a.nh : (it - nq) % a.nkv;
+  const int i = is_q ? it / a.nh : (is_k ? it - nq : it - nq - nk) / a.nkv;
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ int dep[kTreeMax];
+  HeadVals v, w;
+  const float* norm = is_q ? a.qn : a.kn;
+  if (is_q || is_k) {
+    head_load(v, is_q ? a.qp + (size_t)i * a.ldq + (size_t)h * a.dqk * (a.gated ? 2 : 1)
+                      : a.kp + (size_t)i * a.ldk + (size_t)h * a.dqk, a.dqk, half, lane);
+    head_load(w, norm, a.dqk, half, lane);
+  }
   if (threadIdx.x < a.n) {
     int d = a.depth[threadIdx.x];
     if (d < 0 || d >= a.n) {
@@ -139,32 +154,19 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const TreeAttnA
   }
   RopePos rp = a.rope;
   rp.depth = dep;
-  const int lane = threadIdx.x & 31;
-  int it = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-  HeadVals v;
-  if (it < a.n * a.nh) {
-    const int i = it / a.nh, h = it % a.nh;
-    const float* src = a.qp + (size_t)i * a.ldq + (size_t)h * a.dqk * (a.gated ? 2 : 1);
-    head_norm_rope(v, src, a.dqk, a.qn, a.eps, rp, i, a.err, lane);
+  if (is_q) {
+    head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, i, a.err, lane);
     const int kv = h / a.G, r = i * a.G + h % a.G;
-    head_store(v, a.qf + ((size_t)kv * a.R + r) * a.dqk, a.dqk, rp.half, a.qscale, lane);
-    if (a.ns > 0) store_q_tile(a, v, kv, r, rp.half, lane);
-    return;
-  }
-  it -= a.n * a.nh;
-  if (it < a.n * a.nkv) {
-    const int i = it / a.nkv, kv = it % a.nkv;
-    head_norm_rope(v, a.kp + (size_t)i * a.ldk + (size_t)kv * a.dqk, a.dqk, a.kn, a.eps, rp, i,
-                   a.err, lane);
-    head_store(v, a.kc + ((size_t)kv * a.cap + a.L + i) * a.dqk, a.dqk, rp.half, 1.f, lane);
-    return;
-  }
-  it -= a.n * a.nkv;
-  if (it < a.n * a.nkv) {
-    const int i = it / a.nkv, kv = it % a.nkv;
-    const float* src = a.vp + (size_t)i * a.ldv + (size_t)kv * a.dv;
-    float* dst = a.vc + ((size_t)kv * a.cap + a.L + i) * a.dv;
-    for (int c = lane; c < a.dv; c += 32) dst[c] = src[c];
+    head_store(v, a.qf + ((size_t)kv * a.R + r) * a.dqk, a.dqk, half, a.qscale, lane);
+    if (a.ns > 0) store_q_tile(a, v, kv, r, half, lane);
+  } else if (is_k) {
+    head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, i, a.err, lane);
+    head_store(v, a.kc + ((size_t)h * a.cap + a.L + i) * a.dqk, a.dqk, half, 1.f, lane);
+  } else if (it < nq + 2 * nk) {
+    const float* src = a.vp + (size_t)i * a.ldv + (size_t)h * a.dv;
+    float* dst = a.vc + ((size_t)h * a.cap + a.L + i) * a.dv;
+    for (int c = 4 * lane; c < a.dv; c += 128)
+      *reinterpret_cast<float4*>(dst + c) = *reinterpret_cast<const float4*>(src + c);
   }
 }
 
