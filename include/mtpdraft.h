@@ -595,7 +595,10 @@ typedef struct {
  *   query heads a KV head.  d_rope: table with rope_rows rows,
  *   pos_base + cache_len + n of them needed (not read when tree->axes is given
  *   or rot_dim is 0).  d_out [n][n_heads*head_dim_v].
- *   Accuracy: float32 products and sums throughout.
+ *   Accuracy: q, K and V enter as 22-bit operands (f16 high and low parts, a
+ *   power-of-two scale for each query row and each tile of 32 or 64 cached keys;
+ *   elements below 2^-39 of a tile's largest count as 0), sums are float32.
+ *   Infinity or NaN in a K or V row that a node sees gives NaN.
  * ------------------------------------------------------------------------ */
 size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n, int32_t cache_len);
 mtp_status attn_tree_sink(const mtp_attn_geom *g, const mtp_draft_tree *tree, const float *d_qp,
@@ -634,7 +637,8 @@ typedef struct {
  * The step after verify_head_argmax's logits when the request has penalties,
  * biases or a grammar.  Every step rounds to float32.
  *   d_logits [rows][ld]; d_out [rows][ld_out] receives the final logits (d_logits
- *   itself: in place), or NULL.  rows in 1..1024.
+ *   itself with the same stride: in place), or NULL; no other overlap.  rows in
+ *   1..1024; 4-byte alignment is enough here (8 for d_path_mask).
  * ------------------------------------------------------------------------ */
 size_t logit_rules_argmax_workspace_bytes(int32_t rows);
 mtp_status logit_rules_argmax(const mtp_logit_rules *rules, const float *d_logits, int64_t ld,
@@ -656,7 +660,8 @@ mtp_status mtp_tree_accept(const int32_t *d_parents, const int32_t *d_tokens,
                            const int32_t *d_verify, int32_t n, int32_t *d_path, int32_t *d_emitted,
                            int32_t *d_count, void *stream);
 
-/* K/V caches of layers with one geometry; cache [n_kv_heads][cache_cap][dim]. */
+/* K/V caches of layers with one geometry, each cache [n_kv_heads][cache_cap][dim]
+ * and none given twice. */
 typedef struct {
     float *const *h_k;             /* host array of n_layers device pointers */
     float *const *h_v;

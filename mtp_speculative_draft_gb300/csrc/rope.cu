@@ -234,6 +234,8 @@ mtp_status rope_axes_rows(const mtp_rope_axes* axes, const mtp_head_rows* t, int
       return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: strides let heads or rows overlap");
     if (x.x_ld % 4 || x.y_ld % 4 || x.x_hs % 4 || x.y_hs % 4)
       return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: strides must be multiples of 4 floats");
+    if (x.x == x.y && (x.x_ld != x.y_ld || x.x_hs != x.y_hs))
+      return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: in place needs equal strides");
     heads += x.n_heads;
     a.t[i] = x;
     a.head_end[i] = heads;

@@ -21,6 +21,10 @@ namespace mtp {
 constexpr int kRuleThreads = 256;
 constexpr int kRulePer = 8;                          // tokens a thread of a chunk
 constexpr int kRuleChunk = kRuleThreads * kRulePer;  // tokens a CTA
+// CTAs a SM at which a CTA takes further rows: fewer repeat the list building
+// less, more hide the row loop's waits better (64 x 152577: 3 gives 32 us, 2 gives
+// 38, 5 gives 36, one row a CTA 39; 16 x 151936: 13 us against 13, 16 and 16).
+constexpr int kRuleCtas = 3;
 constexpr int kRuleHits = 128;                       // bias entries of a chunk kept at hand
 constexpr int kRuleRows = 16;                        // rows a CTA, at most
 
@@ -327,10 +331,10 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
   const int words = (R->vocab + 31) / 32;
   if (R->d_allow && R->allow_ld != 0 && R->allow_ld < words)
     return fail(MTP_ERR_INVALID_ARG, "logit_rules_argmax: mask rows shorter than the vocabulary");
-  if ((reinterpret_cast<uintptr_t>(d_logits) | reinterpret_cast<uintptr_t>(d_out) |
-       reinterpret_cast<uintptr_t>(R->d_counts) | reinterpret_cast<uintptr_t>(R->d_allow)) & 15 ||
-      (reinterpret_cast<uintptr_t>(R->d_path_mask) & 7) ||
-      ((reinterpret_cast<uintptr_t>(R->d_path_tokens) | reinterpret_cast<uintptr_t>(R->d_bias_tokens) |
+  if ((reinterpret_cast<uintptr_t>(R->d_path_mask) & 7) ||
+      ((reinterpret_cast<uintptr_t>(d_logits) | reinterpret_cast<uintptr_t>(d_out) |
+        reinterpret_cast<uintptr_t>(R->d_counts) | reinterpret_cast<uintptr_t>(R->d_allow) |
+        reinterpret_cast<uintptr_t>(R->d_path_tokens) | reinterpret_cast<uintptr_t>(R->d_bias_tokens) |
         reinterpret_cast<uintptr_t>(R->d_bias) | reinterpret_cast<uintptr_t>(d_tokens) |
         reinterpret_cast<uintptr_t>(d_values)) & 3))
     return fail(MTP_ERR_INVALID_ARG, "logit_rules_argmax: misaligned pointer");
@@ -361,10 +365,7 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
   a.keys = reinterpret_cast<unsigned long long*>(body);
   a.cnt = reinterpret_cast<unsigned*>(body + (size_t)rows * 8);
   const int chunks = (R->vocab + kRuleChunk - 1) / kRuleChunk;
-#ifndef MTP_RULE_CTAS
-#define MTP_RULE_CTAS 3
-#endif
-  a.rows_per_cta = std::min(kRuleRows, std::max(1, (int)((long long)chunks * rows / (sm_count() * MTP_RULE_CTAS))));
+  a.rows_per_cta = std::min(kRuleRows, std::max(1, (int)((long long)chunks * rows / (sm_count() * kRuleCtas))));
   cudaError_t e = launch_pdl(logit_rules_kernel, dim3(chunks, (rows + a.rows_per_cta - 1) / a.rows_per_cta), kRuleThreads, 0,
                              static_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return cuda_fail(e, "logit_rules_argmax launch");
@@ -374,7 +375,7 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
 mtp_status mtp_token_counts(uint32_t* d_counts, int32_t vocab, const int32_t* d_tokens, int32_t n,
                             int32_t prompt, void* d_ws, size_t ws_bytes, void* stream) {
   if (!d_counts || !d_tokens) return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: null pointer");
-  if (((reinterpret_cast<uintptr_t>(d_counts)) & 15) || (reinterpret_cast<uintptr_t>(d_tokens) & 3))
+  if ((reinterpret_cast<uintptr_t>(d_counts) | reinterpret_cast<uintptr_t>(d_tokens)) & 3)
     return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: misaligned pointer");
   if (vocab < 1 || n < 1 || (prompt != 0 && prompt != 1))
     return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: vocab and n must be >= 1, prompt 0 or 1");

@@ -202,11 +202,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
 // column (16 keys: 8 columns of hi parts, 8 of lo parts), and Q hi and lo lie
 // behind the outputs (Q lo in shared memory where they do not fit).
 constexpr int kSplitThreads = 512;
+// Registers a thread at launch, and after the warpgroups share them out anew.
+constexpr int kSplitRegs = 128, kSoftmaxRegs = 168, kConvertRegs = 88;
 constexpr int kConvWarps = 8;
-#ifndef MTP_TREE_AHEAD
-#define MTP_TREE_AHEAD 2
-#endif
-constexpr int kAhead = MTP_TREE_AHEAD;  // tiles prefetched to L2
+constexpr int kAhead = 2;  // tiles prefetched to L2 (1 to 4 measure alike; none: +2 % on long caches)
 constexpr int kScaleRing = 4;  // tiles whose scales are kept: > kStages + 1
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
@@ -352,6 +351,12 @@ struct Waiter {
       set_dev_error(err, kErrMbarTimeout);
     }
   }
+  // After a wait that gave up: time for copies and MMAs in flight to land (a few
+  // milliseconds) before the buffers are reused or freed.
+  __device__ __forceinline__ void settle() {
+    if (dead)
+      for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  }
 };
 
 template <int NK, bool COL>
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   if (warp >= 8) {
     // ---------------- converters: four warps for K, four for V
     const int cw = warp - 8, v = cw >> 2, w4 = cw & 3;
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
     constexpr int RPW = NK / 4;           // rows a warp of a tile
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     static_assert(RPW * SL == 16, "sixteen words a lane");
@@ -524,11 +529,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&full[s]);
     }
+    wait.settle();
     pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     float o[128];
     float ref = 0.f, l = 0.f;
     SplitStates* states = reinterpret_cast<SplitStates*>(sm + 256 * kLaneStride * 4);
@@ -712,6 +718,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       }
       tc5::fence_before_sync();
     }
+    wait.settle();
     pdl_launch_dependents();
     block_sync();
     // Lane states to shared memory (lane i of a warpgroup at i * kLaneStride),
@@ -1023,10 +1030,15 @@ static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   smem = std::max(smem + a.vstages * vstage, 1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
   if (smem > limit) return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr[64];  // per device
+  static_assert(256 * (kSoftmaxRegs + kConvertRegs) == kSplitThreads * kSplitRegs, "register shares");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, tree_split_kernel<NK, COL>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kSplitRegs) return cudaErrorInvalidKernelImage;  // the shares would wait forever
     e = cudaFuncSetAttribute(tree_split_kernel<NK, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)limit);
     if (e != cudaSuccess) return e;

@@ -281,6 +281,8 @@ def kv_caches(k_caches, v_caches) -> KvCaches:
             raise ValueError("kv_caches: caches [n_kv, cap, dim] of one geometry are required")
     ks = (L.vp * n)(*[_ptr(k, _F32, 1, "k_cache", dev) for k in k_caches])
     vs = (L.vp * n)(*[_ptr(v, _F32, 1, "v_cache", dev) for v in v_caches])
+    if len({*ks, *vs}) != 2 * n:
+        raise ValueError("kv_caches: a cache is given twice")
     c = KvCaches(ks, vs, n, nkv, dqk, dv, cap)
     c.tensors = (k_caches, v_caches, ks, vs)
     return c

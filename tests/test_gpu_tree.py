@@ -215,6 +215,45 @@ def test_attn_tree(dev, i):
     call.check(str(CASES[i]))
 
 
+def test_attn_tree_offsets_past_32_bits(dev):
+    """The second KV head's rows start 2^31 values behind the first's."""
+    import torch
+    c = _attn_case(12, nh=4, nkv=2, dqk=32, dv=32, L=200, n=3)
+    c["cap"] = 8
+    call = Call({**c, "cap": 200 + 3}, dev)
+    cap = 1 << 26
+    k, v = torch.empty(2, cap, 32, device=dev), torch.empty(2, cap, 32, device=dev)
+    k[:, :210], v[:, :210] = float("nan"), float("nan")
+    k[:, :200], v[:, :200] = call.k[:, :200], call.v[:, :200]
+    call.k, call.v = k, v
+    call()
+    out, kn, vn = _reference(c)
+    assert_close(call.out.cpu().numpy(), out, "out", ATTN_TOL)
+    assert_close(k[:, 200:203].cpu().numpy(), kn.transpose(1, 0, 2), "K rows", ROPE_TOL)
+    np.testing.assert_array_equal(v[:, 200:203].cpu().numpy(), vn.transpose(1, 0, 2))
+    assert torch.isnan(k[:, 203:210]).all()
+    from mtp_speculative_draft_gb300 import kv_caches, kv_tree_commit
+    before = k[:, 202].clone()
+    kv_tree_commit(kv_caches([k], [v]), torch.tensor([2, -1, -1], dtype=torch.int32, device=dev), 200)
+    assert (k[:, 200] == before).all()
+
+
+def test_attn_tree_workspace_used_by_other_shapes_before(dev):
+    """What an earlier call left in the workspace has no effect."""
+    import torch
+    a = Call(_attn_case(13, nh=16, nkv=1, dqk=256, dv=256, L=600, n=9), dev)
+    b = Call(_attn_case(14, nh=5, nkv=1, dqk=96, dv=96, L=300, n=2), dev)
+    b.ws = a.ws
+    a.ws[1024:] = 255  # NaN everywhere behind the header
+    b()
+    b.check("after a fill")
+    a()
+    b.out.fill_(5.0)
+    b()
+    b.check("after another shape")
+    assert torch.isfinite(b.out).all()
+
+
 def test_attn_tree_repeats_bit_for_bit(dev):
     call = Call(_attn_case(1, nh=40, nkv=8, dqk=128, dv=128, L=900, n=9), dev)
     call()
@@ -382,6 +421,8 @@ def test_wrappers_refuse_what_the_kernels_cannot_read(dev):
     with pytest.raises(ValueError):  # the mask has fewer rows than the logits
         M.logit_rules_argmax(M.logit_rules(100, allow=torch.zeros(3, 4, dtype=torch.int32, device=dev)),
                              torch.zeros(4, 100, device=dev), tok, val)
+    with pytest.raises(ValueError):  # one cache twice
+        M.kv_caches([call.k, call.k], [call.v, call.v.clone()])
     with pytest.raises(M._lib.MtpError):  # rows that overlap
         ax = M.rope_axes((16,), torch.zeros(1, 4, dtype=torch.int32, device=dev), torch.zeros(64, device=dev))
         M.rope_axes_rows(ax, [(torch.zeros(1, 2, 32, device=dev).expand(4, 2, 32), torch.zeros(4, 2, 32, device=dev), None)])
@@ -429,6 +470,8 @@ def _rules_reference(c, dtype=np.float32):
     (1, 151936, dict(n_bias=1000, allow="rows")),
     (130, 300, dict(counts=False, n_bias=1, rep=1.0, freq=0.0, pres=0.0)),
     (9, 70000, dict(counts=False, n_path=64)),                 # the path alone counts
+    (2, 500, dict(n_bias=700, n_path=3)),                      # more bias entries in a chunk than it keeps at hand
+    (70, 4097, dict(n_bias=9, n_path=64, allow="one")),        # several rows a CTA where chunks are few
 ])
 @pytest.mark.parametrize("out", ["none", "new", "in place"])
 def test_logit_rules(dev, rows, V, kw, out):

@@ -58,9 +58,9 @@ def _axes(sections=(24, 20, 20), inter=1, n=None, pos_ld=8, max_pos=100, pos=0x1
 def test_rope_axes_rows_refusals(lib):
     from mtp_speculative_draft_gb300 import _lib
 
-    def call(ax=None, rows=4, d=128, x=0x10000, hs=128, ld=1024, heads=8, ws=P, wsb=1024, eps=1e-6, nt=1):
+    def call(ax=None, rows=4, d=128, x=0x10000, y=0x20000, hs=128, ld=1024, heads=8, ws=P, wsb=1024, eps=1e-6, nt=1):
         ax = _axes() if ax is None else ax
-        t = (_lib.HeadRows * 1)(_lib.HeadRows(x, 0x20000, None, ld, 1024, hs, 128, heads))
+        t = (_lib.HeadRows * 1)(_lib.HeadRows(x, y, None, ld, 1024, hs, 128, heads))
         return lib.rope_axes_rows(C.byref(ax), t, nt, rows, d, eps, ws, wsb, None)
 
     assert call(rows=0) == 1 and call(rows=9) == 1       # no rows; more rows than positions
@@ -68,6 +68,7 @@ def test_rope_axes_rows_refusals(lib):
     assert call(x=None) == 1 and call(x=0x10004) == 1    # null, misaligned
     assert call(hs=96) == 1 and call(ld=1000) == 1       # overlapping heads, rows
     assert call(hs=130, ld=1042) == 1                    # strides not multiples of 4
+    assert call(x=0x20000, ld=1028) == 1                 # in place with another stride
     assert call(heads=0) == 2 and call(nt=0) == 1 and call(nt=5) == 1
     assert call(eps=-1.0) == 1 and call(eps=float("nan")) == 1
     assert call(ws=None) == 4 and call(wsb=1000) == 4
@@ -127,6 +128,7 @@ def test_logit_rules_refusals(lib):
     assert call(n_path=3) == 1 and call(n_path=65, d_path_tokens=0x1000, d_path_mask=0x1000) == 1
     assert call(d_allow=0x1000, allow_ld=31) == 1
     assert call(d_path_tokens=0x1000, d_path_mask=0x1004, n_path=2) == 1
+    assert call(x=0x10002) == 1 and call(d_allow=0x1001, allow_ld=32) == 1
     assert call(wsb=1024) == 4
     assert lib.logit_rules_argmax_workspace_bytes(0) == 0
     assert lib.mtp_token_counts(None, 10, P, 3, 0, P, 1024, None) == 1
