@@ -351,9 +351,9 @@ struct Waiter {
       set_dev_error(err, kErrMbarTimeout);
     }
   }
-  // After a wait that gave up: time for copies and MMAs in flight to land (a few
-  // milliseconds) before the buffers are reused or freed.
-  __device__ __forceinline__ void settle() {
+  // After a wait that gave up (the outputs are not valid): time for copies and
+  // MMAs in flight to land, a few milliseconds, before the memory is freed.
+  __device__ __noinline__ void settle() {
     if (dead)
       for (int i = 0; i < 2000; ++i) __nanosleep(1000);
   }
@@ -529,7 +529,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&full[s]);
     }
-    wait.settle();
     pdl_launch_dependents();
     block_sync();
   } else {
@@ -718,7 +717,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       }
       tc5::fence_before_sync();
     }
-    wait.settle();
     pdl_launch_dependents();
     block_sync();
     // Lane states to shared memory (lane i of a warpgroup at i * kLaneStride),
@@ -768,6 +766,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     }
     *reinterpret_cast<float4*>(a.part_o + (at0 + i) * a.dv + c) = v;
   }
+  wait.settle();
   if (warp == 0) {
     tc5::fence_after_sync();
     tc5::dealloc(tmem, 512);
