@@ -201,6 +201,13 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
 // Q and P are operands in tensor memory: P takes the place of S, column by
 // column (16 keys: 8 columns of hi parts, 8 of lo parts), and Q hi and lo lie
 // behind the outputs (Q lo in shared memory where they do not fit).
+//
+// Measured: 40/8 heads of 128, 64 nodes, 32768 keys: 172 us, 3.7k cycles a tile of
+// 64 keys x 128 rows, of which the tensor pipe works 1.5k (its three products are
+// 77 us at 1967 TFLOP/s); the chain scores -> weights -> P V -> output of a
+// warpgroup's tile bounds it (issue slots 51 %).  16 nodes: 72 us, 3.7 TB/s of
+// cache.  A tile is 64 keys, as two of them, their raw rows and the states fit
+// beside 512 tensor-memory columns (32 where a head size passes 128).
 constexpr int kSplitThreads = 512;
 // Registers a thread at launch, and after the warpgroups share them out anew.
 constexpr int kSplitRegs = 128, kSoftmaxRegs = 168, kConvertRegs = 88;
@@ -777,7 +784,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
 // One CTA a (node, head), its four warps sharing the splits and the keys read one
 // by one; lane l holds dims 4 l .. 4 l + 3 and, past 128 dims, 128 + 4 l ...
 // Bound by the latency of a few dependent reads from L2, so keys go four at a
-// time (a chain of 64 nodes: 27 -> 10 us).
+// time (the whole call of 13 nodes of 16 heads of 256: 39 -> 31 us) and 8 CTAs
+// share an SM (64 nodes of 40 heads: 2560 CTAs, 19 us).
 // H: 128-dim halves of the wider of the two head sizes.
 constexpr int kFinishWarps = 4;
 constexpr int kFinishKeys = 4;  // keys of a step
