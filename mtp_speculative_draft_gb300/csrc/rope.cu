@@ -52,7 +52,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_any_kernel(const __gri
 // rotated dims.  A CTA takes one row (and some of its heads, when rows are few);
 // a lane's units are the same in each of its heads, so it reads the table once a
 // row and keeps the angles in registers.  Bound by HBM: each value is read and
-// written once, and KH heads' loads go out before any arithmetic.
+// written once, and KH heads' loads go out before any arithmetic (8192 rows of
+// 40 + 8 heads of 128: 69 us without the replay, 5.8 TB/s, 0.87 of a copy; one
+// warp a head with 4-byte accesses: 210 us).  Unequal sizes: 48 heads are one step
+// of 16 x 3; single rows spread their heads over CTAs.
 template <int LP, int KH, bool TWO>
 __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeRowsArgs a) {
   constexpr int G = kRopeThreads / LP;  // heads of a step

@@ -866,6 +866,16 @@ __global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish
   pdl_launch_dependents();
   const int h = blockIdx.x, i = blockIdx.y, kv = h / a.G, r = i * a.G + h % a.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // every read that depends on nothing goes out first
+  const int dep = a.dep[i];
+  unsigned long long m = a.mask[i];
+  const int e1 = first_common_key(a);
+  const int dep0 = lane < a.n ? a.dep[lane] : 0, dep1 = lane + 32 < a.n ? a.dep[lane + 32] : 0;
+  const float sink = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+  const int c4 = 4 * threadIdx.x;  // this thread's dims of the output
+  float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.gated && c4 < a.dv)
+    gate = *reinterpret_cast<const float4*>(a.qp + (size_t)i * a.ldq + ((size_t)2 * h + 1) * a.dqk + c4);
   const float* qrow = a.qf + ((size_t)kv * a.R + r) * a.dqk;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 q[H];
@@ -904,11 +914,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish
   }
   const float* kc = a.kc + (size_t)kv * a.cap * a.dqk;
   const float* vc = a.vc + (size_t)kv * a.cap * a.dv;
-  const int dep = a.dep[i];
   int at[kFinishKeys];
   // cached keys at the window's edge: seen by this row, not by every row
   if (a.window > 0) {
-    const int e0 = max(0, a.L + dep - a.window + 1), e1 = first_common_key(a);
+    const int e0 = max(0, a.L + dep - a.window + 1);
 #pragma unroll 1
     for (int k = e0 + warp * kFinishKeys; k < e1; k += kFinishWarps * kFinishKeys) {
 #pragma unroll
@@ -917,13 +926,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish
     }
   }
   // the node's ancestors inside the window
-  unsigned long long m = a.mask[i];
   if (a.n < 64) m &= (1ull << a.n) - 1;
-  if (a.window > 0) {
-    const bool in0 = lane < a.n && a.dep[lane] > dep - a.window,
-               in1 = lane + 32 < a.n && a.dep[lane + 32] > dep - a.window;
-    m &= __ballot_sync(0xffffffffu, in0) | (unsigned long long)__ballot_sync(0xffffffffu, in1) << 32;
-  }
+  if (a.window > 0)
+    m &= __ballot_sync(0xffffffffu, dep0 > dep - a.window) |
+         (unsigned long long)__ballot_sync(0xffffffffu, dep1 > dep - a.window) << 32;
 #pragma unroll 1
   for (int b = 0; m; ++b) {
     int n = 0;
@@ -943,9 +949,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish
 #pragma unroll
   for (int x = 0; x < H; ++x) sm_o[warp][lane + 32 * x] = s.o[x];
   __syncthreads();
-  const int c = threadIdx.x;  // four dims a thread
-  if (4 * c >= a.dv) return;
-  const float sink = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+  if (c4 >= a.dv) return;
   float M = sink;
 #pragma unroll
   for (int w = 0; w < kFinishWarps; ++w) M = fmaxf(M, sm_m[w]);
@@ -955,17 +959,16 @@ __global__ void __launch_bounds__(kFinishWarps * 32, H == 1 ? 8 : 6) tree_finish
   for (int w = 0; w < kFinishWarps; ++w) {
     const float f = sm_m[w] == -INFINITY ? 1.f : exp2f(sm_m[w] - M);  // none or NaN: 0 or NaN stays
     den += f * sm_l[w];
-    add4(o, f, sm_o[w][c]);
+    add4(o, f, sm_o[w][threadIdx.x]);
   }
   scale4(o, den == 0.f ? 0.f : 1.f / den);  // a row that sees nothing: 0
   if (a.gated) {
-    const float4 g = *reinterpret_cast<const float4*>(a.qp + (size_t)i * a.ldq + ((size_t)2 * h + 1) * a.dqk + 4 * c);
-    o.x /= 1.f + expf(-g.x);
-    o.y /= 1.f + expf(-g.y);
-    o.z /= 1.f + expf(-g.z);
-    o.w /= 1.f + expf(-g.w);
+    o.x /= 1.f + expf(-gate.x);
+    o.y /= 1.f + expf(-gate.y);
+    o.z /= 1.f + expf(-gate.z);
+    o.w /= 1.f + expf(-gate.w);
   }
-  *reinterpret_cast<float4*>(a.out + ((size_t)i * a.nh + h) * a.dv + 4 * c) = o;
+  *reinterpret_cast<float4*>(a.out + ((size_t)i * a.nh + h) * a.dv + c4) = o;
 }
 
 // ------------------------------------------------------------------ host
