@@ -22,8 +22,9 @@ constexpr int kRuleThreads = 256;
 constexpr int kRulePer = 8;                          // tokens a thread of a chunk
 constexpr int kRuleChunk = kRuleThreads * kRulePer;  // tokens a CTA
 // CTAs a SM at which a CTA takes further rows: fewer repeat the list building
-// less, more hide the row loop's waits better (64 x 152577: 3 gives 32 us, 2 gives
-// 38, 5 gives 36, one row a CTA 39; 16 x 151936: 13 us against 13, 16 and 16).
+// less, more hide the row loop's waits better (64 x 152577: 3 gave 32 us, 2 gave
+// 38, 5 gave 36, one row a CTA 39; 16 x 151936: 13 us against 13, 16 and 16; with
+// the mask words handed over too, 3 gives 30 us).
 constexpr int kRuleCtas = 3;
 constexpr int kRuleHits = 128;                       // bias entries of a chunk kept at hand
 constexpr int kRuleRows = 16;                        // rows a CTA, at most
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
   __shared__ uint8_t slot[kRuleChunk];                // first path node of the token, or kTreeMax
   __shared__ unsigned long long nodes[kTreeMax + 1];  // the nodes of a slot's token
   __shared__ float hand[2][kRuleChunk];               // their logits of a row and the next
+  __shared__ uint32_t words[2][kRuleChunk / 32];      // and the mask words
   __shared__ int ptok[kTreeMax];
   __shared__ int hit_i[kRuleHits], hit_t[kRuleHits];  // bias entries of the chunk, in any order
   __shared__ float hit_b[kRuleHits];
@@ -210,9 +212,11 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
     int at = 0x7FFFFFFF;
     // listed tokens to the threads that serve them, the others here
     float* xs = hand[q & 1];
+    uint32_t* ok = words[q & 1];
 #pragma unroll
     for (int k = 0; k < kRulePer; ++k) {
       const int i = tid + k * kRuleThreads;
+      if (lane == 0) ok[i >> 5] = w[k];
       if ((listed >> k) & 1u) {
         xs[i] = l[k];
         continue;
@@ -232,7 +236,6 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       const int i = list[e], v = v0 + i;
       if (v >= a.V) continue;
       float t = xs[i];
-      const uint32_t ok = a.allow ? a.allow[(size_t)r * a.allow_ld + (v >> 5)] >> (v & 31) : 1u;
       uint32_t c = cnt[e] + __popcll(nodes[slot[e]] & path);
       if (c) {  // seen
         c &= 0x7FFFFFFFu;
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       }
       const float b = adj[e];
       if (b != 0.f) t = __fadd_rn(t, b);
-      if (!(ok & 1u)) t = -INFINITY;
+      if (!((ok[i >> 5] >> (i & 31)) & 1u)) t = -INFINITY;
       if (y) y[i] = t;
       if (t > top || (t == top && t > -INFINITY && v < at)) {
         top = t;

@@ -428,6 +428,60 @@ def test_wrappers_refuse_what_the_kernels_cannot_read(dev):
         M.rope_axes_rows(ax, [(torch.zeros(1, 2, 32, device=dev).expand(4, 2, 32), torch.zeros(4, 2, 32, device=dev), None)])
 
 
+def test_attn_tree_two_streams_at_once(dev):
+    """Calls with workspaces of their own on two streams at the same time."""
+    import torch
+    calls = [Call(_attn_case(15, nh=40, nkv=8, dqk=128, dv=128, L=3000, n=40), dev),
+             Call(_attn_case(16, nh=16, nkv=2, dqk=256, dv=256, L=2500, n=20, sinks=True), dev)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for call, stream in zip(calls, streams):
+            call(stream)
+    for call in calls:
+        call.check()
+
+
+def test_captured_calls_follow_their_tensors(dev):
+    """A replayed graph reads the tree, the rules' tables and the positions of the replay."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    c = _attn_case(17, nh=8, nkv=2, dqk=64, dv=64, L=70, n=20, axes=(12, 10, 10))
+    call = Call(c, dev)
+    mask, depth, axes = call.tree.tensors
+    rules = _rules_case(3, 20, 3000, n_path=20, n_bias=5, allow="rows")
+    r = _rules_device(rules, dev)
+    logits, out = _t(rules["logits"], dev), torch.zeros(20, 3000, device=dev)
+    tok, val = torch.zeros(20, dtype=torch.int32, device=dev), torch.zeros(20, device=dev)
+    ws = M.workspace(M.logit_rules_argmax_workspace_bytes(20))
+    call()
+    M.logit_rules_argmax(r, logits, tok, val, out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        M.logit_rules_argmax(r, logits, tok, val, out, ws)
+    for seed, kind in ((18, "chain"), (19, "star"), (20, "forest")):
+        n = _attn_case(seed, nh=8, nkv=2, dqk=64, dv=64, L=70, n=20, axes=(12, 10, 10), tree=kind)
+        mask.copy_(_words(n["mask"], dev))
+        depth.copy_(_t(np.array(n["depth"], np.int32), dev))
+        axes.tensors[0].copy_(_t(n["pos"], dev))
+        for x, y in ((call.qp, n["qp"]), (call.kp, n["kp"]), (call.vp, n["vp"]), (call.k[:, :70], n["kc"]),
+                     (call.v[:, :70], n["vc"]), (call.qn, n["qn"]), (call.kn, n["kn"])):
+            x.copy_(_t(y, dev))
+        call.c = n
+        new = _rules_case(seed, 20, 3000, n_path=20, n_bias=5, allow="rows")
+        counts, btok, b, allow, ptok, pmask = r.tensors
+        for x, y in ((counts, np.asarray(new["counts"]).astype(np.uint32).view(np.int32)), (btok, new["bias_tokens"]),
+                     (b, new["bias"]), (allow, new["allow"].view(np.int32)), (ptok, new["path_tokens"]), (logits, new["logits"])):
+            x.copy_(_t(y, dev))
+        pmask.copy_(_words(new["path_mask"], dev))
+        g.replay()
+        call.check(kind)
+        np.testing.assert_array_equal(out.cpu().numpy(), _rules_reference(new))
+        assert tok.tolist() == [t for t, _ in T.greedy(_rules_reference(new))]
+
+
 # ------------------------------------------------------------------ logit rules
 def _rules_case(seed, rows, V, n_path=0, n_bias=0, allow=None, counts=True, rep=1.3, freq=0.4, pres=0.3):
     rng = np.random.default_rng(seed)
