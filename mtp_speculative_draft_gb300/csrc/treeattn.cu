@@ -188,11 +188,15 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
 //
 // Warps: 8 converters (global float32 rows -> f16 hi/lo operand tiles in shared
 // memory with the tile's scale), and two warpgroups that each run softmax on
-// whole rows (thread = row) and issue their own MMAs from their first warp.
+// whole rows (thread = row); a warpgroup's first warp issues P V.
 //   COL = false (dv <= 128): the warpgroups take alternate tiles, each with its
-//     own (ref, l, o), merged at the end: one's softmax overlaps the other's MMAs;
+//     own (ref, l, o), merged at the end: one's softmax overlaps the other's MMAs.
+//     The first warp issues Q K^T too (a converter warp would hold up every tile:
+//     230 us, not 191, at 64 nodes and 32768 keys);
 //   COL = true: they share every tile, each with half of its keys and half of the
-//     output columns, as 256 do not fit a thread's registers.
+//     output columns, as 256 do not fit a thread's registers.  A K converter warp
+//     issues Q K^T (both warpgroups would wait for a softmax warp in the issue
+//     queue: 74 us, not 67, at 16 nodes and 32768 keys of 2 x 256).
 // Few query rows (64 or less) are repeated `rep` times in the 128 lanes: each
 // copy takes its own NK / rep keys of a tile (its P is 0 elsewhere), so all four
 // warps of a warpgroup share the exponentials; the copies' states are merged at
@@ -535,6 +539,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       tc5::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&full[s]);
+      if (COL && cw == 0) {
+        // the tile's scores, once its S tile is free: P(t - 2) V has completed
+        if (t == 0) wait(&sh.qready, 0u);
+        if (t >= 2) wait(&sh.ofull[t & 1], (uint32_t)((t - 2) >> 1) & 1u);
+        wait(&sh.kfull[s], (uint32_t)use & 1u);
+        tc5::fence_after_sync();
+        if (elect_one()) issue_qk(t, t & 1);
+        __syncwarp();
+      }
     }
     pdl_launch_dependents();
     block_sync();
@@ -617,14 +630,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       if (elect_one()) issue_qk(t, t & 1);
       __syncwarp();
     };
-    if (issuer) wait(&sh.qready, 0u);
-    scores(first);
+    if (issuer && !COL) wait(&sh.qready, 0u);
+    if (!COL) scores(first);
 #pragma unroll 1
     for (int t = first, it = 0; t < nt; t += step, ++it) {
       const int slot = t & 1;
       const uint32_t ph2 = COL ? (uint32_t)(t >> 1) & 1u : (uint32_t)it & 1u;  // phase of the slot
       const int s = VS == 1 ? 0 : t & 1, use = VS == 1 ? t : t >> 1;  // of V
-      if (COL) scores(t + 1);  // its S tile is free: P(t - 1) V has completed
       wait(&sh.vfull[s], (uint32_t)use & 1u);  // the tile's scales (and V)
       wait(&sh.sfull[slot], ph2);
       tc5::fence_after_sync();
@@ -980,6 +992,10 @@ struct TreePlan {
 // queries up to 128 dims, 32 above.
 static int split_nk(int dqk, int dv) { return dqk <= 128 && dv <= 128 ? 64 : 32; }
 
+// Keys of a split at least: 32, 64 and 128 take 32.6, 32.1 and 36.9 us on 2047 keys
+// of two heads of 256 dims; 64 writes half of 32's partials.
+constexpr int kMinKeys = 64;
+
 // Splits of the cached keys all rows see: about one CTA per SM.
 static TreePlan tree_plan_splits(const mtp_attn_geom* g, int L, int n) {
   TreePlan p;
@@ -990,7 +1006,7 @@ static TreePlan tree_plan_splits(const mtp_attn_geom* g, int L, int n) {
   p.kper = 0;
   if (keys > 0) {
     int want = std::max(1, sm_count() / (g->n_kv_heads * mt));
-    want = std::min(want, (keys + 31) / 32);
+    want = std::min(want, (keys + kMinKeys - 1) / kMinKeys);
     p.kper = ((keys + want - 1) / want + 15) / 16 * 16;
     p.ns = (keys + p.kper - 1) / p.kper;
   }
