@@ -217,7 +217,11 @@ constexpr int kSplitThreads = 512;
 constexpr int kSplitRegs = 128, kSoftmaxRegs = 168, kConvertRegs = 88;
 constexpr int kConvWarps = 8;
 constexpr int kAhead = 2;  // tiles prefetched to L2 (1 to 4 measure alike; none: +2 % on long caches)
-constexpr int kScaleRing = 4;  // tiles whose scales are kept: > kStages + 1
+// Tiles whose scales are kept.  Tile t's scale is written once its buffer is free, that is once the scores of
+// tile t - kStages are done.  The warpgroup that takes tile t - kStages issues them after its previous tile,
+// t - kStages - 2, so the scales up to that one have been read.  (Written before the wait, tile t's scale could
+// take the place of t - kStages - 2's while that tile still waits for its V.)
+constexpr int kScaleRing = 4;
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
 constexpr int kLaneStride = 132;  // floats of a lane's state: 16-byte accesses without bank conflicts
@@ -516,9 +520,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
       const float4 m4 = *reinterpret_cast<const float4*>(sh.wmax[v][t & 1]);
       float scale;
       const float iv = f16_scale(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), scale);
-      if (w4 == 0 && lane == 0) inv[t % kScaleRing] = iv;
       const int s = ns == 1 ? 0 : t & 1, use = ns == 1 ? t : t >> 1;
       if (use > 0) wait(&empty[s], (uint32_t)(use - 1) & 1u);
+      if (w4 == 0 && lane == 0) inv[t % kScaleRing] = iv;
       uint8_t* dst = sm + off + (uint32_t)s * 2 * part;
       const uint64_t s2 = pack2(scale, scale);
 #pragma unroll
@@ -1046,7 +1050,7 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
 
 template <int NK, bool COL>
 static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
-  static_assert(kScaleRing > kStages + 1, "scales outlive their tile's buffers");
+  static_assert(kScaleRing >= kStages + 2, "a tile's scale stays until its warpgroup has read it");
   static_assert(sizeof(SplitSmem) <= 2048, "beside the dynamic shared memory");
   constexpr size_t limit = 227 * 1024 - 2048;  // beside SplitSmem
   const size_t kstage = (size_t)NK * 256 * ((a.dqk + 63) / 64), vstage = (size_t)NK * 256 * ((a.dv + 63) / 64);
