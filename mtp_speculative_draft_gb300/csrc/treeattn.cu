@@ -50,7 +50,7 @@ struct TreeAttnArgs {
   float2* part_ml; // [nkv][ns][R] running maximum and sum
   int R, mt;              // query rows of a KV head, tiles of 128 of them
   int ns, kper;           // splits, keys a split
-  int vstages;            // V tile buffers of the split kernel (1 or 2)
+  int vstages;            // V tile buffers of the split kernel's COL form (1 or 2)
   int rep;                // copies of the query rows in a tile (see the split kernel)
   int* err;
 };
@@ -225,7 +225,7 @@ constexpr int kScaleRing = 4;
 constexpr float kRefBits = 8.f;   // log2 of the largest weight when the reference is set
 constexpr float kRefMost = 15.5f; // log2 of the largest weight before it moves
 constexpr int kLaneStride = 132;  // floats of a lane's state: 16-byte accesses without bank conflicts
-constexpr int kStages = 2;        // K tile buffers (V: two, or one where they do not fit)
+constexpr int kStages = 2;        // K tile buffers (V: two, or one where COL's do not fit)
 constexpr int kRawBytes = 8192;   // a converter warp's rows of a tile: NK / 4 rows of up to 128 or 256 floats
 
 // f16 A and B, f32 accumulator, M = 128; B is MN-major when mn is set (bit 16).
@@ -388,7 +388,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const int nt = max(0, (k1 - k0 + NK - 1) / NK);  // 0 at a window's end: an empty partial
   const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
   const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
-  const int VS = a.vstages;
+  // one V buffer is for COL alone: warpgroups on alternate tiles would wait for one phase of its barrier on each
+  // of their tiles, which passes before the tile's V is there
+  const int VS = COL ? a.vstages : 2;
   const uint32_t voff = kStages * 2 * kpart, qoff = voff + (uint32_t)VS * 2 * vpart;
   const bool qlo_tm = split_q_lo_fits(NK, COL, a.dqk, a.dv);
   const uint32_t roff = qoff + (qlo_tm ? 0u : (uint32_t)qb * 128 * 128);  // raw rows
@@ -1048,16 +1050,26 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
   return w;
 }
 
+// Dynamic shared memory of the split kernel: operand tiles, the queries' lo parts where tensor memory has no room
+// for them, raw rows, 1024 bytes to align the buffers; and its limit, beside SplitSmem.
+constexpr size_t kSplitSmemLimit = 227 * 1024 - 2048;
+static constexpr size_t split_smem(int NK, bool col, int dqk, int dv, int vstages) {
+  const size_t kstage = (size_t)NK * 256 * ((dqk + 63) / 64), vstage = (size_t)NK * 256 * ((dv + 63) / 64);
+  const size_t qlo = split_q_lo_fits(NK, col, dqk, dv) ? 0 : (size_t)((dqk + 63) / 64) * 128 * 128;
+  return 1024 + kStages * kstage + vstages * vstage + qlo + kConvWarps * kRawBytes;
+}
+
 template <int NK, bool COL>
 static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   static_assert(kScaleRing >= kStages + 2, "a tile's scale stays until its warpgroup has read it");
   static_assert(sizeof(SplitSmem) <= 2048, "beside the dynamic shared memory");
-  constexpr size_t limit = 227 * 1024 - 2048;  // beside SplitSmem
-  const size_t kstage = (size_t)NK * 256 * ((a.dqk + 63) / 64), vstage = (size_t)NK * 256 * ((a.dv + 63) / 64);
-  size_t smem = 1024 + kStages * kstage + kConvWarps * kRawBytes;  // 1024: the buffers' alignment
-  if (!split_q_lo_fits(NK, COL, a.dqk, a.dv)) smem += (size_t)(a.dqk + 63) / 64 * 128 * 128;
-  a.vstages = smem + 2 * vstage <= limit ? 2 : 1;
-  smem = std::max(smem + a.vstages * vstage, 1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
+  // the widest heads of each form (the lo parts are in shared memory at the widest only)
+  static_assert(COL || split_smem(NK, false, NK == 64 ? 128 : 256, 128, 2) <= kSplitSmemLimit,
+                "warpgroups on alternate tiles need two V buffers");
+  constexpr size_t limit = kSplitSmemLimit;
+  a.vstages = split_smem(NK, COL, a.dqk, a.dv, 2) <= limit ? 2 : 1;
+  const size_t smem = std::max(split_smem(NK, COL, a.dqk, a.dv, a.vstages),
+                               1024 + (size_t)256 * kLaneStride * 4 + sizeof(SplitStates));
   if (smem > limit) return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr[64];  // per device
   static_assert(256 * (kSoftmaxRegs + kConvertRegs) == kSplitThreads * kSplitRegs, "register shares");
