@@ -1123,8 +1123,8 @@ extern "C" {
 
 size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom* g, int32_t n, int32_t cache_len) {
   if (!g || n < 1 || n > kTreeMax || cache_len < 0 || g->n_heads < 1 || g->n_kv_heads < 1 ||
-      g->n_kv_heads > 64 || g->n_heads > 4096 || g->head_dim_qk < 1 || g->head_dim_qk > 256 ||
-      g->head_dim_v < 1 || g->head_dim_v > 256)
+      g->n_kv_heads > 64 || g->n_heads > 4096 || g->n_heads % g->n_kv_heads || g->head_dim_qk < 1 ||
+      g->head_dim_qk > 256 || g->head_dim_v < 1 || g->head_dim_v > 256)
     return 0;
   return tree_ws(nullptr, g, n, tree_plan_splits(g, cache_len, n).ns).bytes;
 }
