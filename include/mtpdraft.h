@@ -600,6 +600,7 @@ typedef struct {
  *   elements below 2^-39 of a tile's largest count as 0), sums are float32.
  *   Infinity or NaN in a K or V row that a node sees gives NaN.
  * ------------------------------------------------------------------------ */
+/* Enough for every call of up to n nodes and cache_len cached keys. */
 size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n, int32_t cache_len);
 mtp_status attn_tree_sink(const mtp_attn_geom *g, const mtp_draft_tree *tree, const float *d_qp,
                           const float *d_kp, const float *d_vp, const float *d_q_norm,

@@ -1002,17 +1002,23 @@ static int split_nk(int dqk, int dv) { return dqk <= 128 && dv <= 128 ? 64 : 32;
 // of two heads of 256 dims; 64 writes half of 32's partials.
 constexpr int kMinKeys = 64;
 
-// Splits of the cached keys all rows see: about one CTA per SM.
+// Cached keys that all rows can see: a window's rows have at most window - 1 in
+// common (depth 0 alone).
+static int common_keys(const mtp_attn_geom* g, int L) { return g->window > 0 ? std::min(L, g->window - 1) : L; }
+
+// Splits of these keys at most: about one CTA per SM.
+static int most_splits(const mtp_attn_geom* g, int keys, int n, int sms) {
+  const int mt = (n * (g->n_heads / g->n_kv_heads) + 127) / 128;
+  return std::min(std::max(1, sms / (g->n_kv_heads * mt)), (keys + kMinKeys - 1) / kMinKeys);
+}
+
 static TreePlan tree_plan_splits(const mtp_attn_geom* g, int L, int n) {
   TreePlan p;
-  // a window's rows have at most window - 1 cached keys in common (depth 0 alone)
-  const int keys = g->window > 0 ? std::min(L, g->window - 1) : L;
-  const int mt = (n * (g->n_heads / g->n_kv_heads) + 127) / 128;
+  const int keys = common_keys(g, L);
   p.ns = 0;
   p.kper = 0;
   if (keys > 0) {
-    int want = std::max(1, sm_count() / (g->n_kv_heads * mt));
-    want = std::min(want, (keys + kMinKeys - 1) / kMinKeys);
+    const int want = most_splits(g, keys, n, sm_count());
     p.kper = ((keys + want - 1) / want + 15) / 16 * 16;
     p.ns = (keys + p.kper - 1) / p.kper;
   }
@@ -1029,7 +1035,8 @@ struct TreeWs {
   size_t bytes;
 };
 
-static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
+// `partials`: query rows times splits.
+static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, size_t partials) {
   TreeWs w = {};
   size_t off = sizeof(WsHeader);
   uint8_t* b = static_cast<uint8_t*>(ws);
@@ -1044,10 +1051,20 @@ static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, int ns) {
   const size_t tiles = (size_t)g->n_kv_heads * ((n * (g->n_heads / g->n_kv_heads) + 127) / 128);
   w.qt = take(tiles * 512 * g->head_dim_qk);
   w.qinv = reinterpret_cast<float*>(take(tiles * 128 * 4));
-  w.ml = reinterpret_cast<float2*>(take(8 * rows * ns));
-  w.o = reinterpret_cast<float*>(take(4 * rows * ns * g->head_dim_v));
+  w.ml = reinterpret_cast<float2*>(take(8 * partials));
+  w.o = reinterpret_cast<float*>(take(4 * partials * g->head_dim_v));
   w.bytes = off;
   return w;
+}
+
+// Partials of any call of up to n nodes and L cached keys.  A call's own number falls where its rows fill one
+// more tile of 128, and where its keys a split are rounded up; a workspace of the largest call has to do for all.
+static size_t most_partials(const mtp_attn_geom* g, int n, int L) {
+  const int keys = common_keys(g, L), sms = sm_count();
+  size_t most = 0;
+  for (int i = 1; i <= n && keys > 0; ++i)
+    most = std::max(most, (size_t)i * g->n_heads * most_splits(g, keys, i, sms));
+  return most;
 }
 
 // Dynamic shared memory of the split kernel: operand tiles, the queries' lo parts where tensor memory has no room
@@ -1126,7 +1143,7 @@ size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom* g, int32_t n, int32_t
       g->n_kv_heads > 64 || g->n_heads > 4096 || g->n_heads % g->n_kv_heads || g->head_dim_qk < 1 ||
       g->head_dim_qk > 256 || g->head_dim_v < 1 || g->head_dim_v > 256)
     return 0;
-  return tree_ws(nullptr, g, n, tree_plan_splits(g, cache_len, n).ns).bytes;
+  return tree_ws(nullptr, g, n, most_partials(g, n, cache_len)).bytes;
 }
 
 mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, const float* d_qp,
@@ -1189,7 +1206,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
     a.rope.half = g->rot_dim / 2;
   }
   const TreePlan pl = tree_plan_splits(g, cache_len, n);
-  const TreeWs w = tree_ws(d_ws, g, n, pl.ns);
+  const TreeWs w = tree_ws(d_ws, g, n, (size_t)n * g->n_heads * pl.ns);
   if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
     return fail(MTP_ERR_WORKSPACE, "attn_tree_sink: workspace too small");
   a.qp = d_qp;

@@ -107,3 +107,15 @@ def test_32768_keys(dev, n, pattern):  # noqa: F811
     """40 / 8 heads: 27 tiles a split (2 nodes) and 86 (64 nodes)."""
     c = tiles_case(n, pattern, 64 if pattern == "zigzag" else 2048, nh=40, nkv=8, dqk=128, dv=128, L=32768, n=n)
     check(Call(c, dev), 19, 90)
+
+
+def test_one_workspace_for_every_call_up_to_the_largest(dev):  # noqa: F811
+    """Allocated once for 64 nodes and the longest cache, used with fewer of both."""
+    from mtp_speculative_draft_gb300 import attn_tree_sink_workspace_bytes, workspace
+    kw = dict(nh=40, nkv=8, dqk=128, dv=128)
+    calls = [Call(_attn_case(L + n, L=L, n=n, **kw), dev) for L, n in ((1153, 26), (1152, 25), (1152, 16), (300, 51), (65, 1))]
+    ws = workspace(attn_tree_sink_workspace_bytes(calls[0].g, 64, 1153))
+    for call in calls:
+        call.ws = ws
+        call()
+        call.check()

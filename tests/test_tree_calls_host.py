@@ -24,3 +24,16 @@ def test_workspace_of_heads_that_do_not_group(lib):
             "    g = _lib.AttnGeom(nh, nkv, 64, 64, 64, 0, 0, 1e-6, 0.0)\n"
             "    assert lib.attn_tree_sink_workspace_bytes(C.byref(g), 1, 100) == 0\n")
     assert subprocess.run([sys.executable, "-c", code], cwd=ROOT).returncode == 0
+
+
+@pytest.mark.parametrize("nh,nkv,dqk,dv,window", [(40, 8, 128, 128, 0), (16, 2, 256, 256, 0), (4, 2, 64, 64, 0),
+                                                  (32, 8, 192, 128, 128), (64, 1, 32, 256, 0), (7, 1, 96, 32, 3000)])
+def test_workspace_of_the_largest_call_does_for_all(lib, nh, nkv, dqk, dv, window):
+    """The size grows with the nodes and with the cached keys."""
+    from mtp_speculative_draft_gb300 import _lib
+    g = _lib.AttnGeom(nh, nkv, dqk, dv, dqk, window, 0, 1e-6, 0.0)
+    lengths = list(range(0, 200, 3)) + list(range(1100, 1400)) + [4096, 4097, 8191, 32767, 32768]
+    size = [[lib.attn_tree_sink_workspace_bytes(C.byref(g), n, L) for L in lengths] for n in range(1, 65)]
+    for n, row in enumerate(size):
+        assert all(a <= b for a, b in zip(row, row[1:]))
+        assert n == 0 or all(a <= b for a, b in zip(size[n - 1], row))
