@@ -39,7 +39,10 @@
  *  - Workspaces are caller-owned device buffers of at least the size the
  *    matching *_workspace_bytes() function returns.  Before its first use a
  *    workspace must be cleared once with mtp_workspace_init(); kernels leave
- *    it in that state again when they finish.  Calls that share a workspace
+ *    what calls of their kind need cleared in that state again when they
+ *    finish.  A workspace passes to another kind of call after another
+ *    mtp_workspace_init(); the calls of a draft tree's round (at the end of
+ *    this file) may share one in any order.  Calls that share a workspace
  *    must not overlap on the GPU.
  */
 #ifndef MTPDRAFT_H

@@ -307,7 +307,7 @@ using namespace mtp;
 extern "C" {
 
 size_t logit_rules_argmax_workspace_bytes(int32_t rows) {
-  if (rows < 1 || rows > 1024) return 0;
+  if (rows < 1 || rows > kRuleRowsMax) return 0;
   return sizeof(WsHeader) + (size_t)rows * 16 + 256;
 }
 
@@ -316,7 +316,7 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
                               int64_t ld_out, void* d_ws, size_t ws_bytes, void* stream) {
   if (!R || !d_logits || !d_tokens || !d_values)
     return fail(MTP_ERR_INVALID_ARG, "logit_rules_argmax: null pointer");
-  if (rows < 1 || rows > 1024)
+  if (rows < 1 || rows > kRuleRowsMax)
     return fail(MTP_ERR_UNSUPPORTED, "logit_rules_argmax: rows must be in 1..1024");
   if (R->vocab < 1 || R->vocab > (1 << 28))
     return fail(MTP_ERR_UNSUPPORTED, "logit_rules_argmax: vocab must be in 1..2^28");

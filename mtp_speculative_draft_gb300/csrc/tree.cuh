@@ -7,6 +7,11 @@
 namespace mtp {
 
 constexpr int kTreeMax = 64;  // nodes of a tree: one 64-bit ancestor word per node
+// Behind a workspace's header the joins of logit_rules_argmax, a 64-bit key and a 32-bit counter a row, which are
+// zero between calls.  Other calls of a round that use a workspace's body start behind them, so one workspace
+// serves them all in turn.
+constexpr int kRuleRowsMax = 1024;
+constexpr size_t kRuleJoinBytes = (size_t)kRuleRowsMax * 16;
 
 // Device error codes of these operators (after the ones in common.cuh).
 enum TreeErr : int {

@@ -1038,7 +1038,7 @@ struct TreeWs {
 // `partials`: query rows times splits.
 static TreeWs tree_ws(void* ws, const mtp_attn_geom* g, int n, size_t partials) {
   TreeWs w = {};
-  size_t off = sizeof(WsHeader);
+  size_t off = sizeof(WsHeader) + kRuleJoinBytes;
   uint8_t* b = static_cast<uint8_t*>(ws);
   auto take = [&](size_t bytes) {
     uint8_t* p = b ? b + off : nullptr;

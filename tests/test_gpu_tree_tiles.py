@@ -119,3 +119,23 @@ def test_one_workspace_for_every_call_up_to_the_largest(dev):  # noqa: F811
         call.ws = ws
         call()
         call.check()
+
+
+def test_attention_and_rules_share_a_workspace_in_turn(dev):  # noqa: F811
+    """What attention leaves in a workspace is no state of the rules' chunks, and the other way round."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    from oracle import tree_oracle as T
+    call = Call(_attn_case(31, nh=40, nkv=8, dqk=128, dv=128, L=300, n=16), dev)
+    V, x = 9001, np.random.default_rng(4).standard_normal((1024, 9001)).astype(np.float32)
+    logits, want = torch.from_numpy(x).to(dev), [t for t, _ in T.greedy(x)]
+    call.ws = ws = M.workspace(max(call.ws.numel(), M.logit_rules_argmax_workspace_bytes(1024)))
+    tok, val = torch.empty(1024, dtype=torch.int32, device=dev), torch.empty(1024, device=dev)
+    for rows in (16, 64, 1024, 1):
+        call()
+        tok.fill_(-9)
+        M.logit_rules_argmax(M.logit_rules(V), logits[:rows], tok, val, None, ws)
+        assert tok[:rows].tolist() == want[:rows]
+        call.out.fill_(7.0)
+        call()
+        call.check(f"after rules of {rows} rows")
