@@ -243,8 +243,8 @@ mtp_status rope_axes_rows(const mtp_rope_axes* axes, const mtp_head_rows* t, int
     a.t[i] = x;
     a.head_end[i] = heads;
   }
-  if (!d_ws || ws_bytes < rope_axes_rows_workspace_bytes())
-    return fail(MTP_ERR_WORKSPACE, "rope_axes_rows: workspace too small");
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < rope_axes_rows_workspace_bytes())
+    return fail(MTP_ERR_WORKSPACE, "rope_axes_rows: workspace too small or misaligned");
   a.nt = n_t;
   a.d = head_dim;
   a.rows = rows;

@@ -342,7 +342,7 @@ mtp_status logit_rules_argmax(const mtp_logit_rules* R, const float* d_logits, i
         reinterpret_cast<uintptr_t>(d_values)) & 3))
     return fail(MTP_ERR_INVALID_ARG, "logit_rules_argmax: misaligned pointer");
   if (!d_ws || !aligned16(d_ws) || ws_bytes < logit_rules_argmax_workspace_bytes(rows))
-    return fail(MTP_ERR_WORKSPACE, "logit_rules_argmax: workspace too small");
+    return fail(MTP_ERR_WORKSPACE, "logit_rules_argmax: workspace too small or misaligned");
   RuleArgs a = {};
   a.x = d_logits;
   a.ld = ld;
@@ -382,8 +382,8 @@ mtp_status mtp_token_counts(uint32_t* d_counts, int32_t vocab, const int32_t* d_
     return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: misaligned pointer");
   if (vocab < 1 || n < 1 || (prompt != 0 && prompt != 1))
     return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: vocab and n must be >= 1, prompt 0 or 1");
-  if (!d_ws || ws_bytes < sizeof(WsHeader))
-    return fail(MTP_ERR_WORKSPACE, "mtp_token_counts: workspace too small");
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < sizeof(WsHeader))
+    return fail(MTP_ERR_WORKSPACE, "mtp_token_counts: workspace too small or misaligned");
   cudaError_t e = launch_pdl(token_counts_kernel, dim3((n + 255) / 256), 256, 0,
                              static_cast<cudaStream_t>(stream), d_counts, vocab, d_tokens, n, prompt,
                              &static_cast<WsHeader*>(d_ws)->err);

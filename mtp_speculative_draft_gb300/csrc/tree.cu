@@ -139,8 +139,8 @@ mtp_status mtp_tree_plan(const int32_t* d_parents, int32_t n, uint64_t* d_mask, 
     return fail(MTP_ERR_INVALID_ARG, "mtp_tree_plan: null pointer");
   if (!aligned4(d_parents) || !aligned4(d_depth) || (reinterpret_cast<uintptr_t>(d_mask) & 7))
     return fail(MTP_ERR_INVALID_ARG, "mtp_tree_plan: misaligned pointer");
-  if (!d_ws || ws_bytes < sizeof(WsHeader))
-    return fail(MTP_ERR_WORKSPACE, "mtp_tree_plan: workspace too small");
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < sizeof(WsHeader))
+    return fail(MTP_ERR_WORKSPACE, "mtp_tree_plan: workspace too small or misaligned");
   cudaError_t e = launch_pdl(tree_plan_kernel, dim3(1), kTreeMax, 0, static_cast<cudaStream_t>(stream),
                              d_parents, n, reinterpret_cast<unsigned long long*>(d_mask), d_depth,
                              &static_cast<WsHeader*>(d_ws)->err);
@@ -183,8 +183,8 @@ mtp_status kv_tree_commit(const mtp_kv_caches* C, const int32_t* d_path, int32_t
     if (!C->h_k[l] || !C->h_v[l] || !aligned16(C->h_k[l]) || !aligned16(C->h_v[l]))
       return fail(MTP_ERR_INVALID_ARG, "kv_tree_commit: null or misaligned cache");
   if (!aligned4(d_path)) return fail(MTP_ERR_INVALID_ARG, "kv_tree_commit: misaligned path");
-  if (!d_ws || ws_bytes < sizeof(WsHeader))
-    return fail(MTP_ERR_WORKSPACE, "kv_tree_commit: workspace too small");
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < sizeof(WsHeader))
+    return fail(MTP_ERR_WORKSPACE, "kv_tree_commit: workspace too small or misaligned");
   CommitArgs a = {};
   a.path = d_path;
   a.n = n;

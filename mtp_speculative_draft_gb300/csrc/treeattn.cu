@@ -1208,7 +1208,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   const TreePlan pl = tree_plan_splits(g, cache_len, n);
   const TreeWs w = tree_ws(d_ws, g, n, (size_t)n * g->n_heads * pl.ns);
   if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
-    return fail(MTP_ERR_WORKSPACE, "attn_tree_sink: workspace too small");
+    return fail(MTP_ERR_WORKSPACE, "attn_tree_sink: workspace too small or misaligned");
   a.qp = d_qp;
   a.kp = d_kp;
   a.vp = d_vp;

@@ -37,3 +37,18 @@ def test_workspace_of_the_largest_call_does_for_all(lib, nh, nkv, dqk, dv, windo
     for n, row in enumerate(size):
         assert all(a <= b for a, b in zip(row, row[1:]))
         assert n == 0 or all(a <= b for a, b in zip(size[n - 1], row))
+
+
+def test_misaligned_workspaces_are_refused(lib):
+    """The error word at the workspace's start takes an atomic: 4 bytes off, or 1, is refused."""
+    from mtp_speculative_draft_gb300 import _lib
+    P = C.c_void_p(0x100000)
+    ax = _lib.RopeAxes(0x1000, 0x2000, 1, (C.c_int32 * 4)(64, 0, 0, 0), 0, 8, 100)
+    rows = (_lib.HeadRows * 1)(_lib.HeadRows(0x10000, 0x20000, None, 1024, 1024, 128, 128, 8))
+    caches = _lib.KvCaches((C.c_void_p * 1)(0x1000), (C.c_void_p * 1)(0x2000), 1, 2, 64, 64, 64)
+    for ws in (0x100001, 0x100004, 0x100008):
+        ws = C.c_void_p(ws)
+        assert lib.mtp_tree_plan(P, 4, P, P, ws, 1024, None) == 4
+        assert lib.mtp_token_counts(P, 10, P, 3, 0, ws, 1024, None) == 4
+        assert lib.kv_tree_commit(C.byref(caches), P, 4, 0, ws, 1024, None) == 4
+        assert lib.rope_axes_rows(C.byref(ax), rows, 1, 4, 128, 1e-6, ws, 1024, None) == 4
