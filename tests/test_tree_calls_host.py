@@ -52,3 +52,29 @@ def test_misaligned_workspaces_are_refused(lib):
         assert lib.mtp_token_counts(P, 10, P, 3, 0, ws, 1024, None) == 4
         assert lib.kv_tree_commit(C.byref(caches), P, 4, 0, ws, 1024, None) == 4
         assert lib.rope_axes_rows(C.byref(ax), rows, 1, 4, 128, 1e-6, ws, 1024, None) == 4
+
+
+def test_a_call_that_makes_its_workspace_makes_it_on_its_stream(monkeypatch):
+    """The buffer comes from the pool of the stream that uses it: another stream's pool would hand out memory that
+    stream may still use, and take it back while this one does."""
+    import torch
+    from mtp_speculative_draft_gb300 import api
+    current, made = [None], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(current[-1]))
+    monkeypatch.setattr(api, "mtp_workspace_init", lambda ws, stream=None: None)
+    side = object()
+    api.workspace(5000, stream=side)
+    api.workspace(5000)
+    assert made == [side, None]
