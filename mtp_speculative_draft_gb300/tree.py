@@ -66,10 +66,17 @@ def _rows(t, rows, width, name, device):
     return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
 
 
-def _ws(ws):
-    if not ws.is_cuda or not ws.is_contiguous() or ws.dtype is not torch.uint8:
-        raise ValueError("workspace: a contiguous uint8 device tensor is required")
+def _ws(ws, device):
+    if ws.get_device() != device or not ws.is_contiguous() or ws.dtype is not torch.uint8:
+        raise ValueError("workspace: a contiguous uint8 tensor on the current CUDA device is required")
     return ws.data_ptr(), ws.numel()
+
+
+def _here(desc, device):
+    """Refuses a descriptor whose tensors are on another device than the current one (one that a program filled
+    in by itself has no device)."""
+    if getattr(desc, "device", device) != device:
+        raise ValueError(f"{type(desc).__name__}: its tensors are on device {desc.device}, the current one is {device}")
 
 
 # ------------------------------------------------------------------------------- rotary axes
@@ -85,7 +92,7 @@ def rope_axes(sections, pos: torch.Tensor, rope: torch.Tensor, interleaved=False
     ax = RopeAxes(_ptr(pos, _I32, n, "pos", dev), _ptr(rope, _F32, 2 * half, "rope", dev), n,
                   (L.i32 * 4)(*[int(s) for s in sections]), int(bool(interleaved)), pos.shape[1],
                   rope.numel() // (2 * half))
-    ax.tensors = (pos, rope)
+    ax.tensors, ax.device = (pos, rope), dev
     return ax
 
 
@@ -98,6 +105,7 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
     ``[rows, heads, head_dim]`` (any row and head stride, contiguous head rows; y may be x) and
     norm_w ``[head_dim]`` or None."""
     dev = _device()
+    _here(axes, dev)
     lib = L.load()
     rows, _, d = tensors[0][0].shape
     descs = []
@@ -119,7 +127,7 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
     arr = (HeadRows * len(descs))(*descs)
     if ws is None:
         ws = workspace(lib.rope_axes_rows_workspace_bytes(), stream=stream)
-    check(lib.rope_axes_rows(C.byref(axes), arr, len(arr), rows, d, eps, *_ws(ws), _on(stream, dev)),
+    check(lib.rope_axes_rows(C.byref(axes), arr, len(arr), rows, d, eps, *_ws(ws, dev), _on(stream, dev)),
           "rope_axes_rows")
     return ws
 
@@ -131,9 +139,11 @@ def draft_tree(mask: torch.Tensor, depth: torch.Tensor, axes: RopeAxes | None = 
     n = mask.numel()
     if mask.dtype not in (torch.int64, torch.uint64):
         raise TypeError("draft_tree: mask holds 64-bit words")
+    if axes is not None:
+        _here(axes, dev)
     t = DraftTree(_ptr(mask, mask.dtype, 1, "mask", dev), _ptr(depth, _I32, n, "depth", dev),
                   C.pointer(axes) if axes is not None else None, n, int(pos_base), 0, 0, 0)
-    t.tensors = (mask, depth, axes)
+    t.tensors, t.device = (mask, depth, axes), dev
     return t
 
 
@@ -151,7 +161,7 @@ def mtp_tree_plan(parents, mask, depth, ws=None, stream=None):
         raise TypeError("mtp_tree_plan: mask holds 64-bit words")
     check(L.load().mtp_tree_plan(_ptr(parents, _I32, n, "parents", dev), n,
                                  _ptr(mask, mask.dtype, n, "mask", dev),
-                                 _ptr(depth, _I32, n, "depth", dev), *_ws(ws), _on(stream, dev)),
+                                 _ptr(depth, _I32, n, "depth", dev), *_ws(ws, dev), _on(stream, dev)),
           "mtp_tree_plan")
     return ws
 
@@ -165,6 +175,7 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
     """Attention of a tree's rows ``qp [n, q_rows]``, ``kp``, ``vp`` (any row stride) over the cache
     ``[n_kv, cap, dim]`` and their ancestors; appends the rows at ``cache_len`` onwards."""
     dev = _device()
+    _here(tree, dev)
     lib = L.load()
     n, nh, nkv, dqk, dv = tree.n, g.n_heads, g.n_kv_heads, g.head_dim_qk, g.head_dim_v
     pq, ldq = _rows(qp, n, nh * dqk * (2 if g.gated_q else 1), "qp", dev)
@@ -183,7 +194,7 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
         rope.numel() // g.rot_dim if rope is not None and g.rot_dim > 0 else 0,
         _ptr(sinks, _F32, nh, "sinks", dev), _ptr(k_cache, _F32, 0, "k_cache", dev),
         _ptr(v_cache, _F32, 0, "v_cache", dev), int(cache_len), cap,
-        _ptr(out, _F32, n * nh * dv, "out", dev), *_ws(ws), _on(stream, dev)), "attn_tree_sink")
+        _ptr(out, _F32, n * nh * dv, "out", dev), *_ws(ws, dev), _on(stream, dev)), "attn_tree_sink")
     return ws
 
 
@@ -214,6 +225,8 @@ def logit_rules(vocab, repetition=1.0, frequency=0.0, presence=0.0, counts=None,
     r.rows = min([1 << 30] + [t.shape[0] for t in (allow if allow is not None and allow.dim() == 2 else None,
                                                    path_mask) if t is not None])
     r.tensors = (counts, bias_tokens, bias, allow, path_tokens, path_mask)
+    if any(t is not None for t in r.tensors):
+        r.device = dev
     return r
 
 
@@ -225,6 +238,7 @@ def logit_rules_argmax(rules: LogitRules, logits, tokens, values, out=None, ws=N
     """Applies ``rules`` to ``logits [rows, vocab]`` (any row stride) and takes each row's argmax;
     ``out`` (or ``logits`` itself) receives the final logits."""
     dev = _device()
+    _here(rules, dev)
     lib = L.load()
     rows = logits.shape[0]
     if rows > rules.rows:
@@ -235,7 +249,7 @@ def logit_rules_argmax(rules: LogitRules, logits, tokens, values, out=None, ws=N
     if ws is None:
         ws = workspace(lib.logit_rules_argmax_workspace_bytes(rows), stream=stream)
     check(lib.logit_rules_argmax(C.byref(rules), px, ld or vocab, rows, _ptr(tokens, _I32, rows, "tokens", dev),
-                                 _ptr(values, _F32, rows, "values", dev), py, ldy or vocab, *_ws(ws),
+                                 _ptr(values, _F32, rows, "values", dev), py, ldy or vocab, *_ws(ws, dev),
                                  _on(stream, dev)), "logit_rules_argmax")
     return ws
 
@@ -249,7 +263,7 @@ def mtp_token_counts(counts, tokens, prompt=False, ws=None, stream=None):
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     n = tokens.numel()
     check(L.load().mtp_token_counts(_ptr(counts, counts.dtype, 1, "counts", dev), counts.numel(),
-                                    _ptr(tokens, _I32, n, "tokens", dev), n, int(bool(prompt)), *_ws(ws),
+                                    _ptr(tokens, _I32, n, "tokens", dev), n, int(bool(prompt)), *_ws(ws, dev),
                                     _on(stream, dev)), "mtp_token_counts")
     return ws
 
@@ -284,16 +298,17 @@ def kv_caches(k_caches, v_caches) -> KvCaches:
     if len({*ks, *vs}) != 2 * n:
         raise ValueError("kv_caches: a cache is given twice")
     c = KvCaches(ks, vs, n, nkv, dqk, dv, cap)
-    c.tensors = (k_caches, v_caches, ks, vs)
+    c.tensors, c.device = (k_caches, v_caches, ks, vs), dev
     return c
 
 
 def kv_tree_commit(caches: KvCaches, path, cache_len, ws=None, stream=None):
     """Moves the rows of ``path [n]`` (nodes of the tree, -1 past the end) to ``cache_len`` onwards."""
     dev = _device()
+    _here(caches, dev)
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     n = path.numel()
     check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, int(cache_len),
-                                  *_ws(ws), _on(stream, dev)), "kv_tree_commit")
+                                  *_ws(ws, dev), _on(stream, dev)), "kv_tree_commit")
     return ws

@@ -78,3 +78,88 @@ def test_a_call_that_makes_its_workspace_makes_it_on_its_stream(monkeypatch):
     api.workspace(5000, stream=side)
     api.workspace(5000)
     assert made == [side, None]
+
+
+class _Tensor:
+    """What the wrappers look at, of a tensor on a device that this machine need not have."""
+
+    def __init__(self, device, dtype, *shape, stride=None):
+        import math
+        self.device, self.dtype, self.shape, self.is_cuda = device, dtype, shape, True
+        self._stride = stride or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
+
+    get_device = lambda self: self.device  # noqa: E731
+    is_contiguous = lambda self: True  # noqa: E731
+    data_ptr = lambda self: 0x100000  # noqa: E731
+    dim = lambda self: len(self.shape)  # noqa: E731
+
+    def numel(self):
+        import math
+        return math.prod(self.shape)
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+
+class _Lib:
+    """Counts what gets through to the library."""
+
+    def __init__(self):
+        self.calls = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls += 1
+            return 0
+        return call
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Workspaces and descriptors made on device 0, the current device is 1."""
+    import torch
+    from mtp_speculative_draft_gb300 import _lib, tree as W
+    i32, i64, f32, u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+    current, lib = [0], _Lib()
+    monkeypatch.setattr(W, "_device", lambda: current[0])
+    monkeypatch.setattr(W, "_on", lambda stream, device: None)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+
+    def make(d):
+        ax = W.rope_axes((32,), _Tensor(d, i32, 1, 3), _Tensor(d, f32, 10, 32, 2))
+        return dict(ax=ax, tree=W.draft_tree(_Tensor(d, i64, 3), _Tensor(d, i32, 3), ax), ws=_Tensor(d, u8, 4096),
+                    rules=W.logit_rules(100, counts=_Tensor(d, i32, 100)), caches=W.kv_caches([_Tensor(d, f32, 1, 20, 64)], [_Kv(d)]))
+
+    class _Kv(_Tensor):
+        def __init__(self, d):
+            super().__init__(d, f32, 1, 20, 64)
+
+        data_ptr = lambda self: 0x200000  # noqa: E731
+
+    def calls(s, d):
+        g = _lib.AttnGeom(1, 1, 64, 64, 64, 0, 0, 1e-6, 0.0)
+        r, k, n = _Tensor(d, f32, 3, 64), _Tensor(d, f32, 1, 20, 64), _Tensor(d, i32, 3)
+        x, v = _Tensor(d, f32, 3, 100), _Tensor(d, f32, 3)
+        return dict(
+            rope=lambda: W.rope_axes_rows(s["ax"], [(_Tensor(d, f32, 3, 1, 64), _Tensor(d, f32, 3, 1, 64), None)], s["ws"]),
+            attn=lambda: W.attn_tree_sink(g, s["tree"], r, r, r, None, None, None, None, k, k, 5, r, s["ws"]),
+            plan=lambda: W.mtp_tree_plan(n, _Tensor(d, i64, 3), n, s["ws"]),
+            rules=lambda: W.logit_rules_argmax(s["rules"], x, n, v, None, s["ws"]),
+            counts=lambda: W.mtp_token_counts(n, n, False, s["ws"]),
+            commit=lambda: W.kv_tree_commit(s["caches"], n, 5, s["ws"]))
+
+    on0 = make(0)
+    for name, call in calls(on0, 0).items():
+        lib.calls = 0
+        call()
+        assert lib.calls, name
+    current[0] = 1
+    on1 = make(1)
+    for key, names in dict(ws=("rope", "attn", "plan", "rules", "counts", "commit"), ax=("rope",), tree=("attn",),
+                           rules=("rules",), caches=("commit",)).items():
+        for name in names:
+            lib.calls = 0
+            with pytest.raises(ValueError):
+                calls({**on1, key: on0[key]}, 1)[name]()
+            assert not lib.calls, (key, name)
+    with pytest.raises(ValueError):  # a tree whose positions are elsewhere
+        W.draft_tree(_Tensor(1, i64, 3), _Tensor(1, i32, 3), on0["ax"])
