@@ -236,9 +236,8 @@ __global__ void __launch_bounds__(kRuleThreads, 4) logit_rules_kernel(const __gr
       const int i = list[e], v = v0 + i;
       if (v >= a.V) continue;
       float t = xs[i];
-      uint32_t c = cnt[e] + __popcll(nodes[slot[e]] & path);
-      if (c) {  // seen
-        c &= 0x7FFFFFFFu;
+      const uint32_t word = cnt[e], c = (word & 0x7FFFFFFFu) + __popcll(nodes[slot[e]] & path);  // up to 2^31 + 63
+      if (word | c) {  // seen
         t = t > 0.f ? __fdiv_rn(t, a.rep) : __fmul_rn(t, a.rep);
         t = __fsub_rn(t, __fadd_rn(__fmul_rn((float)c, a.freq), c ? a.pres : 0.f));
       }

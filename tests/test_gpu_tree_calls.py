@@ -3,9 +3,30 @@
 import numpy as np
 import pytest
 
+from oracle import tree_oracle as T
 from test_gpu_tree import dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def test_largest_counts(dev):  # noqa: F811
+    """A path that adds to the largest count of a word, with the prompt's bit and without."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    V = 200
+    words = np.zeros(V, np.uint32)
+    words[[3, 50]], words[[4, 51]], words[[5, 52]] = 0x7FFFFFFF, 0xFFFFFFFF, 0x80000000
+    x = np.random.default_rng(1).standard_normal((2, V)).astype(np.float32)
+    path = [3, 4, 5, 6, 4]
+    i32 = lambda a: torch.from_numpy(np.asarray(a, np.uint32).view(np.int32)).to(dev)  # noqa: E731
+    rules = M.logit_rules(V, 1.5, 2.0 ** -20, 0.25, i32(words), path_tokens=i32(path),
+                          path_mask=torch.tensor([0b11111, 0], dtype=torch.int64, device=dev))
+    out, tok, val = torch.zeros(2, V, device=dev), torch.zeros(2, dtype=torch.int32, device=dev), torch.zeros(2, device=dev)
+    M.logit_rules_argmax(rules, torch.from_numpy(x).to(dev), tok, val, out)
+    ref = T.logit_rules(x, words, 1.5, 2.0 ** -20, 0.25, path_tokens=path, path_mask=[0b11111, 0], dtype=np.float32)
+    assert ref[0, 3] < -2000 and ref[0, 4] < -2000  # 2^31 and more
+    np.testing.assert_array_equal(out.cpu().numpy(), ref)
+    assert tok.tolist() == [t for t, _ in T.greedy(ref)]
 
 
 def test_workspaces_come_from_the_pool_of_their_stream(dev):  # noqa: F811
