@@ -547,12 +547,14 @@ typedef struct {
     int32_t max_pos;         /* a position outside [0, max_pos) sets device error 6 */
 } mtp_rope_axes;
 
-/* Rows of heads: head h of row r starts at x + r*x_ld + h*x_hs (floats). */
+/* Rows of heads: head h of row r starts at x + r*x_ld + h*x_hs (floats), either
+ * [rows][heads] (a row's heads between two rows) or [heads][rows] (a head's rows
+ * between two heads, as in a cache). */
 typedef struct {
     const float *x;          /* input */
     float *y;                /* output: x itself with the same strides (in place), or no overlap */
     const float *norm_w;     /* [head_dim] weight of a per-head RMSNorm before the rotation, or NULL */
-    int64_t x_ld, y_ld;      /* row strides */
+    int64_t x_ld, y_ld;      /* row strides, >= head_dim */
     int32_t x_hs, y_hs;      /* head strides, >= head_dim */
     int32_t n_heads;
 } mtp_head_rows;

@@ -165,6 +165,13 @@ static cudaError_t launch_rope_rows(const RopeRowsArgs& a, cudaStream_t st) {
                     dim3(a.rows, split), kRopeThreads, 0, st, a);
 }
 
+// Whether no two head rows share a value: a row's heads between two rows, or a
+// head's rows between two heads.
+static bool rows_apart(int64_t ld, int32_t hs, int rows, int heads, int d) {
+  if (hs < d || ld < d) return false;
+  return ld >= (int64_t)(heads - 1) * hs + d || rows == 1 || ld <= (hs - d) / (rows - 1);
+}
+
 mtp_status fill_rope_axes(RopePos* out, const mtp_rope_axes* ax, int half, int rows,
                           const char* who) {
   const std::string w(who);
@@ -232,8 +239,7 @@ mtp_status rope_axes_rows(const mtp_rope_axes* axes, const mtp_head_rows* t, int
       return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: pointers must be 16-byte aligned");
     if (x.n_heads < 1 || x.n_heads > 4096)
       return fail(MTP_ERR_UNSUPPORTED, "rope_axes_rows: 1..4096 heads a tensor");
-    if (x.x_hs < head_dim || x.y_hs < head_dim || x.x_ld < (int64_t)(x.n_heads - 1) * x.x_hs + head_dim ||
-        x.y_ld < (int64_t)(x.n_heads - 1) * x.y_hs + head_dim)
+    if (!rows_apart(x.x_ld, x.x_hs, rows, x.n_heads, head_dim) || !rows_apart(x.y_ld, x.y_hs, rows, x.n_heads, head_dim))
       return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: strides let heads or rows overlap");
     if (x.x_ld % 4 || x.y_ld % 4 || x.x_hs % 4 || x.y_hs % 4)
       return fail(MTP_ERR_INVALID_ARG, "rope_axes_rows: strides must be multiples of 4 floats");

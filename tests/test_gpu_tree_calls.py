@@ -43,3 +43,34 @@ def test_workspaces_come_from_the_pool_of_their_stream(dev):  # noqa: F811
         at = [s["stream"] for s in torch.cuda.memory_snapshot()
               if s["address"] <= ws.data_ptr() < s["address"] + s["total_size"]]
         assert at == [side.cuda_stream]
+
+
+@pytest.mark.parametrize("rows,d,half", [(1, 64, 32), (37, 64, 32), (5, 128, 30), (300, 96, 16)])
+def test_rotation_of_head_major_rows(dev, rows, d, half):  # noqa: F811
+    """[heads, rows, head_dim]: queries from such a tensor, keys straight into the rows of a cache, and in place."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    from helpers import assert_close
+    rng = np.random.default_rng(rows)
+    nh, nkv, cap, at = 6, 2, rows + 11, 4
+    q, k = (rng.standard_normal((n, rows, d)).astype(np.float32) for n in (nh, nkv))
+    w = (1 + 0.1 * rng.standard_normal(d)).astype(np.float32)
+    up = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+    pos = rng.integers(0, 400, (1, rows)).astype(np.int32)
+    table = torch.empty(400 * 2 * half, device=dev)
+    M.mtp_rope_table(table, 400, 2 * half, 1e4)
+    tq, tk, cache = up(q), up(k), torch.full((nkv, cap, d), float("nan"), device=dev)
+    M.rope_axes_rows(M.rope_axes((half,), up(pos), table),
+                     [(tq.transpose(0, 1), tq.transpose(0, 1), up(w)),
+                      (tk.transpose(0, 1), cache[:, at:at + rows].transpose(0, 1), None)])
+    turn = lambda x, w: T.rope_axes(T.head_norm(x.transpose(1, 0, 2), w, 1e-6), pos, (half,), False, 1e4).transpose(1, 0, 2)  # noqa: E731
+    assert_close(tq.cpu().numpy(), turn(q, w), "q", 2e-6)  # the roundings of a rotation counted beside its other tests
+    assert_close(cache[:, at:at + rows].cpu().numpy(), turn(k, None), "k", 2e-6)
+    assert torch.isnan(cache[:, :at]).all() and torch.isnan(cache[:, at + rows:]).all()
+    assert (tk == up(k)).all()
+    y = torch.zeros(nh, rows, d, device=dev).transpose(0, 1)
+    if rows > 1:
+        for bad in (tq.transpose(0, 1).as_strided((rows, nh, d), (d // 2, rows * d, 1)),       # rows overlap
+                    tq.transpose(0, 1).as_strided((rows, nh, d), (d, (rows - 1) * d, 1))):     # heads overlap
+            with pytest.raises(M._lib.MtpError):
+                M.rope_axes_rows(M.rope_axes((half,), up(pos), table), [(bad, y, None)])
