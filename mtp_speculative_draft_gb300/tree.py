@@ -16,6 +16,7 @@ from ._lib import AttnGeom, DraftTree, HeadRows, KvCaches, LogitRules, RopeAxes,
 from .api import workspace
 
 _I32, _F32 = torch.int32, torch.float32
+_MOST = (1 << 31) - 1
 
 
 def _refuse(t, dtype, numel, name):
@@ -35,6 +36,14 @@ def _ptr(t, dtype, numel, name, device):
     if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.numel() < numel:
         _refuse(t, dtype, numel, name)
     return t.data_ptr()
+
+
+def _int(v, name):
+    """A number that the library takes in 32 bits (ctypes would cut a longer one off)."""
+    v = int(v)
+    if not -_MOST <= v <= _MOST:
+        raise ValueError(f"{name}: {v} does not fit in 32 bits")
+    return v
 
 
 def _device():
@@ -90,8 +99,8 @@ def rope_axes(sections, pos: torch.Tensor, rope: torch.Tensor, interleaved=False
     if pos.dim() != 2 or pos.shape[0] != n:
         raise ValueError(f"rope_axes: pos [{n}, rows] is required")
     ax = RopeAxes(_ptr(pos, _I32, n, "pos", dev), _ptr(rope, _F32, 2 * half, "rope", dev), n,
-                  (L.i32 * 4)(*[int(s) for s in sections]), int(bool(interleaved)), pos.shape[1],
-                  rope.numel() // (2 * half))
+                  (L.i32 * 4)(*[_int(s, "sections") for s in sections]), int(bool(interleaved)),
+                  _int(pos.shape[1], "pos"), min(rope.numel() // (2 * half), _MOST))
     ax.tensors, ax.device = (pos, rope), dev
     return ax
 
@@ -123,6 +132,8 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
             xh = yh = d
         if rows == 1:
             xr, yr = n * xh, n * yh
+        if xh > _MOST or yh > _MOST:
+            raise ValueError("rope_axes_rows: a head stride does not fit in 32 bits")
         descs.append(HeadRows(x.data_ptr(), y.data_ptr(), _ptr(w, _F32, d, "norm_w", dev), xr, yr, xh, yh, n))
     arr = (HeadRows * len(descs))(*descs)
     if ws is None:
@@ -136,13 +147,13 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
 def draft_tree(mask: torch.Tensor, depth: torch.Tensor, axes: RopeAxes | None = None, pos_base=0) -> DraftTree:
     """The new rows of a tree: ancestor words ``mask [n]`` (int64 or uint64) and ``depth [n]``."""
     dev = _device()
-    n = mask.numel()
+    n = _int(mask.numel(), "mask")
     if mask.dtype not in (torch.int64, torch.uint64):
         raise TypeError("draft_tree: mask holds 64-bit words")
     if axes is not None:
         _here(axes, dev)
     t = DraftTree(_ptr(mask, mask.dtype, 1, "mask", dev), _ptr(depth, _I32, n, "depth", dev),
-                  C.pointer(axes) if axes is not None else None, n, int(pos_base), 0, 0, 0)
+                  C.pointer(axes) if axes is not None else None, n, _int(pos_base, "pos_base"), 0, 0, 0)
     t.tensors, t.device = (mask, depth, axes), dev
     return t
 
@@ -154,7 +165,7 @@ def mtp_tree_workspace_bytes() -> int:
 def mtp_tree_plan(parents, mask, depth, ws=None, stream=None):
     """Ancestor words and depths of a tree from its ``parents [n]`` (int32, -1 for a root)."""
     dev = _device()
-    n = parents.numel()
+    n = _int(parents.numel(), "parents")
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     if mask.dtype not in (torch.int64, torch.uint64):
@@ -167,7 +178,7 @@ def mtp_tree_plan(parents, mask, depth, ws=None, stream=None):
 
 
 def attn_tree_sink_workspace_bytes(g: AttnGeom, n: int, cache_len: int) -> int:
-    return L.load().attn_tree_sink_workspace_bytes(C.byref(g), int(n), int(cache_len))
+    return L.load().attn_tree_sink_workspace_bytes(C.byref(g), _int(n, "n"), _int(cache_len, "cache_len"))
 
 
 def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rope, sinks, k_cache,
@@ -176,6 +187,7 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
     ``[n_kv, cap, dim]`` and their ancestors; appends the rows at ``cache_len`` onwards."""
     dev = _device()
     _here(tree, dev)
+    cache_len = _int(cache_len, "cache_len")
     lib = L.load()
     n, nh, nkv, dqk, dv = tree.n, g.n_heads, g.n_kv_heads, g.head_dim_qk, g.head_dim_v
     pq, ldq = _rows(qp, n, nh * dqk * (2 if g.gated_q else 1), "qp", dev)
@@ -191,9 +203,9 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
     check(lib.attn_tree_sink(
         C.byref(g), C.byref(tree), pq, pk, pv, _ptr(q_norm, _F32, dqk, "q_norm", dev),
         _ptr(k_norm, _F32, dqk, "k_norm", dev), _ptr(rope, _F32, 0, "rope", dev),
-        rope.numel() // g.rot_dim if rope is not None and g.rot_dim > 0 else 0,
+        min(rope.numel() // g.rot_dim, _MOST) if rope is not None and g.rot_dim > 0 else 0,
         _ptr(sinks, _F32, nh, "sinks", dev), _ptr(k_cache, _F32, 0, "k_cache", dev),
-        _ptr(v_cache, _F32, 0, "v_cache", dev), int(cache_len), cap,
+        _ptr(v_cache, _F32, 0, "v_cache", dev), cache_len, cap,
         _ptr(out, _F32, n * nh * dv, "out", dev), *_ws(ws, dev), _on(stream, dev)), "attn_tree_sink")
     return ws
 
@@ -206,20 +218,21 @@ def logit_rules(vocab, repetition=1.0, frequency=0.0, presence=0.0, counts=None,
     tree's ``path_tokens [n]`` with each row's ancestor word ``path_mask [rows]``."""
     dev = _device()
     word = lambda t: t.dtype if t is not None and t.dtype in (_I32, torch.uint32) else _I32  # noqa: E731
-    nb = 0 if bias is None else bias.numel()
-    npath = 0 if path_tokens is None else path_tokens.numel()
-    words = (int(vocab) + 31) // 32
+    nb = 0 if bias is None else _int(bias.numel(), "bias")
+    npath = 0 if path_tokens is None else _int(path_tokens.numel(), "path_tokens")
+    vocab = _int(vocab, "vocab")
+    words = (vocab + 31) // 32
     if (bias is None) != (bias_tokens is None) or (path_tokens is None) != (path_mask is None):
         raise ValueError("logit_rules: bias with bias_tokens, path_tokens with path_mask")
     if allow is not None and (allow.dim() not in (1, 2) or allow.shape[-1] < words):
         raise ValueError(f"logit_rules: allow needs {words} words a row")
     if path_mask is not None and path_mask.dtype not in (torch.int64, torch.uint64):
         raise TypeError("logit_rules: path_mask holds 64-bit words")
-    r = LogitRules(int(vocab), repetition, frequency, presence,
+    r = LogitRules(vocab, repetition, frequency, presence,
                    _ptr(counts, word(counts), vocab, "counts", dev),
                    _ptr(bias_tokens, _I32, nb, "bias_tokens", dev), _ptr(bias, _F32, nb, "bias", dev), nb,
                    _ptr(allow, word(allow), words, "allow", dev),
-                   allow.shape[1] if allow is not None and allow.dim() == 2 else 0,
+                   _int(allow.shape[1], "allow") if allow is not None and allow.dim() == 2 else 0,
                    _ptr(path_tokens, _I32, npath, "path_tokens", dev),
                    _ptr(path_mask, None if path_mask is None else path_mask.dtype, 1, "path_mask", dev), npath)
     r.rows = min([1 << 30] + [t.shape[0] for t in (allow if allow is not None and allow.dim() == 2 else None,
@@ -231,7 +244,7 @@ def logit_rules(vocab, repetition=1.0, frequency=0.0, presence=0.0, counts=None,
 
 
 def logit_rules_argmax_workspace_bytes(rows: int) -> int:
-    return L.load().logit_rules_argmax_workspace_bytes(int(rows))
+    return L.load().logit_rules_argmax_workspace_bytes(_int(rows, "rows"))
 
 
 def logit_rules_argmax(rules: LogitRules, logits, tokens, values, out=None, ws=None, stream=None):
@@ -259,10 +272,10 @@ def mtp_token_counts(counts, tokens, prompt=False, ws=None, stream=None):
     dev = _device()
     if counts.dtype not in (_I32, torch.uint32):
         raise TypeError("mtp_token_counts: counts holds 32-bit words")
+    vocab, n = _int(counts.numel(), "counts"), _int(tokens.numel(), "tokens")
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
-    n = tokens.numel()
-    check(L.load().mtp_token_counts(_ptr(counts, counts.dtype, 1, "counts", dev), counts.numel(),
+    check(L.load().mtp_token_counts(_ptr(counts, counts.dtype, 1, "counts", dev), vocab,
                                     _ptr(tokens, _I32, n, "tokens", dev), n, int(bool(prompt)), *_ws(ws, dev),
                                     _on(stream, dev)), "mtp_token_counts")
     return ws
@@ -273,7 +286,7 @@ def mtp_tree_accept(parents, tokens, verify, path, emitted, count, stream=None):
     """The accepted path of a tree: nodes into ``path [n]``, the verifier's tokens on it into
     ``emitted [n]`` (both -1 past the end), their number into ``count [1]``."""
     dev = _device()
-    n = parents.numel()
+    n = _int(parents.numel(), "parents")
     check(L.load().mtp_tree_accept(
         _ptr(parents, _I32, n, "parents", dev), _ptr(tokens, _I32, n, "tokens", dev),
         _ptr(verify, _I32, n, "verify", dev), n, _ptr(path, _I32, n, "path", dev),
@@ -297,7 +310,7 @@ def kv_caches(k_caches, v_caches) -> KvCaches:
     vs = (L.vp * n)(*[_ptr(v, _F32, 1, "v_cache", dev) for v in v_caches])
     if len({*ks, *vs}) != 2 * n:
         raise ValueError("kv_caches: a cache is given twice")
-    c = KvCaches(ks, vs, n, nkv, dqk, dv, cap)
+    c = KvCaches(ks, vs, n, nkv, dqk, dv, _int(cap, "cap"))
     c.tensors, c.device = (k_caches, v_caches, ks, vs), dev
     return c
 
@@ -308,7 +321,7 @@ def kv_tree_commit(caches: KvCaches, path, cache_len, ws=None, stream=None):
     _here(caches, dev)
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
-    n = path.numel()
-    check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, int(cache_len),
+    n = _int(path.numel(), "path")
+    check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, _int(cache_len, "cache_len"),
                                   *_ws(ws, dev), _on(stream, dev)), "kv_tree_commit")
     return ws

@@ -163,3 +163,43 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
             assert not lib.calls, (key, name)
     with pytest.raises(ValueError):  # a tree whose positions are elsewhere
         W.draft_tree(_Tensor(1, i64, 3), _Tensor(1, i32, 3), on0["ax"])
+
+
+def test_numbers_past_32_bits_are_refused(monkeypatch):
+    """The library takes 32-bit lengths and head strides: a longer one is refused, not cut off."""
+    import torch
+    from mtp_speculative_draft_gb300 import _lib, tree as W
+    i32, i64, f32, u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+    lib, big = _Lib(), 1 << 32
+    monkeypatch.setattr(W, "_device", lambda: 0)
+    monkeypatch.setattr(W, "_on", lambda stream, device: None)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+    n, ws, k = _Tensor(0, i32, 3), _Tensor(0, u8, 4096), _Tensor(0, f32, 1, 20, 64)
+    v = _Tensor(0, f32, 1, 20, 64)
+    v.data_ptr = lambda: 0x200000
+    ax = W.rope_axes((32,), _Tensor(0, i32, 1, 3), _Tensor(0, f32, 10, 32, 2))
+    tree, caches, r = W.draft_tree(_Tensor(0, i64, 3), n), W.kv_caches([k], [v]), _Tensor(0, f32, 3, 64)
+    g = _lib.AttnGeom(1, 1, 64, 64, 64, 0, 0, 1e-6, 0.0)
+    wide = _Tensor(0, f32, 3, 2, 64, stride=(64, big + 128, 1))
+    for call in (lambda: W.attn_tree_sink(g, tree, r, r, r, None, None, None, None, k, v, big + 5, r, ws),
+                 lambda: W.attn_tree_sink_workspace_bytes(g, 3, big + 5),
+                 lambda: W.attn_tree_sink_workspace_bytes(g, big + 3, 5),
+                 lambda: W.kv_tree_commit(caches, n, big + 5, ws),
+                 lambda: W.draft_tree(_Tensor(0, i64, 3), n, None, big),
+                 lambda: W.logit_rules(big + 100),
+                 lambda: W.logit_rules(100, bias_tokens=_Tensor(0, i32, big + 1), bias=_Tensor(0, f32, big + 1)),
+                 lambda: W.logit_rules(100, path_tokens=_Tensor(0, i32, big + 1), path_mask=_Tensor(0, i64, 1)),
+                 lambda: W.logit_rules(100, allow=_Tensor(0, i32, 1, big + 4)),
+                 lambda: W.logit_rules_argmax_workspace_bytes(big + 4),
+                 lambda: W.mtp_token_counts(_Tensor(0, i32, big + 9), n, False, ws),
+                 lambda: W.mtp_token_counts(n, _Tensor(0, i32, big + 9), False, ws),
+                 lambda: W.mtp_tree_accept(*[_Tensor(0, i32, big + 9)] * 6),
+                 lambda: W.mtp_tree_plan(_Tensor(0, i32, big + 9), _Tensor(0, i64, big + 9), _Tensor(0, i32, big + 9), ws),
+                 lambda: W.rope_axes((32,), _Tensor(0, i32, 1, big + 3), _Tensor(0, f32, 10, 32, 2)),
+                 lambda: W.rope_axes((big + 32,), _Tensor(0, i32, 1, 3), _Tensor(0, f32, big + 32, 2)),
+                 lambda: W.rope_axes_rows(ax, [(wide, wide, None)], ws)):
+        with pytest.raises(ValueError):
+            call()
+    assert not lib.calls
+    # a longer table is no fault
+    assert W.rope_axes((1,), _Tensor(0, i32, 1, 3), _Tensor(0, f32, big + 1, 2)).max_pos == (1 << 31) - 1
