@@ -383,7 +383,7 @@ mtp_status mtp_token_counts(uint32_t* d_counts, int32_t vocab, const int32_t* d_
     return fail(MTP_ERR_INVALID_ARG, "mtp_token_counts: vocab and n must be >= 1, prompt 0 or 1");
   if (!d_ws || !aligned16(d_ws) || ws_bytes < sizeof(WsHeader))
     return fail(MTP_ERR_WORKSPACE, "mtp_token_counts: workspace too small or misaligned");
-  cudaError_t e = launch_pdl(token_counts_kernel, dim3((n + 255) / 256), 256, 0,
+  cudaError_t e = launch_pdl(token_counts_kernel, dim3((n - 1) / 256 + 1), 256, 0,
                              static_cast<cudaStream_t>(stream), d_counts, vocab, d_tokens, n, prompt,
                              &static_cast<WsHeader*>(d_ws)->err);
   if (e != cudaSuccess) return cuda_fail(e, "mtp_token_counts launch");

@@ -74,3 +74,14 @@ def test_rotation_of_head_major_rows(dev, rows, d, half):  # noqa: F811
                     tq.transpose(0, 1).as_strided((rows, nh, d), (d, (rows - 1) * d, 1))):     # heads overlap
             with pytest.raises(M._lib.MtpError):
                 M.rope_axes_rows(M.rope_axes((half,), up(pos), table), [(bad, y, None)])
+
+
+def test_token_counts_of_the_longest_list(dev):  # noqa: F811
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    n = (1 << 31) - 1
+    tokens = torch.full((n,), -1, dtype=torch.int32, device=dev)
+    tokens[0], tokens[n - 257], tokens[n - 1] = 3, 4, 3
+    counts = torch.zeros(9, dtype=torch.int32, device=dev)
+    ws = M.mtp_token_counts(counts, tokens)
+    assert counts.tolist() == [0, 0, 0, 2, 1, 0, 0, 0, 0] and M.mtp_workspace_status(ws) == 0
