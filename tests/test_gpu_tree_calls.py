@@ -85,3 +85,57 @@ def test_token_counts_of_the_longest_list(dev):  # noqa: F811
     counts = torch.zeros(9, dtype=torch.int32, device=dev)
     ws = M.mtp_token_counts(counts, tokens)
     assert counts.tolist() == [0, 0, 0, 2, 1, 0, 0, 0, 0] and M.mtp_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("eps,scale", [(1e-2, 0.0), (1e-6, 0.3), (0.0, 0.02)])
+def test_attention_with_other_scales_and_sections(dev, inter, eps, scale):  # noqa: F811
+    """``eps`` and ``scale`` of the geometry, and sections one after another."""
+    import test_gpu_tree as G
+    from helpers import assert_close
+    from mtp_speculative_draft_gb300 import attn_geom, rope_axes
+    c = G._attn_case(5, nh=6, nkv=2, dqk=96, dv=64, L=150, n=7, axes=(14, 6, 10), rot=60)
+    c["qp"] *= np.float32(0.1)  # eps 0.01 counts
+    c["kp"] *= np.float32(0.1)
+    call = G.Call(c, dev)
+    call.g = attn_geom(6, 2, 96, 64, 60, eps=eps, scale=scale)
+    pos, table = call.tree.tensors[2].tensors
+    ax = rope_axes((14, 6, 10), pos, table, interleaved=inter)
+    call.tree = __import__("mtp_speculative_draft_gb300").draft_tree(*call.tree.tensors[:2], ax)
+    call()
+    q = T.rope_axes(T.head_norm(c["qp"].reshape(7, 6, 96), c["qn"], eps), c["pos"], (14, 6, 10), inter, 1e4)
+    k = T.rope_axes(T.head_norm(c["kp"].reshape(7, 2, 96), c["kn"], eps), c["pos"], (14, 6, 10), inter, 1e4)
+    ref = T.tree_attention(q, c["kc"], c["vc"], k, c["vp"].reshape(7, 2, 64), c["mask"], c["depth"],
+                           scale=scale if scale else None)
+    # logits of three times the usual size at scale 0.3 (1 / sqrt(96) is 0.1)
+    assert_close(call.out.cpu().numpy(), ref.reshape(7, -1), "out", 3 * G.ATTN_TOL)
+
+
+def test_first_call_of_a_process_is_captured(dev):  # noqa: F811
+    """Each call's first launch in a process may be under capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import numpy as np, torch
+import test_gpu_tree as G
+import mtp_speculative_draft_gb300 as M
+dev = torch.device("cuda:0")
+torch.zeros(1, device=dev)
+for kw in (dict(nh=8, nkv=2, dqk=64, dv=64), dict(nh=4, nkv=2, dqk=160, dv=128), dict(nh=4, nkv=2, dqk=64, dv=160)):
+    call = G.Call(G._attn_case(3, L=300, n=5, norm=False, rot=0, **kw), dev)
+    x, tok, val = torch.randn(2, 9000, device=dev), torch.zeros(2, dtype=torch.int32, device=dev), torch.zeros(2, device=dev)
+    rules, ws = M.logit_rules(9000), M.workspace(M.logit_rules_argmax_workspace_bytes(2))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        M.logit_rules_argmax(rules, x, tok, val, None, ws)
+    g.replay()
+    call.check()
+    assert (tok == x.argmax(1)).all()
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTHONPATH": os.pathsep.join([here, os.path.dirname(here)])}
+    done = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]

@@ -12,8 +12,8 @@ high part is off by 2^-11 of the value at most, the low part by 2^-11 of that):
 * the output: the weights' errors times |v| + |o| (numerator and denominator), and relative to the sum
   of magnitudes: pairs of P and V and their left out product (3 h), 3 * 4 tensor-core steps a tile (17 u
   each), a move of the reference a tile (h), the sums over T tiles and over the splits (u each), three
-  exponentials of merging (h) and at most 40 further roundings (u); a weight below 2^-33 of the largest
-  may be lost in its pair.
+  exponentials of merging (h) and at most 40 further roundings (u); a weight's pair has an absolute error
+  of 2^-25, where the largest weight is 2^8 at least, and none above the weight itself: min(p, 2^-33).
 
 Terms of second order are covered by a tenth on top.
 """
@@ -53,7 +53,7 @@ def exact_and_bound(c, splits, tiles):
         rel = H * (3 + 3 + tiles) + U * (12 * 17 + tiles + splits + 40)
         mags = p @ av
         bound[g] = 1.1 * ((p * eps) @ av + (p * eps).sum(1, keepdims=True) * np.abs(o) + rel * (mags + np.abs(o)) +
-                          (2.0 ** -33 * (L + n) + 2.0 ** -38) * av.max())
+                          np.minimum(p, 2.0 ** -33) @ av + 2.0 ** -38 * av.max())
         out[g] = o
     order = lambda x: x.reshape(nkv, n, G, dv).transpose(1, 0, 2, 3).reshape(n, nh * dv)  # noqa: E731
     return order(out), order(bound)
@@ -139,3 +139,14 @@ def test_attention_and_rules_share_a_workspace_in_turn(dev):  # noqa: F811
         call.out.fill_(7.0)
         call()
         call.check(f"after rules of {rows} rows")
+
+
+@pytest.mark.parametrize("dqk,dv", [(64, 64), (64, 160)])
+def test_a_row_far_larger_than_its_tile(dev, dqk, dv):  # noqa: F811
+    """A key that no query looks at (its logit is far below the others') with a K row 2^20 and a V row 2^24 times
+    its tile's: the tile's other values keep an absolute error of 2^-39 of the largest, which the bound counts."""
+    c = _attn_case(41, nh=8, nkv=8, dqk=dqk, dv=dv, L=200, n=3, rot=0, norm=False)
+    c["qp"] = np.abs(c["qp"])
+    c["kc"][:, 70] = -2.0 ** 20
+    c["vc"][:, 70] *= np.float32(2.0 ** 24)
+    check(Call(c, dev), 19, 4)
