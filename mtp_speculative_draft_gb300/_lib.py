@@ -74,6 +74,7 @@ class SpecStats(C.Structure):
 
 
 class RopeAxes(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
     _fields_ = [("d_pos", vp), ("d_rope", vp), ("n_axes", i32), ("section", i32 * 4),
                 ("interleaved", i32), ("pos_ld", i32), ("max_pos", i32)]
 
@@ -84,11 +85,13 @@ class HeadRows(C.Structure):
 
 
 class DraftTree(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
     _fields_ = [("d_mask", vp), ("d_depth", vp), ("axes", C.POINTER(RopeAxes)), ("n", i32),
                 ("pos_base", i32), ("ld_q", C.c_int64), ("ld_k", C.c_int64), ("ld_v", C.c_int64)]
 
 
 class LogitRules(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
     _fields_ = [("vocab", i32), ("repetition", f32), ("frequency", f32), ("presence", f32),
                 ("d_counts", vp), ("d_bias_tokens", vp), ("d_bias", vp), ("n_bias", i32),
                 ("d_allow", vp), ("allow_ld", i32), ("d_path_tokens", vp), ("d_path_mask", vp),
@@ -96,6 +99,7 @@ class LogitRules(C.Structure):
 
 
 class KvCaches(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
     _fields_ = [("h_k", C.POINTER(vp)), ("h_v", C.POINTER(vp)), ("n_layers", i32),
                 ("n_kv_heads", i32), ("head_dim_qk", i32), ("head_dim_v", i32), ("cache_cap", i32)]
 

@@ -84,7 +84,7 @@ def _ws(ws, device):
 def _here(desc, device):
     """Refuses a descriptor whose tensors are on another device than the current one (one that a program filled
     in by itself has no device)."""
-    if getattr(desc, "device", device) != device:
+    if desc.device not in (None, device):
         raise ValueError(f"{type(desc).__name__}: its tensors are on device {desc.device}, the current one is {device}")
 
 
@@ -114,7 +114,8 @@ def rope_axes_rows(axes: RopeAxes, tensors, ws=None, eps=1e-6, stream=None):
     ``[rows, heads, head_dim]`` (any row and head stride, contiguous head rows; y may be x) and
     norm_w ``[head_dim]`` or None."""
     dev = _device()
-    _here(axes, dev)
+    if axes.device != dev:
+        _here(axes, dev)
     lib = L.load()
     rows, _, d = tensors[0][0].shape
     descs = []
@@ -165,7 +166,9 @@ def mtp_tree_workspace_bytes() -> int:
 def mtp_tree_plan(parents, mask, depth, ws=None, stream=None):
     """Ancestor words and depths of a tree from its ``parents [n]`` (int32, -1 for a root)."""
     dev = _device()
-    n = _int(parents.numel(), "parents")
+    n = parents.numel()
+    if n > _MOST:
+        _int(n, "parents")
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     if mask.dtype not in (torch.int64, torch.uint64):
@@ -186,8 +189,10 @@ def attn_tree_sink(g: AttnGeom, tree: DraftTree, qp, kp, vp, q_norm, k_norm, rop
     """Attention of a tree's rows ``qp [n, q_rows]``, ``kp``, ``vp`` (any row stride) over the cache
     ``[n_kv, cap, dim]`` and their ancestors; appends the rows at ``cache_len`` onwards."""
     dev = _device()
-    _here(tree, dev)
-    cache_len = _int(cache_len, "cache_len")
+    if tree.device != dev:
+        _here(tree, dev)
+    if type(cache_len) is not int or not -_MOST <= cache_len <= _MOST:
+        cache_len = _int(cache_len, "cache_len")
     lib = L.load()
     n, nh, nkv, dqk, dv = tree.n, g.n_heads, g.n_kv_heads, g.head_dim_qk, g.head_dim_v
     pq, ldq = _rows(qp, n, nh * dqk * (2 if g.gated_q else 1), "qp", dev)
@@ -251,7 +256,8 @@ def logit_rules_argmax(rules: LogitRules, logits, tokens, values, out=None, ws=N
     """Applies ``rules`` to ``logits [rows, vocab]`` (any row stride) and takes each row's argmax;
     ``out`` (or ``logits`` itself) receives the final logits."""
     dev = _device()
-    _here(rules, dev)
+    if rules.device != dev:
+        _here(rules, dev)
     lib = L.load()
     rows = logits.shape[0]
     if rows > rules.rows:
@@ -286,7 +292,9 @@ def mtp_tree_accept(parents, tokens, verify, path, emitted, count, stream=None):
     """The accepted path of a tree: nodes into ``path [n]``, the verifier's tokens on it into
     ``emitted [n]`` (both -1 past the end), their number into ``count [1]``."""
     dev = _device()
-    n = _int(parents.numel(), "parents")
+    n = parents.numel()
+    if n > _MOST:
+        _int(n, "parents")
     check(L.load().mtp_tree_accept(
         _ptr(parents, _I32, n, "parents", dev), _ptr(tokens, _I32, n, "tokens", dev),
         _ptr(verify, _I32, n, "verify", dev), n, _ptr(path, _I32, n, "path", dev),
@@ -318,10 +326,13 @@ def kv_caches(k_caches, v_caches) -> KvCaches:
 def kv_tree_commit(caches: KvCaches, path, cache_len, ws=None, stream=None):
     """Moves the rows of ``path [n]`` (nodes of the tree, -1 past the end) to ``cache_len`` onwards."""
     dev = _device()
-    _here(caches, dev)
+    if caches.device != dev:
+        _here(caches, dev)
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
-    n = _int(path.numel(), "path")
-    check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, _int(cache_len, "cache_len"),
+    n = path.numel()
+    if n > _MOST or type(cache_len) is not int or not -_MOST <= cache_len <= _MOST:
+        n, cache_len = _int(n, "path"), _int(cache_len, "cache_len")
+    check(L.load().kv_tree_commit(C.byref(caches), _ptr(path, _I32, n, "path", dev), n, cache_len,
                                   *_ws(ws, dev), _on(stream, dev)), "kv_tree_commit")
     return ws

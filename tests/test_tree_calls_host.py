@@ -184,7 +184,8 @@ def test_numbers_past_32_bits_are_refused(monkeypatch):
     for call in (lambda: W.attn_tree_sink(g, tree, r, r, r, None, None, None, None, k, v, big + 5, r, ws),
                  lambda: W.attn_tree_sink_workspace_bytes(g, 3, big + 5),
                  lambda: W.attn_tree_sink_workspace_bytes(g, big + 3, 5),
-                 lambda: W.kv_tree_commit(caches, n, big + 5, ws),
+                 lambda: W.attn_tree_sink(g, tree, r, r, r, None, None, None, None, k, v, 5 - big, r, ws),
+                 lambda: W.kv_tree_commit(caches, n, big + 5, ws), lambda: W.kv_tree_commit(caches, n, 5 - big, ws),
                  lambda: W.draft_tree(_Tensor(0, i64, 3), n, None, big),
                  lambda: W.logit_rules(big + 100),
                  lambda: W.logit_rules(100, bias_tokens=_Tensor(0, i32, big + 1), bias=_Tensor(0, f32, big + 1)),
