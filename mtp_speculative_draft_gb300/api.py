@@ -60,7 +60,8 @@ def affine4_bf16_scales(q: torch.Tensor, s: torch.Tensor, b: torch.Tensor) -> Af
 def workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
     """A cleared workspace of ``nbytes`` bytes (uint8 device tensor), from the allocator's pool of the stream
     that uses it (``stream``, or the current one)."""
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+    on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+    with contextlib.nullcontext() if on is None else torch.cuda.stream(on):
         ws = torch.empty(max(int(nbytes), 1024), dtype=torch.uint8, device=device)
     mtp_workspace_init(ws, stream)
     return ws

@@ -74,10 +74,13 @@ def test_a_call_that_makes_its_workspace_makes_it_on_its_stream(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", On)
     monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(current[-1]))
     monkeypatch.setattr(api, "mtp_workspace_init", lambda ws, stream=None: None)
-    side = object()
+    monkeypatch.setattr(torch.cuda, "Stream", type("Stream", (), {}))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    side, handle = torch.cuda.Stream(), type("Handle", (), dict(cuda_stream=7))()  # any object with a cudaStream_t
     api.workspace(5000, stream=side)
     api.workspace(5000)
-    assert made == [side, None]
+    api.workspace(5000, stream=handle)
+    assert made == [side, None, ("external", 7)]
 
 
 class _Tensor:
