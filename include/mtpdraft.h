@@ -600,10 +600,15 @@ typedef struct {
  *   query heads a KV head.  d_rope: table with rope_rows rows,
  *   pos_base + cache_len + n of them needed (not read when tree->axes is given
  *   or rot_dim is 0).  d_out [n][n_heads*head_dim_v].
- *   Accuracy: q, K and V enter as 22-bit operands (f16 high and low parts, a
- *   power-of-two scale for each query row and each tile of 32 or 64 cached keys;
- *   elements below 2^-39 of a tile's largest count as 0), sums are float32.
- *   Infinity or NaN in a K or V row that a node sees gives NaN.
+ *   Accuracy: q, K, V and the weights enter the products with cached keys as
+ *   22-bit operands (f16 high and low parts, a power-of-two scale for each query
+ *   row and each tile of 32 or 64 cached keys), sums are float32.  An element
+ *   keeps its 22 bits down to 2^-16 of its row's or tile's largest and has an
+ *   absolute error of 2^-39 of that largest below (a V row 2^24 times its tile's
+ *   others leaves them 15 bits); a weight's absolute error is 2^-33 of the
+ *   largest weight.  New rows and the keys at a window's edge are read as float32.
+ *   NaN in a K or V row that a node sees gives NaN.  Infinity gives NaN in a
+ *   cached row that all nodes see, and what the formula gives in the others.
  * ------------------------------------------------------------------------ */
 /* Enough for every call of up to n nodes and cache_len cached keys. */
 size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n, int32_t cache_len);
@@ -623,7 +628,9 @@ typedef struct {
                                       the prompt, low 31 bits: times it was generated */
     const int32_t *d_bias_tokens;  /* [n_bias] (ids outside the vocabulary are ignored) */
     const float *d_bias;           /* [n_bias]: added; entries of one token sum in list order */
-    int32_t n_bias;                /* 0..65536 */
+    int32_t n_bias;                /* 0..65536; more than 128 entries among 2048 tokens that start at a
+                                      multiple of 2048 cost a scan of the list for each of these tokens
+                                      (10000 entries over 152k tokens: 1 to 2 ms, 65536: 20 ms) */
     const uint32_t *d_allow;       /* mask [rows][allow_ld]: token v allowed when bit v%32 of word
                                       v/32 is set; NULL: all allowed */
     int32_t allow_ld;              /* words per row, >= ceil(vocab/32); 0: one row for all */

@@ -26,7 +26,10 @@ constexpr int kRuleChunk = kRuleThreads * kRulePer;  // tokens a CTA
 // 38, 5 gave 36, one row a CTA 39; 16 x 151936: 13 us against 13, 16 and 16; with
 // the mask words handed over too, 3 gives 30 us).
 constexpr int kRuleCtas = 3;
-constexpr int kRuleHits = 128;                       // bias entries of a chunk kept at hand
+// Bias entries of a chunk kept at hand.  With more, each biased token of the chunk scans the whole list: 64 rows
+// of 151936 tokens take 27, 29 and 43 us with 300, 1000 and 5000 entries, and 1.8, 5.9 and 22 ms with 10000, 30000
+// and 65536 (the torch form: 0.65 ms whatever the list).
+constexpr int kRuleHits = 128;
 constexpr int kRuleRows = 16;                        // rows a CTA, at most
 
 struct RuleArgs {

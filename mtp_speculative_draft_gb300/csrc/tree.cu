@@ -93,7 +93,9 @@ struct CommitArgs {
 };
 
 // grid (KV heads, layers, K or V); one thread a 16-byte column.  Path entries
-// satisfy path[j] >= j, so a row is read before any later step writes it.
+// satisfy path[j] >= j, so a row is read before any later step writes it.  Rows
+// go one after another, each a read from memory behind the last one's write:
+// 48 layers of 8 heads of 2 x 128 take 5, 12 and 19 us for 5, 32 and 60 rows.
 __global__ void __launch_bounds__(64) kv_commit_kernel(const __grid_constant__ CommitArgs a) {
   pdl_wait();
   pdl_launch_dependents();

@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prep_kernel(const __grid_co
 // column (16 keys: 8 columns of hi parts, 8 of lo parts), and Q hi and lo lie
 // behind the outputs (Q lo in shared memory where they do not fit).
 //
-// Measured: 40/8 heads of 128, 64 nodes, 32768 keys: 172 us, 3.7k cycles a tile of
-// 64 keys x 128 rows, of which the tensor pipe works 1.5k (its three products are
-// 77 us at 1967 TFLOP/s); the chain scores -> weights -> P V -> output of a
+// Measured: 40/8 heads of 128, 64 nodes, 32768 keys: 170 us, 3.7k cycles a tile of
+// 64 keys x 128 rows, of which the tensor pipe works 1.5k (its three products of
+// three row tiles are 81 us at 1904 TFLOP/s); the chain scores -> weights -> P V -> output of a
 // warpgroup's tile bounds it (issue slots 51 %).  16 nodes: 72 us, 3.7 TB/s of
 // cache.  A tile is 64 keys, as two of them, their raw rows and the states fit
 // beside 512 tensor-memory columns (32 where a head size passes 128).
@@ -999,7 +999,8 @@ struct TreePlan {
 static int split_nk(int dqk, int dv) { return dqk <= 128 && dv <= 128 ? 64 : 32; }
 
 // Keys of a split at least: 32, 64 and 128 take 32.6, 32.1 and 36.9 us on 2047 keys
-// of two heads of 256 dims; 64 writes half of 32's partials.
+// of two heads of 256 dims; 64 writes half of 32's partials (and leaves SMs without
+// a split there: 64 splits for 152).
 constexpr int kMinKeys = 64;
 
 // Cached keys that all rows can see: a window's rows have at most window - 1 in

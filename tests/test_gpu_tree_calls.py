@@ -139,3 +139,28 @@ for kw in (dict(nh=8, nkv=2, dqk=64, dv=64), dict(nh=4, nkv=2, dqk=160, dv=128),
     env = {**os.environ, "PYTHONPATH": os.pathsep.join([here, os.path.dirname(here)])}
     done = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_infinities_in_visible_rows(dev):  # noqa: F811
+    """In a new row what the formula gives (a logit of -inf has weight 0), in a cached row that all see NaN."""
+    import test_gpu_tree as G
+    from helpers import assert_close
+    c = G._attn_case(6, nh=4, nkv=2, dqk=64, dv=64, L=100, n=5, rot=0, norm=False, tree="chain")
+    c["qp"] = np.abs(c["qp"])
+    c["kp"][2, 3] = -np.inf   # KV head 0: nodes 2 to 4 see node 2 with weight 0
+    c["vp"][3, 64 + 7] = np.inf  # KV head 1, column 7: infinite for nodes 3 and 4
+    call = G.Call(c, dev)
+    call()
+    got = call.out.cpu().numpy()
+    q, k = c["qp"].reshape(5, 4, 64), c["kp"].reshape(5, 2, 64)
+    ref = T.tree_attention(q, c["kc"], c["vc"], k, c["vp"].reshape(5, 2, 64), c["mask"], c["depth"]).reshape(5, -1)
+    far = np.zeros((5, 4, 64), bool)
+    far[3:, 2:, 7] = True
+    far = far.reshape(5, -1)
+    assert (ref[far] == np.inf).all() and (got[far] == np.inf).all() and np.isfinite(got[~far]).all()
+    assert_close(got[~far], ref[~far], "the rest", G.ATTN_TOL)
+    c["kc"][1, 50, 9] = -np.inf
+    call = G.Call(c, dev)
+    call()
+    got = call.out.cpu().numpy().reshape(5, 4, 64)
+    assert np.isnan(got[:, 2:]).all() and np.isfinite(got[:, :2]).all()
