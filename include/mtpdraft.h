@@ -41,8 +41,8 @@
  *    workspace must be cleared once with mtp_workspace_init(); kernels leave
  *    what calls of their kind need cleared in that state again when they
  *    finish.  A workspace passes to another kind of call after another
- *    mtp_workspace_init(); the calls of a draft tree's round (at the end of
- *    this file) may share one in any order.  Calls that share a workspace
+ *    mtp_workspace_init(); the calls of a draft tree's round and of a beam
+ *    search's step (at the end of this file) may share one in any order.  Calls that share a workspace
  *    must not overlap on the GPU.
  */
 #ifndef MTPDRAFT_H
@@ -90,10 +90,12 @@ mtp_status mtp_workspace_init(void *d_ws, size_t bytes, void *stream);
  *   for the previous projection's output gave up; 4 a wait of the attention
  *   splits of a KV head for each other's partials gave up;
  *   5 a draft tree's parent, depth or path entry outside its range (see the
- *   call); 6 a rotary position outside the table (position 0 was used).
+ *   call); 6 a rotary position outside the table (position 0 was used);
+ *   7 a length or parent of a batch of sequences outside its range (see the
+ *   call).
  * After code 1, 3 or 4 a launch stopped part-way (its outputs are not
  * valid) and may have left completion counters set: clear the workspace
- * with mtp_workspace_init() before its next use.  Codes 2, 5 and 6 leave the
+ * with mtp_workspace_init() before its next use.  Codes 2, 5, 6 and 7 leave the
  * workspace usable.  The waits behind codes 3 and 4 need every CTA of the
  * launch resident at once (the launches size their grids for that); a
  * device shared with other work at the same time can make them give up, so
@@ -690,6 +692,70 @@ typedef struct {
  * the move.  The caller's cache length becomes cache_len + the accepted count. */
 mtp_status kv_tree_commit(const mtp_kv_caches *caches, const int32_t *d_path, int32_t n,
                           int32_t cache_len, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Beams.  A step of a beam search, or of several samples of one prompt: the
+ * sequences of a prompt share its K/V rows (prefix), which are kept and read
+ * once, and have tails of their own.  The target's forward of the new rows uses
+ * attn_prefix_sink in every layer, the head gives logits (logit_rules_argmax
+ * corrects them), beam_select takes the best extensions, kv_beam_reorder gives
+ * the survivors their tails.  Lengths stay on the device, so a step can be
+ * captured once and replayed.
+ * ------------------------------------------------------------------------ */
+
+/* New rows of sequences that share prompts: sequence b continues prompt
+ * b / (n_seqs/n_groups). */
+typedef struct {
+    const int32_t *d_prefix_len; /* [n_groups] rows of each prompt, 0..prefix_max (may be NULL when
+                                    prefix_max is 0) */
+    const int32_t *d_tail_len;   /* [n_seqs] rows of each tail before the call, ..tail_max; negative:
+                                    no sequence (nothing is appended, its output rows stay as they
+                                    are).  A length above its range, or a negative prompt, sets device
+                                    error 7 and the nearest value is used */
+    const mtp_rope_axes *axes;   /* rotary positions (row b*m + i for new row i of sequence b) and table,
+                                    or NULL: the row rotates at pos_base + prefix + tail + i in the call's
+                                    table */
+    int32_t n_groups;            /* 1.. */
+    int32_t n_seqs;              /* ..1024, a multiple of n_groups */
+    int32_t m;                   /* new rows a sequence, 1..16 (a chain of drafts; 1 for beams) */
+    int32_t prefix_max, tail_max; /* the most rows that a prompt and a tail may have in this call: they
+                                    size the launches, so a close bound is faster than a loose one */
+    int32_t pos_base;
+    int64_t ld_q, ld_k, ld_v;    /* row strides of d_qp, d_kp, d_vp in floats (multiples of 4),
+                                    0 for contiguous rows */
+} mtp_prefix_batch;
+
+/* ------------------------------------------------------------------------
+ * attn_prefix_sink: attn_decode_sink for the m new rows of each sequence of a
+ * batch.  New row i of sequence b, at position P + t + i (P, t: the lengths of
+ * its prompt and tail), sees the prompt's rows and the tail's rows up to its
+ * own, inside a window W those at positions above P + t + i - W; a row that it
+ * does not see has no effect on it, whatever it holds.
+ *   geometry, norms, sinks, gate: as attn_decode_sink; up to 64 query heads a KV
+ *   head.  d_qp [n_seqs*m][q_rows], d_kp, d_vp, d_out [n_seqs*m][n_heads*dv]:
+ *   row b*m + i.  d_rope: table with rope_rows rows, pos_base + prefix_max +
+ *   tail_max + m of them needed (not read when batch->axes is given or rot_dim
+ *   is 0).
+ *   d_k_prefix, d_v_prefix [n_groups][n_kv][prefix_cap][dim]: read.
+ *   d_k_tail, d_v_tail [n_seqs][n_kv][tail_cap][dim]: rows below a tail's length
+ *   are read, the m new ones written behind them; others stay as they are.
+ *   The lengths are the caller's to advance.
+ *   Accuracy: prompt rows that all of a prompt's sequences see enter as 22-bit
+ *   operands, as attn_tree_sink's cached keys do (its statement holds, with the
+ *   prompt's sequences for a tree's nodes); other rows are read as float32.  NaN
+ *   in a K or V row that a row sees gives NaN there; NaN or infinity in a prompt
+ *   row gives NaN for all of the prompt's sequences that see it.
+ * ------------------------------------------------------------------------ */
+/* Enough for every call of up to these sizes (and any lengths of tails). */
+size_t attn_prefix_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n_groups, int32_t n_seqs,
+                                        int32_t m, int32_t prefix_max);
+mtp_status attn_prefix_sink(const mtp_attn_geom *g, const mtp_prefix_batch *batch,
+                            const float *d_qp, const float *d_kp, const float *d_vp,
+                            const float *d_q_norm, const float *d_k_norm, const float *d_rope,
+                            int32_t rope_rows, const float *d_sinks, const float *d_k_prefix,
+                            const float *d_v_prefix, int32_t prefix_cap, float *d_k_tail,
+                            float *d_v_tail, int32_t tail_cap, float *d_out, void *d_ws,
+                            size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -16,5 +16,8 @@ from .tree import (  # noqa: F401
     logit_rules_argmax, logit_rules_argmax_workspace_bytes, mtp_token_counts, mtp_tree_accept,
     mtp_tree_plan, mtp_tree_workspace_bytes, rope_axes, rope_axes_rows, rope_axes_rows_workspace_bytes,
 )
+from .beams import (  # noqa: F401
+    attn_prefix_sink, attn_prefix_sink_workspace_bytes, prefix_batch,
+)
 from ._lib import MimoLayerState, SpecStats  # noqa: F401
 from .layer import DraftLayer, DraftChain  # noqa: F401

@@ -104,6 +104,13 @@ class KvCaches(C.Structure):
                 ("n_kv_heads", i32), ("head_dim_qk", i32), ("head_dim_v", i32), ("cache_cap", i32)]
 
 
+class PrefixBatch(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
+    _fields_ = [("d_prefix_len", vp), ("d_tail_len", vp), ("axes", C.POINTER(RopeAxes)), ("n_groups", i32),
+                ("n_seqs", i32), ("m", i32), ("prefix_max", i32), ("tail_max", i32), ("pos_base", i32),
+                ("ld_q", C.c_int64), ("ld_k", C.c_int64), ("ld_v", C.c_int64)]
+
+
 class StepOut(C.Structure):
     _fields_ = [("d_token", vp), ("d_value", vp), ("d_hidden_out", vp), ("d_u2", vp),
                 ("d_logits", vp)]
@@ -162,6 +169,9 @@ EXPORTS = {
     "mtp_token_counts": (C.c_int, [vp, i32, vp, i32, i32, vp, sz, vp]),
     "mtp_tree_accept": (C.c_int, [vp, vp, vp, i32, vp, vp, vp, vp]),
     "kv_tree_commit": (C.c_int, [C.POINTER(KvCaches), vp, i32, i32, vp, sz, vp]),
+    "attn_prefix_sink_workspace_bytes": (sz, [C.POINTER(AttnGeom), i32, i32, i32, i32]),
+    "attn_prefix_sink": (C.c_int, [C.POINTER(AttnGeom), C.POINTER(PrefixBatch), vp, vp, vp, vp, vp, vp,
+                                   i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]),
     "mtp_kv_catch_up_workspace_bytes": (sz, [C.POINTER(LayerDesc), i32]),
     "mtp_kv_catch_up": (C.c_int, [C.POINTER(LayerDesc), vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
 }

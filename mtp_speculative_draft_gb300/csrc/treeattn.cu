@@ -24,17 +24,13 @@
 #include <atomic>
 #include <cmath>
 
-#include "tc5.cuh"
-#include "tree.cuh"
+#include "prefix.cuh"
 
 namespace mtp {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct TreeAttnArgs {
-  int nh, nkv, G, dqk, dv, n, L, window, gated;
-  long long cap;
-  float eps, qscale;  // qscale: logit scale times log2(e)
+struct TreeAttnArgs : SplitArgs {
+  int nh, nkv, G, n, L, window, gated;
+  float eps;
   const float *qp, *kp, *vp, *qn, *kn, *sinks;
   long long ldq, ldk, ldv;
   RopePos rope;
@@ -43,16 +39,8 @@ struct TreeAttnArgs {
   const int* depth;
   float* out;
   float* qf;       // [nkv][R][dqk] scaled queries, row r = i * G + g
-  uint8_t* qt;     // [nkv][mt] tiles of 128 rows: f16 hi parts, then lo parts
-  float* qinv;     // [nkv][mt * 128] power of two that undoes a row's f16 scale
   int* dep;        // [n] depths inside [0, n), then at kTreeMax the largest
-  float* part_o;   // [nkv][ns][R][dv]
-  float2* part_ml; // [nkv][ns][R] running maximum and sum
-  int R, mt;              // query rows of a KV head, tiles of 128 of them
-  int ns, kper;           // splits, keys a split
-  int vstages;            // V tile buffers of the split kernel's COL form (1 or 2)
-  int rep;                // copies of the query rows in a tile (see the split kernel)
-  int* err;
+  int kper;        // keys a split
 };
 
 // First cached key that every row sees (the prep launch has left the depths).
@@ -62,60 +50,15 @@ __device__ __forceinline__ int first_common_key(const TreeAttnArgs& a) {
   return k <= 0 ? 0 : k < a.L ? (int)k : a.L;
 }
 
+// Keys [k0, k1) of a split.
+__device__ __forceinline__ void split_keys(const TreeAttnArgs& a, int, int sp, int& k0, int& k1) {
+  if (a.window > 0) pdl_wait();  // the first key comes from the depths
+  k0 = first_common_key(a) + sp * a.kper;
+  k1 = min(a.L, k0 + a.kper);
+}
+
 // ------------------------------------------------------------------ prep
 constexpr int kPrepThreads = 128;
-
-// Power-of-two scale of values for their f16 parts: the largest |x| lands in
-// [2^14, 2^15), so hi + lo hold 22 bits of every element down to 2^-16 of the
-// largest.  Infinity keeps scale 1; values below 2^-95 are scaled by at most
-// 2^109.  Returns the inverse, exactly.
-__device__ __forceinline__ float f16_scale(float largest, float& scale) {
-  uint32_t e = __float_as_uint(largest) >> 23;
-  e = e == 255u ? 141u : max(e, 32u);
-  scale = __uint_as_float((268u - e) << 23);
-  return __uint_as_float((e - 14u) << 23);
-}
-
-// Byte offset of value c of row r in an operand tile of `rows` rows: blocks of
-// 64 values, rows of 128 bytes, 16-byte chunks swizzled by the row (the layout
-// of a K-major operand with c along K, and of an MN-major one with r along K).
-__device__ __forceinline__ uint32_t tile_off(int r, int c, int rows) {
-  return (uint32_t)((c >> 6) * rows * 128 + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2);
-}
-
-// Writes a query row's f16 hi and lo parts for the split kernel: 16-byte chunks
-// of 8 dims, a chunk's 128 rows consecutive, hi chunks then lo chunks.
-__device__ __forceinline__ void store_q_tile(const TreeAttnArgs& a, const HeadVals& v, int kv, int r,
-                                             int half, int lane) {
-  float mx = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(v.a[j]), fabsf(v.b[j])));
-#pragma unroll
-  for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v.c[j]));
-  float scale;
-  const float inv = f16_scale(warp_max(mx * a.qscale), scale);
-  const int rr = r & 127, tile = r >> 7, rows = 128 / a.rep;
-  __half* hi = reinterpret_cast<__half*>(a.qt + ((size_t)kv * a.mt + tile) * 512 * a.dqk);
-  if (lane == 0) a.qinv[((size_t)kv * a.mt + tile) * 128 + rr] = inv;
-  auto put = [&](int c, float x) {
-    x = x * a.qscale * scale;
-    const __half h = __float2half_rn(x), l = __float2half_rn(x - __half2float(h));
-    for (int i = rr; i < 128; i += rows) {
-      const int at = ((c >> 3) * 128 + i) * 8 + (c & 7);
-      hi[at] = h;
-      hi[128 * a.dqk + at] = l;
-    }
-  };
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (lane + 32 * j < half) {
-      put(lane + 32 * j, v.a[j]);
-      put(lane + 32 * j + half, v.b[j]);
-    }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (2 * half + lane + 32 * j < a.dqk) put(2 * half + lane + 32 * j, v.c[j]);
-}
 
 // One warp an item: n * nh query heads, then n * nkv key heads, then values.
 // Bound by its dependent reads; a row's values are on their way before the
@@ -281,28 +224,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// Two floats in one 64-bit register pair (packed float32 arithmetic).
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Two values as packed f16 hi and lo parts.
 __device__ __forceinline__ void split_f16x2(uint64_t v, uint32_t& hi, uint32_t& lo) {
   const float2 x = unpack2(v);
@@ -315,11 +236,6 @@ __device__ __forceinline__ void split_f16x2(uint64_t v, uint32_t& hi, uint32_t& 
 
 __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ float max16(const float (&v)[16]) {
   float t[8];
@@ -355,27 +271,8 @@ __host__ __device__ constexpr bool split_q_lo_fits(int NK, bool col, int dqk, in
   return split_q_col(NK, col, dv) + dqk <= 512;
 }
 
-// A wait that gives up marks the launch (error 1) and lets every later wait of
-// the thread through, so the barriers below are still met by every thread.
-struct Waiter {
-  int* err;
-  bool dead;
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (!dead && !mbar_wait_bounded(bar, parity)) {
-      dead = true;
-      set_dev_error(err, kErrMbarTimeout);
-    }
-  }
-  // After a wait that gave up (the outputs are not valid): time for copies and
-  // MMAs in flight to land, a few milliseconds, before the memory is freed.
-  __device__ __noinline__ void settle() {
-    if (dead)
-      for (int i = 0; i < 2000; ++i) __nanosleep(1000);
-  }
-};
-
-template <int NK, bool COL>
-__global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const TreeAttnArgs a) {
+template <int NK, bool COL, class Args>
+__global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Args a) {
   extern __shared__ __align__(1024) uint8_t smraw[];
   __shared__ SplitSmem sh;
   const uint32_t base = (smem_u32(smraw) + 1023u) & ~1023u;
@@ -383,8 +280,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int sp = blockIdx.x, mt = blockIdx.y, kv = blockIdx.z;
-  if (a.window > 0) pdl_wait();  // the first key comes from the depths
-  const int k0 = first_common_key(a) + sp * a.kper, k1 = min(a.L, k0 + a.kper);
+  int k0, k1;
+  split_keys(a, kv, sp, k0, k1);
   const int nt = max(0, (k1 - k0 + NK - 1) / NK);  // 0 at a window's end: an empty partial
   const int qb = (a.dqk + 63) / 64, vb = (a.dv + 63) / 64;  // blocks of 64 values
   const uint32_t kpart = (uint32_t)qb * NK * 128, vpart = (uint32_t)vb * NK * 128;
@@ -399,8 +296,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
   auto prefetch = [&](int t) {
     if (t >= nt) return;
     const int row0 = k0 + t * NK, n = min(NK, k1 - row0);
-    l2_prefetch(a.kc + ((size_t)kv * a.cap + row0) * a.dqk, (uint32_t)n * a.dqk * 4);
-    l2_prefetch(a.vc + ((size_t)kv * a.cap + row0) * a.dv, (uint32_t)n * a.dv * 4);
+    l2_prefetch(a.keys + ((size_t)kv * a.cap + row0) * a.dqk, (uint32_t)n * a.dqk * 4);
+    l2_prefetch(a.values + ((size_t)kv * a.cap + row0) * a.dv, (uint32_t)n * a.dv * 4);
   };
   const bool fetcher = tid == 9 * 32;
   if (fetcher)
@@ -472,7 +369,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Tree
     constexpr int SL = NK == 64 ? 1 : 2;  // 16-byte words a lane of a row
     static_assert(RPW * SL == 16, "sixteen words a lane");
     const int d = v ? a.dv : a.dqk, r0 = w4 * RPW;
-    const float* src = v ? a.vc + (size_t)kv * a.cap * a.dv : a.kc + (size_t)kv * a.cap * a.dqk;
+    const float* src = v ? a.values + (size_t)kv * a.cap * a.dv : a.keys + (size_t)kv * a.cap * a.dqk;
     const uint32_t part = v ? vpart : kpart, off = v ? voff : 0u;
     uint64_t* full = v ? sh.vfull : sh.kfull;
     uint64_t* empty = v ? sh.vempty : sh.kempty;
@@ -814,25 +711,6 @@ struct RowState {
   float4 o[H];
 };
 
-__device__ __forceinline__ float4 dims4(const float* row, int d, int lane, int h) {
-  const int c = 128 * h + 4 * lane;
-  return c < d ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
-__device__ __forceinline__ void scale4(float4& v, float f) {
-  v.x *= f;
-  v.y *= f;
-  v.z *= f;
-  v.w *= f;
-}
-
-__device__ __forceinline__ void add4(float4& v, float f, const float4& x) {
-  v.x = fmaf(f, x.x, v.x);
-  v.y = fmaf(f, x.y, v.y);
-  v.z = fmaf(f, x.z, v.z);
-  v.w = fmaf(f, x.w, v.w);
-}
-
 // Cache rows at[0 .. n) (n <= kFinishKeys) against a warp's query row.
 template <int H>
 __device__ __forceinline__ void keys_step(RowState<H>& s, const float4 (&q)[H], const float* kc,
@@ -1077,8 +955,8 @@ static constexpr size_t split_smem(int NK, bool col, int dqk, int dv, int vstage
   return 1024 + kStages * kstage + vstages * vstage + qlo + kConvWarps * kRawBytes;
 }
 
-template <int NK, bool COL>
-static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
+template <int NK, bool COL, class Args>
+static cudaError_t launch_split_as(Args a, int heads, cudaStream_t st) {
   static_assert(kScaleRing >= kStages + 2, "a tile's scale stays until its warpgroup has read it");
   static_assert(sizeof(SplitSmem) <= 2048, "beside the dynamic shared memory");
   // the widest heads of each form (the lo parts are in shared memory at the widest only)
@@ -1096,21 +974,25 @@ static cudaError_t launch_split_as(TreeAttnArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, tree_split_kernel<NK, COL>);
+    e = cudaFuncGetAttributes(&fa, tree_split_kernel<NK, COL, Args>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kSplitRegs) return cudaErrorInvalidKernelImage;  // the shares would wait forever
-    e = cudaFuncSetAttribute(tree_split_kernel<NK, COL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(tree_split_kernel<NK, COL, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)limit);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
-  return launch_pdl(tree_split_kernel<NK, COL>, dim3(a.ns, a.mt, a.nkv), kSplitThreads, smem, st, a);
+  return launch_pdl(tree_split_kernel<NK, COL, Args>, dim3(a.ns, a.mt, heads), kSplitThreads, smem, st, a);
 }
 
-static cudaError_t launch_split(const TreeAttnArgs& a, cudaStream_t st) {
-  if (split_nk(a.dqk, a.dv) == 64) return launch_split_as<64, false>(a, st);
-  return a.dv > 128 ? launch_split_as<32, true>(a, st) : launch_split_as<32, false>(a, st);
+template <class Args>
+static cudaError_t launch_split(const Args& a, int heads, cudaStream_t st) {
+  if (split_nk(a.dqk, a.dv) == 64) return launch_split_as<64, false>(a, heads, st);
+  return a.dv > 128 ? launch_split_as<32, true>(a, heads, st) : launch_split_as<32, false>(a, heads, st);
 }
+
+int split_tile_keys(int dqk, int dv) { return split_nk(dqk, dv); }
+cudaError_t launch_prefix_split(const PrefixArgs& a, cudaStream_t st) { return launch_split(a, a.groups * a.nkv, st); }
 
 static mtp_status check_tree_geom(const mtp_attn_geom* g, int n) {
   if (!g) return fail(MTP_ERR_INVALID_ARG, "attn_tree_sink: null geometry");
@@ -1218,6 +1100,8 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   a.sinks = d_sinks;
   a.kc = d_k_cache;
   a.vc = d_v_cache;
+  a.keys = d_k_cache;
+  a.values = d_v_cache;
   a.mask = reinterpret_cast<const unsigned long long*>(tree->d_mask);
   a.depth = tree->d_depth;
   a.out = d_out;
@@ -1238,7 +1122,7 @@ mtp_status attn_tree_sink(const mtp_attn_geom* g, const mtp_draft_tree* tree, co
   cudaError_t e = launch_pdl(tree_prep_kernel, dim3((items + kPrepThreads / 32 - 1) / (kPrepThreads / 32)),
                              kPrepThreads, 0, st, a);
   if (e == cudaSuccess && a.ns > 0)
-    e = launch_split(a, st);
+    e = launch_split(a, a.nkv, st);
   if (e == cudaSuccess)
     e = launch_pdl(std::max(a.dqk, a.dv) > 128 ? tree_finish_kernel<2> : tree_finish_kernel<1>, dim3(a.nh, n),
                    kFinishWarps * 32, 0, st, a);
