@@ -757,6 +757,63 @@ mtp_status attn_prefix_sink(const mtp_attn_geom *g, const mtp_prefix_batch *batc
                             float *d_v_tail, int32_t tail_cap, float *d_out, void *d_ws,
                             size_t ws_bytes, void *stream);
 
+/* The beams of n_seqs prompts: beam b of prompt s is row s*beams + b. */
+typedef struct {
+    const float *d_score;        /* [rows] log-probabilities so far; a beam without a finite one offers
+                                    nothing (a search starts with one beam at 0, the others at -inf) */
+    const int32_t *d_len;        /* [rows] tokens of each beam so far, or NULL */
+    const int32_t *d_done;       /* [rows] non-zero: finished, or NULL: none is */
+    int32_t n_seqs;
+    int32_t beams;               /* 1..64; n_seqs*beams <= 1024 */
+    int32_t vocab;               /* 1..2^30 */
+    int32_t eos;                 /* the token that finishes a beam, -1: none does (d_done is NULL then) */
+    float length_penalty;        /* alpha: ranks are score / length^alpha (within 1e+-200); 0: the scores.
+                                    Needs d_len otherwise */
+} mtp_beam_set;
+
+/* ------------------------------------------------------------------------
+ * beam_select: for each prompt the k best of its beams' extensions, best first.
+ * Beam b, not finished, offers each token v of its row l (d_logits [rows][ld])
+ * that is not at -inf (or NaN) with the score
+ *   score_b + l_v - log(sum_u exp(l_u))   and the length len_b + 1;
+ * a finished beam offers itself alone, with token eos and its own score and
+ * length; its row is not read.  A row with +infinity, or with nothing above
+ * -infinity, offers nothing.  Candidates go by rank; equal ranks by the lower
+ * beam, then the lower token.  Ranks are compared in 64 bits, tokens of one beam
+ * by their float32 logits (of several logits whose scores round to one 64-bit
+ * rank, equal ranks' order takes effect among the k largest of each beam).
+ *   d_parent [n_seqs][k]: the beam extended (within its prompt), d_token its
+ *   token, d_score_out its score; -1, -1 and -inf where there are fewer than k.
+ *   d_len_out (needs d_len), d_done_out [n_seqs][k] or NULL: the new beam's
+ *   length, and 1 where it is finished (0 and 0 where there is none).
+ *   With k = beams the outputs are the next step's beams; d_score_out, d_len_out
+ *   and d_done_out may then be d_score, d_len and d_done themselves.  No other
+ *   overlap.  k in 1..128; 4-byte alignment is enough here.
+ * The step after logit_rules_argmax's (or verify_head_argmax's) logits; with more
+ * candidates than beams a caller takes finished hypotheses out between steps, and
+ * the levels of a draft tree can be drawn the same way.
+ * ------------------------------------------------------------------------ */
+size_t beam_select_workspace_bytes(int32_t n_seqs, int32_t beams, int32_t vocab, int32_t k);
+mtp_status beam_select(const mtp_beam_set *set, const float *d_logits, int64_t ld, int32_t k,
+                       int32_t *d_parent, int32_t *d_token, float *d_score_out,
+                       int32_t *d_len_out, int32_t *d_done_out, void *d_ws, size_t ws_bytes,
+                       void *stream);
+
+/* kv_beam_reorder: in every layer and KV head, rows 0 .. d_len[r]-1 of beam r's
+ * tail (r = s*beams + b) become those of beam d_parent[r] of prompt s, as they
+ * were before the call.  Other rows stay as they are, and so does a beam whose
+ * parent is negative.  d_parent, d_len [n_seqs*beams]; beam_select's outputs with
+ * k = beams (the new length, the row appended in this step included).  A parent
+ * >= beams (the beam stays) or a length above max_len (max_len is taken) sets
+ * device error 7.
+ *   tails: caches [n_seqs*beams][n_kv_heads][cache_cap][dim] of each layer (an
+ *   mtp_kv_caches with one such array a layer); max_len <= cache_cap sizes the
+ *   launch; 1..64 beams, n_seqs*beams <= 1024. */
+size_t kv_beam_workspace_bytes(void);
+mtp_status kv_beam_reorder(const mtp_kv_caches *tails, const int32_t *d_parent, int32_t n_seqs,
+                           int32_t beams, const int32_t *d_len, int32_t max_len, void *d_ws,
+                           size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

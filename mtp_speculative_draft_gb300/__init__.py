@@ -17,7 +17,8 @@ from .tree import (  # noqa: F401
     mtp_tree_plan, mtp_tree_workspace_bytes, rope_axes, rope_axes_rows, rope_axes_rows_workspace_bytes,
 )
 from .beams import (  # noqa: F401
-    attn_prefix_sink, attn_prefix_sink_workspace_bytes, prefix_batch,
+    attn_prefix_sink, attn_prefix_sink_workspace_bytes, beam_select, beam_select_workspace_bytes, beam_set,
+    kv_beam_reorder, kv_beam_workspace_bytes, kv_tails, prefix_batch,
 )
 from ._lib import MimoLayerState, SpecStats  # noqa: F401
 from .layer import DraftLayer, DraftChain  # noqa: F401

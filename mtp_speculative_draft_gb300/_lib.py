@@ -111,6 +111,12 @@ class PrefixBatch(C.Structure):
                 ("ld_q", C.c_int64), ("ld_k", C.c_int64), ("ld_v", C.c_int64)]
 
 
+class BeamSet(C.Structure):
+    device = None  # of the tensors, where a wrapper made the descriptor
+    _fields_ = [("d_score", vp), ("d_len", vp), ("d_done", vp), ("n_seqs", i32), ("beams", i32), ("vocab", i32),
+                ("eos", i32), ("length_penalty", f32)]
+
+
 class StepOut(C.Structure):
     _fields_ = [("d_token", vp), ("d_value", vp), ("d_hidden_out", vp), ("d_u2", vp),
                 ("d_logits", vp)]
@@ -172,6 +178,10 @@ EXPORTS = {
     "attn_prefix_sink_workspace_bytes": (sz, [C.POINTER(AttnGeom), i32, i32, i32, i32]),
     "attn_prefix_sink": (C.c_int, [C.POINTER(AttnGeom), C.POINTER(PrefixBatch), vp, vp, vp, vp, vp, vp,
                                    i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]),
+    "beam_select_workspace_bytes": (sz, [i32, i32, i32, i32]),
+    "beam_select": (C.c_int, [C.POINTER(BeamSet), vp, C.c_int64, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+    "kv_beam_workspace_bytes": (sz, []),
+    "kv_beam_reorder": (C.c_int, [C.POINTER(KvCaches), vp, i32, i32, vp, i32, vp, sz, vp]),
     "mtp_kv_catch_up_workspace_bytes": (sz, [C.POINTER(LayerDesc), i32]),
     "mtp_kv_catch_up": (C.c_int, [C.POINTER(LayerDesc), vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]),
 }

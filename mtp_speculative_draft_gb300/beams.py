@@ -12,7 +12,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
-from ._lib import AttnGeom, PrefixBatch, RopeAxes, check
+from ._lib import AttnGeom, BeamSet, KvCaches, PrefixBatch, RopeAxes, check
 from .api import workspace
 from .tree import _F32, _I32, _MOST, _device, _here, _int, _on, _ptr, _rows, _ws
 
@@ -74,4 +74,86 @@ def attn_prefix_sink(g: AttnGeom, batch: PrefixBatch, qp, kp, vp, q_norm, k_norm
         _ptr(v_prefix, _F32, 0, "v_prefix", dev), pcap, _ptr(k_tail, _F32, 0, "k_tail", dev),
         _ptr(v_tail, _F32, 0, "v_tail", dev), tcap, _ptr(out, _F32, rows * nh * dv, "out", dev), *_ws(ws, dev),
         _on(stream, dev)), "attn_prefix_sink")
+    return ws
+
+
+# ------------------------------------------------------------------------------- selection
+def beam_set(n_seqs, beams, vocab, score: torch.Tensor, length=None, done=None, eos=-1, length_penalty=0.0) -> BeamSet:
+    """The beams of ``n_seqs`` prompts: ``score [n_seqs * beams]`` (float32), ``length`` and ``done`` (int32)."""
+    dev = _device()
+    n_seqs, beams, vocab = _int(n_seqs, "n_seqs"), _int(beams, "beams"), _int(vocab, "vocab")
+    rows = max(1, n_seqs * beams)
+    b = BeamSet(_ptr(score, _F32, rows, "score", dev), _ptr(length, _I32, rows, "length", dev),
+                _ptr(done, _I32, rows, "done", dev), n_seqs, beams, vocab, _int(eos, "eos"), length_penalty)
+    b.tensors, b.device = (score, length, done), dev
+    return b
+
+
+def beam_select_workspace_bytes(beams: BeamSet, k: int) -> int:
+    return L.load().beam_select_workspace_bytes(beams.n_seqs, beams.beams, beams.vocab, _int(k, "k"))
+
+
+def beam_select(beams: BeamSet, logits, k, parent, token, score, length=None, done=None, ws=None, stream=None):
+    """The ``k`` best extensions of each prompt's beams by ``logits [n_seqs * beams, vocab]`` (any row
+    stride) into ``parent``, ``token``, ``score`` and, if given, ``length`` and ``done [n_seqs, k]``."""
+    dev = _device()
+    if beams.device != dev:
+        _here(beams, dev)
+    lib = L.load()
+    if type(k) is not int or not -_MOST <= k <= _MOST:
+        k = _int(k, "k")
+    n, vocab = beams.n_seqs * k, beams.vocab
+    px, ld = _rows(logits, beams.n_seqs * beams.beams, vocab, "logits", dev)
+    if ws is None:
+        ws = workspace(lib.beam_select_workspace_bytes(beams.n_seqs, beams.beams, vocab, k), stream=stream)
+    check(lib.beam_select(C.byref(beams), px, ld or vocab, k, _ptr(parent, _I32, n, "parent", dev),
+                          _ptr(token, _I32, n, "token", dev), _ptr(score, _F32, n, "score", dev),
+                          _ptr(length, _I32, n, "length", dev), _ptr(done, _I32, n, "done", dev), *_ws(ws, dev),
+                          _on(stream, dev)), "beam_select")
+    return ws
+
+
+# ------------------------------------------------------------------------------- survivors' tails
+def kv_tails(k_tails, v_tails, beams) -> KvCaches:
+    """The K and V tails ``[n_seqs * beams, n_kv, cap, dim]`` of layers with one geometry."""
+    dev = _device()
+    k_tails, v_tails = list(k_tails), list(v_tails)
+    n, beams = len(k_tails), _int(beams, "beams")
+    if n < 1 or len(v_tails) != n:
+        raise ValueError("kv_tails: one K and one V tail a layer")
+    if k_tails[0].dim() != 4:
+        raise ValueError("kv_tails: tails [n_seqs * beams, n_kv, cap, dim] are required")
+    rows, nkv, cap, dqk = k_tails[0].shape
+    dv = v_tails[0].shape[-1]
+    if beams < 1 or rows % beams:
+        raise ValueError(f"kv_tails: {rows} tails are no whole number of prompts of {beams} beams")
+    for k, v in zip(k_tails, v_tails):
+        if tuple(k.shape) != (rows, nkv, cap, dqk) or tuple(v.shape) != (rows, nkv, cap, dv):
+            raise ValueError("kv_tails: tails [n_seqs * beams, n_kv, cap, dim] of one geometry are required")
+    ks = (L.vp * n)(*[_ptr(k, _F32, 1, "k_tail", dev) for k in k_tails])
+    vs = (L.vp * n)(*[_ptr(v, _F32, 1, "v_tail", dev) for v in v_tails])
+    if len({*ks, *vs}) != 2 * n:
+        raise ValueError("kv_tails: a tail is given twice")
+    c = KvCaches(ks, vs, n, nkv, dqk, dv, _int(cap, "cap"))
+    c.tensors, c.device, c.seqs, c.beams = (k_tails, v_tails, ks, vs), dev, rows // beams, beams
+    return c
+
+
+def kv_beam_workspace_bytes() -> int:
+    return L.load().kv_beam_workspace_bytes()
+
+
+def kv_beam_reorder(tails: KvCaches, parent, length, max_len, ws=None, stream=None):
+    """Rows ``0 .. length[r] - 1`` of beam r become those of its ``parent``, in all layers (``parent`` and
+    ``length [n_seqs * beams]``, int32; a negative parent: the beam stays)."""
+    dev = _device()
+    if tails.device != dev:
+        _here(tails, dev)
+    lib = L.load()
+    if ws is None:
+        ws = workspace(lib.kv_beam_workspace_bytes(), stream=stream)
+    rows = tails.seqs * tails.beams
+    check(lib.kv_beam_reorder(C.byref(tails), _ptr(parent, _I32, rows, "parent", dev), tails.seqs, tails.beams,
+                              _ptr(length, _I32, rows, "length", dev), _int(max_len, "max_len"), *_ws(ws, dev),
+                              _on(stream, dev)), "kv_beam_reorder")
     return ws

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmtpdraft.so")
 SOURCES = ["api.cu", "gemv.cu", "norm.cu", "attn.cu", "moe.cu", "spec.cu", "catchup.cu",
-           "rope.cu", "rules.cu", "tree.cu", "treeattn.cu", "prefix.cu"]
+           "rope.cu", "rules.cu", "tree.cu", "treeattn.cu", "prefix.cu",
+           "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,625 @@
+// A beam search's selection over beams and vocabulary, and the move of the
+// surviving beams' K/V tails.
+//
+// "cortiq-engine 0.8.49 src/mimo_mtp.rs" keeps one hypothesis (mimo_spec_round
+// takes each row's argmax, mimo_verify_rewind cuts the caches back); here a
+// prompt has several, as its target's logits allow:
+//   candidate (b, v) of a prompt: s = score_b + l_bv - log sum_u exp(l_bu),
+//   ranked by s / length^alpha; a finished beam's only candidate is itself.
+// Two launches for the selection:
+//   1. rows:   a CTA a chunk of a row: its largest logit, the sum of
+//              exponentials, and at most 2 k logits among which are its k largest;
+//   2. merge:  a CTA a prompt: the rows' normalisers, the candidates' ranks, the
+//              best k in order.
+// Within a row candidates go by their logits, between rows by ranks in 64 bits:
+// float32 scores of about -30 are 2e-6 apart, and candidates that close are
+// common among 150k tokens.  Sums of exponentials: 32 terms in float32 a thread,
+// the rest in 64 bits.
+#include <algorithm>
+#include <cmath>
+
+#include "prefix.cuh"
+
+namespace mtp {
+
+constexpr int kSelThreads = 256;
+constexpr int kSelPer = 32;                         // logits a thread
+constexpr int kSelChunk = kSelThreads * kSelPer;    // logits a CTA
+constexpr int kBeamsMost = 64, kBeamTop = 128;      // beams and candidates of a prompt
+constexpr int kBeamRows = 1024;                     // beams of a call
+constexpr int kSelVocab = 1 << 30;                  // tokens
+constexpr int kMergeThreads = 512;
+constexpr int kMergeList = 1024;                    // candidates that are put in order at once
+
+struct SelArgs {
+  const float* x;
+  long long ld;
+  int beams, V, k, chunks, cap, eos;
+  float alpha;
+  const float* score;
+  const int *len, *done;
+  int *parent, *token, *len_out, *done_out;
+  float* score_out;
+  double* sum;                // [rows][chunks] sum of exponentials, of which
+  float* top;                 // [rows][chunks] is the largest logit
+  int* count;                 // [rows][chunks] candidates
+  unsigned long long* cand;   // [rows][chunks][cap] logit key, ~token
+  int* err;
+};
+
+// Floats as unsigned integers in the same order (-0 and 0 alike; NaN below all
+// others, with -infinity).
+__device__ __forceinline__ uint32_t float_key(float x) {
+  x = x == x ? x + 0.f : -INFINITY;
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // of -infinity
+__device__ __forceinline__ unsigned long long double_key(double x) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+  return u ^ ((u >> 63) ? 0xFFFFFFFFFFFFFFFFull : 0x8000000000000000ull);
+}
+
+// A beam that offers candidates of its row: not finished, with a finite score.
+__device__ __forceinline__ bool beam_live(const SelArgs& a, int r) {
+  return (!a.done || a.done[r] == 0) && fabsf(a.score[r]) < INFINITY;
+}
+
+// grid (chunks, rows).  Bound by HBM on many rows; a row's logits are read once
+// and stay in registers.  The k-th largest of the threads' largest logits bounds
+// the chunk's k-th largest from below, so the few logits at or above it hold the
+// chunk's k largest; where equal logits make them more than 2 k, the k largest
+// are found exactly (lower tokens first among equals).
+__global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ float wmax[kSelThreads / 32];
+  __shared__ double wsum[kSelThreads / 32];
+  __shared__ int n;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x, r = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  const size_t slot = (size_t)r * a.chunks + c;
+  if (!beam_live(a, r)) {  // the row is not read
+    if (tid == 0) a.count[slot] = 0;
+    return;
+  }
+  const float* x = a.x + (size_t)r * a.ld;
+  // chunks start at 16-byte boundaries: logit e of the row is number e + skew
+  const int skew = (int)((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
+  const int e0 = c * kSelChunk - skew + 4 * tid;
+  float v[kSelPer];
+#pragma unroll
+  for (int j = 0; j < kSelPer / 4; ++j) {
+    const int e = e0 + j * 4 * kSelThreads;
+    float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (e >= 0 && e <= a.V - 4) {
+      f = __ldcs(reinterpret_cast<const float4*>(x + e));
+    } else {
+      if (e >= 0 && e < a.V) f.x = x[e];
+      if (e + 1 >= 0 && e + 1 < a.V) f.y = x[e + 1];
+      if (e + 2 >= 0 && e + 2 < a.V) f.z = x[e + 2];
+      if (e + 3 >= 0 && e + 3 < a.V) f.w = x[e + 3];
+    }
+    v[4 * j] = f.x;
+    v[4 * j + 1] = f.y;
+    v[4 * j + 2] = f.z;
+    v[4 * j + 3] = f.w;
+  }
+  if (tid == 0) n = 0;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kSelPer; ++j) mx = fmaxf(mx, v[j]);  // NaN takes no part
+  // sum of exponentials relative to the warp's largest logit
+  const float wm = warp_max(mx), ref = wm == -INFINITY ? 0.f : wm;
+  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kSelPer; ++j) s4[j & 3] += v[j] == v[j] ? expf(v[j] - ref) : 0.f;
+  double s = (double)(s4[0] + s4[1]) + (double)(s4[2] + s4[3]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) {
+    wmax[warp] = wm;
+    wsum[warp] = s;
+  }
+  // the largest 16 bits of a key that k threads reach
+  const uint32_t top = float_key(mx);
+  uint32_t low = 0;
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t t = low | 1u << bit;
+    if (__syncthreads_count(top >= t) >= a.k) low = t;
+  }
+  low = max(low, kNoKey + 1);
+  int here = 0;
+  if (top >= low) {
+#pragma unroll
+    for (int j = 0; j < kSelPer; ++j) here += float_key(v[j]) >= low;
+  }
+  int at = here ? atomicAdd(&n, here) : 0;
+  __syncthreads();
+  const int total = n;
+  unsigned long long* out = a.cand + slot * a.cap;
+  if (total <= a.cap) {
+    if (here) {
+#pragma unroll
+      for (int j = 0; j < kSelPer; ++j) {
+        const uint32_t key = float_key(v[j]);
+        const uint32_t tok = (uint32_t)(e0 + (j >> 2) * 4 * kSelThreads + (j & 3));
+        if (key >= low) out[at++] = (unsigned long long)key << 32 | (0xFFFFFFFFu - tok);
+      }
+    }
+    if (tid == 0) a.count[slot] = total;
+  } else {
+    // the k-th largest key, then how many of that key are wanted, and up to which token
+    uint32_t kth = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = kth | 1u << bit;
+      int m = 0;
+#pragma unroll
+      for (int j = 0; j < kSelPer; ++j) m += float_key(v[j]) >= t;
+      __syncthreads();
+      if (tid == 0) n = 0;
+      __syncthreads();
+      m = __reduce_add_sync(0xffffffffu, m);
+      if (lane == 0) atomicAdd(&n, m);
+      __syncthreads();
+      if (n >= a.k) kth = t;
+    }
+    // of the tokens with that key, the lowest below `end` are taken: the least
+    // end at which k tokens are there
+    int end = 0;
+#pragma unroll 1
+    for (int bit = 30; bit >= 0; --bit) {
+      const int t = end + (1 << bit);  // end stays below 2^30, t below 2^31
+      int m = 0;
+#pragma unroll
+      for (int j = 0; j < kSelPer; ++j) {
+        const int tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
+        const uint32_t key = float_key(v[j]);
+        m += key > kth || (key == kth && tok < t);
+      }
+      __syncthreads();
+      if (tid == 0) n = 0;
+      __syncthreads();
+      m = __reduce_add_sync(0xffffffffu, m);
+      if (lane == 0) atomicAdd(&n, m);
+      __syncthreads();
+      if (n < a.k) end = t;
+    }
+    __syncthreads();
+    if (tid == 0) n = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < kSelPer; ++j) {
+      float f = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSelPer; ++i)
+        if (i == j) f = v[i];
+      const int tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
+      const uint32_t key = float_key(f);
+      if (key > kth || (key == kth && tok <= end))
+        out[atomicAdd(&n, 1)] = (unsigned long long)key << 32 | (0xFFFFFFFFu - (uint32_t)tok);
+    }
+    if (tid == 0) a.count[slot] = a.k;
+  }
+  if (warp == 0) {
+    float m = lane < kSelThreads / 32 ? wmax[lane] : -INFINITY;
+    const float M = warp_max(m);
+    // +infinity, in whichever warp, makes the sum NaN
+    double t = lane < kSelThreads / 32 && m != -INFINITY ? wsum[lane] * (double)expf(m - M) : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) {
+      a.top[slot] = M;
+      a.sum[slot] = t;
+    }
+  }
+}
+
+struct MergeSmem {
+  double base[kBeamsMost];   // log of the row's normaliser
+  double score[kBeamsMost], norm[kBeamsMost];  // length^alpha of a candidate
+  int len[kBeamsMost], kind[kBeamsMost];       // 0 nothing, 1 tokens, 2 itself
+  unsigned long long key[kMergeList];          // ranks
+  uint32_t beam[kMergeList], tok[kMergeList];
+  unsigned long long best_key[kMergeThreads / 32];
+  unsigned long long best_id[kMergeThreads / 32];
+  unsigned long long last_key, last_id;
+  int n;
+};
+
+// One CTA a prompt; warps take (row, chunk) lists in turn.
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ MergeSmem sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int seq = blockIdx.x, row0 = seq * a.beams;
+  constexpr int kWarps = kMergeThreads / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) sh.n = 0;
+  for (int b = warp; b < a.beams; b += kWarps) {
+    const int r = row0 + b;
+    const float score = a.score[r];
+    const bool done = a.done && a.done[r] != 0;
+    int kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
+    double lse = 0.0;
+    if (kind == 1) {
+      float M = -INFINITY;
+      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, a.top[(size_t)r * a.chunks + c]);
+      M = warp_max(M);
+      double s = 0.0;
+      for (int c = lane; c < a.chunks; c += 32) {
+        const float m = a.top[(size_t)r * a.chunks + c];
+        if (m != -INFINITY) s += a.sum[(size_t)r * a.chunks + c] * exp((double)m - (double)M);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      lse = (double)M + log(s);
+      if (!(fabs(lse) < INFINITY)) kind = 0;  // no token, +infinity
+    }
+    if (lane == 0) {
+      const int len = a.len ? a.len[r] : 0;
+      const int next = len + (kind == 1);
+      sh.base[b] = lse;
+      sh.score[b] = (double)score;
+      // within 1e+-200, so that a rank times it is the score again
+      sh.norm[b] = a.alpha != 0.f ? fmin(fmax(pow((double)max(next, 1), (double)a.alpha), 1e-200), 1e200) : 1.0;
+      sh.len[b] = next;
+      sh.kind[b] = kind;
+    }
+  }
+  __syncthreads();
+  auto rank = [&](int b, float logit) { return ((sh.score[b] + ((double)logit - sh.base[b]))) / sh.norm[b]; };
+  const int lists = a.beams * a.chunks;
+  // calls f(key, beam, token) for this thread's candidates
+  auto each = [&](auto f) {
+    for (int q = warp; q < lists; q += kWarps) {
+      const int b = q / a.chunks;
+      if (sh.kind[b] != 1) continue;
+      const size_t slot = (size_t)row0 * a.chunks + q;
+      const int n = a.count[slot];
+      for (int i = lane; i < n; i += 32) {
+        const unsigned long long w = a.cand[slot * a.cap + i];
+        f(double_key(rank(b, key_float((uint32_t)(w >> 32)))), (uint32_t)b, 0xFFFFFFFFu - (uint32_t)w);
+      }
+    }
+    if (tid < a.beams && sh.kind[tid] == 2) f(double_key(sh.score[tid] / sh.norm[tid]), (uint32_t)tid, (uint32_t)a.eos);
+  };
+  unsigned long long mine = 0;
+  each([&](unsigned long long key, uint32_t, uint32_t) { mine = key > mine ? key : mine; });
+  // the upper half of the k-th largest of the threads' best ranks, from below
+  uint32_t low = 0;
+  const uint32_t top = (uint32_t)(mine >> 32);
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t t = low | 1u << bit;
+    if (__syncthreads_count(top >= t) >= a.k) low = t;
+  }
+  if (low == 0) low = 1;  // fewer than k threads have any
+  each([&](unsigned long long key, uint32_t b, uint32_t tok) {
+    if ((uint32_t)(key >> 32) < low) return;
+    const int i = atomicAdd(&sh.n, 1);
+    if (i < kMergeList) {
+      sh.key[i] = key;
+      sh.beam[i] = b;
+      sh.tok[i] = tok;
+    }
+  });
+  __syncthreads();
+  const int n = sh.n;
+  auto put = [&](int at, uint32_t b, uint32_t tok, float score) {
+    const size_t o = (size_t)seq * a.k + at;
+    const bool none = b == 0xFFFFFFFFu;
+    a.parent[o] = none ? -1 : (int)b;
+    a.token[o] = none ? -1 : (int)tok;
+    a.score_out[o] = none ? -INFINITY : score;
+    if (a.len_out) a.len_out[o] = none ? 0 : sh.len[b];
+    if (a.done_out) a.done_out[o] = none ? 0 : (sh.kind[b] == 2 || (int)tok == a.eos);
+  };
+  // a candidate's score, from its place in the lists
+  auto score_of = [&](uint32_t b, unsigned long long key) {
+    unsigned long long u = key ^ ((key >> 63) ? 0x8000000000000000ull : 0xFFFFFFFFFFFFFFFFull);
+    return __longlong_as_double((long long)u) * sh.norm[b];
+  };
+  if (n <= kMergeList) {
+    // a candidate's place is the number of better ones
+    for (int i = tid; i < n; i += kMergeThreads) {
+      const unsigned long long key = sh.key[i];
+      const uint32_t b = sh.beam[i], t = sh.tok[i];
+      int at = 0;
+      for (int j = 0; j < n; ++j)
+        at += sh.key[j] > key || (sh.key[j] == key && (sh.beam[j] < b || (sh.beam[j] == b && sh.tok[j] < t)));
+      if (at < a.k) put(at, b, t, (float)score_of(b, key));
+    }
+    for (int i = n + tid; i < a.k; i += kMergeThreads) put(i, 0xFFFFFFFFu, 0, 0.f);
+    return;
+  }
+  // many equal ranks: one after another, each the best behind the last
+  if (tid == 0) {
+    sh.last_key = ~0ull;
+    sh.last_id = 0;
+  }
+  __syncthreads();
+  for (int i = 0; i < a.k; ++i) {
+    const unsigned long long lk = sh.last_key, li = sh.last_id;
+    unsigned long long bk = 0, bi = ~0ull;  // best rank, then lowest beam and token
+    each([&](unsigned long long key, uint32_t b, uint32_t tok) {
+      const unsigned long long id = (unsigned long long)b << 32 | tok;
+      if (key > lk || (key == lk && id <= li && lk != ~0ull)) return;
+      if (key > bk || (key == bk && id < bi)) {
+        bk = key;
+        bi = id;
+      }
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, bk, o), i2 = __shfl_xor_sync(0xffffffffu, bi, o);
+      if (k2 > bk || (k2 == bk && i2 < bi)) {
+        bk = k2;
+        bi = i2;
+      }
+    }
+    if (lane == 0) {
+      sh.best_key[warp] = bk;
+      sh.best_id[warp] = bi;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWarps; ++w)
+        if (sh.best_key[w] > bk || (sh.best_key[w] == bk && sh.best_id[w] < bi)) {
+          bk = sh.best_key[w];
+          bi = sh.best_id[w];
+        }
+      sh.last_key = bk;
+      sh.last_id = bi;
+      const uint32_t b = (uint32_t)(bi >> 32);
+      put(i, b, (uint32_t)bi, (float)score_of(b, bk));
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ reorder
+constexpr int kMoveLayers = 64;  // layers of one launch
+constexpr int kMoveThreads = 256;
+constexpr int kMoveWords = 16;   // 16-byte words a thread
+
+struct MoveArgs {
+  float* k[kMoveLayers];
+  float* v[kMoveLayers];
+  const int *parent, *len;
+  int seqs, beams, nkv, dqk, dv, most, rows, tiles;  // rows a tile
+  long long cap;
+  int* err;
+};
+
+// grid (row tiles x prompts, KV heads x K or V, layers).  In place: a CTA reads
+// its rows of every beam that changes into registers before it writes any of
+// them, so beams may exchange places, or several take one beam's tail.
+__global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_constant__ MoveArgs a) {
+  __shared__ int to[kBeamsMost], from[kBeamsMost], words[kBeamsMost];
+  __shared__ int n;
+  const int tid = threadIdx.x;
+  const int seq = blockIdx.x / a.tiles, r0 = blockIdx.x % a.tiles * a.rows;
+  const int kv = blockIdx.y >> 1, d = blockIdx.y & 1 ? a.dv : a.dqk;
+  float* base = (blockIdx.y & 1 ? a.v[blockIdx.z] : a.k[blockIdx.z]) +
+                (((size_t)seq * a.beams * a.nkv + kv) * a.cap + r0) * d;
+  const size_t beam_step = (size_t)a.nkv * a.cap * d;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid < 32) {
+    int have = 0;
+    for (int b0 = 0; b0 < a.beams; b0 += 32) {
+      const int b = b0 + tid;
+      int p = -1, len = 0;
+      if (b < a.beams) {
+        p = a.parent[seq * a.beams + b];
+        len = a.len[seq * a.beams + b];
+        if (p >= a.beams || len > a.most) {
+          set_dev_error(a.err, kErrBadLength);
+          if (p >= a.beams) p = -1;
+          len = min(len, a.most);
+        }
+      }
+      const int rows = min(a.rows, len - r0);
+      const bool moves = p >= 0 && p != b && rows > 0;
+      const unsigned m = __ballot_sync(0xffffffffu, moves);
+      if (moves) {
+        const int i = have + __popc(m & ((1u << tid) - 1));
+        to[i] = b;
+        from[i] = p;
+        words[i] = rows * d / 4;
+      }
+      have += __popc(m);
+    }
+    if (tid == 0) n = have;
+  }
+  __syncthreads();
+  const int seg = a.rows * d / 4, all = n * seg;
+  float4 x[kMoveWords];
+#pragma unroll
+  for (int i = 0; i < kMoveWords; ++i) {
+    const int e = tid + i * kMoveThreads, j = e / seg, w = e - j * seg;
+    if (e < all && w < words[j]) x[i] = *reinterpret_cast<const float4*>(base + from[j] * beam_step + 4 * w);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMoveWords; ++i) {
+    const int e = tid + i * kMoveThreads, j = e / seg, w = e - j * seg;
+    if (e < all && w < words[j]) *reinterpret_cast<float4*>(base + to[j] * beam_step + 4 * w) = x[i];
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct SelWs {
+  double* sum;
+  unsigned long long* cand;
+  float* top;
+  int* count;
+  size_t bytes;
+};
+
+// Chunks of a row of V logits at any alignment.
+static int sel_chunks(int V) { return (int)(((int64_t)V + 3 + kSelChunk - 1) / kSelChunk); }
+
+static SelWs sel_ws(void* ws, int rows, int V, int k) {
+  SelWs w = {};
+  size_t off = sizeof(WsHeader) + kRuleJoinBytes;
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  auto take = [&](size_t bytes) {
+    uint8_t* p = b ? b + off : nullptr;
+    off = (off + bytes + 255) & ~size_t(255);
+    return p;
+  };
+  const size_t slots = (size_t)rows * sel_chunks(V);
+  w.sum = reinterpret_cast<double*>(take(8 * slots));
+  w.cand = reinterpret_cast<unsigned long long*>(take(8 * slots * 2 * k));
+  w.top = reinterpret_cast<float*>(take(4 * slots));
+  w.count = reinterpret_cast<int*>(take(4 * slots));
+  w.bytes = off;
+  return w;
+}
+
+static bool sel_sizes(int64_t seqs, int64_t beams, int V, int k) {
+  return seqs >= 1 && beams >= 1 && beams <= kBeamsMost && seqs * beams <= kBeamRows && V >= 1 &&
+         V <= kSelVocab && k >= 1 && k <= kBeamTop;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static bool overlap(const void* p, size_t pn, const void* q, size_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + qn && b < a + pn;
+}
+
+}  // namespace mtp
+
+using namespace mtp;
+
+extern "C" {
+
+size_t beam_select_workspace_bytes(int32_t n_seqs, int32_t beams, int32_t vocab, int32_t k) {
+  return sel_sizes(n_seqs, beams, vocab, k) ? sel_ws(nullptr, n_seqs * beams, vocab, k).bytes : 0;
+}
+
+mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld, int32_t k, int32_t* d_parent,
+                       int32_t* d_token, float* d_score_out, int32_t* d_len_out, int32_t* d_done_out, void* d_ws,
+                       size_t ws_bytes, void* stream) {
+  if (!B || !B->d_score || !d_logits || !d_parent || !d_token || !d_score_out)
+    return fail(MTP_ERR_INVALID_ARG, "beam_select: null pointer");
+  if (!sel_sizes(B->n_seqs, B->beams, B->vocab, k))
+    return fail(MTP_ERR_UNSUPPORTED,
+                "beam_select: 1..64 beams a prompt, 1..1024 in all, 1..2^30 tokens, 1..128 candidates");
+  if (ld < B->vocab) return fail(MTP_ERR_INVALID_ARG, "beam_select: row stride below the vocabulary");
+  if (B->eos < -1 || B->eos >= B->vocab || (B->d_done && B->eos < 0))
+    return fail(MTP_ERR_INVALID_ARG, "beam_select: finished beams need an eos token of the vocabulary");
+  if (!std::isfinite(B->length_penalty) || (!B->d_len && (B->length_penalty != 0.f || d_len_out)))
+    return fail(MTP_ERR_INVALID_ARG, "beam_select: a length penalty and new lengths need the beams' lengths");
+  const void* in[3] = {B->d_score, B->d_len, B->d_done};
+  const void* out[5] = {d_score_out, d_len_out, d_done_out, d_parent, d_token};
+  for (const void* p : in)
+    if (!aligned4(p)) return fail(MTP_ERR_INVALID_ARG, "beam_select: misaligned pointer");
+  for (const void* p : out)
+    if (!aligned4(p)) return fail(MTP_ERR_INVALID_ARG, "beam_select: misaligned pointer");
+  if (!aligned4(d_logits)) return fail(MTP_ERR_INVALID_ARG, "beam_select: misaligned pointer");
+  const int rows = B->n_seqs * B->beams;
+  const size_t nin = 4 * (size_t)rows, nout = 4 * (size_t)B->n_seqs * k;
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(out[i], nout, in[j], nin) && !(i == j && out[i] == in[j] && k == B->beams))
+        return fail(MTP_ERR_INVALID_ARG,
+                    "beam_select: an output overlaps an input (in place: its own, with as many candidates as beams)");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], nout, out[j], nout))
+        return fail(MTP_ERR_INVALID_ARG, "beam_select: outputs overlap");
+    if (overlap(out[i], nout, d_logits, 4 * ((size_t)(rows - 1) * ld + B->vocab)))
+      return fail(MTP_ERR_INVALID_ARG, "beam_select: an output overlaps the logits");
+  }
+  const SelWs w = sel_ws(d_ws, rows, B->vocab, k);
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
+    return fail(MTP_ERR_WORKSPACE, "beam_select: workspace too small or misaligned");
+  SelArgs a = {};
+  a.x = d_logits;
+  a.ld = ld;
+  a.beams = B->beams;
+  a.V = B->vocab;
+  a.k = k;
+  a.chunks = sel_chunks(B->vocab);
+  a.cap = 2 * k;
+  a.eos = B->eos;
+  a.alpha = B->length_penalty;
+  a.score = B->d_score;
+  a.len = B->d_len;
+  a.done = B->d_done;
+  a.parent = d_parent;
+  a.token = d_token;
+  a.score_out = d_score_out;
+  a.len_out = d_len_out;
+  a.done_out = d_done_out;
+  a.sum = w.sum;
+  a.top = w.top;
+  a.count = w.count;
+  a.cand = w.cand;
+  a.err = &static_cast<WsHeader*>(d_ws)->err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pdl(beam_rows_kernel, dim3(a.chunks, rows), kSelThreads, 0, st, a);
+  if (e == cudaSuccess) e = launch_pdl(beam_merge_kernel, dim3(B->n_seqs), kMergeThreads, 0, st, a);
+  if (e != cudaSuccess) return cuda_fail(e, "beam_select launch");
+  return MTP_OK;
+}
+
+size_t kv_beam_workspace_bytes(void) { return sizeof(WsHeader); }
+
+mtp_status kv_beam_reorder(const mtp_kv_caches* C, const int32_t* d_parent, int32_t n_seqs, int32_t beams,
+                           const int32_t* d_len, int32_t max_len, void* d_ws, size_t ws_bytes, void* stream) {
+  if (!C || !C->h_k || !C->h_v || !d_parent || !d_len)
+    return fail(MTP_ERR_INVALID_ARG, "kv_beam_reorder: null pointer");
+  if (n_seqs < 1 || beams < 1 || beams > kBeamsMost || (int64_t)n_seqs * beams > kBeamRows)
+    return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: 1..64 beams a prompt, 1..1024 in all");
+  if (C->n_layers < 1 || C->n_layers > 4096 || C->n_kv_heads < 1 || C->n_kv_heads > 64)
+    return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: 1..4096 layers, 1..64 KV heads");
+  if (C->head_dim_qk < 4 || C->head_dim_qk % 4 || C->head_dim_qk > 256 || C->head_dim_v < 4 ||
+      C->head_dim_v % 4 || C->head_dim_v > 256)
+    return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: head dims must be multiples of 4, <= 256");
+  if (max_len < 0 || C->cache_cap < 1) return fail(MTP_ERR_INVALID_ARG, "kv_beam_reorder: bad length");
+  if (max_len > C->cache_cap)
+    return fail(MTP_ERR_CAPACITY, "kv_beam_reorder: max_len exceeds the tails' capacity");
+  for (int l = 0; l < C->n_layers; ++l)
+    if (!C->h_k[l] || !C->h_v[l] || !aligned16(C->h_k[l]) || !aligned16(C->h_v[l]))
+      return fail(MTP_ERR_INVALID_ARG, "kv_beam_reorder: null or misaligned tails");
+  if (!aligned4(d_parent) || !aligned4(d_len)) return fail(MTP_ERR_INVALID_ARG, "kv_beam_reorder: misaligned pointer");
+  if (!d_ws || !aligned16(d_ws) || ws_bytes < kv_beam_workspace_bytes())
+    return fail(MTP_ERR_WORKSPACE, "kv_beam_reorder: workspace too small or misaligned");
+  if (max_len == 0) return MTP_OK;
+  MoveArgs a = {};
+  a.parent = d_parent;
+  a.len = d_len;
+  a.seqs = n_seqs;
+  a.beams = beams;
+  a.nkv = C->n_kv_heads;
+  a.dqk = C->head_dim_qk;
+  a.dv = C->head_dim_v;
+  a.most = max_len;
+  // a tile of every beam fits the CTA's registers: 64 KB, or a row each of 64 beams of 256 dims
+  a.rows = std::min(max_len, kMoveThreads * kMoveWords / (beams * std::max(a.dqk, a.dv) / 4));
+  a.tiles = (max_len + a.rows - 1) / a.rows;
+  if ((int64_t)a.tiles * n_seqs > 0x7FFFFFFF)
+    return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: more than 2^31 tiles of rows");
+  a.cap = C->cache_cap;
+  a.err = &static_cast<WsHeader*>(d_ws)->err;
+  for (int l0 = 0; l0 < C->n_layers; l0 += kMoveLayers) {
+    const int nl = std::min(kMoveLayers, C->n_layers - l0);
+    for (int l = 0; l < nl; ++l) {
+      a.k[l] = C->h_k[l0 + l];
+      a.v[l] = C->h_v[l0 + l];
+    }
+    cudaError_t e = launch_pdl(kv_beam_kernel, dim3((unsigned)a.tiles * n_seqs, 2 * a.nkv, nl), kMoveThreads, 0,
+                               static_cast<cudaStream_t>(stream), a);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_beam_reorder launch");
+  }
+  return MTP_OK;
+}
+
+}  // extern "C"
