@@ -22,6 +22,9 @@
 
 namespace mtp {
 
+#ifndef MTP_SEL_CTAS
+#define MTP_SEL_CTAS 4
+#endif
 constexpr int kSelThreads = 256;
 constexpr int kSelPer = 32;                         // logits a thread
 constexpr int kSelChunk = kSelThreads * kSelPer;    // logits a CTA
@@ -42,8 +45,8 @@ struct SelArgs {
   float* score_out;
   double* sum;                // [rows][chunks] sum of exponentials, of which
   float* top;                 // [rows][chunks] is the largest logit
-  int* count;                 // [rows][chunks] candidates
-  unsigned long long* cand;   // [rows][chunks][cap] logit key, ~token
+  unsigned long long* cand;   // [rows][chunks][cap] logit key, ~token; 0: none
+  unsigned long long* ranks;  // [rows][chunks][cap] their ranks, where many are equal
   int* err;
 };
 
@@ -73,7 +76,7 @@ __device__ __forceinline__ bool beam_live(const SelArgs& a, int r) {
 // the chunk's k-th largest from below, so the few logits at or above it hold the
 // chunk's k largest; where equal logits make them more than 2 k, the k largest
 // are found exactly (lower tokens first among equals).
-__global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(const __grid_constant__ SelArgs a) {
   __shared__ float wmax[kSelThreads / 32];
   __shared__ double wsum[kSelThreads / 32];
   __shared__ int n;
@@ -82,10 +85,7 @@ __global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_con
   pdl_wait();
   pdl_launch_dependents();
   const size_t slot = (size_t)r * a.chunks + c;
-  if (!beam_live(a, r)) {  // the row is not read
-    if (tid == 0) a.count[slot] = 0;
-    return;
-  }
+  if (!beam_live(a, r)) return;  // the row is not read
   const float* x = a.x + (size_t)r * a.ld;
   // chunks start at 16-byte boundaries: logit e of the row is number e + skew
   const int skew = (int)((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_con
   const float wm = warp_max(mx), ref = wm == -INFINITY ? 0.f : wm;
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < kSelPer; ++j) s4[j & 3] += v[j] == v[j] ? expf(v[j] - ref) : 0.f;
+  for (int j = 0; j < kSelPer; ++j) s4[j & 3] += v[j] == v[j] ? ex2((v[j] - ref) * kLog2e) : 0.f;
   double s = (double)(s4[0] + s4[1]) + (double)(s4[2] + s4[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_con
         if (key >= low) out[at++] = (unsigned long long)key << 32 | (0xFFFFFFFFu - tok);
       }
     }
-    if (tid == 0) a.count[slot] = total;
+    for (int i = total + tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate
   } else {
     // the k-th largest key, then how many of that key are wanted, and up to which token
     uint32_t kth = 0;
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_con
       if (key > kth || (key == kth && tok <= end))
         out[atomicAdd(&n, 1)] = (unsigned long long)key << 32 | (0xFFFFFFFFu - (uint32_t)tok);
     }
-    if (tid == 0) a.count[slot] = a.k;
+    for (int i = a.k + tid; i < a.cap; i += kSelThreads) out[i] = 0;
   }
   if (warp == 0) {
     float m = lane < kSelThreads / 32 ? wmax[lane] : -INFINITY;
@@ -220,110 +220,190 @@ __global__ void __launch_bounds__(kSelThreads) beam_rows_kernel(const __grid_con
 }
 
 struct MergeSmem {
-  double base[kBeamsMost];   // log of the row's normaliser
-  double score[kBeamsMost], norm[kBeamsMost];  // length^alpha of a candidate
+  double lse[kBeamsMost], score[kBeamsMost];
+  double norm[kBeamsMost];                     // length^alpha of a candidate
+  float base[kBeamsMost], inv[kBeamsMost];     // score - lse, and least norm / norm
+  float top[kBeamsMost];
+  double sum[kBeamsMost];
+  double least[2];
   int len[kBeamsMost], kind[kBeamsMost];       // 0 nothing, 1 tokens, 2 itself
   unsigned long long key[kMergeList];          // ranks
   uint32_t beam[kMergeList], tok[kMergeList];
+  float logit[kMergeList];
   unsigned long long best_key[kMergeThreads / 32];
   unsigned long long best_id[kMergeThreads / 32];
   unsigned long long last_key, last_id;
   int n;
 };
 
-// One CTA a prompt; warps take (row, chunk) lists in turn.
+// One CTA a prompt.  64-bit arithmetic is slow here (two products a cycle and SM),
+// so candidates are first compared by float32 ranks with a bound of their error;
+// only those that may be among the k best get a rank in 64 bits.  What depends on
+// the beams alone is worked out while the rows are still being read.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
   __shared__ MergeSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.x, row0 = seq * a.beams;
   constexpr int kWarps = kMergeThreads / 32;
-  pdl_wait();
-  pdl_launch_dependents();
   if (tid == 0) sh.n = 0;
-  for (int b = warp; b < a.beams; b += kWarps) {
-    const int r = row0 + b;
+  // scores, lengths and flags were final before the call's first launch
+  if (tid < a.beams) {
+    const int r = row0 + tid;
     const float score = a.score[r];
     const bool done = a.done && a.done[r] != 0;
-    int kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
-    double lse = 0.0;
-    if (kind == 1) {
-      float M = -INFINITY;
-      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, a.top[(size_t)r * a.chunks + c]);
+    const int kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
+    const int next = (a.len ? a.len[r] : 0) + (kind == 1);
+    sh.score[tid] = (double)score;
+    sh.kind[tid] = kind;
+    sh.len[tid] = next;
+    // within 1e+-200, so that a rank times it is the score again
+    sh.norm[tid] = a.alpha != 0.f ? fmin(fmax(pow((double)max(next, 1), (double)a.alpha), 1e-200), 1e200) : 1.0;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  for (int b = warp; b < a.beams; b += kWarps) {
+    if (sh.kind[b] != 1) continue;
+    const size_t at = (size_t)(row0 + b) * a.chunks;
+    float M = -INFINITY;
+    double s = 0.0;
+    if (a.chunks <= 32) {
+      const float m = lane < a.chunks ? a.top[at + lane] : -INFINITY;
+      const double part = lane < a.chunks ? a.sum[at + lane] : 0.0;
+      M = warp_max(m);
+      if (m != -INFINITY) s = part * (double)expf(m - M);
+    } else {
+      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, a.top[at + c]);
       M = warp_max(M);
-      double s = 0.0;
       for (int c = lane; c < a.chunks; c += 32) {
-        const float m = a.top[(size_t)r * a.chunks + c];
-        if (m != -INFINITY) s += a.sum[(size_t)r * a.chunks + c] * exp((double)m - (double)M);
+        const float m = a.top[at + c];
+        if (m != -INFINITY) s += a.sum[at + c] * (double)expf(m - M);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      lse = (double)M + log(s);
-      if (!(fabs(lse) < INFINITY)) kind = 0;  // no token, +infinity
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
-      const int len = a.len ? a.len[r] : 0;
-      const int next = len + (kind == 1);
-      sh.base[b] = lse;
-      sh.score[b] = (double)score;
-      // within 1e+-200, so that a rank times it is the score again
-      sh.norm[b] = a.alpha != 0.f ? fmin(fmax(pow((double)max(next, 1), (double)a.alpha), 1e-200), 1e200) : 1.0;
-      sh.len[b] = next;
-      sh.kind[b] = kind;
+      sh.top[b] = M;
+      sh.sum[b] = s;
     }
   }
   __syncthreads();
-  auto rank = [&](int b, float logit) { return ((sh.score[b] + ((double)logit - sh.base[b]))) / sh.norm[b]; };
-  const int lists = a.beams * a.chunks;
-  // calls f(key, beam, token) for this thread's candidates
-  auto each = [&](auto f) {
-    for (int q = warp; q < lists; q += kWarps) {
-      const int b = q / a.chunks;
-      if (sh.kind[b] != 1) continue;
-      const size_t slot = (size_t)row0 * a.chunks + q;
-      const int n = a.count[slot];
-      for (int i = lane; i < n; i += 32) {
-        const unsigned long long w = a.cand[slot * a.cap + i];
-        f(double_key(rank(b, key_float((uint32_t)(w >> 32)))), (uint32_t)b, 0xFFFFFFFFu - (uint32_t)w);
+  if (tid < kBeamsMost) {  // two whole warps
+    double norm = 1e300;
+    if (tid < a.beams) {
+      if (sh.kind[tid] == 1) {
+        sh.lse[tid] = (double)sh.top[tid] + log(sh.sum[tid]);
+        if (!(fabs(sh.lse[tid]) < INFINITY)) sh.kind[tid] = 0;  // no token, or +infinity
+      } else {
+        sh.lse[tid] = 0.0;
       }
+      if (sh.kind[tid] != 0) norm = sh.norm[tid];
     }
-    if (tid < a.beams && sh.kind[tid] == 2) f(double_key(sh.score[tid] / sh.norm[tid]), (uint32_t)tid, (uint32_t)a.eos);
+    double least = norm;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = fmin(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) sh.least[warp] = least;  // of 32 beams
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    least = fmin(sh.least[0], sh.least[1]);
+    if (tid < a.beams) {
+      sh.base[tid] = (float)(sh.score[tid] - sh.lse[tid]);
+      sh.inv[tid] = a.alpha != 0.f ? (float)(least / sh.norm[tid]) : 1.f;
+    }
+  }
+  __syncthreads();
+
+  // Candidate `e` of the prompt's lists, with its beam; 0: none.
+  // (64 beams of 2^30 tokens: just above 2^31 candidates)
+  const uint32_t per_row = (uint32_t)a.chunks * a.cap, all = a.beams * per_row;
+  const unsigned long long* cand = a.cand + (size_t)row0 * per_row;
+  auto load = [&](uint32_t e) {
+    if (e >= all) return 0ull;
+    return sh.kind[e / per_row] == 1 ? cand[e] : 0ull;
   };
-  unsigned long long mine = 0;
-  each([&](unsigned long long key, uint32_t, uint32_t) { mine = key > mine ? key : mine; });
-  // the upper half of the k-th largest of the threads' best ranks, from below
+  // float32 rank (in units of the least norm) from below and from above: four
+  // roundings of numbers up to |base| + |logit|, and what is too small for a float
+  auto bounds = [&](int b, float logit, float& lo, float& hi) {
+    const float size = fabsf(sh.base[b]) + fabsf(logit), rank = (sh.base[b] + logit) * sh.inv[b];
+    const float e = size * (sh.inv[b] * 0x1p-21f + 0x1p-100f) + 0x1p-120f;
+    lo = rank - e;
+    hi = rank + e;
+  };
+  auto rank = [&](int b, float logit) {
+    const double s = sh.kind[b] == 1 ? sh.score[b] + ((double)logit - sh.lse[b]) : sh.score[b];
+    return double_key(s / sh.norm[b]);
+  };
+  constexpr int kRound = 8;  // candidates a thread at once
+  unsigned long long w[kRound];
+  const uint32_t rounds = (all + kRound * kMergeThreads - 1) / (kRound * kMergeThreads);
+  auto load_round = [&](uint32_t q) {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) w[i] = load((q * kRound + i) * kMergeThreads + tid);
+  };
+  auto beam_at = [&](uint32_t q, int i) { return (int)(((q * kRound + i) * kMergeThreads + tid) / per_row); };
+  float best = -INFINITY;
+  for (uint32_t q = 0; q < rounds; ++q) {
+    load_round(q);
+#pragma unroll
+    for (int i = 0; i < kRound; ++i)
+      if (w[i]) {
+        float lo, hi;
+        bounds(beam_at(q, i), key_float((uint32_t)(w[i] >> 32)), lo, hi);
+        best = fmaxf(best, lo);  // NaN takes no part
+      }
+  }
+  const bool itself = tid < a.beams && sh.kind[tid] == 2;  // a finished beam
+  float self_lo = 0.f, self_hi = 0.f;
+  if (itself) {
+    bounds(tid, 0.f, self_lo, self_hi);
+    best = fmaxf(best, self_lo);
+  }
+  // the k-th largest of the threads' best, to 24 bits from below
   uint32_t low = 0;
-  const uint32_t top = (uint32_t)(mine >> 32);
-  for (int bit = 31; bit >= 0; --bit) {
+  const uint32_t top = float_key(best);
+  for (int bit = 31; bit >= 8; --bit) {
     const uint32_t t = low | 1u << bit;
     if (__syncthreads_count(top >= t) >= a.k) low = t;
   }
-  if (low == 0) low = 1;  // fewer than k threads have any
-  each([&](unsigned long long key, uint32_t b, uint32_t tok) {
-    if ((uint32_t)(key >> 32) < low) return;
+  auto collect = [&](int b, uint32_t tok, float logit) {
     const int i = atomicAdd(&sh.n, 1);
     if (i < kMergeList) {
-      sh.key[i] = key;
       sh.beam[i] = b;
       sh.tok[i] = tok;
+      sh.logit[i] = logit;
     }
-  });
+  };
+  for (uint32_t q = 0; q < rounds; ++q) {
+    if (rounds > 1) load_round(q);
+#pragma unroll
+    for (int i = 0; i < kRound; ++i)
+      if (w[i]) {
+        const int b = beam_at(q, i);
+        const float logit = key_float((uint32_t)(w[i] >> 32));
+        float lo, hi;
+        bounds(b, logit, lo, hi);
+        if (!(float_key(hi) < low) || hi != hi) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], logit);
+      }
+  }
+  if (itself && (!(float_key(self_hi) < low) || self_hi != self_hi)) collect(tid, (uint32_t)a.eos, 0.f);
   __syncthreads();
   const int n = sh.n;
-  auto put = [&](int at, uint32_t b, uint32_t tok, float score) {
+  auto put = [&](int at, uint32_t b, uint32_t tok, unsigned long long key) {
     const size_t o = (size_t)seq * a.k + at;
     const bool none = b == 0xFFFFFFFFu;
     a.parent[o] = none ? -1 : (int)b;
     a.token[o] = none ? -1 : (int)tok;
-    a.score_out[o] = none ? -INFINITY : score;
+    float score = -INFINITY;
+    if (!none) {
+      const unsigned long long u = key ^ ((key >> 63) ? 0x8000000000000000ull : 0xFFFFFFFFFFFFFFFFull);
+      score = (float)(__longlong_as_double((long long)u) * sh.norm[b]);
+    }
+    a.score_out[o] = score;
     if (a.len_out) a.len_out[o] = none ? 0 : sh.len[b];
     if (a.done_out) a.done_out[o] = none ? 0 : (sh.kind[b] == 2 || (int)tok == a.eos);
   };
-  // a candidate's score, from its place in the lists
-  auto score_of = [&](uint32_t b, unsigned long long key) {
-    unsigned long long u = key ^ ((key >> 63) ? 0x8000000000000000ull : 0xFFFFFFFFFFFFFFFFull);
-    return __longlong_as_double((long long)u) * sh.norm[b];
-  };
   if (n <= kMergeList) {
+    for (int i = tid; i < n; i += kMergeThreads) sh.key[i] = rank(sh.beam[i], sh.logit[i]);
+    __syncthreads();
     // a candidate's place is the number of better ones
     for (int i = tid; i < n; i += kMergeThreads) {
       const unsigned long long key = sh.key[i];
@@ -331,12 +411,19 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       int at = 0;
       for (int j = 0; j < n; ++j)
         at += sh.key[j] > key || (sh.key[j] == key && (sh.beam[j] < b || (sh.beam[j] == b && sh.tok[j] < t)));
-      if (at < a.k) put(at, b, t, (float)score_of(b, key));
+      if (at < a.k) put(at, b, t, key);
     }
-    for (int i = n + tid; i < a.k; i += kMergeThreads) put(i, 0xFFFFFFFFu, 0, 0.f);
+    for (int i = n + tid; i < a.k; i += kMergeThreads) put(i, 0xFFFFFFFFu, 0, 0);
     return;
   }
-  // many equal ranks: one after another, each the best behind the last
+  // many (nearly) equal ranks: all of them in 64 bits, then one candidate after
+  // another, each the best behind the last
+  unsigned long long* ranks = a.ranks + (size_t)row0 * per_row;
+  for (uint32_t e = tid; e < all; e += kMergeThreads) {
+    const unsigned long long x = load(e);
+    ranks[e] = x ? rank((int)(e / per_row), key_float((uint32_t)(x >> 32))) : 0ull;
+  }
+  const unsigned long long self_key = itself ? rank(tid, 0.f) : 0ull;
   if (tid == 0) {
     sh.last_key = ~0ull;
     sh.last_id = 0;
@@ -345,14 +432,19 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   for (int i = 0; i < a.k; ++i) {
     const unsigned long long lk = sh.last_key, li = sh.last_id;
     unsigned long long bk = 0, bi = ~0ull;  // best rank, then lowest beam and token
-    each([&](unsigned long long key, uint32_t b, uint32_t tok) {
-      const unsigned long long id = (unsigned long long)b << 32 | tok;
-      if (key > lk || (key == lk && id <= li && lk != ~0ull)) return;
+    auto see = [&](unsigned long long key, unsigned long long id) {
+      if (key == 0 || key > lk || (key == lk && id <= li)) return;  // lk starts above every rank
       if (key > bk || (key == bk && id < bi)) {
         bk = key;
         bi = id;
       }
-    });
+    };
+    for (uint32_t e = tid; e < all; e += kMergeThreads) {
+      const unsigned long long key = ranks[e];
+      if (key >= bk && key != 0)
+        see(key, (unsigned long long)(e / per_row) << 32 | (0xFFFFFFFFu - (uint32_t)cand[e]));
+    }
+    see(self_key, (unsigned long long)tid << 32 | (uint32_t)a.eos);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long k2 = __shfl_xor_sync(0xffffffffu, bk, o), i2 = __shfl_xor_sync(0xffffffffu, bi, o);
@@ -367,15 +459,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     }
     __syncthreads();
     if (tid == 0) {
-      for (int w = 0; w < kWarps; ++w)
-        if (sh.best_key[w] > bk || (sh.best_key[w] == bk && sh.best_id[w] < bi)) {
-          bk = sh.best_key[w];
-          bi = sh.best_id[w];
+      for (int x = 0; x < kWarps; ++x)
+        if (sh.best_key[x] > bk || (sh.best_key[x] == bk && sh.best_id[x] < bi)) {
+          bk = sh.best_key[x];
+          bi = sh.best_id[x];
         }
       sh.last_key = bk;
       sh.last_id = bi;
-      const uint32_t b = (uint32_t)(bi >> 32);
-      put(i, b, (uint32_t)bi, (float)score_of(b, bk));
+      put(i, (uint32_t)(bi >> 32), (uint32_t)bi, bk);
     }
     __syncthreads();
   }
@@ -456,8 +547,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_cons
 struct SelWs {
   double* sum;
   unsigned long long* cand;
+  unsigned long long* ranks;
   float* top;
-  int* count;
   size_t bytes;
 };
 
@@ -476,8 +567,8 @@ static SelWs sel_ws(void* ws, int rows, int V, int k) {
   const size_t slots = (size_t)rows * sel_chunks(V);
   w.sum = reinterpret_cast<double*>(take(8 * slots));
   w.cand = reinterpret_cast<unsigned long long*>(take(8 * slots * 2 * k));
+  w.ranks = reinterpret_cast<unsigned long long*>(take(8 * slots * 2 * k));
   w.top = reinterpret_cast<float*>(take(4 * slots));
-  w.count = reinterpret_cast<int*>(take(4 * slots));
   w.bytes = off;
   return w;
 }
@@ -560,7 +651,7 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.done_out = d_done_out;
   a.sum = w.sum;
   a.top = w.top;
-  a.count = w.count;
+  a.ranks = w.ranks;
   a.cand = w.cand;
   a.err = &static_cast<WsHeader*>(d_ws)->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -17,14 +17,15 @@
 //   2. split: all query rows of a prompt's KV head against the prompt's keys
 //             that every one of them sees, on tcgen05 (tree_split_kernel): the
 //             prompt is read once for all its sequences;
-//   3. tail:  a cluster of CTAs a (sequence, KV head, new row) reads the
-//             sequence's own keys (and a window's edge in the prompt), joins
-//             the splits' partials; sink, gate, output.
+//   3. tail:  a few CTAs a (sequence, KV head, new row) read the sequence's own
+//             keys (and a window's edge in the prompt) and the splits' partials;
+//             the last of them joins their parts; sink, gate, output.
 // Without a long prompt the second launch is left out and the third reads the
 // prompt too.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "prefix.cuh"
 
@@ -52,6 +53,9 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
     head_load(w, norm, a.dqk, half, lane);
   }
   if (threadIdx.x == 0) zero = 0;
+  if (a.parts > 1)
+    for (int u = blockIdx.x * kPrefixPrepThreads + threadIdx.x; u < a.groups * a.per * a.nkv * a.items; u += gridDim.x * kPrefixPrepThreads)
+      a.tail_count[u] = 0;
   __syncthreads();
   if (it >= nq + 2 * nk) return;
   const int b = row / a.m, i = row % a.m, p = b / a.per;
@@ -88,25 +92,30 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 
 // ------------------------------------------------------------------ tail
 // Warps take steps of 8 keys in turn; a step's K and V rows come by bulk copy
-// into the warp's ring of buffers.  Lane (ks, l) has keys ks and ks + 4 of the
-// step and dims 32 j + 4 l .. + 3, for q.k as for p.v, so both are read from
-// shared memory without bank conflicts and a lane's part of the output covers
-// its keys alone; the four key groups' outputs meet once, at the end.  The eight
-// lanes' parts of the 2 RG products are summed by halves, so that each lane ends
-// with one or two of them and no exponential is taken twice.  All query rows of
-// a CTA are heads of one new row: they see the same keys, and no mask is needed.
-// RG: query rows (heads) a CTA; C: 32-dim blocks a head at most.
+// into the warp's buffers.  For q.k lane (ks, l) has keys ks and ks + 4 of the
+// step and dims 32 j + 4 l .. + 3; the eight lanes' parts of the 2 RG products are
+// summed by halves, so that each lane ends with one or two of them and no
+// exponential is taken twice.  The weights go through shared memory; for p.v a
+// lane has dims 4 l .. and 128 + 4 l .. of every key, so the output takes few
+// registers, many warps share an SM and hide each other's waits.  All query rows
+// of a CTA are heads of one new row: they see the same keys, and no mask is needed.
+// RG: query rows (heads) a CTA; H: 128-dim halves of the wider head size.
 //
 // float32 throughout (packed pairs).  Weights are relative to a reference that
 // moves only when a logit passes it by 2^8.
+#ifndef MTP_TAIL_SMEM
+#define MTP_TAIL_SMEM 72
+#endif
 constexpr int kTailWarps = 4;
 constexpr int kTailKeys = 8;
 constexpr float kTailMove = 8.f;
-constexpr int kTailStages = 3;  // buffers a warp at most
+constexpr int kTailStages = 2;  // buffers a warp at most
 
 struct alignas(16) TailSmem {
+  float2 p[kTailWarps][kTailKeys][8];        // a step's weights, each twice
   uint64_t full[kTailWarps][kTailStages];
   float m[kTailWarps][8], l[kTailWarps][8];  // a warp's state of each row
+  int last;                                  // this part is the last to arrive
 };
 
 __device__ __forceinline__ void bulk_load_keep(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -115,54 +124,27 @@ __device__ __forceinline__ void bulk_load_keep(void* dst, const void* src, uint3
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-// Shared memory of CTA `rank` of the cluster at this CTA's address.
-__device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
+// Lane's part of the products: PR rows (a power of two, RG or more), rows RG .. are 0.
+__host__ __device__ constexpr int tail_padded(int rg) { return rg <= 2 ? 2 : rg <= 4 ? 4 : 8; }
 
-template <int RG, int C>
-__global__ void __launch_bounds__(kTailWarps * 32, 2) prefix_tail_kernel(const __grid_constant__ PrefixArgs a, int stages) {
+// CTAs a SM that the registers allow.
+__host__ __device__ constexpr int tail_ctas(int rg, int h) { return h == 1 || rg <= 4 ? 4 : 3; }
+
+template <int RG, int H>
+__global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
+    prefix_tail_kernel(const __grid_constant__ PrefixArgs a, const int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ TailSmem sh;
-  static_assert(RG * C >= 4 && RG * C <= 32, "outputs in registers, at least one block a key group");
+  constexpr int PR = tail_padded(RG);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ks = lane >> 3, l8 = lane & 7;
-  const int rank = (int)cluster_rank(), csize = (int)cluster_size();
-  const int b = blockIdx.z, kv = blockIdx.y, item = blockIdx.x / csize;
+  const int b = blockIdx.z, kv = blockIdx.y, part = blockIdx.x / a.items, item = blockIdx.x % a.items;
   const int blocks = (a.G + RG - 1) / RG, i = item / blocks, g0 = item % blocks * RG;
   const int p = b / a.per, head = p * a.nkv + kv, nr = min(RG, a.G - g0);
-  const int cq = a.dqk / 32, cv = a.dv / 32;
+  const int cq = a.dqk / 32;
   const int r0 = ((b - p * a.per) * a.m + i) * a.G + g0;  // first query row
   float* qs = reinterpret_cast<float*>(sm);               // [RG][dqk]
-  const uint32_t kbytes = kTailKeys * a.dqk * 4, vbytes = kTailKeys * a.dv * 4;
-  uint8_t* ring = sm + RG * a.dqk * 4 + (size_t)warp * stages * (kbytes + vbytes);
+  const uint32_t kbytes = kTailKeys * a.dqk * 4, vbytes = kTailKeys * a.dv * 4, sbytes = kbytes + vbytes;
+  uint8_t* ring = sm + RG * a.dqk * 4 + warp * stages * sbytes;
   if (lane == 0) {
     for (int s = 0; s < kTailStages; ++s) mbar_init(&sh.full[warp][s], 1);
     mbar_fence_init();
@@ -175,33 +157,35 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) prefix_tail_kernel(const _
   const int e0 = min(sees, P), e1 = a.ns > 0 ? max(first, e0) : P;    // keys of the prompt
   const int t0 = max(0, sees - P), t1 = t + i + 1;                   // and of the tail
   const int ne = (e1 - e0 + kTailKeys - 1) / kTailKeys, nt = t < 0 ? 0 : ne + (t1 - t0 + kTailKeys - 1) / kTailKeys;
-  const int w0 = rank * kTailWarps + warp, stride = csize * kTailWarps;  // this warp's steps: w0, w0 + stride, ..
+  // the sequence's parts: as many as its keys need, each with every parts-th of
+  // the steps and of the splits' partials
+  const int parts = max(1, min(a.parts, (nt * kTailKeys + a.part_keys - 1) / a.part_keys));
+  if (part >= parts) return;
+  const int w0 = part * kTailWarps + warp, stride = parts * kTailWarps;  // this warp's steps: w0, w0 + stride, ..
+  const float* const kpre = a.keys + ((size_t)head * a.cap + e0) * a.dqk;
+  const float* const vpre = a.values + ((size_t)head * a.cap + e0) * a.dv;
+  const float* const kown = a.kt + (((size_t)b * a.nkv + kv) * a.tcap + t0) * a.dqk;
+  const float* const vown = a.vt + (((size_t)b * a.nkv + kv) * a.tcap + t0) * a.dv;
   Waiter wait{a.err, false};
-  auto step_keys = [&](int s, const float*& k, const float*& v) {
-    if (s < ne) {
-      const int k0 = e0 + s * kTailKeys;
-      k = a.keys + ((size_t)head * a.cap + k0) * a.dqk;
-      v = a.values + ((size_t)head * a.cap + k0) * a.dv;
-      return min(kTailKeys, e1 - k0);
-    }
-    const int k0 = t0 + (s - ne) * kTailKeys;
-    k = a.kt + (((size_t)b * a.nkv + kv) * a.tcap + k0) * a.dqk;
-    v = a.vt + (((size_t)b * a.nkv + kv) * a.tcap + k0) * a.dv;
-    return min(kTailKeys, t1 - k0);
-  };
+  auto step_size = [&](int s) { return min(kTailKeys, s < ne ? e1 - e0 - s * kTailKeys : t1 - t0 - (s - ne) * kTailKeys); };
   auto fetch = [&](int s, int slot) {
-    if (s >= nt || lane != 0) return;
-    const float *k, *v;
-    const int n = step_keys(s, k, v);
-    uint8_t* dst = ring + (size_t)slot * (kbytes + vbytes);
+    if (lane != 0) return;
+    const int n = step_size(s);
+    const size_t row = (size_t)(s < ne ? s : s - ne) * kTailKeys;
+    uint8_t* dst = ring + slot * sbytes;
     mbar_arrive_expect_tx(&sh.full[warp][slot], (uint32_t)n * (a.dqk + a.dv) * 4);
-    bulk_load_keep(dst, k, (uint32_t)n * a.dqk * 4, &sh.full[warp][slot]);
-    bulk_load_keep(dst + kbytes, v, (uint32_t)n * a.dv * 4, &sh.full[warp][slot]);
+    bulk_load_keep(dst, (s < ne ? kpre : kown) + row * a.dqk, (uint32_t)n * a.dqk * 4, &sh.full[warp][slot]);
+    bulk_load_keep(dst + kbytes, (s < ne ? vpre : vown) + row * a.dv, (uint32_t)n * a.dv * 4, &sh.full[warp][slot]);
   };
+  // steps below `early` hold no row that this call appends
+  const int early = min(nt, ne + max(0, t - t0) / kTailKeys);
+  for (int s = 0; s < stages; ++s)
+    if (w0 + s * stride < early) fetch(w0 + s * stride, s);
   pdl_wait();
   pdl_launch_dependents();
   fence_proxy_async_global();
-  for (int s = 0; s < stages; ++s) fetch(w0 + s * stride, s);
+  for (int s = 0; s < stages; ++s)
+    if (w0 + s * stride >= early && w0 + s * stride < nt) fetch(w0 + s * stride, s);
   for (int c = 4 * threadIdx.x; c < RG * a.dqk; c += 4 * kTailWarps * 32) {
     const bool in = c < nr * a.dqk && t >= 0;
     *reinterpret_cast<float4*>(qs + c) =
@@ -209,64 +193,137 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) prefix_tail_kernel(const _
   }
   __syncthreads();
 
-  uint64_t o[RG][C][2];
+  uint64_t o[RG][H][2];
 #pragma unroll
   for (int r = 0; r < RG; ++r)
 #pragma unroll
-    for (int j = 0; j < C; ++j) o[r][j][0] = o[r][j][1] = 0ull;
-  constexpr int PL = RG * 2 / 8 > 0 ? RG * 2 / 8 : 1;  // products a lane ends with
+    for (int h = 0; h < H; ++h) o[r][h][0] = o[r][h][1] = 0ull;
+  constexpr int PL = PR == 8 ? 2 : 1;  // products a lane ends with
+  // this lane's row and keys: PR = 8: row l8, keys ks and ks + 4; 4: row l8 / 2,
+  // key ks + 4 (l8 % 2); 2: row l8 / 4, key ks + 4 (l8 / 2 % 2), twice
+  const int mine = ks + 4 * (PR == 8 ? 0 : PR == 4 ? l8 & 1 : l8 >> 1 & 1), row = l8 / (8 / PR);
+  int vcol[H];  // this lane's dims of a value (past the last one: any, and not stored)
+#pragma unroll
+  for (int h = 0; h < H; ++h) vcol[h] = min(128 * h + 4 * lane, a.dv - 4);
   float ref = -INFINITY, l = 0.f;
+  // the warp starts from its share of the splits' partials, in the layout of its
+  // own output, while the first keys are on their way
+  if (a.ns > 0 && t >= 0) {
+    const size_t at = (size_t)head * a.ns * a.R + r0;
+    const float2* ml_at = a.part_ml + at + min(row, nr - 1);
+    constexpr int NB = RG * H <= 5 ? 3 : RG * H <= 8 ? 2 : 1;  // splits at once: their reads wait together
+#pragma unroll 1
+    for (int s0 = w0; s0 < a.ns; s0 += NB * stride) {
+      ulonglong2 v[NB][RG][H];
+      float2 ml[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int s = s0 + k * stride;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (s < a.ns) ml[k] = ml_at[(size_t)s * a.R];
+        const float* po = a.part_o + (at + (size_t)s * a.R) * a.dv;
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            v[k][r][h] = make_ulonglong2(0ull, 0ull);
+            if (s < a.ns) v[k][r][h] = *reinterpret_cast<const ulonglong2*>(po + (size_t)min(r, nr - 1) * a.dv + vcol[h]);
+          }
+      }
+      float to = ref;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) to = fmaxf(to, ml[k].x);
+      const float corr = ref == -INFINITY ? 1.f : ex2(ref - to);  // nothing, or NaN, was summed without a reference
+      ref = to;
+      l *= corr;
+      float f[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        // a partial of NaN logits alone has no maximum, and its sum is NaN
+        f[k] = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - ref);
+        if (mine == 0) l += f[k] * ml[k].y;
+      }
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        const float c1 = __shfl_sync(0xffffffffu, corr, r * (8 / PR), 8);
+        const uint64_t c2 = pack2(c1, c1);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          o[r][h][0] = mul2(o[r][h][0], c2);
+          o[r][h][1] = mul2(o[r][h][1], c2);
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          const float w = __shfl_sync(0xffffffffu, f[k], r * (8 / PR), 8);
+          const uint64_t w2 = pack2(w, w);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            o[r][h][0] = fma2(w2, v[k][r][h].x, o[r][h][0]);
+            o[r][h][1] = fma2(w2, v[k][r][h].y, o[r][h][1]);
+          }
+        }
+      }
+    }
+  }
   int slot = 0;
   uint32_t phase = 0;
 #pragma unroll 1
   for (int s = w0; s < nt; s += stride) {
-    const float *kg, *vg;
-    const int n = step_keys(s, kg, vg);
-    float* kb = reinterpret_cast<float*>(ring + (size_t)slot * (kbytes + vbytes));
-    float* vb = reinterpret_cast<float*>(ring + (size_t)slot * (kbytes + vbytes) + kbytes);
+    const int n = step_size(s);
+    float* kb = reinterpret_cast<float*>(ring + slot * sbytes);
+    float* vb = reinterpret_cast<float*>(ring + slot * sbytes + kbytes);
     wait(&sh.full[warp][slot], phase);
     if (n < kTailKeys) {  // rows behind the last key take part with weight 0
       for (int c = n * a.dv + 4 * lane; c < kTailKeys * a.dv; c += 128)
         *reinterpret_cast<float4*>(vb + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      __syncwarp();
+      fence_proxy_async_shared_cta();  // before a later copy into the buffer
     }
     uint64_t acc[RG][2];
 #pragma unroll
     for (int r = 0; r < RG; ++r) acc[r][0] = acc[r][1] = 0ull;
+    // blocks of 128, 64 and 32 dims, each without a branch, so that its reads go out together
+    auto dots = [&](int c, auto blocks) {
+      constexpr int N = decltype(blocks)::value;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (j < cq) {
-        const int c = 32 * j + 4 * l8;
-        const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(kb + ks * a.dqk + c);
-        const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(kb + (ks + 4) * a.dqk + c);
+      for (int j = 0; j < N; ++j) {
+        const ulonglong2 k0 = *reinterpret_cast<const ulonglong2*>(kb + ks * a.dqk + c + 32 * j);
+        const ulonglong2 k1 = *reinterpret_cast<const ulonglong2*>(kb + (ks + 4) * a.dqk + c + 32 * j);
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + r * a.dqk + c);
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qs + r * a.dqk + c + 32 * j);
           acc[r][0] = fma2(q.x, k0.x, acc[r][0]);
           acc[r][1] = fma2(q.x, k1.x, acc[r][1]);
           acc[r][0] = fma2(q.y, k0.y, acc[r][0]);
           acc[r][1] = fma2(q.y, k1.y, acc[r][1]);
         }
       }
-    }
+    };
+    int c = 4 * l8;
+    if (cq >= 4) dots(c, std::integral_constant<int, 4>{}), c += 128;
+    if (H == 2 && cq >= 8) dots(c, std::integral_constant<int, 4>{}), c += 128;
+    if (cq & 2) dots(c, std::integral_constant<int, 2>{}), c += 64;
+    if (cq & 1) dots(c, std::integral_constant<int, 1>{});
     // product 2 r + k of row r and key ks + 4 k, summed over the eight lanes
-    float x[2 * RG];
+    float x[2 * PR];
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
+    for (int r = 0; r < PR; ++r)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float2 f = unpack2(acc[r][k]);
-        x[2 * r + k] = f.x + f.y;
+        x[2 * r + k] = 0.f;
+        if (r < RG) {
+          const float2 f = unpack2(acc[r][k]);
+          x[2 * r + k] = f.x + f.y;
+        }
       }
     {
-      int left = 2 * RG;
+      int left = 2 * PR;
 #pragma unroll
       for (int d = 4; d > 0; d >>= 1) {
         if (left > 1) {
           left /= 2;
           const bool upper = l8 & d;
 #pragma unroll
-          for (int y = 0; y < RG; ++y)
+          for (int y = 0; y < PR; ++y)
             if (y < left) {
               const float give = upper ? x[y] : x[y + left], keep = upper ? x[y + left] : x[y];
               x[y] = keep + __shfl_xor_sync(0xffffffffu, give, d);
@@ -276,17 +333,13 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) prefix_tail_kernel(const _
         }
       }
     }
-    // this lane's row and keys: RG = 8: row l8, both keys; 4: row l8 / 2, key
-    // l8 % 2; 2: row l8 / 4, key l8 / 2 % 2 (twice)
-    const int mine = ks + 4 * (RG == 8 ? 0 : RG == 4 ? l8 & 1 : l8 >> 1 & 1);
     float mx;
-    if (RG == 8) {
-      if (mine >= n) x[0] = -INFINITY;
+    if (mine >= n) x[0] = -INFINITY;
+    if (PR == 8) {
       if (mine + 4 >= n) x[PL - 1] = -INFINITY;
       mx = fmaxf(x[0], x[PL - 1]);
     } else {
-      if (mine >= n) x[0] = -INFINITY;
-      mx = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], RG == 4 ? 1 : 2));
+      mx = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], PR == 4 ? 1 : 2));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -298,222 +351,224 @@ __global__ void __launch_bounds__(kTailWarps * 32, 2) prefix_tail_kernel(const _
       l *= corr;
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
-        const float f = __shfl_sync(0xffffffffu, corr, r * (8 / RG), 8);
+        const float f = __shfl_sync(0xffffffffu, corr, r * (8 / PR), 8);
         const uint64_t f2 = pack2(f, f);
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          o[r][j][0] = mul2(o[r][j][0], f2);
-          o[r][j][1] = mul2(o[r][j][1], f2);
+        for (int h = 0; h < H; ++h) {
+          o[r][h][0] = mul2(o[r][h][0], f2);
+          o[r][h][1] = mul2(o[r][h][1], f2);
         }
       }
     }
     const float nref = ref == -INFINITY ? 0.f : ref;
-    float pr[PL];
 #pragma unroll
     for (int k = 0; k < PL; ++k) {
-      pr[k] = ex2(x[k] - nref);
-      l += pr[k];
+      const float w = ex2(x[k] - nref);
+      l += w;
+      sh.p[warp][mine + 4 * k][row] = make_float2(w, w);
     }
-    uint64_t w[RG][2];
+    __syncwarp();
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
+    for (int k = 0; k < kTailKeys; ++k) {
+      uint64_t w[8];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float f = RG == 8 ? __shfl_sync(0xffffffffu, pr[PL == 2 ? k : 0], r, 8)
-                                : __shfl_sync(0xffffffffu, pr[0], RG == 4 ? 2 * r + k : 4 * r + 2 * k, 8);
-        w[r][k] = pack2(f, f);
+      for (int r = 0; r < RG; r += 2) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&sh.p[warp][k][r]);
+        w[r] = u.x;
+        w[r + 1] = u.y;
       }
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (j < cv) {
-        const int c = 32 * j + 4 * l8;
-        const ulonglong2 v0 = *reinterpret_cast<const ulonglong2*>(vb + ks * a.dv + c);
-        const ulonglong2 v1 = *reinterpret_cast<const ulonglong2*>(vb + (ks + 4) * a.dv + c);
+      for (int h = 0; h < H; ++h) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(vb + k * a.dv + vcol[h]);
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
-          o[r][j][0] = fma2(w[r][0], v0.x, o[r][j][0]);
-          o[r][j][1] = fma2(w[r][0], v0.y, o[r][j][1]);
-          o[r][j][0] = fma2(w[r][1], v1.x, o[r][j][0]);
-          o[r][j][1] = fma2(w[r][1], v1.y, o[r][j][1]);
+          o[r][h][0] = fma2(w[r], v.x, o[r][h][0]);
+          o[r][h][1] = fma2(w[r], v.y, o[r][h][1]);
         }
       }
     }
-    // every lane has read the buffer before it is filled anew
-    fence_proxy_async_shared_cta();
-    __syncwarp();
-    fetch(s + stages * stride, slot);
+    __syncwarp();  // every lane has read the buffer before it is filled anew
+    if (s + stages * stride < nt) fetch(s + stages * stride, slot);
     if (++slot == stages) {
       slot = 0;
       phase ^= 1u;
     }
   }
-  // the warp's state: sums over the key groups, each lane keeping a quarter of
-  // its blocks
+  // the warp's state
   l += __shfl_xor_sync(0xffffffffu, l, 8);
   l += __shfl_xor_sync(0xffffffffu, l, 16);
-  if (RG == 4) l += __shfl_xor_sync(0xffffffffu, l, 1);
-  if (RG == 2) l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (ks == 0 && l8 % (8 / RG) == 0) {
-    sh.m[warp][l8 / (8 / RG)] = ref;
-    sh.l[warp][l8 / (8 / RG)] = l;
+  if (PR == 4) l += __shfl_xor_sync(0xffffffffu, l, 1);
+  if (PR == 2) l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (ks == 0 && l8 % (8 / PR) == 0) {
+    sh.m[warp][row] = ref;
+    sh.l[warp][row] = l;
   }
-  {
-    float y[RG * C * 4];
+  float* const states = reinterpret_cast<float*>(sm + RG * a.dqk * 4);  // a warp's at the start of its buffers
+  const int wstep = stages * sbytes / 4;
 #pragma unroll
-    for (int r = 0; r < RG; ++r)
+  for (int r = 0; r < RG; ++r)
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const float2 u = unpack2(o[r][j][0]), v = unpack2(o[r][j][1]);
-        y[(r * C + j) * 4] = u.x;
-        y[(r * C + j) * 4 + 1] = u.y;
-        y[(r * C + j) * 4 + 2] = v.x;
-        y[(r * C + j) * 4 + 3] = v.y;
-      }
-    constexpr int N = RG * C * 4;
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      const float give = lane & 16 ? y[e] : y[e + N / 2], keep = lane & 16 ? y[e + N / 2] : y[e];
-      y[e] = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+    for (int h = 0; h < H; ++h) {
+      const int c = 128 * h + 4 * lane;
+      if (c < a.dv) *reinterpret_cast<ulonglong2*>(states + warp * wstep + r * a.dv + c) = make_ulonglong2(o[r][h][0], o[r][h][1]);
     }
-#pragma unroll
-    for (int e = 0; e < N / 4; ++e) {
-      const float give = lane & 8 ? y[e] : y[e + N / 4], keep = lane & 8 ? y[e + N / 4] : y[e];
-      y[e] = keep + __shfl_xor_sync(0xffffffffu, give, 8);
-    }
-    float* st = reinterpret_cast<float*>(ring);  // [RG][dv]
-    const int from = (lane >> 4) * (RG * C / 2) + (lane >> 3 & 1) * (RG * C / 4);
-#pragma unroll
-    for (int e = 0; e < RG * C / 4; ++e) {
-      const int r = (from + e) / C, j = (from + e) % C;
-      if (j < cv)
-        *reinterpret_cast<float4*>(st + r * a.dv + 32 * j + 4 * l8) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-    }
-  }
-  cluster_sync();
+  __syncthreads();
 
-  // Join: a warp a row, over the cluster; lane l has dims 4 l .. and 128 + 4 l ..
-  constexpr int H = C / 4;
-  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  const uint32_t ring_at = smem_u32(sm) + RG * a.dqk * 4, ring_step = stages * (kbytes + vbytes);
-  const int states = csize * kTailWarps;
-#pragma unroll 1
-  for (int r = w0; r < nr && t >= 0; r += stride) {
+  // Join: a warp a row; lane l has dims 4 l .. and 128 + 4 l ..  A state of NaN
+  // logits alone has no maximum, and its sum is NaN.
+  auto weight = [](float m, float sum, float top) { return m == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2(m - top); };
+  float4 y[H];
+  auto finish = [&](int r, float M, float den) {
     const int h = kv * a.G + g0 + r;
-    const float sink = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
-    float4 gate[H];
-    if (a.gated)
+    if (a.sinks) {
+      const float sink = a.sinks[h] * kLog2e, to = fmaxf(M, sink);
+      if (to != M) {  // M may be -infinity: then nothing was summed
+        const float f = weight(M, den, to);
+        den *= f;
 #pragma unroll
-      for (int x = 0; x < H; ++x)
-        gate[x] = dims4(a.qp + (size_t)(b * a.m + i) * a.ldq + ((size_t)2 * h + 1) * a.dqk, a.dqk, lane, x);
-    float sm_ = -INFINITY, sl = 0.f;
-    if (lane < states) {
-      sm_ = ld_peer(peer(smem_u32(&sh.m[lane % kTailWarps][r]), lane / kTailWarps));
-      sl = ld_peer(peer(smem_u32(&sh.l[lane % kTailWarps][r]), lane / kTailWarps));
-    }
-    float M = fmaxf(sink, warp_max(sm_));
-    const size_t at = (size_t)head * a.ns * a.R + r0 + r;
-    for (int s = lane; s < a.ns; s += 32) M = fmaxf(M, a.part_ml[at + (size_t)s * a.R].x);
-    M = warp_max(M);
-    // a state of NaN logits alone has no maximum, and its sum is NaN
-    auto weight = [&](float m, float sum) { return m == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2(m - M); };
-    float den = 0.f;
-    float4 y[H];
-#pragma unroll
-    for (int x = 0; x < H; ++x) y[x] = none;
-    {
-      const float f = lane < states ? weight(sm_, sl) : 0.f;
-      den += warp_sum(f * sl);
-      unsigned there = __ballot_sync(0xffffffffu, lane < states && !(sl == 0.f));
-#pragma unroll 1
-      while (there) {
-        const int s = __ffs(there) - 1;
-        there &= there - 1;
-        const float w = __shfl_sync(0xffffffffu, f, s);
-        const uint32_t src = peer(ring_at + (uint32_t)(s % kTailWarps) * ring_step + (uint32_t)r * a.dv * 4, s / kTailWarps);
-#pragma unroll
-        for (int x = 0; x < H; ++x)
-          if (128 * x + 4 * lane < a.dv) add4(y[x], w, ld_peer4(src + (128 * x + 4 * lane) * 4));
+        for (int x = 0; x < H; ++x) scale4(y[x], f);
       }
+      if (sink != -INFINITY) den += ex2(sink - to);
     }
-#pragma unroll 1
-    for (int s0 = 0; s0 < a.ns; s0 += 32) {
-      const float2 ml = s0 + lane < a.ns ? a.part_ml[at + (size_t)(s0 + lane) * a.R] : make_float2(-INFINITY, 0.f);
-      const float f = weight(ml.x, ml.y);
-      den += warp_sum(f * ml.y);
-      const float* po = a.part_o + (at + (size_t)s0 * a.R) * a.dv;
-      const int n = min(32, a.ns - s0);
-#pragma unroll 4
-      for (int s = 0; s < n; ++s) {
-        const float w = __shfl_sync(0xffffffffu, f, s);
-#pragma unroll
-        for (int x = 0; x < H; ++x) add4(y[x], w, dims4(po + (size_t)s * a.R * a.dv, a.dv, lane, x));
-      }
-    }
-    if (sink != -INFINITY) den += ex2(sink - M);
     const float inv = den == 0.f ? 0.f : 1.f / den;
+    const size_t at = (size_t)(b * a.m + i);
 #pragma unroll
     for (int x = 0; x < H; ++x) {
       const int c = 128 * x + 4 * lane;
       scale4(y[x], inv);
       if (a.gated) {
-        y[x].x /= 1.f + expf(-gate[x].x);
-        y[x].y /= 1.f + expf(-gate[x].y);
-        y[x].z /= 1.f + expf(-gate[x].z);
-        y[x].w /= 1.f + expf(-gate[x].w);
+        const float4 g = dims4(a.qp + at * a.ldq + ((size_t)2 * h + 1) * a.dqk, a.dqk, lane, x);
+        y[x].x = __fdividef(y[x].x, 1.f + expf(-g.x));
+        y[x].y = __fdividef(y[x].y, 1.f + expf(-g.y));
+        y[x].z = __fdividef(y[x].z, 1.f + expf(-g.z));
+        y[x].w = __fdividef(y[x].w, 1.f + expf(-g.w));
       }
-      if (c < a.dv) *reinterpret_cast<float4*>(a.out + ((size_t)(b * a.m + i) * a.nh + h) * a.dv + c) = y[x];
+      if (c < a.dv) *reinterpret_cast<float4*>(a.out + (at * a.nh + h) * a.dv + c) = y[x];
+    }
+  };
+  // the four warps' states of a row
+  auto own = [&](int r, float& M, float& den) {
+    M = -INFINITY;
+    den = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTailWarps; ++w) M = fmaxf(M, sh.m[w][r]);
+#pragma unroll
+    for (int x = 0; x < H; ++x) y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kTailWarps; ++w) {
+      const float f = weight(sh.m[w][r], sh.l[w][r], M);
+      den += f * sh.l[w][r];
+#pragma unroll
+      for (int x = 0; x < H; ++x) add4(y[x], f, dims4(states + w * wstep + r * a.dv, a.dv, lane, x));
+    }
+  };
+  if (parts == 1) {
+#pragma unroll 1
+    for (int r = warp; r < nr && t >= 0; r += kTailWarps) {
+      float M, den;
+      own(r, M, den);
+      finish(r, M, den);
+    }
+  } else {
+    // the part's state to memory; the last part to arrive joins them all
+    const size_t unit = ((size_t)b * a.nkv + kv) * a.items + item;
+    float2* const ml = a.tail_ml + (unit * a.parts + part) * RG;
+    float* const po = a.tail_o + (unit * a.parts + part) * RG * a.dv;
+#pragma unroll 1
+    for (int r = warp; r < nr; r += kTailWarps) {
+      float M, den;
+      own(r, M, den);
+      if (lane == 0) __stcg(ml + r, make_float2(M, den));
+#pragma unroll
+      for (int x = 0; x < H; ++x)
+        if (128 * x + 4 * lane < a.dv) __stcg(reinterpret_cast<float4*>(po + r * a.dv + 128 * x + 4 * lane), y[x]);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.last = atom_add_acq_rel_gpu(a.tail_count + unit, 1u) == (unsigned)parts - 1;
+    __syncthreads();
+    if (sh.last) {
+      const float2* const ml0 = a.tail_ml + unit * a.parts * RG;
+      const float* const po0 = a.tail_o + unit * a.parts * RG * a.dv;
+#pragma unroll 1
+      for (int r = warp; r < nr && t >= 0; r += kTailWarps) {
+        const float2 m = lane < parts ? __ldcg(ml0 + lane * RG + r) : make_float2(-INFINITY, 0.f);  // lane s has part s's
+        const float M = warp_max(m.x), f = weight(m.x, m.y, M), den = warp_sum(f * m.y);
+#pragma unroll
+        for (int x = 0; x < H; ++x) y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+          const float w = __shfl_sync(0xffffffffu, f, s);
+#pragma unroll
+          for (int x = 0; x < H; ++x)
+            if (128 * x + 4 * lane < a.dv)
+              add4(y[x], w, __ldcg(reinterpret_cast<const float4*>(po0 + ((size_t)s * RG + r) * a.dv + 128 * x + 4 * lane)));
+        }
+        finish(r, M, den);
+      }
     }
   }
-  cluster_sync();  // the peers have read this CTA's states
   wait.settle();
 }
 
 // ------------------------------------------------------------------ host
+// Heads a CTA of the tail launch: a KV head's in as few CTAs as 8 a CTA allow, as
+// even as they go.
+static int tail_rows(int G) {
+  const int blocks = (G + 7) / 8, each = (G + blocks - 1) / blocks;
+  return each <= 2 ? 2 : each <= 4 ? 4 : each == 7 ? 8 : each;
+}
 static size_t tail_smem(int rg, int dqk, int dv, int stages) {
   return (size_t)rg * dqk * 4 + (size_t)kTailWarps * stages * kTailKeys * (dqk + dv) * 4;
 }
+// Two buffers a warp where three CTAs with them fit an SM.
+static int tail_stages(int rg, int dqk, int dv) { return tail_smem(rg, dqk, dv, kTailStages) <= MTP_TAIL_SMEM * 1024 ? kTailStages : 1; }
 
-template <int RG, int C>
-static cudaError_t launch_tail_as(const PrefixArgs& a, int csize, cudaStream_t st) {
-  const int stages = tail_smem(RG, a.dqk, a.dv, kTailStages) <= 112 * 1024 ? kTailStages : 2;
-  const size_t smem = tail_smem(RG, a.dqk, a.dv, stages);
+template <int RG, int H>
+static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
+  const int stages = tail_stages(RG, a.dqk, a.dv);
+  static_assert(RG <= kTailKeys, "a warp's state fits one buffer of values");
   static std::atomic<bool> attr[64];  // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(csize * a.m * ((a.G + RG - 1) / RG), a.nkv, a.groups * a.per);
-  cfg.blockDim = dim3(kTailWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = csize;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 2 : 1;
-  launch_mark(st);
-  return cudaLaunchKernelEx(&cfg, prefix_tail_kernel<RG, C>, a, stages);
+  return launch_pdl(prefix_tail_kernel<RG, H>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
+                    tail_smem(RG, a.dqk, a.dv, stages), st, a, stages);
 }
 
-static cudaError_t launch_tail(const PrefixArgs& a, int csize, cudaStream_t st) {
-  if (a.dqk <= 128 && a.dv <= 128) {
-    if (a.G <= 2) return launch_tail_as<2, 4>(a, csize, st);
-    return a.G <= 4 ? launch_tail_as<4, 4>(a, csize, st) : launch_tail_as<8, 4>(a, csize, st);
+template <int H>
+static cudaError_t launch_tail_h(const PrefixArgs& a, cudaStream_t st) {
+  switch (tail_rows(a.G)) {
+    case 2: return launch_tail_as<2, H>(a, st);
+    case 4: return launch_tail_as<4, H>(a, st);
+    case 5: return launch_tail_as<5, H>(a, st);
+    case 6: return launch_tail_as<6, H>(a, st);
+    default: return launch_tail_as<8, H>(a, st);
   }
-  return a.G <= 2 ? launch_tail_as<2, 8>(a, csize, st) : launch_tail_as<4, 8>(a, csize, st);
 }
 
-// Query heads a CTA of the tail launch.
-static int tail_rows(int dqk, int dv, int G) {
-  return G <= 2 ? 2 : G <= 4 || dqk > 128 || dv > 128 ? 4 : 8;
+static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
+  return a.dqk <= 128 && a.dv <= 128 ? launch_tail_h<1>(a, st) : launch_tail_h<2>(a, st);
+}
+
+// Parts of a sequence's keys, for `units` (sequence, KV head, new row, block of
+// heads): up to kTailCtas CTAs a SM, of kPartBytes of keys and values or more; one
+// warp joins them.
+constexpr int kTailCtas = 4, kPartBytes = 64 * 1024;
+
+struct TailPlan {
+  int parts, keys;  // keys a part
+};
+static TailPlan tail_plan(long long units, long long own, int dims, int sms) {
+  const long long most = std::min<long long>(32, std::max<long long>(1, (long long)kTailCtas * sms / units));
+  TailPlan p;
+  p.keys = (int)std::min<long long>(1 << 30, (std::max<long long>(kPartBytes / (4 * dims), (own + most - 1) / most) + 31) / 32 * 32);
+  p.parts = (int)std::max<long long>(1, (own + p.keys - 1) / p.keys);
+  return p;
 }
 
 // Splits of a prompt's keys: the fewest waves of CTAs (one a SM) times the keys
@@ -551,8 +606,9 @@ struct PrefixWs {
   float* qf;
   uint8_t* qt;
   float* qinv;
-  float2* ml;
-  float* o;
+  unsigned* tail_count;
+  float2 *ml, *tail_ml;
+  float *o, *tail_o;
   size_t bytes;
 };
 
@@ -564,7 +620,9 @@ static size_t most_partials(const mtp_attn_geom* g, size_t tiles, size_t rows, i
   return std::min(rows * ((keys + kSplitKeys - 1) / kSplitKeys), 128 * std::max(tiles, (size_t)kSplitWaves * sms));
 }
 
-static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs, int m, size_t partials) {
+// `partials`: split partials' rows; `units`, `parts`: of the tail launch, where it joins several parts.
+static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs, int m, size_t partials, size_t units,
+                          size_t tails) {
   PrefixWs w = {};
   size_t off = sizeof(WsHeader) + kRuleJoinBytes;
   uint8_t* b = static_cast<uint8_t*>(ws);
@@ -581,13 +639,18 @@ static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs
   w.qinv = reinterpret_cast<float*>(take(tiles * 128 * 4));
   w.ml = reinterpret_cast<float2*>(take(8 * partials));
   w.o = reinterpret_cast<float*>(take(4 * partials * g->head_dim_v));
+  w.tail_count = reinterpret_cast<unsigned*>(take(4 * units));
+  w.tail_ml = reinterpret_cast<float2*>(take(8 * tails));
+  w.tail_o = reinterpret_cast<float*>(take(4 * tails * g->head_dim_v));
   w.bytes = off;
   return w;
 }
 
 static size_t prefix_ws_bound(const mtp_attn_geom* g, int groups, int seqs, int m, int pmax) {
   const size_t rows = (size_t)seqs * m * g->n_heads, tiles = rows / 128 + (size_t)groups * g->n_kv_heads;
-  return prefix_ws(nullptr, g, groups, seqs, m, most_partials(g, tiles, rows, pmax, sm_count())).bytes;
+  // several parts: at most kTailCtas CTAs a SM, of at most 8 rows
+  const size_t ctas = (size_t)kTailCtas * sm_count();
+  return prefix_ws(nullptr, g, groups, seqs, m, most_partials(g, tiles, rows, pmax, sm_count()), ctas, 8 * ctas).bytes;
 }
 
 static mtp_status check_prefix_geom(const mtp_attn_geom* g) {
@@ -699,7 +762,18 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   const int sms = sm_count(), heads = a.groups * a.nkv;
   const int keys = shared_keys(g, m, pmax);
   a.ns = pmax <= kTailPrompt ? 0 : prefix_splits(heads * a.mt, keys, sms);
-  const PrefixWs w = prefix_ws(d_ws, g, a.groups, B->n_seqs, m, (size_t)heads * a.R * a.ns);
+  // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
+  const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
+  long long own = (long long)edge + tmax + m;
+  if (a.window > 0) own = std::min<long long>(own, a.window);
+  const int rg = tail_rows(a.G);
+  a.items = m * ((a.G + rg - 1) / rg);
+  const long long units = (long long)B->n_seqs * a.nkv * a.items;
+  const TailPlan tp = tail_plan(units, own, a.dqk + a.dv, sms);
+  a.parts = tp.parts;
+  a.part_keys = tp.keys;
+  const PrefixWs w = prefix_ws(d_ws, g, a.groups, B->n_seqs, m, (size_t)heads * a.R * a.ns, tp.parts > 1 ? units : 0,
+                               tp.parts > 1 ? (size_t)units * tp.parts * rg : 0);
   if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
     return fail(MTP_ERR_WORKSPACE, "attn_prefix_sink: workspace too small or misaligned");
   a.keys = d_k_prefix;
@@ -722,19 +796,16 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   a.qinv = w.qinv;
   a.part_o = w.o;
   a.part_ml = w.ml;
+  a.tail_count = w.tail_count;
+  a.tail_ml = w.tail_ml;
+  a.tail_o = w.tail_o;
   a.err = &static_cast<WsHeader*>(d_ws)->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long items = (long long)B->n_seqs * m * (a.nh + 2 * a.nkv);
-  // CTAs of a sequence's keys: two a SM in all, of 64 keys or more each
-  const int edge = a.ns > 0 ? (a.window > 0 ? std::min(pmax, tmax + m) : 0) : pmax;
-  const long long own = a.window > 0 ? std::min<long long>((long long)edge + tmax + m, a.window) : (long long)edge + tmax + m;
-  const long long ctas = (long long)B->n_seqs * a.nkv * m * ((a.G + tail_rows(a.dqk, a.dv, a.G) - 1) / tail_rows(a.dqk, a.dv, a.G));
-  int csize = 1;
-  while (csize < 8 && ctas * csize < 2 * sms && own > 64 * csize) csize *= 2;
   cudaError_t e = launch_pdl(prefix_prep_kernel, dim3((unsigned)((items + kPrefixPrepThreads / 32 - 1) / (kPrefixPrepThreads / 32))),
                              kPrefixPrepThreads, 0, st, a);
   if (e == cudaSuccess && a.ns > 0) e = launch_prefix_split(a, st);
-  if (e == cudaSuccess) e = launch_tail(a, csize, st);
+  if (e == cudaSuccess) e = launch_tail(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "attn_prefix_sink launch");
   return MTP_OK;
 }

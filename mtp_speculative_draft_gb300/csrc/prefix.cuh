@@ -24,6 +24,11 @@ struct PrefixArgs : SplitArgs {
   const int *plen, *tlen;
   float* out;
   float* qf;                     // [groups * nkv][R][dqk] scaled queries
+  int items;                     // CTAs of a sequence's KV head: new rows times blocks of query heads
+  int parts, part_keys;          // parts of a sequence's own keys at most, keys of a part
+  unsigned* tail_count;          // [seqs][nkv][items] parts that have arrived
+  float2* tail_ml;               // [seqs][nkv][items][parts][rows] their states
+  float* tail_o;                 // [seqs][nkv][items][parts][rows][dv]
 };
 
 __device__ __forceinline__ int prompt_len(const PrefixArgs& a, int p) {
