@@ -31,13 +31,14 @@ constexpr int kSelChunk = kSelThreads * kSelPer;    // logits a CTA
 constexpr int kBeamsMost = 64, kBeamTop = 128;      // beams and candidates of a prompt
 constexpr int kBeamRows = 1024;                     // beams of a call
 constexpr int kSelVocab = 1 << 30;                  // tokens
-constexpr int kMergeThreads = 512;
+constexpr int kMergeThreads = 1024;
 constexpr int kMergeList = 1024;                    // candidates that are put in order at once
 
 struct SelArgs {
   const float* x;
   long long ld;
   int beams, V, k, chunks, cap, eos;
+  unsigned long long magic;   // 2^64 / (chunks * cap), rounded up: an index' row by a product
   float alpha;
   const float* score;
   const int *len, *done;
@@ -71,17 +72,44 @@ __device__ __forceinline__ bool beam_live(const SelArgs& a, int r) {
   return (!a.done || a.done[r] == 0) && fabsf(a.score[r]) < INFINITY;
 }
 
+// The k-th largest of n keys in shared memory (n a multiple of 4, above or equal
+// to k), by counting for each the ones before it: threads below n, one of which
+// finds it.
+__device__ __forceinline__ void kth_largest(const uint32_t* keys, int n, int k, uint32_t* found) {
+  const int tid = threadIdx.x;
+  if (tid >= n) return;
+  const uint32_t mine = keys[tid];
+  int before = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; i += 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(keys + i);
+    before += (x.x > mine || (x.x == mine && i < tid)) + (x.y > mine || (x.y == mine && i + 1 < tid)) +
+              (x.z > mine || (x.z == mine && i + 2 < tid)) + (x.w > mine || (x.w == mine && i + 3 < tid));
+  }
+  if (before == k - 1) *found = mine;
+}
+
+struct RowsSmem {
+  alignas(16) uint32_t group[kSelThreads];        // largest keys of groups of threads
+  alignas(16) uint32_t wmax[kSelThreads / 32];    // and of warps
+  uint32_t sum[kSelThreads / 32][2];              // a warp's sum, in 2^-20 and 2^-40
+  uint32_t low;
+  int n;
+};
+
 // grid (chunks, rows).  Bound by HBM on many rows; a row's logits are read once
-// and stay in registers.  The k-th largest of the threads' largest logits bounds
-// the chunk's k-th largest from below, so the few logits at or above it hold the
-// chunk's k largest; where equal logits make them more than 2 k, the k largest
-// are found exactly (lower tokens first among equals).
+// and stay in registers.  The k-th largest of the largest logits of groups of
+// threads bounds the chunk's k-th largest from below, so the few logits at or
+// above it hold the chunk's k largest; where equal logits make them more than
+// `cap`, the k largest are found exactly (lower tokens first among equals).
+// A thread's sum of exponentials has 6 roundings a term; the threads' are added
+// exactly, in integers of 2^-20 and 2^-40 (a 64-bit addition costs a warp 16 cycles
+// of an SM: 64 rows of 152577 took 16 us with them, 9 without).
 __global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(const __grid_constant__ SelArgs a) {
-  __shared__ float wmax[kSelThreads / 32];
-  __shared__ double wsum[kSelThreads / 32];
-  __shared__ int n;
+  __shared__ RowsSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, r = blockIdx.y;
+  constexpr int kWarps = kSelThreads / 32;
   pdl_wait();
   pdl_launch_dependents();
   const size_t slot = (size_t)r * a.chunks + c;
@@ -103,53 +131,76 @@ __global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(co
       if (e + 2 >= 0 && e + 2 < a.V) f.z = x[e + 2];
       if (e + 3 >= 0 && e + 3 < a.V) f.w = x[e + 3];
     }
-    v[4 * j] = f.x;
-    v[4 * j + 1] = f.y;
-    v[4 * j + 2] = f.z;
-    v[4 * j + 3] = f.w;
+    v[4 * j] = fmaxf(f.x, -INFINITY);  // NaN counts as -infinity
+    v[4 * j + 1] = fmaxf(f.y, -INFINITY);
+    v[4 * j + 2] = fmaxf(f.z, -INFINITY);
+    v[4 * j + 3] = fmaxf(f.w, -INFINITY);
   }
-  if (tid == 0) n = 0;
+  if (tid == 0) sh.n = 0;
   float mx = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kSelPer; ++j) mx = fmaxf(mx, v[j]);  // NaN takes no part
-  // sum of exponentials relative to the warp's largest logit
-  const float wm = warp_max(mx), ref = wm == -INFINITY ? 0.f : wm;
-  float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < kSelPer; ++j) s4[j & 3] += v[j] == v[j] ? ex2((v[j] - ref) * kLog2e) : 0.f;
-  double s = (double)(s4[0] + s4[1]) + (double)(s4[2] + s4[3]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) {
-    wmax[warp] = wm;
-    wsum[warp] = s;
+  for (int j = 0; j < kSelPer; ++j) mx = fmaxf(mx, v[j]);
+  const uint32_t top = float_key(mx), wtop = __reduce_max_sync(0xffffffffu, top);
+  // groups of 4 threads do for few candidates (64 groups, 18 logits at or above
+  // the 16th's), single threads for many
+  uint32_t gtop = top;
+  const bool quads = a.k <= 16;
+  if (quads) {
+    gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 1));
+    gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 2));
   }
-  // the largest 16 bits of a key that k threads reach
-  const uint32_t top = float_key(mx);
-  uint32_t low = 0;
-  for (int bit = 31; bit >= 16; --bit) {
-    const uint32_t t = low | 1u << bit;
-    if (__syncthreads_count(top >= t) >= a.k) low = t;
-  }
-  low = max(low, kNoKey + 1);
-  int here = 0;
-  if (top >= low) {
-#pragma unroll
-    for (int j = 0; j < kSelPer; ++j) here += float_key(v[j]) >= low;
-  }
-  int at = here ? atomicAdd(&n, here) : 0;
+  if (!quads || (lane & 3) == 0) sh.group[quads ? tid >> 2 : tid] = gtop;
+  if (lane == 0) sh.wmax[warp] = wtop;
   __syncthreads();
-  const int total = n;
-  unsigned long long* out = a.cand + slot * a.cap;
-  if (total <= a.cap) {
-    if (here) {
+  uint32_t mtop = 0;
 #pragma unroll
-      for (int j = 0; j < kSelPer; ++j) {
-        const uint32_t key = float_key(v[j]);
-        const uint32_t tok = (uint32_t)(e0 + (j >> 2) * 4 * kSelThreads + (j & 3));
-        if (key >= low) out[at++] = (unsigned long long)key << 32 | (0xFFFFFFFFu - tok);
-      }
+  for (int w = 0; w < kWarps; ++w) mtop = max(mtop, sh.wmax[w]);
+  const float M = key_float(mtop), ref = M == -INFINITY ? 0.f : M;  // the chunk's largest logit
+  kth_largest(sh.group, quads ? kSelThreads / 4 : kSelThreads, a.k, &sh.low);
+  float s8[8] = {};
+#pragma unroll
+  for (int j = 0; j < kSelPer; ++j) s8[j & 7] += ex2((v[j] - ref) * kLog2e);
+  const float s = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+  // at most 32; NaN (+infinity in the row) is marked by a sum that no row has
+  const bool bad = __any_sync(0xffffffffu, s != s);
+  const uint32_t s1 = (uint32_t)(s * 0x1p20f), s2 = (uint32_t)((s * 0x1p20f - (float)s1) * 0x1p20f);
+  const uint32_t t1 = __reduce_add_sync(0xffffffffu, s1), t2 = __reduce_add_sync(0xffffffffu, s2);
+  if (lane == 0) {
+    sh.sum[warp][0] = bad ? 0xFFFFFFFFu : t1;
+    sh.sum[warp][1] = t2;
+  }
+  __syncthreads();
+  const float low = key_float(max(sh.low, kNoKey + 1));
+  unsigned long long* out = a.cand + slot * a.cap;
+  if (mx >= low) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < kSelPer; ++j) mask |= v[j] >= low ? 1u << j : 0u;
+    int at = atomicAdd(&sh.n, __popc(mask));
+#pragma unroll 1
+    for (; mask; mask &= mask - 1, ++at) {
+      const int j = __ffs(mask) - 1, tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
+      if (at < a.cap) out[at] = (unsigned long long)float_key(x[tok]) << 32 | (0xFFFFFFFFu - (uint32_t)tok);
     }
+  }
+  if (warp == kWarps - 1) {
+    double t = 0.0;
+    bool nan = false;
+    if (lane < kWarps) {
+      nan = sh.sum[lane][0] == 0xFFFFFFFFu;
+      t = (double)sh.sum[lane][0] * 0x1p-20 + (double)sh.sum[lane][1] * 0x1p-40;
+    }
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    nan = __any_sync(0xffffffffu, nan);
+    if (lane == 0) {
+      a.top[slot] = M;
+      a.sum[slot] = nan ? __longlong_as_double(0x7FF8000000000000ll) : t;
+    }
+  }
+  __syncthreads();
+  const int total = sh.n;
+  if (total <= a.cap) {
     for (int i = total + tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate
   } else {
     // the k-th largest key, then how many of that key are wanted, and up to which token
@@ -161,12 +212,12 @@ __global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(co
 #pragma unroll
       for (int j = 0; j < kSelPer; ++j) m += float_key(v[j]) >= t;
       __syncthreads();
-      if (tid == 0) n = 0;
+      if (tid == 0) sh.n = 0;
       __syncthreads();
       m = __reduce_add_sync(0xffffffffu, m);
-      if (lane == 0) atomicAdd(&n, m);
+      if (lane == 0) atomicAdd(&sh.n, m);
       __syncthreads();
-      if (n >= a.k) kth = t;
+      if (sh.n >= a.k) kth = t;
     }
     // of the tokens with that key, the lowest below `end` are taken: the least
     // end at which k tokens are there
@@ -182,15 +233,15 @@ __global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(co
         m += key > kth || (key == kth && tok < t);
       }
       __syncthreads();
-      if (tid == 0) n = 0;
+      if (tid == 0) sh.n = 0;
       __syncthreads();
       m = __reduce_add_sync(0xffffffffu, m);
-      if (lane == 0) atomicAdd(&n, m);
+      if (lane == 0) atomicAdd(&sh.n, m);
       __syncthreads();
-      if (n < a.k) end = t;
+      if (sh.n < a.k) end = t;
     }
     __syncthreads();
-    if (tid == 0) n = 0;
+    if (tid == 0) sh.n = 0;
     __syncthreads();
 #pragma unroll 1
     for (int j = 0; j < kSelPer; ++j) {
@@ -201,33 +252,51 @@ __global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(co
       const int tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
       const uint32_t key = float_key(f);
       if (key > kth || (key == kth && tok <= end))
-        out[atomicAdd(&n, 1)] = (unsigned long long)key << 32 | (0xFFFFFFFFu - (uint32_t)tok);
+        out[atomicAdd(&sh.n, 1)] = (unsigned long long)key << 32 | (0xFFFFFFFFu - (uint32_t)tok);
     }
     for (int i = a.k + tid; i < a.cap; i += kSelThreads) out[i] = 0;
   }
-  if (warp == 0) {
-    float m = lane < kSelThreads / 32 ? wmax[lane] : -INFINITY;
-    const float M = warp_max(m);
-    // +infinity, in whichever warp, makes the sum NaN
-    double t = lane < kSelThreads / 32 && m != -INFINITY ? wsum[lane] * (double)expf(m - M) : 0.0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) {
-      a.top[slot] = M;
-      a.sum[slot] = t;
-    }
-  }
 }
+
+// Tables of logarithms and powers, worked out by the compiler: of the middles
+// c = 1 + (i + 1/2) / 128, log c = 2 artanh((c - 1) / (c + 1)) and 1 / c; of
+// exponents i / 32, exp(i / 32 log 2) by its series.
+constexpr int kLogSteps = 128, kExpSteps = 32;
+constexpr double kLn2 = 0.69314718055994530942;
+struct MathTables {
+  double logs[kLogSteps], inverse[kLogSteps], powers[kExpSteps];
+};
+constexpr MathTables make_tables() {
+  MathTables t = {};
+  for (int i = 0; i < kLogSteps; ++i) {
+    const double c = 1.0 + (i + 0.5) / kLogSteps, z = (c - 1) / (c + 1);
+    double sum = 0.0, term = z;
+    for (int n = 1; n < 60; n += 2, term *= z * z) sum += term / n;
+    t.logs[i] = 2 * sum;
+    t.inverse[i] = 1 / c;
+  }
+  for (int i = 0; i < kExpSteps; ++i) {
+    double sum = 0.0, term = 1.0;
+    for (int n = 1; n < 30; ++n) {
+      sum += term;
+      term *= i * kLn2 / kExpSteps / n;
+    }
+    t.powers[i] = sum;
+  }
+  return t;
+}
+__device__ const MathTables kTables = make_tables();
 
 struct MergeSmem {
   double lse[kBeamsMost], score[kBeamsMost];
-  double norm[kBeamsMost];                     // length^alpha of a candidate
-  float base[kBeamsMost], inv[kBeamsMost];     // score - lse, and least norm / norm
-  float top[kBeamsMost];
-  double sum[kBeamsMost];
+  double norm[kBeamsMost], inverse[kBeamsMost];  // length^alpha of a candidate, and its inverse
+  MathTables math;
   double least[2];
-  int len[kBeamsMost], kind[kBeamsMost];       // 0 nothing, 1 tokens, 2 itself
-  unsigned long long key[kMergeList];          // ranks
+  float base[kBeamsMost], inv[kBeamsMost];       // score - lse, and inverse / the largest inverse
+  int len[kBeamsMost], kind[kBeamsMost];         // 0 nothing, 1 tokens, 2 itself
+  alignas(16) uint32_t group[256];
+  uint32_t low;
+  unsigned long long key[kMergeList];            // ranks
   uint32_t beam[kMergeList], tok[kMergeList];
   float logit[kMergeList];
   unsigned long long best_key[kMergeThreads / 32];
@@ -236,134 +305,131 @@ struct MergeSmem {
   int n;
 };
 
+// log of a finite s >= 2^-1022 after P. T. P. Tang's table-driven method (1990):
+// s = 2^e f, f = c (1 + u) with c the middle of f's step, |u| <= 2^-8; the series of
+// log(1 + u) up to u^5 leaves less than 2^-50.
+__device__ __forceinline__ double table_log(const MathTables& t, double s) {
+  const unsigned long long w = (unsigned long long)__double_as_longlong(s);
+  const int e = (int)(w >> 52) - 1023, i = (int)(w >> 45) & (kLogSteps - 1);
+  const double f = __longlong_as_double((long long)((w & 0xFFFFFFFFFFFFFull) | 0x3FF0000000000000ull));
+  const double u = (f - (1.0 + (i + 0.5) / kLogSteps)) * t.inverse[i];
+  return e * kLn2 + (t.logs[i] + u * (1.0 + u * (-1.0 / 2 + u * (1.0 / 3 + u * (-1.0 / 4 + u * (1.0 / 5))))));
+}
+// exp of |x| < 700 after his method for exponentials (1989): x = (32 e + i) log 2 / 32
+// + u, |u| <= 0.0109; the series of exp u up to u^6 leaves less than 2^-57.
+__device__ __forceinline__ double table_exp(const MathTables& t, double x) {
+  const int n = __float2int_rn((float)x * (float)(kExpSteps / kLn2));
+  const double u = x - n * (kLn2 / kExpSteps);
+  const double p = 1.0 + u * (1.0 + u * (1.0 / 2 + u * (1.0 / 6 + u * (1.0 / 24 + u * (1.0 / 120 + u * (1.0 / 720))))));
+  const int e = n >> 5;  // rounded down
+  return t.powers[n & (kExpSteps - 1)] * p * __longlong_as_double((long long)(e + 1023) << 52);
+}
+
 // One CTA a prompt.  64-bit arithmetic is slow here (two products a cycle and SM),
 // so candidates are first compared by float32 ranks with a bound of their error;
 // only those that may be among the k best get a rank in 64 bits.  What depends on
-// the beams alone is worked out while the rows are still being read.
+// the beams alone is worked out while the rows are still being read.  Bound by the
+// latency of its steps and of fetching its instructions, which are few for that.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
   __shared__ MergeSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.x, row0 = seq * a.beams;
   constexpr int kWarps = kMergeThreads / 32;
   if (tid == 0) sh.n = 0;
+  if (tid < (int)(sizeof(MathTables) / 8)) reinterpret_cast<double*>(&sh.math)[tid] = reinterpret_cast<const double*>(&kTables)[tid];
   // scores, lengths and flags were final before the call's first launch
+  int next = 1, kind = 0;
   if (tid < a.beams) {
     const int r = row0 + tid;
     const float score = a.score[r];
     const bool done = a.done && a.done[r] != 0;
-    const int kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
-    const int next = (a.len ? a.len[r] : 0) + (kind == 1);
+    kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
+    next = (a.len ? a.len[r] : 0) + (kind == 1);
     sh.score[tid] = (double)score;
+    sh.base[tid] = score;  // of a finished beam
     sh.kind[tid] = kind;
     sh.len[tid] = next;
-    // within 1e+-200, so that a rank times it is the score again
-    sh.norm[tid] = a.alpha != 0.f ? fmin(fmax(pow((double)max(next, 1), (double)a.alpha), 1e-200), 1e200) : 1.0;
+    sh.lse[tid] = 0.0;
+    sh.norm[tid] = sh.inverse[tid] = 1.0;
+    sh.inv[tid] = 1.f;
   }
+  __syncthreads();
+  if (a.alpha != 0.f && tid < kBeamsMost) {  // two whole warps
+    // within 1e+-200, so that a rank times it is the score again
+    double most = 0.0, inverse = 0.0;
+    if (tid < a.beams) {
+      const double x = fmin(fmax((double)a.alpha * table_log(sh.math, (double)max(next, 1)), -460.5), 460.5);
+      sh.norm[tid] = table_exp(sh.math, x);
+      sh.inverse[tid] = inverse = table_exp(sh.math, -x);
+      if (kind) most = inverse;
+    }
+    for (int o = 16; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) sh.least[warp] = most;
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+    most = fmax(sh.least[0], sh.least[1]);
+    if (tid < a.beams && kind) sh.inv[tid] = (float)(inverse / most);
+  }
+  // Candidate `e` of the prompt's lists; 0: none.  (64 beams of 2^30 tokens: just
+  // above 2^31 candidates.)
+  const uint32_t per_row = (uint32_t)a.chunks * a.cap, all = a.beams * per_row;
+  const unsigned long long* cand = a.cand + (size_t)row0 * per_row;
+  auto beam_of = [&](uint32_t e) { return (int)__umul64hi((unsigned long long)e, a.magic); };
+  constexpr int kRound = 4;  // candidates a thread at once
+  const uint32_t rounds = (all + kRound * kMergeThreads - 1) / (kRound * kMergeThreads);
+  unsigned long long w[kRound];
+  auto load_round = [&](uint32_t q) {
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const uint32_t e = (q * kRound + i) * kMergeThreads + tid;
+      w[i] = e < all ? cand[e] : 0ull;  // anything where a row was not read
+    }
+  };
   pdl_wait();
   pdl_launch_dependents();
-  __syncthreads();
+  load_round(0);  // on their way while the rows' normalisers are worked out
+#pragma unroll 1
   for (int b = warp; b < a.beams; b += kWarps) {
     if (sh.kind[b] != 1) continue;
     const size_t at = (size_t)(row0 + b) * a.chunks;
-    float M = -INFINITY;
+    float m = -INFINITY;
     double s = 0.0;
-    if (a.chunks <= 32) {
-      const float m = lane < a.chunks ? a.top[at + lane] : -INFINITY;
-      const double part = lane < a.chunks ? a.sum[at + lane] : 0.0;
-      M = warp_max(m);
-      if (m != -INFINITY) s = part * (double)expf(m - M);
-    } else {
-      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, a.top[at + c]);
-      M = warp_max(M);
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float m = a.top[at + c];
-        if (m != -INFINITY) s += a.sum[at + c] * (double)expf(m - M);
-      }
+    if (lane < a.chunks) {
+      m = a.top[at + lane];
+      s = a.sum[at + lane];
     }
-#pragma unroll
+    float M = m;
+    for (int c = lane + 32; c < a.chunks; c += 32) M = fmaxf(M, a.top[at + c]);
+    M = warp_max(M);
+    s = m == -INFINITY ? 0.0 : s * (double)expf(m - M);
+    for (int c = lane + 32; c < a.chunks; c += 32) {
+      m = a.top[at + c];
+      if (m != -INFINITY) s += a.sum[at + c] * (double)expf(m - M);
+    }
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
-      sh.top[b] = M;
-      sh.sum[b] = s;
-    }
-  }
-  __syncthreads();
-  if (tid < kBeamsMost) {  // two whole warps
-    double norm = 1e300;
-    if (tid < a.beams) {
-      if (sh.kind[tid] == 1) {
-        sh.lse[tid] = (double)sh.top[tid] + log(sh.sum[tid]);
-        if (!(fabs(sh.lse[tid]) < INFINITY)) sh.kind[tid] = 0;  // no token, or +infinity
+      if (fabsf(M) < INFINITY && s == s) {
+        const double lse = (double)M + table_log(sh.math, s);
+        sh.lse[b] = lse;
+        sh.base[b] = (float)(sh.score[b] - lse);
       } else {
-        sh.lse[tid] = 0.0;
+        sh.kind[b] = 0;  // no token, or +infinity
       }
-      if (sh.kind[tid] != 0) norm = sh.norm[tid];
-    }
-    double least = norm;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) least = fmin(least, __shfl_xor_sync(0xffffffffu, least, o));
-    if (lane == 0) sh.least[warp] = least;  // of 32 beams
-    asm volatile("bar.sync 1, 64;" ::: "memory");
-    least = fmin(sh.least[0], sh.least[1]);
-    if (tid < a.beams) {
-      sh.base[tid] = (float)(sh.score[tid] - sh.lse[tid]);
-      sh.inv[tid] = a.alpha != 0.f ? (float)(least / sh.norm[tid]) : 1.f;
     }
   }
   __syncthreads();
 
-  // Candidate `e` of the prompt's lists, with its beam; 0: none.
-  // (64 beams of 2^30 tokens: just above 2^31 candidates)
-  const uint32_t per_row = (uint32_t)a.chunks * a.cap, all = a.beams * per_row;
-  const unsigned long long* cand = a.cand + (size_t)row0 * per_row;
-  auto load = [&](uint32_t e) {
-    if (e >= all) return 0ull;
-    return sh.kind[e / per_row] == 1 ? cand[e] : 0ull;
-  };
-  // float32 rank (in units of the least norm) from below and from above: four
+  // float32 rank (in units of the largest inverse) from below and from above: four
   // roundings of numbers up to |base| + |logit|, and what is too small for a float
   auto bounds = [&](int b, float logit, float& lo, float& hi) {
-    const float size = fabsf(sh.base[b]) + fabsf(logit), rank = (sh.base[b] + logit) * sh.inv[b];
-    const float e = size * (sh.inv[b] * 0x1p-21f + 0x1p-100f) + 0x1p-120f;
+    const float inv = sh.inv[b], base = sh.base[b], size = fabsf(base) + fabsf(logit), rank = (base + logit) * inv;
+    const float e = size * (inv * 0x1p-21f + 0x1p-100f) + 0x1p-120f;
     lo = rank - e;
     hi = rank + e;
   };
   auto rank = [&](int b, float logit) {
     const double s = sh.kind[b] == 1 ? sh.score[b] + ((double)logit - sh.lse[b]) : sh.score[b];
-    return double_key(s / sh.norm[b]);
+    return double_key(s * sh.inverse[b]);
   };
-  constexpr int kRound = 8;  // candidates a thread at once
-  unsigned long long w[kRound];
-  const uint32_t rounds = (all + kRound * kMergeThreads - 1) / (kRound * kMergeThreads);
-  auto load_round = [&](uint32_t q) {
-#pragma unroll
-    for (int i = 0; i < kRound; ++i) w[i] = load((q * kRound + i) * kMergeThreads + tid);
-  };
-  auto beam_at = [&](uint32_t q, int i) { return (int)(((q * kRound + i) * kMergeThreads + tid) / per_row); };
-  float best = -INFINITY;
-  for (uint32_t q = 0; q < rounds; ++q) {
-    load_round(q);
-#pragma unroll
-    for (int i = 0; i < kRound; ++i)
-      if (w[i]) {
-        float lo, hi;
-        bounds(beam_at(q, i), key_float((uint32_t)(w[i] >> 32)), lo, hi);
-        best = fmaxf(best, lo);  // NaN takes no part
-      }
-  }
-  const bool itself = tid < a.beams && sh.kind[tid] == 2;  // a finished beam
-  float self_lo = 0.f, self_hi = 0.f;
-  if (itself) {
-    bounds(tid, 0.f, self_lo, self_hi);
-    best = fmaxf(best, self_lo);
-  }
-  // the k-th largest of the threads' best, to 24 bits from below
-  uint32_t low = 0;
-  const uint32_t top = float_key(best);
-  for (int bit = 31; bit >= 8; --bit) {
-    const uint32_t t = low | 1u << bit;
-    if (__syncthreads_count(top >= t) >= a.k) low = t;
-  }
   auto collect = [&](int b, uint32_t tok, float logit) {
     const int i = atomicAdd(&sh.n, 1);
     if (i < kMergeList) {
@@ -372,19 +438,45 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       sh.logit[i] = logit;
     }
   };
-  for (uint32_t q = 0; q < rounds; ++q) {
-    if (rounds > 1) load_round(q);
+  // first the threads' best from below, of which the k-th largest bounds the k best;
+  // then every candidate that may reach it
+  const bool itself = tid < a.beams && sh.kind[tid] == 2;  // a finished beam
+  float best = -INFINITY, self_hi = -INFINITY;
+  if (itself) bounds(tid, 0.f, best, self_hi);
+  uint32_t low = 0xFFFFFFFFu, hik[kRound];
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (uint32_t q = 0; q < rounds; ++q) {
+      if (rounds > 1 && q + pass > 0) load_round(q);
 #pragma unroll
-    for (int i = 0; i < kRound; ++i)
-      if (w[i]) {
-        const int b = beam_at(q, i);
-        const float logit = key_float((uint32_t)(w[i] >> 32));
-        float lo, hi;
-        bounds(b, logit, lo, hi);
-        if (!(float_key(hi) < low) || hi != hi) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], logit);
+      for (int i = 0; i < kRound; ++i) {
+        const int b = min(beam_of((q * kRound + i) * kMergeThreads + tid), a.beams - 1);
+        if (pass == 0 || rounds > 1) {
+          hik[i] = 0;
+          if (w[i] != 0 && sh.kind[b] == 1) {
+            float lo, hi;
+            bounds(b, key_float((uint32_t)(w[i] >> 32)), lo, hi);
+            best = fmaxf(best, lo);  // NaN takes no part
+            hik[i] = hi == hi ? float_key(hi) : 0xFFFFFFFFu;
+          }
+        }
+        if (hik[i] >= low) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], key_float((uint32_t)(w[i] >> 32)));
       }
+    }
+    if (pass == 0) {
+      uint32_t top = float_key(best);
+      const int share = a.k <= 16 ? kMergeThreads / 64 : kMergeThreads / 256;  // threads a group
+      for (int o = 1; o < share; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (tid % share == 0) sh.group[tid / share] = top;
+      __syncthreads();
+      kth_largest(sh.group, kMergeThreads / share, a.k, &sh.low);
+      __syncthreads();
+      low = max(sh.low, 1u);  // 0: no candidate
+    } else if (itself && (self_hi != self_hi || float_key(self_hi) >= low)) {
+      collect(tid, (uint32_t)a.eos, 0.f);
+    }
   }
-  if (itself && (!(float_key(self_hi) < low) || self_hi != self_hi)) collect(tid, (uint32_t)a.eos, 0.f);
   __syncthreads();
   const int n = sh.n;
   auto put = [&](int at, uint32_t b, uint32_t tok, unsigned long long key) {
@@ -404,14 +496,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   if (n <= kMergeList) {
     for (int i = tid; i < n; i += kMergeThreads) sh.key[i] = rank(sh.beam[i], sh.logit[i]);
     __syncthreads();
-    // a candidate's place is the number of better ones
-    for (int i = tid; i < n; i += kMergeThreads) {
+    // a candidate's place is the number of better ones: a warp a candidate
+    for (int i = warp; i < n; i += kWarps) {
       const unsigned long long key = sh.key[i];
       const uint32_t b = sh.beam[i], t = sh.tok[i];
       int at = 0;
-      for (int j = 0; j < n; ++j)
+      for (int j = lane; j < n; j += 32)
         at += sh.key[j] > key || (sh.key[j] == key && (sh.beam[j] < b || (sh.beam[j] == b && sh.tok[j] < t)));
-      if (at < a.k) put(at, b, t, key);
+      at = __reduce_add_sync(0xffffffffu, at);
+      if (lane == 0 && at < a.k) put(at, b, t, key);
     }
     for (int i = n + tid; i < a.k; i += kMergeThreads) put(i, 0xFFFFFFFFu, 0, 0);
     return;
@@ -420,8 +513,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   // another, each the best behind the last
   unsigned long long* ranks = a.ranks + (size_t)row0 * per_row;
   for (uint32_t e = tid; e < all; e += kMergeThreads) {
-    const unsigned long long x = load(e);
-    ranks[e] = x ? rank((int)(e / per_row), key_float((uint32_t)(x >> 32))) : 0ull;
+    const int b = beam_of(e);
+    const unsigned long long x = sh.kind[b] == 1 ? cand[e] : 0ull;
+    ranks[e] = x ? rank(b, key_float((uint32_t)(x >> 32))) : 0ull;
   }
   const unsigned long long self_key = itself ? rank(tid, 0.f) : 0ull;
   if (tid == 0) {
@@ -442,7 +536,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     for (uint32_t e = tid; e < all; e += kMergeThreads) {
       const unsigned long long key = ranks[e];
       if (key >= bk && key != 0)
-        see(key, (unsigned long long)(e / per_row) << 32 | (0xFFFFFFFFu - (uint32_t)cand[e]));
+        see(key, (unsigned long long)beam_of(e) << 32 | (0xFFFFFFFFu - (uint32_t)cand[e]));
     }
     see(self_key, (unsigned long long)tid << 32 | (uint32_t)a.eos);
 #pragma unroll
@@ -552,6 +646,10 @@ struct SelWs {
   size_t bytes;
 };
 
+// Candidates of a chunk that are kept: about as many as reach the k-th largest of
+// the groups' largest (18 for 16 candidates, 73 for 64, 176 for 128), and some.
+static int sel_cap(int k) { return k + k / 4 + k * k / 256 + 8; }
+
 // Chunks of a row of V logits at any alignment.
 static int sel_chunks(int V) { return (int)(((int64_t)V + 3 + kSelChunk - 1) / kSelChunk); }
 
@@ -566,8 +664,8 @@ static SelWs sel_ws(void* ws, int rows, int V, int k) {
   };
   const size_t slots = (size_t)rows * sel_chunks(V);
   w.sum = reinterpret_cast<double*>(take(8 * slots));
-  w.cand = reinterpret_cast<unsigned long long*>(take(8 * slots * 2 * k));
-  w.ranks = reinterpret_cast<unsigned long long*>(take(8 * slots * 2 * k));
+  w.cand = reinterpret_cast<unsigned long long*>(take(8 * slots * sel_cap(k)));
+  w.ranks = reinterpret_cast<unsigned long long*>(take(8 * slots * sel_cap(k)));
   w.top = reinterpret_cast<float*>(take(4 * slots));
   w.bytes = off;
   return w;
@@ -638,7 +736,8 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.V = B->vocab;
   a.k = k;
   a.chunks = sel_chunks(B->vocab);
-  a.cap = 2 * k;
+  a.cap = sel_cap(k);
+  a.magic = ~0ull / ((unsigned long long)a.chunks * a.cap) + 1;
   a.eos = B->eos;
   a.alpha = B->length_penalty;
   a.score = B->d_score;
