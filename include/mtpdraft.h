@@ -740,11 +740,11 @@ typedef struct {
  *   d_k_tail, d_v_tail [n_seqs][n_kv][tail_cap][dim]: rows below a tail's length
  *   are read, the m new ones written behind them; others stay as they are.
  *   The lengths are the caller's to advance.
- *   Accuracy: prompt rows that all of a prompt's sequences see enter as 22-bit
+ *   Accuracy: prompt rows that all of a prompt's sequences see may enter as 22-bit
  *   operands, as attn_tree_sink's cached keys do (its statement holds, with the
  *   prompt's sequences for a tree's nodes); other rows are read as float32.  NaN
- *   in a K or V row that a row sees gives NaN there; NaN or infinity in a prompt
- *   row gives NaN for all of the prompt's sequences that see it.
+ *   in a K or V row that a row sees gives NaN there.  Infinity gives NaN in a prompt
+ *   row that entered as above, and what the formula gives in the others.
  * ------------------------------------------------------------------------ */
 /* Enough for every call of up to these sizes (and any lengths of tails). */
 size_t attn_prefix_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n_groups, int32_t n_seqs,

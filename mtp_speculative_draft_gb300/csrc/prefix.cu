@@ -20,8 +20,8 @@
 //   3. tail:  a few CTAs a (sequence, KV head, new row) read the sequence's own
 //             keys (and a window's edge in the prompt) and the splits' partials;
 //             the last of them joins their parts; sink, gate, output.
-// Without a long prompt the second launch is left out and the third reads the
-// prompt too.
+// Where there is little of the prompt to share, the third launch reads it too,
+// prepares its queries and new keys itself, and is the only one.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -36,13 +36,14 @@ constexpr int kPrefixPrepThreads = 128;
 
 // One warp an item: the q heads of all new rows, then k heads, then v heads.
 __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const __grid_constant__ PrefixArgs a) {
-  __shared__ int zero;
   const int lane = threadIdx.x & 31, half = a.rope.half;
   const int it = blockIdx.x * (kPrefixPrepThreads / 32) + (threadIdx.x >> 5);
   const int rows = a.groups * a.per * a.m, nq = rows * a.nh, nk = rows * a.nkv;
+  if (it >= nq + 2 * nk) return;
   const bool is_q = it < nq, is_k = !is_q && it < nq + nk;
   const int h = is_q ? it % a.nh : (it - nq) % a.nkv;
   const int row = is_q ? it / a.nh : (is_k ? it - nq : it - nq - nk) / a.nkv;
+  const int b = row / a.m, i = row % a.m, p = b / a.per;
   pdl_wait();
   pdl_launch_dependents();
   HeadVals v, w;
@@ -52,41 +53,28 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
                       : a.kp + (size_t)row * a.ldk + (size_t)h * a.dqk, a.dqk, half, lane);
     head_load(w, norm, a.dqk, half, lane);
   }
-  if (threadIdx.x == 0) zero = 0;
-  if (a.parts > 1)
-    for (int u = blockIdx.x * kPrefixPrepThreads + threadIdx.x; u < a.groups * a.per * a.nkv * a.items; u += gridDim.x * kPrefixPrepThreads)
-      a.tail_count[u] = 0;
-  __syncthreads();
-  if (it >= nq + 2 * nk) return;
-  const int b = row / a.m, i = row % a.m, p = b / a.per;
-  const int P = a.pmax > 0 ? a.plen[p] : 0, t0 = a.tlen[b];
-  if (lane == 0 && (P < 0 || P > a.pmax || t0 > a.tmax)) set_dev_error(a.err, kErrBadLength);
-  const int t = min(t0, a.tmax);
-  RopePos rp = a.rope;
-  if (!rp.pos) {  // the row's own position
-    rp.base += prompt_len(a, p) + max(t, 0) + i;
-    rp.depth = &zero;
-  }
-  const int at = rp.pos ? row : 0;
+  const int P = prompt_len(a, p), t = tail_len(a, b);
+  int at;
+  const RopePos rp = row_position(a, b, i, P, t, at);
+  const size_t to = ((size_t)b * a.nkv + h) * a.tcap + t + i;  // in the tails
   if (is_q) {
-    const int kv = h / a.G, r = ((b - p * a.per) * a.m + i) * a.G + h % a.G, head = p * a.nkv + kv;
+    const int r = ((b - p * a.per) * a.m + i) * a.G + h % a.G, head = p * a.nkv + h / a.G;
     if (t < 0) {  // no sequence: rows of zeros, so that the split meets no stale values
       v = HeadVals{};
     } else {
       head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
       head_store(v, a.qf + ((size_t)head * a.R + r) * a.dqk, a.dqk, half, a.qscale, lane);
     }
-    if (a.ns > 0) store_q_tile(a, v, head, r, half, lane);
+    store_q_tile(a, v, head, r, half, lane);
   } else if (t < 0) {
     return;
   } else if (is_k) {
     head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
-    head_store(v, a.kt + (((size_t)b * a.nkv + h) * a.tcap + t + i) * a.dqk, a.dqk, half, 1.f, lane);
+    head_store(v, a.kt + to * a.dqk, a.dqk, half, 1.f, lane);
   } else {
     const float* src = a.vp + (size_t)row * a.ldv + (size_t)h * a.dv;
-    float* dst = a.vt + (((size_t)b * a.nkv + h) * a.tcap + t + i) * a.dv;
     for (int c = 4 * lane; c < a.dv; c += 128)
-      *reinterpret_cast<float4*>(dst + c) = *reinterpret_cast<const float4*>(src + c);
+      *reinterpret_cast<float4*>(a.vt + to * a.dv + c) = *reinterpret_cast<const float4*>(src + c);
   }
 }
 
@@ -150,13 +138,26 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     mbar_fence_init();
   }
   __syncwarp();
-  // lengths and earlier rows were final before the call's first launch
+  // Behind a split launch, everything before the call is through once that launch
+  // has released this one; its partials are waited for below.
+  if (a.ns == 0) pdl_wait();
   const int P = prompt_len(a, p), t = tail_len(a, b);
+  if (blockIdx.x == 0 && kv == 0 && threadIdx.x == 0) {
+    const int P0 = a.pmax > 0 ? a.plen[p] : 0;
+    if (P0 < 0 || P0 > a.pmax || a.tlen[b] > a.tmax) set_dev_error(a.err, kErrBadLength);
+  }
+  if (t < 0) {  // no sequence
+    if (a.ns > 0) pdl_wait();  // a launch ends behind the ones before it
+    return;
+  }
   const int first = first_shared_key(a, p, P);
+  // Keys: without a split launch the new rows j0 .. i, which are prepared below; the
+  // prompt's e0 .. e1; the tail's t0 .. t2; in steps of their own.
   const int sees = a.window > 0 ? (int)max(0ll, (long long)P + t + i + 1 - a.window) : 0;  // lowest position
-  const int e0 = min(sees, P), e1 = a.ns > 0 ? max(first, e0) : P;    // keys of the prompt
-  const int t0 = max(0, sees - P), t1 = t + i + 1;                   // and of the tail
-  const int ne = (e1 - e0 + kTailKeys - 1) / kTailKeys, nt = t < 0 ? 0 : ne + (t1 - t0 + kTailKeys - 1) / kTailKeys;
+  const int e0 = min(sees, P), e1 = a.ns > 0 ? max(first, e0) : P;
+  const int t2 = a.ns > 0 ? t + i + 1 : t, t0 = min(max(0, sees - P), t2), j0 = max(0, sees - P - t);
+  auto steps_of = [](int n) { return (n + kTailKeys - 1) / kTailKeys; };
+  const int nn = a.ns > 0 ? 0 : steps_of(i + 1 - j0), ne = nn + steps_of(e1 - e0), nt = ne + steps_of(t2 - t0);
   // the sequence's parts: as many as its keys need, each with every parts-th of
   // the steps and of the splits' partials
   const int parts = max(1, min(a.parts, (nt * kTailKeys + a.part_keys - 1) / a.part_keys));
@@ -164,33 +165,84 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   const int w0 = part * kTailWarps + warp, stride = parts * kTailWarps;  // this warp's steps: w0, w0 + stride, ..
   const float* const kpre = a.keys + ((size_t)head * a.cap + e0) * a.dqk;
   const float* const vpre = a.values + ((size_t)head * a.cap + e0) * a.dv;
-  const float* const kown = a.kt + (((size_t)b * a.nkv + kv) * a.tcap + t0) * a.dqk;
-  const float* const vown = a.vt + (((size_t)b * a.nkv + kv) * a.tcap + t0) * a.dv;
+  const size_t own_row = ((size_t)b * a.nkv + kv) * a.tcap;
+  const float* const kown = a.kt + (own_row + t0) * a.dqk;
+  const float* const vown = a.vt + (own_row + t0) * a.dv;
   Waiter wait{a.err, false};
-  auto step_size = [&](int s) { return min(kTailKeys, s < ne ? e1 - e0 - s * kTailKeys : t1 - t0 - (s - ne) * kTailKeys); };
+  auto step_size = [&](int s) {
+    return min(kTailKeys, s < nn ? i + 1 - j0 - s * kTailKeys : s < ne ? e1 - e0 - (s - nn) * kTailKeys : t2 - t0 - (s - ne) * kTailKeys);
+  };
   auto fetch = [&](int s, int slot) {
     if (lane != 0) return;
     const int n = step_size(s);
-    const size_t row = (size_t)(s < ne ? s : s - ne) * kTailKeys;
+    const size_t row = (size_t)(s < ne ? s - nn : s - ne) * kTailKeys;
     uint8_t* dst = ring + slot * sbytes;
     mbar_arrive_expect_tx(&sh.full[warp][slot], (uint32_t)n * (a.dqk + a.dv) * 4);
     bulk_load_keep(dst, (s < ne ? kpre : kown) + row * a.dqk, (uint32_t)n * a.dqk * 4, &sh.full[warp][slot]);
     bulk_load_keep(dst + kbytes, (s < ne ? vpre : vown) + row * a.dv, (uint32_t)n * a.dv * 4, &sh.full[warp][slot]);
   };
-  // steps below `early` hold no row that this call appends
-  const int early = min(nt, ne + max(0, t - t0) / kTailKeys);
-  for (int s = 0; s < stages; ++s)
-    if (w0 + s * stride < early) fetch(w0 + s * stride, s);
-  pdl_wait();
-  pdl_launch_dependents();
+  // steps from nn to `early` hold no row that this call appends
+  const int early = a.ns > 0 ? min(nt, ne + max(0, t - t0) / kTailKeys) : nt;
   fence_proxy_async_global();
   for (int s = 0; s < stages; ++s)
-    if (w0 + s * stride >= early && w0 + s * stride < nt) fetch(w0 + s * stride, s);
-  for (int c = 4 * threadIdx.x; c < RG * a.dqk; c += 4 * kTailWarps * 32) {
-    const bool in = c < nr * a.dqk && t >= 0;
-    *reinterpret_cast<float4*>(qs + c) =
-        in ? *reinterpret_cast<const float4*>(a.qf + ((size_t)head * a.R + r0) * a.dqk + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (w0 + s * stride >= nn && w0 + s * stride < early) fetch(w0 + s * stride, s);
+  const int half = a.rope.half;
+  if (a.ns > 0) {
+    pdl_wait();
+    fence_proxy_async_global();
+    for (int s = 0; s < stages; ++s)
+      if (w0 + s * stride >= early && w0 + s * stride < nt) fetch(w0 + s * stride, s);
+    const float* src = a.qf + ((size_t)head * a.R + r0) * a.dqk;
+    for (int c = 4 * threadIdx.x; c < RG * a.dqk; c += 4 * kTailWarps * 32)
+      *reinterpret_cast<float4*>(qs + c) = c < nr * a.dqk ? *reinterpret_cast<const float4*>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    // The query rows, normalised, rotated and scaled (log2 domain): up to two a warp,
+    // whose reads go out together.  Warp 0, which has the new key, comes last.
+    HeadVals hv[2], hw;
+    const int rq = (warp + kTailWarps - 1) % kTailWarps;
+#pragma unroll
+    for (int x = 0; x < (RG + kTailWarps - 1) / kTailWarps; ++x) {
+      const int r = rq + x * kTailWarps;
+      hv[x] = HeadVals{};
+      if (r < nr)
+        head_load(hv[x], a.qp + (size_t)(b * a.m + i) * a.ldq + (size_t)(kv * a.G + g0 + r) * a.dqk * (a.gated ? 2 : 1), a.dqk, half, lane);
+    }
+    head_load(hw, a.qn, a.dqk, half, lane);
+    int at;
+    const RopePos rp = row_position(a, b, i, P, t, at);
+#pragma unroll
+    for (int x = 0; x < (RG + kTailWarps - 1) / kTailWarps; ++x) {
+      const int r = rq + x * kTailWarps;
+      if (r < nr) head_norm_rope(hv[x], hw, a.qn != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
+      if (r < RG) head_store(hv[x], qs + r * a.dqk, a.dqk, half, a.qscale, lane);
+    }
+    // A step of new rows, which is a warp's first, is written into its buffer; the
+    // CTA of a row's first heads appends it to the tail.
+    if (w0 < nn) {
+#pragma unroll 1
+      for (int j = j0 + w0 * kTailKeys, y = 0; j <= i && y < kTailKeys; ++j, ++y) {
+        const size_t row = (size_t)b * a.m + j;
+        head_load(hv[0], a.kp + row * a.ldk + (size_t)kv * a.dqk, a.dqk, half, lane);
+        head_load(hw, a.kn, a.dqk, half, lane);
+        int to;
+        const RopePos rk = row_position(a, b, j, P, t, to);
+        head_norm_rope(hv[0], hw, a.kn != nullptr, a.dqk, a.eps, rk, to, a.err, lane);
+        head_store(hv[0], reinterpret_cast<float*>(ring) + y * a.dqk, a.dqk, half, 1.f, lane);
+        const bool append = j == i && g0 == 0;
+        if (append) head_store(hv[0], a.kt + (own_row + t + i) * a.dqk, a.dqk, half, 1.f, lane);
+        const float* src = a.vp + row * a.ldv + (size_t)kv * a.dv;
+        for (int c = 4 * lane; c < a.dv; c += 128) {
+          const float4 x = *reinterpret_cast<const float4*>(src + c);
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring + kbytes) + y * a.dv + c) = x;
+          if (append) *reinterpret_cast<float4*>(a.vt + (own_row + t + i) * a.dv + c) = x;
+        }
+      }
+      fence_proxy_async_shared_cta();  // before a later copy into the buffer
+      __syncwarp();
+      if (lane == 0) tc5::mbar_arrive(&sh.full[warp][0]);
+    }
   }
+  pdl_launch_dependents();
   __syncthreads();
 
   uint64_t o[RG][H][2];
@@ -208,7 +260,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   float ref = -INFINITY, l = 0.f;
   // the warp starts from its share of the splits' partials, in the layout of its
   // own output, while the first keys are on their way
-  if (a.ns > 0 && t >= 0) {
+  if (a.ns > 0) {
     const size_t at = (size_t)head * a.ns * a.R + r0;
     const float2* ml_at = a.part_ml + at + min(row, nr - 1);
     constexpr int NB = RG * H <= 5 ? 3 : RG * H <= 8 ? 2 : 1;  // splits at once: their reads wait together
@@ -464,7 +516,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   };
   if (parts == 1) {
 #pragma unroll 1
-    for (int r = warp; r < nr && t >= 0; r += kTailWarps) {
+    for (int r = warp; r < nr; r += kTailWarps) {
       float M, den;
       own(r, M, den);
       finish(r, M, den);
@@ -487,10 +539,11 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     if (threadIdx.x == 0) sh.last = atom_add_acq_rel_gpu(a.tail_count + unit, 1u) == (unsigned)parts - 1;
     __syncthreads();
     if (sh.last) {
+      if (threadIdx.x == 0) a.tail_count[unit] = 0;  // for the next call
       const float2* const ml0 = a.tail_ml + unit * a.parts * RG;
       const float* const po0 = a.tail_o + unit * a.parts * RG * a.dv;
 #pragma unroll 1
-      for (int r = warp; r < nr && t >= 0; r += kTailWarps) {
+      for (int r = warp; r < nr; r += kTailWarps) {
         const float2 m = lane < parts ? __ldcg(ml0 + lane * RG + r) : make_float2(-INFINITY, 0.f);  // lane s has part s's
         const float M = warp_max(m.x), f = weight(m.x, m.y, M), den = warp_sum(f * m.y);
 #pragma unroll
@@ -556,15 +609,23 @@ static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
 }
 
 // Parts of a sequence's keys, for `units` (sequence, KV head, new row, block of
-// heads): up to kTailCtas CTAs a SM, of kPartBytes of keys and values or more; one
-// warp joins them.
+// heads): as many as the SMs hold at once (`ctas`), of kPartBytes of keys and values
+// or more; tails that differ in length get a third more (24 of up to 2048 rows: 69
+// us, not 75).  One warp joins them.
 constexpr int kTailCtas = 4, kPartBytes = 64 * 1024;
+
+// CTAs of the tail launch that an SM holds.
+static int tail_resident(int rg, int dqk, int dv) {
+  const size_t smem = tail_smem(rg, dqk, dv, tail_stages(rg, dqk, dv)) + sizeof(TailSmem) + 1024;
+  return std::min(tail_ctas(rg, dqk <= 128 && dv <= 128 ? 1 : 2), (int)(228 * 1024 / smem));
+}
 
 struct TailPlan {
   int parts, keys;  // keys a part
 };
-static TailPlan tail_plan(long long units, long long own, int dims, int sms) {
-  const long long most = std::min<long long>(32, std::max<long long>(1, (long long)kTailCtas * sms / units));
+static TailPlan tail_plan(long long units, long long own, int dims, long long ctas, bool even) {
+  const long long most = std::min<long long>(32, std::max<long long>(1, (even ? ctas : ctas * 4 / 3) / units));
+  static_assert(kTailCtas * 256 / 2 <= kPartCounts, "a counter a unit, where units have several parts");
   TailPlan p;
   p.keys = (int)std::min<long long>(1 << 30, (std::max<long long>(kPartBytes / (4 * dims), (own + most - 1) / most) + 31) / 32 * 32);
   p.parts = (int)std::max<long long>(1, (own + p.keys - 1) / p.keys);
@@ -599,14 +660,26 @@ static int shared_keys(const mtp_attn_geom* g, int m, int pmax) {
   return g->window > 0 ? std::max(0, std::min(pmax, g->window - m)) : pmax;
 }
 
-// Prompts of this many keys are read by the tail launch, once a sequence.
-constexpr int kTailPrompt = 64;
+// Whether the tail launch reads the prompts itself: `keys` of a prompt that a row
+// sees, once for each of `units` (sequence, KV head, new row, block of up to `rg`
+// heads).  It is then the only launch (8 us at least, against 17 of three), and
+// reads at 5.3 TB/s from L2.  40/8 heads of 128, us alone and as three launches:
+//   1 sequence   2048 keys 20, 24   4096 25, 24   32768 73, 64
+//   4 sequences  1024 keys 18, 19   2048 22, 26   4096 30, 28
+//   16           256 keys 15, 19    512 19, 19    1024 27, 25
+// 16/2 heads of 256, 4 sequences: 2048 keys 26, 28, 4096 33, 32; up to four heads a
+// KV head take 96 MB rather than 64 (32/8 heads, 8 sequences, 1024 keys: 16, 20).
+constexpr long long kSoloBytes = 64 << 20, kSoloBytesFew = 96 << 20, kSoloPrompt = 32 << 20;
+constexpr int kSoloKeys = 6144;  // a CTA's share grows: 4/2 heads of 64, 4096 keys 14, 16, 32768 keys 35, 24
+static bool tail_alone(long long units, long long heads, long long keys, int dims, int rg) {
+  const long long head = keys * dims * 4;
+  return keys <= kSoloKeys && units * head <= (rg <= 4 ? kSoloBytesFew : kSoloBytes) && heads * head <= kSoloPrompt;
+}
 
 struct PrefixWs {
   float* qf;
   uint8_t* qt;
   float* qinv;
-  unsigned* tail_count;
   float2 *ml, *tail_ml;
   float *o, *tail_o;
   size_t bytes;
@@ -620,9 +693,8 @@ static size_t most_partials(const mtp_attn_geom* g, size_t tiles, size_t rows, i
   return std::min(rows * ((keys + kSplitKeys - 1) / kSplitKeys), 128 * std::max(tiles, (size_t)kSplitWaves * sms));
 }
 
-// `partials`: split partials' rows; `units`, `parts`: of the tail launch, where it joins several parts.
-static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs, int m, size_t partials, size_t units,
-                          size_t tails) {
+// `partials`, `tails`: rows of split partials, and of the tail launch's parts where it joins several.
+static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs, int m, size_t partials, size_t tails) {
   PrefixWs w = {};
   size_t off = sizeof(WsHeader) + kRuleJoinBytes;
   uint8_t* b = static_cast<uint8_t*>(ws);
@@ -639,7 +711,6 @@ static PrefixWs prefix_ws(void* ws, const mtp_attn_geom* g, int groups, int seqs
   w.qinv = reinterpret_cast<float*>(take(tiles * 128 * 4));
   w.ml = reinterpret_cast<float2*>(take(8 * partials));
   w.o = reinterpret_cast<float*>(take(4 * partials * g->head_dim_v));
-  w.tail_count = reinterpret_cast<unsigned*>(take(4 * units));
   w.tail_ml = reinterpret_cast<float2*>(take(8 * tails));
   w.tail_o = reinterpret_cast<float*>(take(4 * tails * g->head_dim_v));
   w.bytes = off;
@@ -650,7 +721,7 @@ static size_t prefix_ws_bound(const mtp_attn_geom* g, int groups, int seqs, int 
   const size_t rows = (size_t)seqs * m * g->n_heads, tiles = rows / 128 + (size_t)groups * g->n_kv_heads;
   // several parts: at most kTailCtas CTAs a SM, of at most 8 rows
   const size_t ctas = (size_t)kTailCtas * sm_count();
-  return prefix_ws(nullptr, g, groups, seqs, m, most_partials(g, tiles, rows, pmax, sm_count()), ctas, 8 * ctas).bytes;
+  return prefix_ws(nullptr, g, groups, seqs, m, most_partials(g, tiles, rows, pmax, sm_count()), 8 * ctas).bytes;
 }
 
 static mtp_status check_prefix_geom(const mtp_attn_geom* g) {
@@ -761,18 +832,19 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   a.mt = (a.R + 127) / 128;  // 1 where rows are repeated
   const int sms = sm_count(), heads = a.groups * a.nkv;
   const int keys = shared_keys(g, m, pmax);
-  a.ns = pmax <= kTailPrompt ? 0 : prefix_splits(heads * a.mt, keys, sms);
+  const int rg = tail_rows(a.G);
+  a.items = m * ((a.G + rg - 1) / rg);
+  const long long units = (long long)B->n_seqs * a.nkv * a.items;
+  const bool alone = tail_alone(units, heads, a.window > 0 ? std::min(pmax, a.window) : pmax, a.dqk + a.dv, rg);
+  a.ns = alone ? 0 : prefix_splits(heads * a.mt, keys, sms);
   // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
   const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
   long long own = (long long)edge + tmax + m;
   if (a.window > 0) own = std::min<long long>(own, a.window);
-  const int rg = tail_rows(a.G);
-  a.items = m * ((a.G + rg - 1) / rg);
-  const long long units = (long long)B->n_seqs * a.nkv * a.items;
-  const TailPlan tp = tail_plan(units, own, a.dqk + a.dv, sms);
+  const TailPlan tp = tail_plan(units, own, a.dqk + a.dv, (long long)tail_resident(rg, a.dqk, a.dv) * sms, a.ns == 0);
   a.parts = tp.parts;
   a.part_keys = tp.keys;
-  const PrefixWs w = prefix_ws(d_ws, g, a.groups, B->n_seqs, m, (size_t)heads * a.R * a.ns, tp.parts > 1 ? units : 0,
+  const PrefixWs w = prefix_ws(d_ws, g, a.groups, B->n_seqs, m, (size_t)heads * a.R * a.ns,
                                tp.parts > 1 ? (size_t)units * tp.parts * rg : 0);
   if (!d_ws || !aligned16(d_ws) || ws_bytes < w.bytes)
     return fail(MTP_ERR_WORKSPACE, "attn_prefix_sink: workspace too small or misaligned");
@@ -796,15 +868,18 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   a.qinv = w.qinv;
   a.part_o = w.o;
   a.part_ml = w.ml;
-  a.tail_count = w.tail_count;
+  a.tail_count = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(d_ws) + sizeof(WsHeader) + kPartCountAt);
   a.tail_ml = w.tail_ml;
   a.tail_o = w.tail_o;
   a.err = &static_cast<WsHeader*>(d_ws)->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long items = (long long)B->n_seqs * m * (a.nh + 2 * a.nkv);
-  cudaError_t e = launch_pdl(prefix_prep_kernel, dim3((unsigned)((items + kPrefixPrepThreads / 32 - 1) / (kPrefixPrepThreads / 32))),
-                             kPrefixPrepThreads, 0, st, a);
-  if (e == cudaSuccess && a.ns > 0) e = launch_prefix_split(a, st);
+  cudaError_t e = cudaSuccess;
+  if (a.ns > 0) {
+    e = launch_pdl(prefix_prep_kernel, dim3((unsigned)((items + kPrefixPrepThreads / 32 - 1) / (kPrefixPrepThreads / 32))),
+                   kPrefixPrepThreads, 0, st, a);
+    if (e == cudaSuccess) e = launch_prefix_split(a, st);
+  }
   if (e == cudaSuccess) e = launch_tail(a, st);
   if (e != cudaSuccess) return cuda_fail(e, "attn_prefix_sink launch");
   return MTP_OK;

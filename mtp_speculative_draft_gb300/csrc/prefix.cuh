@@ -26,7 +26,7 @@ struct PrefixArgs : SplitArgs {
   float* qf;                     // [groups * nkv][R][dqk] scaled queries
   int items;                     // CTAs of a sequence's KV head: new rows times blocks of query heads
   int parts, part_keys;          // parts of a sequence's own keys at most, keys of a part
-  unsigned* tail_count;          // [seqs][nkv][items] parts that have arrived
+  unsigned* tail_count;          // [seqs][nkv][items] parts that have arrived, zero at rest
   float2* tail_ml;               // [seqs][nkv][items][parts][rows] their states
   float* tail_o;                 // [seqs][nkv][items][parts][rows][dv]
 };
@@ -44,6 +44,15 @@ __device__ __forceinline__ int first_shared_key(const PrefixArgs& a, int p, int 
   for (int b = threadIdx.x & 31; b < a.per; b += 32) t = max(t, tail_len(a, p * a.per + b));
   const long long k = (long long)P + __reduce_max_sync(0xffffffffu, t) + a.m - a.window;
   return k <= 0 ? 0 : k < P ? (int)k : P;
+}
+
+// Rotary positions of new row i of sequence b, whose prompt and tail have P and t
+// rows; `row` is its row in them.
+__device__ __forceinline__ RopePos row_position(const PrefixArgs& a, int b, int i, int P, int t, int& row) {
+  RopePos r = a.rope;
+  if (!r.pos) r.base += P + t + i;
+  row = r.pos ? b * a.m + i : 0;
+  return r;
 }
 
 // Keys [k0, k1) of a split.  The lengths were final before the call's first

@@ -11,7 +11,9 @@ constexpr int kTreeMax = 64;  // nodes of a tree: one 64-bit ancestor word per n
 // zero between calls.  Other calls of a round that use a workspace's body start behind them, so one workspace
 // serves them all in turn.
 constexpr int kRuleRowsMax = 1024;
-constexpr size_t kRuleJoinBytes = (size_t)kRuleRowsMax * 16;
+// Behind these, in the same zero bytes, the counters of attn_prefix_sink's parts.
+constexpr size_t kRuleJoinBytes = (size_t)kRuleRowsMax * 16, kPartCountAt = (size_t)kRuleRowsMax * 12;
+constexpr int kPartCounts = kRuleRowsMax;
 
 // Device error codes of these operators (after the ones in common.cuh).
 enum TreeErr : int {
@@ -21,7 +23,7 @@ enum TreeErr : int {
 
 // Rotary positions of `rows` rows.  Pair i of a row takes its angle from the
 // table row pos[axis(i)][row].  pos == nullptr: every pair of row r sits at
-// base + depth[r].
+// base + depth[r] (base where depth is null).
 struct RopePos {
   const float* table;  // [max_pos][half][2] cos, sin
   const int* pos;      // [n_axes][pos_ld] or null
@@ -50,7 +52,7 @@ __device__ __forceinline__ int rope_axis(const RopePos& r, int i) {
 
 // Table entry (cos, sin) of pair i of row `row`.
 __device__ __forceinline__ float2 rope_entry(const RopePos& r, int row, int i, int* err) {
-  int p = r.pos ? r.pos[(size_t)rope_axis(r, i) * r.pos_ld + row] : r.base + r.depth[row];
+  int p = r.pos ? r.pos[(size_t)rope_axis(r, i) * r.pos_ld + row] : r.base + (r.depth ? r.depth[row] : 0);
   if (p < 0 || p >= r.max_pos) {
     set_dev_error(err, kErrBadPosition);
     p = 0;
