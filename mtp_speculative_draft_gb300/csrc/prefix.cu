@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 // lane has dims 4 l .. and 128 + 4 l .. of every key, so the output takes few
 // registers, many warps share an SM and hide each other's waits.  All query rows
 // of a CTA are heads of one new row: they see the same keys, and no mask is needed.
-// RG: query rows (heads) a CTA; H: 128-dim halves of the wider head size.
+// RG: query rows (heads) a CTA; H: 128-dim halves of the wider head size; ALONE:
+// without a split launch.
 //
 // float32 throughout (packed pairs).  Weights are relative to a reference that
 // moves only when a logit passes it by 2^8.
@@ -118,7 +119,7 @@ __host__ __device__ constexpr int tail_padded(int rg) { return rg <= 2 ? 2 : rg 
 // CTAs a SM that the registers allow.
 __host__ __device__ constexpr int tail_ctas(int rg, int h) { return h == 1 || rg <= 4 ? 4 : 3; }
 
-template <int RG, int H>
+template <int RG, int H, bool ALONE>
 __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     prefix_tail_kernel(const __grid_constant__ PrefixArgs a, const int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
@@ -140,24 +141,24 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   __syncwarp();
   // Behind a split launch, everything before the call is through once that launch
   // has released this one; its partials are waited for below.
-  if (a.ns == 0) pdl_wait();
+  if (ALONE) pdl_wait();
   const int P = prompt_len(a, p), t = tail_len(a, b);
   if (blockIdx.x == 0 && kv == 0 && threadIdx.x == 0) {
     const int P0 = a.pmax > 0 ? a.plen[p] : 0;
     if (P0 < 0 || P0 > a.pmax || a.tlen[b] > a.tmax) set_dev_error(a.err, kErrBadLength);
   }
   if (t < 0) {  // no sequence
-    if (a.ns > 0) pdl_wait();  // a launch ends behind the ones before it
+    if (!ALONE) pdl_wait();  // a launch ends behind the ones before it
     return;
   }
-  const int first = first_shared_key(a, p, P);
+  const int first = ALONE ? P : first_shared_key(a, p, P);
   // Keys: without a split launch the new rows j0 .. i, which are prepared below; the
   // prompt's e0 .. e1; the tail's t0 .. t2; in steps of their own.
   const int sees = a.window > 0 ? (int)max(0ll, (long long)P + t + i + 1 - a.window) : 0;  // lowest position
-  const int e0 = min(sees, P), e1 = a.ns > 0 ? max(first, e0) : P;
-  const int t2 = a.ns > 0 ? t + i + 1 : t, t0 = min(max(0, sees - P), t2), j0 = max(0, sees - P - t);
+  const int e0 = min(sees, P), e1 = ALONE ? P : max(first, e0);
+  const int t2 = ALONE ? t : t + i + 1, t0 = min(max(0, sees - P), t2), j0 = max(0, sees - P - t);
   auto steps_of = [](int n) { return (n + kTailKeys - 1) / kTailKeys; };
-  const int nn = a.ns > 0 ? 0 : steps_of(i + 1 - j0), ne = nn + steps_of(e1 - e0), nt = ne + steps_of(t2 - t0);
+  const int nn = ALONE ? steps_of(i + 1 - j0) : 0, ne = nn + steps_of(e1 - e0), nt = ne + steps_of(t2 - t0);
   // the sequence's parts: as many as its keys need, each with every parts-th of
   // the steps and of the splits' partials
   const int parts = max(1, min(a.parts, (nt * kTailKeys + a.part_keys - 1) / a.part_keys));
@@ -182,12 +183,12 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     bulk_load_keep(dst + kbytes, (s < ne ? vpre : vown) + row * a.dv, (uint32_t)n * a.dv * 4, &sh.full[warp][slot]);
   };
   // steps from nn to `early` hold no row that this call appends
-  const int early = a.ns > 0 ? min(nt, ne + max(0, t - t0) / kTailKeys) : nt;
+  const int early = ALONE ? nt : min(nt, ne + max(0, t - t0) / kTailKeys);
   fence_proxy_async_global();
   for (int s = 0; s < stages; ++s)
     if (w0 + s * stride >= nn && w0 + s * stride < early) fetch(w0 + s * stride, s);
   const int half = a.rope.half;
-  if (a.ns > 0) {
+  if (!ALONE) {
     pdl_wait();
     fence_proxy_async_global();
     for (int s = 0; s < stages; ++s)
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   float ref = -INFINITY, l = 0.f;
   // the warp starts from its share of the splits' partials, in the layout of its
   // own output, while the first keys are on their way
-  if (a.ns > 0) {
+  if (!ALONE) {
     const size_t at = (size_t)head * a.ns * a.R + r0;
     const float2* ml_at = a.part_ml + at + min(row, nr - 1);
     constexpr int NB = RG * H <= 5 ? 3 : RG * H <= 8 ? 2 : 1;  // splits at once: their reads wait together
@@ -576,7 +577,7 @@ static size_t tail_smem(int rg, int dqk, int dv, int stages) {
 // Two buffers a warp where three CTAs with them fit an SM.
 static int tail_stages(int rg, int dqk, int dv) { return tail_smem(rg, dqk, dv, kTailStages) <= MTP_TAIL_SMEM * 1024 ? kTailStages : 1; }
 
-template <int RG, int H>
+template <int RG, int H, bool ALONE>
 static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
   const int stages = tail_stages(RG, a.dqk, a.dv);
   static_assert(RG <= kTailKeys, "a warp's state fits one buffer of values");
@@ -585,27 +586,28 @@ static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H, ALONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
-  return launch_pdl(prefix_tail_kernel<RG, H>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
+  return launch_pdl(prefix_tail_kernel<RG, H, ALONE>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
                     tail_smem(RG, a.dqk, a.dv, stages), st, a, stages);
 }
 
-template <int H>
+template <int H, bool ALONE>
 static cudaError_t launch_tail_h(const PrefixArgs& a, cudaStream_t st) {
   switch (tail_rows(a.G)) {
-    case 2: return launch_tail_as<2, H>(a, st);
-    case 4: return launch_tail_as<4, H>(a, st);
-    case 5: return launch_tail_as<5, H>(a, st);
-    case 6: return launch_tail_as<6, H>(a, st);
-    default: return launch_tail_as<8, H>(a, st);
+    case 2: return launch_tail_as<2, H, ALONE>(a, st);
+    case 4: return launch_tail_as<4, H, ALONE>(a, st);
+    case 5: return launch_tail_as<5, H, ALONE>(a, st);
+    case 6: return launch_tail_as<6, H, ALONE>(a, st);
+    default: return launch_tail_as<8, H, ALONE>(a, st);
   }
 }
 
 static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
-  return a.dqk <= 128 && a.dv <= 128 ? launch_tail_h<1>(a, st) : launch_tail_h<2>(a, st);
+  if (a.dqk <= 128 && a.dv <= 128) return a.ns > 0 ? launch_tail_h<1, false>(a, st) : launch_tail_h<1, true>(a, st);
+  return a.ns > 0 ? launch_tail_h<2, false>(a, st) : launch_tail_h<2, true>(a, st);
 }
 
 // Parts of a sequence's keys, for `units` (sequence, KV head, new row, block of
