@@ -54,22 +54,20 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
     head_load(w, norm, a.dqk, half, lane);
   }
   const int P = prompt_len(a, p), t = tail_len(a, b);
-  int at;
-  const RopePos rp = row_position(a, b, i, P, t, at);
   const size_t to = ((size_t)b * a.nkv + h) * a.tcap + t + i;  // in the tails
   if (is_q) {
     const int r = ((b - p * a.per) * a.m + i) * a.G + h % a.G, head = p * a.nkv + h / a.G;
     if (t < 0) {  // no sequence: rows of zeros, so that the split meets no stale values
       v = HeadVals{};
     } else {
-      head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
+      head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, a.rope, row, a.err, lane, P + t + i);
       head_store(v, a.qf + ((size_t)head * a.R + r) * a.dqk, a.dqk, half, a.qscale, lane);
     }
     store_q_tile(a, v, head, r, half, lane);
   } else if (t < 0) {
     return;
   } else if (is_k) {
-    head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
+    head_norm_rope(v, w, norm != nullptr, a.dqk, a.eps, a.rope, row, a.err, lane, P + t + i);
     head_store(v, a.kt + to * a.dqk, a.dqk, half, 1.f, lane);
   } else {
     const float* src = a.vp + (size_t)row * a.ldv + (size_t)h * a.dv;
@@ -80,7 +78,7 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 
 // ------------------------------------------------------------------ tail
 // Warps take steps of 8 keys in turn; a step's K and V rows come by bulk copy
-// into the warp's buffers.  For q.k lane (ks, l) has keys ks and ks + 4 of the
+// into the warp's buffers, the next step's while this one's are worked on.  For q.k lane (ks, l) has keys ks and ks + 4 of the
 // step and dims 32 j + 4 l .. + 3; the eight lanes' parts of the 2 RG products are
 // summed by halves, so that each lane ends with one or two of them and no
 // exponential is taken twice.  The weights go through shared memory; for p.v a
@@ -92,17 +90,13 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 //
 // float32 throughout (packed pairs).  Weights are relative to a reference that
 // moves only when a logit passes it by 2^8.
-#ifndef MTP_TAIL_SMEM
-#define MTP_TAIL_SMEM 72
-#endif
 constexpr int kTailWarps = 4;
 constexpr int kTailKeys = 8;
 constexpr float kTailMove = 8.f;
-constexpr int kTailStages = 2;  // buffers a warp at most
 
 struct alignas(16) TailSmem {
   float2 p[kTailWarps][kTailKeys][8];        // a step's weights, each twice
-  uint64_t full[kTailWarps][kTailStages];
+  uint64_t kfull[kTailWarps], vfull[kTailWarps];  // a warp's keys, values have arrived
   float m[kTailWarps][8], l[kTailWarps][8];  // a warp's state of each row
   int last;                                  // this part is the last to arrive
 };
@@ -121,7 +115,7 @@ __host__ __device__ constexpr int tail_ctas(int rg, int h) { return h == 1 || rg
 
 template <int RG, int H, bool ALONE>
 __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
-    prefix_tail_kernel(const __grid_constant__ PrefixArgs a, const int stages) {
+    prefix_tail_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ TailSmem sh;
   constexpr int PR = tail_padded(RG);
@@ -132,10 +126,12 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   const int cq = a.dqk / 32;
   const int r0 = ((b - p * a.per) * a.m + i) * a.G + g0;  // first query row
   float* qs = reinterpret_cast<float*>(sm);               // [RG][dqk]
-  const uint32_t kbytes = kTailKeys * a.dqk * 4, vbytes = kTailKeys * a.dv * 4, sbytes = kbytes + vbytes;
-  uint8_t* ring = sm + RG * a.dqk * 4 + warp * stages * sbytes;
+  const uint32_t kbytes = kTailKeys * a.dqk * 4, wbytes = kbytes + kTailKeys * a.dv * 4;
+  float* const kb = reinterpret_cast<float*>(sm + RG * a.dqk * 4 + warp * wbytes);  // [8][dqk]
+  float* const vb = kb + kTailKeys * a.dqk;                                          // [8][dv]
   if (lane == 0) {
-    for (int s = 0; s < kTailStages; ++s) mbar_init(&sh.full[warp][s], 1);
+    mbar_init(&sh.kfull[warp], 1);
+    mbar_init(&sh.vfull[warp], 1);
     mbar_fence_init();
   }
   __syncwarp();
@@ -173,26 +169,33 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   auto step_size = [&](int s) {
     return min(kTailKeys, s < nn ? i + 1 - j0 - s * kTailKeys : s < ne ? e1 - e0 - (s - nn) * kTailKeys : t2 - t0 - (s - ne) * kTailKeys);
   };
-  auto fetch = [&](int s, int slot) {
+  auto fetch_k = [&](int s) {
     if (lane != 0) return;
-    const int n = step_size(s);
-    const size_t row = (size_t)(s < ne ? s - nn : s - ne) * kTailKeys;
-    uint8_t* dst = ring + slot * sbytes;
-    mbar_arrive_expect_tx(&sh.full[warp][slot], (uint32_t)n * (a.dqk + a.dv) * 4);
-    bulk_load_keep(dst, (s < ne ? kpre : kown) + row * a.dqk, (uint32_t)n * a.dqk * 4, &sh.full[warp][slot]);
-    bulk_load_keep(dst + kbytes, (s < ne ? vpre : vown) + row * a.dv, (uint32_t)n * a.dv * 4, &sh.full[warp][slot]);
+    const uint32_t bytes = (uint32_t)step_size(s) * a.dqk * 4;
+    mbar_arrive_expect_tx(&sh.kfull[warp], bytes);
+    bulk_load_keep(kb, (s < ne ? kpre : kown) + (size_t)(s < ne ? s - nn : s - ne) * kTailKeys * a.dqk, bytes, &sh.kfull[warp]);
+  };
+  auto fetch_v = [&](int s) {
+    if (lane != 0) return;
+    const uint32_t bytes = (uint32_t)step_size(s) * a.dv * 4;
+    mbar_arrive_expect_tx(&sh.vfull[warp], bytes);
+    bulk_load_keep(vb, (s < ne ? vpre : vown) + (size_t)(s < ne ? s - nn : s - ne) * kTailKeys * a.dv, bytes, &sh.vfull[warp]);
+  };
+  // the warp's first step, of those in [from, to)
+  auto fetch_first = [&](int from, int to) {
+    if (w0 < from || w0 >= to) return;
+    fetch_k(w0);
+    fetch_v(w0);
   };
   // steps from nn to `early` hold no row that this call appends
   const int early = ALONE ? nt : min(nt, ne + max(0, t - t0) / kTailKeys);
   fence_proxy_async_global();
-  for (int s = 0; s < stages; ++s)
-    if (w0 + s * stride >= nn && w0 + s * stride < early) fetch(w0 + s * stride, s);
+  fetch_first(nn, early);
   const int half = a.rope.half;
   if (!ALONE) {
     pdl_wait();
     fence_proxy_async_global();
-    for (int s = 0; s < stages; ++s)
-      if (w0 + s * stride >= early && w0 + s * stride < nt) fetch(w0 + s * stride, s);
+    fetch_first(early, nt);
     const float* src = a.qf + ((size_t)head * a.R + r0) * a.dqk;
     for (int c = 4 * threadIdx.x; c < RG * a.dqk; c += 4 * kTailWarps * 32)
       *reinterpret_cast<float4*>(qs + c) = c < nr * a.dqk ? *reinterpret_cast<const float4*>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -209,15 +212,13 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
         head_load(hv[x], a.qp + (size_t)(b * a.m + i) * a.ldq + (size_t)(kv * a.G + g0 + r) * a.dqk * (a.gated ? 2 : 1), a.dqk, half, lane);
     }
     head_load(hw, a.qn, a.dqk, half, lane);
-    int at;
-    const RopePos rp = row_position(a, b, i, P, t, at);
 #pragma unroll
     for (int x = 0; x < (RG + kTailWarps - 1) / kTailWarps; ++x) {
       const int r = rq + x * kTailWarps;
-      if (r < nr) head_norm_rope(hv[x], hw, a.qn != nullptr, a.dqk, a.eps, rp, at, a.err, lane);
+      if (r < nr) head_norm_rope(hv[x], hw, a.qn != nullptr, a.dqk, a.eps, a.rope, b * a.m + i, a.err, lane, P + t + i);
       if (r < RG) head_store(hv[x], qs + r * a.dqk, a.dqk, half, a.qscale, lane);
     }
-    // A step of new rows, which is a warp's first, is written into its buffer; the
+    // A step of new rows, which is a warp's first, is written into its buffers; the
     // CTA of a row's first heads appends it to the tail.
     if (w0 < nn) {
 #pragma unroll 1
@@ -225,22 +226,23 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
         const size_t row = (size_t)b * a.m + j;
         head_load(hv[0], a.kp + row * a.ldk + (size_t)kv * a.dqk, a.dqk, half, lane);
         head_load(hw, a.kn, a.dqk, half, lane);
-        int to;
-        const RopePos rk = row_position(a, b, j, P, t, to);
-        head_norm_rope(hv[0], hw, a.kn != nullptr, a.dqk, a.eps, rk, to, a.err, lane);
-        head_store(hv[0], reinterpret_cast<float*>(ring) + y * a.dqk, a.dqk, half, 1.f, lane);
+        head_norm_rope(hv[0], hw, a.kn != nullptr, a.dqk, a.eps, a.rope, (int)row, a.err, lane, P + t + j);
+        head_store(hv[0], kb + y * a.dqk, a.dqk, half, 1.f, lane);
         const bool append = j == i && g0 == 0;
         if (append) head_store(hv[0], a.kt + (own_row + t + i) * a.dqk, a.dqk, half, 1.f, lane);
         const float* src = a.vp + row * a.ldv + (size_t)kv * a.dv;
         for (int c = 4 * lane; c < a.dv; c += 128) {
           const float4 x = *reinterpret_cast<const float4*>(src + c);
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(ring + kbytes) + y * a.dv + c) = x;
+          *reinterpret_cast<float4*>(vb + y * a.dv + c) = x;
           if (append) *reinterpret_cast<float4*>(a.vt + (own_row + t + i) * a.dv + c) = x;
         }
       }
-      fence_proxy_async_shared_cta();  // before a later copy into the buffer
+      fence_proxy_async_shared_cta();  // before a later copy into the buffers
       __syncwarp();
-      if (lane == 0) tc5::mbar_arrive(&sh.full[warp][0]);
+      if (lane == 0) {
+        tc5::mbar_arrive(&sh.kfull[warp]);
+        tc5::mbar_arrive(&sh.vfull[warp]);
+      }
     }
   }
   pdl_launch_dependents();
@@ -318,19 +320,11 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       }
     }
   }
-  int slot = 0;
   uint32_t phase = 0;
 #pragma unroll 1
   for (int s = w0; s < nt; s += stride) {
     const int n = step_size(s);
-    float* kb = reinterpret_cast<float*>(ring + slot * sbytes);
-    float* vb = reinterpret_cast<float*>(ring + slot * sbytes + kbytes);
-    wait(&sh.full[warp][slot], phase);
-    if (n < kTailKeys) {  // rows behind the last key take part with weight 0
-      for (int c = n * a.dv + 4 * lane; c < kTailKeys * a.dv; c += 128)
-        *reinterpret_cast<float4*>(vb + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      fence_proxy_async_shared_cta();  // before a later copy into the buffer
-    }
+    wait(&sh.kfull[warp], phase);
     uint64_t acc[RG][2];
 #pragma unroll
     for (int r = 0; r < RG; ++r) acc[r][0] = acc[r][1] = 0ull;
@@ -356,6 +350,8 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     if (H == 2 && cq >= 8) dots(c, std::integral_constant<int, 4>{}), c += 128;
     if (cq & 2) dots(c, std::integral_constant<int, 2>{}), c += 64;
     if (cq & 1) dots(c, std::integral_constant<int, 1>{});
+    __syncwarp();  // every lane has read the keys before their buffer is filled anew
+    if (s + stride < nt) fetch_k(s + stride);
     // product 2 r + k of row r and key ks + 4 k, summed over the eight lanes
     float x[2 * PR];
 #pragma unroll
@@ -420,6 +416,13 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       l += w;
       sh.p[warp][mine + 4 * k][row] = make_float2(w, w);
     }
+    wait(&sh.vfull[warp], phase);
+    phase ^= 1u;
+    if (n < kTailKeys) {  // rows behind the last key take part with weight 0
+      for (int c = n * a.dv + 4 * lane; c < kTailKeys * a.dv; c += 128)
+        *reinterpret_cast<float4*>(vb + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      fence_proxy_async_shared_cta();  // before a later copy into the buffer
+    }
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kTailKeys; ++k) {
@@ -440,12 +443,8 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
         }
       }
     }
-    __syncwarp();  // every lane has read the buffer before it is filled anew
-    if (s + stages * stride < nt) fetch(s + stages * stride, slot);
-    if (++slot == stages) {
-      slot = 0;
-      phase ^= 1u;
-    }
+    __syncwarp();  // every lane has read the values
+    if (s + stride < nt) fetch_v(s + stride);
   }
   // the warp's state
   l += __shfl_xor_sync(0xffffffffu, l, 8);
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     sh.l[warp][row] = l;
   }
   float* const states = reinterpret_cast<float*>(sm + RG * a.dqk * 4);  // a warp's at the start of its buffers
-  const int wstep = stages * sbytes / 4;
+  const int wstep = wbytes / 4;
 #pragma unroll
   for (int r = 0; r < RG; ++r)
 #pragma unroll
@@ -571,27 +570,22 @@ static int tail_rows(int G) {
   const int blocks = (G + 7) / 8, each = (G + blocks - 1) / blocks;
   return each <= 2 ? 2 : each <= 4 ? 4 : each == 7 ? 8 : each;
 }
-static size_t tail_smem(int rg, int dqk, int dv, int stages) {
-  return (size_t)rg * dqk * 4 + (size_t)kTailWarps * stages * kTailKeys * (dqk + dv) * 4;
-}
-// Two buffers a warp where three CTAs with them fit an SM.
-static int tail_stages(int rg, int dqk, int dv) { return tail_smem(rg, dqk, dv, kTailStages) <= MTP_TAIL_SMEM * 1024 ? kTailStages : 1; }
+static size_t tail_smem(int rg, int dqk, int dv) { return (size_t)rg * dqk * 4 + (size_t)kTailWarps * kTailKeys * (dqk + dv) * 4; }
 
 template <int RG, int H, bool ALONE>
 static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
-  const int stages = tail_stages(RG, a.dqk, a.dv);
   static_assert(RG <= kTailKeys, "a warp's state fits one buffer of values");
   static std::atomic<bool> attr[64];  // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H, ALONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H, ALONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
   return launch_pdl(prefix_tail_kernel<RG, H, ALONE>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
-                    tail_smem(RG, a.dqk, a.dv, stages), st, a, stages);
+                    tail_smem(RG, a.dqk, a.dv), st, a);
 }
 
 template <int H, bool ALONE>
@@ -618,7 +612,7 @@ constexpr int kTailCtas = 4, kPartBytes = 64 * 1024;
 
 // CTAs of the tail launch that an SM holds.
 static int tail_resident(int rg, int dqk, int dv) {
-  const size_t smem = tail_smem(rg, dqk, dv, tail_stages(rg, dqk, dv)) + sizeof(TailSmem) + 1024;
+  const size_t smem = tail_smem(rg, dqk, dv) + sizeof(TailSmem) + 1024;
   return std::min(tail_ctas(rg, dqk <= 128 && dv <= 128 ? 1 : 2), (int)(228 * 1024 / smem));
 }
 

@@ -46,15 +46,6 @@ __device__ __forceinline__ int first_shared_key(const PrefixArgs& a, int p, int 
   return k <= 0 ? 0 : k < P ? (int)k : P;
 }
 
-// Rotary positions of new row i of sequence b, whose prompt and tail have P and t
-// rows; `row` is its row in them.
-__device__ __forceinline__ RopePos row_position(const PrefixArgs& a, int b, int i, int P, int t, int& row) {
-  RopePos r = a.rope;
-  if (!r.pos) r.base += P + t + i;
-  row = r.pos ? b * a.m + i : 0;
-  return r;
-}
-
 // Keys [k0, k1) of a split.  The lengths were final before the call's first
 // launch, which releases this one after its own wait.
 __device__ __forceinline__ void split_keys(const PrefixArgs& a, int head, int sp, int& k0, int& k1) {

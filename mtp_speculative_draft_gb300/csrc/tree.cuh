@@ -51,8 +51,9 @@ __device__ __forceinline__ int rope_axis(const RopePos& r, int i) {
 }
 
 // Table entry (cos, sin) of pair i of row `row`.
-__device__ __forceinline__ float2 rope_entry(const RopePos& r, int row, int i, int* err) {
-  int p = r.pos ? r.pos[(size_t)rope_axis(r, i) * r.pos_ld + row] : r.base + (r.depth ? r.depth[row] : 0);
+// (`shift`: positions to add to the base, where pos is null.)
+__device__ __forceinline__ float2 rope_entry(const RopePos& r, int row, int i, int* err, int shift = 0) {
+  int p = r.pos ? r.pos[(size_t)rope_axis(r, i) * r.pos_ld + row] : r.base + shift + (r.depth ? r.depth[row] : 0);
   if (p < 0 || p >= r.max_pos) {
     set_dev_error(err, kErrBadPosition);
     p = 0;
@@ -86,11 +87,11 @@ __device__ __forceinline__ void head_load(HeadVals& h, const float* src, int d, 
 // RMS-normalises a loaded head row (with its loaded weight, when norm) and
 // rotates its pairs.
 __device__ __forceinline__ void head_norm_rope(HeadVals& h, const HeadVals& w, bool norm, int d, float eps,
-                                               const RopePos& r, int row, int* err, int lane) {
+                                               const RopePos& r, int row, int* err, int lane, int shift = 0) {
   float2 cs[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    cs[j] = lane + 32 * j < r.half ? rope_entry(r, row, lane + 32 * j, err) : make_float2(1.f, 0.f);
+    cs[j] = lane + 32 * j < r.half ? rope_entry(r, row, lane + 32 * j, err, shift) : make_float2(1.f, 0.f);
   if (norm) {
     float ss = 0.f;
 #pragma unroll
