@@ -636,12 +636,12 @@ constexpr int kSplitWaves = 3;   // CTAs a SM at most, where a prompt has severa
 
 static int prefix_splits(int heads_tiles, int keys, int sms) {
   if (keys <= 0) return 0;
-  const int most = std::min((keys + kSplitKeys - 1) / kSplitKeys, std::max(1, kSplitWaves * sms / heads_tiles));
+  const int most = (keys + kSplitKeys - 1) / kSplitKeys;
   int best = 1;
   long long cost = -1;
-  for (int ns = 1; ns <= most; ++ns) {
-    const long long waves = ((long long)heads_tiles * ns + sms - 1) / sms;
-    const long long c = waves * ((keys + ns - 1) / ns + kSplitCost);
+  for (int waves = 1; waves <= kSplitWaves; ++waves) {  // as many splits as the waves hold
+    const int ns = std::min(most, std::max(1, waves * sms / heads_tiles));
+    const long long w = ((long long)heads_tiles * ns + sms - 1) / sms, c = w * ((keys + ns - 1) / ns + kSplitCost);
     if (cost < 0 || c < cost) {
       cost = c;
       best = ns;

@@ -481,15 +481,24 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Args
     {
       const uint4* src = reinterpret_cast<const uint4*>(a.qt + ((size_t)kv * a.mt + mt) * 512 * a.dqk) +
                          wg * 16 * a.dqk + row;
-#pragma unroll 8
-      for (int c = 0; c < a.dqk; c += 16) {
-        const uint4 u = __ldcg(src + c * 16), v = __ldcg(src + c * 16 + 128);
-        if (wg == 0 || qlo_tm) {
-          const uint32_t r[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-          tmem_st8((wg == 0 ? qhi : qlo) + lanes + c / 2, r);
-        } else {
-          *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c, 128)) = u;
-          *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c + 8, 128)) = v;
+      // all reads of 128 dims go out before the first store
+#pragma unroll 1
+      for (int c0 = 0; c0 < a.dqk; c0 += 128) {
+        uint4 u[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (c0 + 8 * k < a.dqk) u[k] = __ldcg(src + (c0 + 8 * k) * 16);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+          const int c = c0 + 8 * k;
+          if (c >= a.dqk) break;
+          if (wg == 0 || qlo_tm) {
+            const uint32_t r[8] = {u[k].x, u[k].y, u[k].z, u[k].w, u[k + 1].x, u[k + 1].y, u[k + 1].z, u[k + 1].w};
+            tmem_st8((wg == 0 ? qhi : qlo) + lanes + c / 2, r);
+          } else {
+            *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c, 128)) = u[k];
+            *reinterpret_cast<uint4*>(sm + qoff + tile_off(row, c + 8, 128)) = u[k + 1];
+          }
         }
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
