@@ -22,9 +22,6 @@
 
 namespace mtp {
 
-#ifndef MTP_SEL_CTAS
-#define MTP_SEL_CTAS 4
-#endif
 constexpr int kSelThreads = 256;
 constexpr int kSelPer = 32;                         // logits a thread
 constexpr int kSelChunk = kSelThreads * kSelPer;    // logits a CTA
@@ -105,7 +102,7 @@ struct RowsSmem {
 // A thread's sum of exponentials has 6 roundings a term; the threads' are added
 // exactly, in integers of 2^-20 and 2^-40 (a 64-bit addition costs a warp 16 cycles
 // of an SM: 64 rows of 152577 took 16 us with them, 9 without).
-__global__ void __launch_bounds__(kSelThreads, MTP_SEL_CTAS) beam_rows_kernel(const __grid_constant__ SelArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_constant__ SelArgs a) {
   __shared__ RowsSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, r = blockIdx.y;

@@ -135,8 +135,9 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     mbar_fence_init();
   }
   __syncwarp();
-  // Behind a split launch, everything before the call is through once that launch
-  // has released this one; its partials are waited for below.
+  // Behind a split launch, that launch has released this one after its own wait for
+  // the prep launch, so all that both wait for is through, queries and appended rows
+  // among it; the splits' partials are waited for below, behind the own keys.
   if (ALONE) pdl_wait();
   const int P = prompt_len(a, p), t = tail_len(a, b);
   if (blockIdx.x == 0 && kv == 0 && threadIdx.x == 0) {
@@ -181,24 +182,16 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     mbar_arrive_expect_tx(&sh.vfull[warp], bytes);
     bulk_load_keep(vb, (s < ne ? vpre : vown) + (size_t)(s < ne ? s - nn : s - ne) * kTailKeys * a.dv, bytes, &sh.vfull[warp]);
   };
-  // the warp's first step, of those in [from, to)
-  auto fetch_first = [&](int from, int to) {
-    if (w0 < from || w0 >= to) return;
+  fence_proxy_async_global();
+  if (w0 >= nn && w0 < nt) {
     fetch_k(w0);
     fetch_v(w0);
-  };
-  // steps from nn to `early` hold no row that this call appends
-  const int early = ALONE ? nt : min(nt, ne + max(0, t - t0) / kTailKeys);
-  fence_proxy_async_global();
-  fetch_first(nn, early);
+  }
   const int half = a.rope.half;
   if (!ALONE) {
-    pdl_wait();
-    fence_proxy_async_global();
-    fetch_first(early, nt);
     const float* src = a.qf + ((size_t)head * a.R + r0) * a.dqk;
     for (int c = 4 * threadIdx.x; c < RG * a.dqk; c += 4 * kTailWarps * 32)
-      *reinterpret_cast<float4*>(qs + c) = c < nr * a.dqk ? *reinterpret_cast<const float4*>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4*>(qs + c) = c < nr * a.dqk ? __ldcg(reinterpret_cast<const float4*>(src + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
     // The query rows, normalised, rotated and scaled (log2 domain): up to two a warp,
     // whose reads go out together.  Warp 0, which has the new key, comes last.
@@ -245,7 +238,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       }
     }
   }
-  pdl_launch_dependents();
+  if (ALONE) pdl_launch_dependents();
   __syncthreads();
 
   uint64_t o[RG][H][2];
@@ -261,65 +254,6 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
 #pragma unroll
   for (int h = 0; h < H; ++h) vcol[h] = min(128 * h + 4 * lane, a.dv - 4);
   float ref = -INFINITY, l = 0.f;
-  // the warp starts from its share of the splits' partials, in the layout of its
-  // own output, while the first keys are on their way
-  if (!ALONE) {
-    const size_t at = (size_t)head * a.ns * a.R + r0;
-    const float2* ml_at = a.part_ml + at + min(row, nr - 1);
-    constexpr int NB = RG * H <= 5 ? 3 : RG * H <= 8 ? 2 : 1;  // splits at once: their reads wait together
-#pragma unroll 1
-    for (int s0 = w0; s0 < a.ns; s0 += NB * stride) {
-      ulonglong2 v[NB][RG][H];
-      float2 ml[NB];
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int s = s0 + k * stride;
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (s < a.ns) ml[k] = ml_at[(size_t)s * a.R];
-        const float* po = a.part_o + (at + (size_t)s * a.R) * a.dv;
-#pragma unroll
-        for (int r = 0; r < RG; ++r)
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            v[k][r][h] = make_ulonglong2(0ull, 0ull);
-            if (s < a.ns) v[k][r][h] = *reinterpret_cast<const ulonglong2*>(po + (size_t)min(r, nr - 1) * a.dv + vcol[h]);
-          }
-      }
-      float to = ref;
-#pragma unroll
-      for (int k = 0; k < NB; ++k) to = fmaxf(to, ml[k].x);
-      const float corr = ref == -INFINITY ? 1.f : ex2(ref - to);  // nothing, or NaN, was summed without a reference
-      ref = to;
-      l *= corr;
-      float f[NB];
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        // a partial of NaN logits alone has no maximum, and its sum is NaN
-        f[k] = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - ref);
-        if (mine == 0) l += f[k] * ml[k].y;
-      }
-#pragma unroll
-      for (int r = 0; r < RG; ++r) {
-        const float c1 = __shfl_sync(0xffffffffu, corr, r * (8 / PR), 8);
-        const uint64_t c2 = pack2(c1, c1);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          o[r][h][0] = mul2(o[r][h][0], c2);
-          o[r][h][1] = mul2(o[r][h][1], c2);
-        }
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          const float w = __shfl_sync(0xffffffffu, f[k], r * (8 / PR), 8);
-          const uint64_t w2 = pack2(w, w);
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            o[r][h][0] = fma2(w2, v[k][r][h].x, o[r][h][0]);
-            o[r][h][1] = fma2(w2, v[k][r][h].y, o[r][h][1]);
-          }
-        }
-      }
-    }
-  }
   uint32_t phase = 0;
 #pragma unroll 1
   for (int s = w0; s < nt; s += stride) {
@@ -446,6 +380,66 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     __syncwarp();  // every lane has read the values
     if (s + stride < nt) fetch_v(s + stride);
   }
+  // the warp's share of the splits' partials, in the layout of its own output
+  if (!ALONE) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const size_t at = (size_t)head * a.ns * a.R + r0;
+    const float2* ml_at = a.part_ml + at + min(row, nr - 1);
+    constexpr int NB = RG * H <= 5 ? 3 : RG * H <= 8 ? 2 : 1;  // splits at once: their reads wait together
+#pragma unroll 1
+    for (int s0 = w0; s0 < a.ns; s0 += NB * stride) {
+      ulonglong2 v[NB][RG][H];
+      float2 ml[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int s = s0 + k * stride;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (s < a.ns) ml[k] = ml_at[(size_t)s * a.R];
+        const float* po = a.part_o + (at + (size_t)s * a.R) * a.dv;
+#pragma unroll
+        for (int r = 0; r < RG; ++r)
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            v[k][r][h] = make_ulonglong2(0ull, 0ull);
+            if (s < a.ns) v[k][r][h] = *reinterpret_cast<const ulonglong2*>(po + (size_t)min(r, nr - 1) * a.dv + vcol[h]);
+          }
+      }
+      float to = ref;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) to = fmaxf(to, ml[k].x);
+      const float corr = ref == -INFINITY ? 1.f : ex2(ref - to);  // nothing, or NaN, was summed without a reference
+      ref = to;
+      l *= corr;
+      float f[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        // a partial of NaN logits alone has no maximum, and its sum is NaN
+        f[k] = ml[k].x == -INFINITY ? (ml[k].y == 0.f ? 0.f : 1.f) : ex2(ml[k].x - ref);
+        if (mine == 0) l += f[k] * ml[k].y;
+      }
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        const float c1 = __shfl_sync(0xffffffffu, corr, r * (8 / PR), 8);
+        const uint64_t c2 = pack2(c1, c1);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          o[r][h][0] = mul2(o[r][h][0], c2);
+          o[r][h][1] = mul2(o[r][h][1], c2);
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          const float w = __shfl_sync(0xffffffffu, f[k], r * (8 / PR), 8);
+          const uint64_t w2 = pack2(w, w);
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            o[r][h][0] = fma2(w2, v[k][r][h].x, o[r][h][0]);
+            o[r][h][1] = fma2(w2, v[k][r][h].y, o[r][h][1]);
+          }
+        }
+      }
+    }
+  }
   // the warp's state
   l += __shfl_xor_sync(0xffffffffu, l, 8);
   l += __shfl_xor_sync(0xffffffffu, l, 16);
@@ -490,10 +484,10 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       scale4(y[x], inv);
       if (a.gated) {
         const float4 g = dims4(a.qp + at * a.ldq + ((size_t)2 * h + 1) * a.dqk, a.dqk, lane, x);
-        y[x].x = __fdividef(y[x].x, 1.f + expf(-g.x));
-        y[x].y = __fdividef(y[x].y, 1.f + expf(-g.y));
-        y[x].z = __fdividef(y[x].z, 1.f + expf(-g.z));
-        y[x].w = __fdividef(y[x].w, 1.f + expf(-g.w));
+        y[x].x *= __frcp_rn(1.f + expf(-g.x));
+        y[x].y *= __frcp_rn(1.f + expf(-g.y));
+        y[x].z *= __frcp_rn(1.f + expf(-g.z));
+        y[x].w *= __frcp_rn(1.f + expf(-g.w));
       }
       if (c < a.dv) *reinterpret_cast<float4*>(a.out + (at * a.nh + h) * a.dv + c) = y[x];
     }
@@ -608,7 +602,7 @@ static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
 // heads): as many as the SMs hold at once (`ctas`), of kPartBytes of keys and values
 // or more; tails that differ in length get a third more (24 of up to 2048 rows: 69
 // us, not 75).  One warp joins them.
-constexpr int kTailCtas = 4, kPartBytes = 64 * 1024;
+constexpr int kTailCtas = 6, kPartBytes = 64 * 1024;  // CTAs a SM at most
 
 // CTAs of the tail launch that an SM holds.
 static int tail_resident(int rg, int dqk, int dv) {
@@ -620,8 +614,9 @@ struct TailPlan {
   int parts, keys;  // keys a part
 };
 static TailPlan tail_plan(long long units, long long own, int dims, long long ctas, bool even) {
-  const long long most = std::min<long long>(32, std::max<long long>(1, (even ? ctas : ctas * 4 / 3) / units));
+  static_assert(3 * kTailCtas >= 4 * 4, "four CTAs a SM at most, and a third more");
   static_assert(kTailCtas * 256 / 2 <= kPartCounts, "a counter a unit, where units have several parts");
+  const long long most = std::min<long long>(32, std::max<long long>(1, (even ? ctas : ctas * 4 / 3) / units));
   TailPlan p;
   p.keys = (int)std::min<long long>(1 << 30, (std::max<long long>(kPartBytes / (4 * dims), (own + most - 1) / most) + 31) / 32 * 32);
   p.parts = (int)std::max<long long>(1, (own + p.keys - 1) / p.keys);

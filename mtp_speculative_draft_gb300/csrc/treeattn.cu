@@ -452,7 +452,6 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Args
         __syncwarp();
       }
     }
-    pdl_launch_dependents();
     block_sync();
   } else {
     // ---------------- softmax and MMA issue
@@ -648,7 +647,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1) tree_split_kernel(const Args
       }
       tc5::fence_before_sync();
     }
-    pdl_launch_dependents();
+    pdl_launch_dependents();  // by warps that have waited for the launch before: it is through when the next begins
     block_sync();
     // Lane states to shared memory (lane i of a warpgroup at i * kLaneStride),
     // then a row's states weighted and summed.  The code that runs once is kept

@@ -10,7 +10,7 @@ import pytest
 from oracle import beam_oracle as B
 from oracle import tree_oracle as T
 
-INVALID, UNSUPPORTED, CAPACITY, WORKSPACE = 1, 2, 3, 4
+INVALID, UNSUPPORTED, CAPACITY, WORKSPACE, CUDA = 1, 2, 3, 4, 5
 
 
 @pytest.fixture(scope="module")
@@ -145,8 +145,13 @@ def test_workspace_of_the_largest_call_does_for_all(lib, nh, nkv, dqk, dv, windo
                 assert need <= size(groups, groups * (per + 1), m, L)
             if per * (groups + 1) <= 1024:
                 assert need <= size(groups + 1, (groups + 1) * per, m, L)
-            b = _batch(groups=groups, seqs=groups * per, m=m, pmax=L)
-            assert _attn(lib, g, b, pcap=40000, tcap=40, rope_rows=60000, ws_bytes=18000) == WORKSPACE
+            # no call of that size or of a smaller one, with tails of any length, is refused its workspace (it then
+            # fails for want of a GPU)
+            for groups2, per2, m2, L2, tmax in ((groups, per, m, L, 20), (groups, per, m, L, 5000), (1, max(1, per // 2), m, L, 40000),
+                                                (1, 1, 1, L, 100000), (groups, per, 1, L // 2, 300), (1, max(1, per // 3), 1, L, 3000)):
+                b = _batch(groups=groups2, seqs=groups2 * per2, m=m2, pmax=L2, tmax=tmax)
+                call = lambda n: _attn(lib, g, b, pcap=40000, tcap=200000, rope_rows=200000, ws_bytes=n)  # noqa: E731
+                assert call(18000) == WORKSPACE and call(need) == CUDA, (groups2, per2, m2, L2, tmax)
     for bad in ((0, 1, 1, 5), (2, 3, 1, 5), (1, 1025, 1, 5), (1, 4, 17, 5), (1, 4, 1, -1)):
         assert size(*bad) == 0
     assert lib.attn_prefix_sink_workspace_bytes(None, 1, 1, 1, 5) == 0
