@@ -542,13 +542,24 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
         const float M = warp_max(m.x), f = weight(m.x, m.y, M), den = warp_sum(f * m.y);
 #pragma unroll
         for (int x = 0; x < H; ++x) y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int s = 0; s < parts; ++s) {
-          const float w = __shfl_sync(0xffffffffu, f, s);
+        constexpr int NB = 16 / H;  // parts at once: their reads wait together
+#pragma unroll 1
+        for (int s0 = 0; s0 < parts; s0 += NB) {
+          float4 v[NB][H];
 #pragma unroll
-          for (int x = 0; x < H; ++x)
-            if (128 * x + 4 * lane < a.dv)
-              add4(y[x], w, __ldcg(reinterpret_cast<const float4*>(po0 + ((size_t)s * RG + r) * a.dv + 128 * x + 4 * lane)));
+          for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int x = 0; x < H; ++x) {
+              v[k][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (s0 + k < parts && 128 * x + 4 * lane < a.dv)
+                v[k][x] = __ldcg(reinterpret_cast<const float4*>(po0 + ((size_t)(s0 + k) * RG + r) * a.dv + 128 * x + 4 * lane));
+            }
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f, (s0 + k) & 31);  // 0 past the parts
+#pragma unroll
+            for (int x = 0; x < H; ++x) add4(y[x], w, v[k][x]);
+          }
         }
         finish(r, M, den);
       }
@@ -651,20 +662,22 @@ static int shared_keys(const mtp_attn_geom* g, int m, int pmax) {
   return g->window > 0 ? std::max(0, std::min(pmax, g->window - m)) : pmax;
 }
 
-// Whether the tail launch reads the prompts itself: `keys` of a prompt that a row
-// sees, once for each of `units` (sequence, KV head, new row, block of up to `rg`
-// heads).  It is then the only launch (8 us at least, against 17 of three), and
-// reads at 5.3 TB/s from L2.  40/8 heads of 128, us alone and as three launches:
-//   1 sequence   2048 keys 20, 24   4096 25, 24   32768 73, 64
-//   4 sequences  1024 keys 18, 19   2048 22, 26   4096 30, 28
-//   16           256 keys 15, 19    512 19, 19    1024 27, 25
-// 16/2 heads of 256, 4 sequences: 2048 keys 26, 28, 4096 33, 32; up to four heads a
-// KV head take 96 MB rather than 64 (32/8 heads, 8 sequences, 1024 keys: 16, 20).
-constexpr long long kSoloBytes = 64 << 20, kSoloBytesFew = 96 << 20, kSoloPrompt = 32 << 20;
-constexpr int kSoloKeys = 6144;  // a CTA's share grows: 4/2 heads of 64, 4096 keys 14, 16, 32768 keys 35, 24
+// Whether the tail launch reads the prompts itself: `keys` of a prompt that a split
+// launch would take (with a window: beside the longest tail), once for each of `units` (sequence, KV head, new row, block of up to `rg`
+// heads) rather than once for each of `heads` (prompts' KV heads).  It is then the
+// only launch, which saves 6 us, and reads what is not shared at about 5.5 TB/s from
+// L2.  us alone, and as three launches, 40/8 heads of 128:
+//   2 sequences  4096 keys 21, 22   8192 30, 28
+//   8            512 keys 14, 16    1024 18, 18    2048 26, 20
+//   32           128 keys 15, 17    256 19, 18
+// 16/2 heads of 256, 8 sequences: 1024 keys 19, 21, 2048 24, 24, 4096 31, 29.  Few
+// heads a KV head cost the one launch less: 32/8 heads, 8 sequences, 1024 keys 15, 17,
+// 2048 21, 20.  A CTA's share grows with the keys: 4/2 heads of 64, one sequence, 8192
+// keys 13, 14, 32768 keys 32, 23.
+constexpr long long kAloneBytes = 52 << 20, kAloneBytesFew = 72 << 20;
+constexpr int kAloneKeys = 12288;
 static bool tail_alone(long long units, long long heads, long long keys, int dims, int rg) {
-  const long long head = keys * dims * 4;
-  return keys <= kSoloKeys && units * head <= (rg <= 4 ? kSoloBytesFew : kSoloBytes) && heads * head <= kSoloPrompt;
+  return keys <= kAloneKeys && (units - heads) * keys * dims * 4 <= (rg <= 4 ? kAloneBytesFew : kAloneBytes);
 }
 
 struct PrefixWs {
@@ -826,7 +839,8 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   const int rg = tail_rows(a.G);
   a.items = m * ((a.G + rg - 1) / rg);
   const long long units = (long long)B->n_seqs * a.nkv * a.items;
-  const bool alone = tail_alone(units, heads, a.window > 0 ? std::min(pmax, a.window) : pmax, a.dqk + a.dv, rg);
+  const long long common = a.window > 0 ? std::min<long long>(pmax, std::max<long long>(0, (long long)a.window - m - tmax)) : pmax;
+  const bool alone = tail_alone(units, heads, common, a.dqk + a.dv, rg);
   a.ns = alone ? 0 : prefix_splits(heads * a.mt, keys, sms);
   // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
   const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
