@@ -1,0 +1,230 @@
+"""The beam search's step as a program may call it: long prompts (three launches) beside short ones (one), first calls
+under capture, two calls at once, workspaces passed around, lengths at the ends of their ranges."""
+
+import numpy as np
+import pytest
+
+from helpers import assert_close
+from oracle import beam_oracle as B
+from oracle import tree_oracle as T
+from test_gpu_beams import ATTN_TOL, Call, Select, _attn_case, _beams, _reference, dev  # noqa: F401
+from test_gpu_tree import _t
+
+pytestmark = pytest.mark.gpu
+
+# more keys than one launch takes
+LONG = [
+    dict(nh=1, nkv=1, dqk=32, dv=32, plen=[12300], tlen=[0]),
+    dict(nh=4, nkv=2, dqk=64, dv=64, plen=[12400, 0, 77], tlen=[5, -1, 9, 0, 64, 7]),          # an empty prompt among others
+    dict(nh=2, nkv=2, dqk=64, dv=64, plen=[12300], tlen=[-1, -1, -1]),                         # no sequence at all
+    dict(nh=8, nkv=1, dqk=128, dv=128, plen=[12289], tlen=[17, 0, -1, 300], gated=True),
+    dict(nh=5, nkv=1, dqk=128, dv=128, plen=[12500], tlen=[9] * 30, gated=True),               # 150 rows: two tiles
+    dict(nh=16, nkv=2, dqk=256, dv=256, plen=[12300, 300], tlen=[40, 0, 31, 129], axes=(44, 42, 42)),
+    dict(nh=8, nkv=2, dqk=192, dv=128, plen=[13000], tlen=[77, 3, 200], m=4, window=12600, norm=False, sinks=True),
+    dict(nh=6, nkv=6, dqk=64, dv=96, plen=[12500], tlen=[3, 0], m=16, window=12450),
+    dict(nh=12, nkv=1, dqk=160, dv=224, plen=[12515], tlen=[11, 12, 700], rot=40),
+    dict(nh=64, nkv=1, dqk=32, dv=256, plen=[12329], tlen=[3, 90, 1], rot=0),
+    dict(nh=128, nkv=2, dqk=32, dv=64, plen=[12400], tlen=[300, 2], m=3),
+    dict(nh=3, nkv=3, dqk=32, dv=32, plen=[12331], tlen=[31] * 20, rot=10, sinks=True),
+    dict(nh=2, nkv=1, dqk=256, dv=128, plen=[12370], tlen=[1500, 3], loose=(0, 400)),
+    dict(nh=4, nkv=1, dqk=64, dv=64, plen=[5, 12400, 6000, 64], tlen=[7, 2, 0, 4], loose=(9000, 0)),
+]
+
+
+@pytest.mark.parametrize("i", range(len(LONG)))
+def test_attention_over_long_prompts(dev, i):  # noqa: F811
+    call = Call(_attn_case(700 + i, **LONG[i]), dev, pad=4 * (i % 3))
+    call()
+    call.check(str(LONG[i]))
+    first = call.out.clone()
+    call.out.fill_(7.0)
+    call()
+    assert (call.out == first).all()
+
+
+def test_one_launch_and_three_agree(dev):  # noqa: F811
+    """The same batch with a bound that one launch takes, and with one that it does not."""
+    outs = []
+    for loose in (0, 12288):
+        c = _attn_case(5, nh=40, nkv=8, dqk=128, dv=128, plen=[700], tlen=[30, 100, 0], m=2, gated=True, sinks=True)
+        c["pmax"] += loose
+        for n in ("kpre", "vpre"):
+            c[n] = np.pad(c[n], ((0, 0), (0, 0), (0, loose), (0, 0)), constant_values=np.nan)
+        call = Call(c, dev)
+        call()
+        call.check(f"loose by {loose}")
+        outs.append((call.out.cpu().numpy(), call.kt.cpu().numpy()))
+    assert_close(outs[0][0], outs[1][0], "outputs", 2 * ATTN_TOL)
+    np.testing.assert_array_equal(outs[0][1], outs[1][1])
+
+
+def test_hidden_rows_behind_long_prompts(dev):  # noqa: F811
+    """NaN and infinity below a window's edge, in later new rows, in other prompts and sequences."""
+    c = _attn_case(6, nh=4, nkv=2, dqk=64, dv=64, plen=[13000, 12900], tlen=[40, 0, 10, 60], m=3, window=12700)
+    lo = 13000 + 0 + 1 - 12700                               # the first prompt's row that sequence 1's row 0 still sees
+    c["kpre"][0, :, :lo], c["vpre"][0, :, :lo] = np.nan, np.inf
+    c["kp"][2], c["vp"][2] = np.nan, np.inf                   # row 2 of sequence 0
+    c["vpre"][0, 1, lo + 3] = np.nan                          # an edge that sequence 1 sees and sequence 0 does not
+    c["kt"][2, :, 4] = np.nan                                 # sequence 2 sees NaN
+    call = Call(c, dev)
+    call()
+    got, ref = call.out.cpu().numpy().reshape(12, 4, 64), _reference(c)[0]
+    for r in range(12):
+        nan = np.isnan(ref[r])
+        assert (np.isnan(got[r]) == nan).all(), r
+        if not nan.all():
+            assert_close(got[r][~nan], ref[r][~nan], f"row {r}", ATTN_TOL)
+    assert [bool(np.isnan(ref[r]).any()) for r in range(12)] == [False, False, True, True, True, True, True, True, True, False, False, False]
+
+
+def test_nan_in_a_long_prompt_that_is_seen(dev):  # noqa: F811
+    c = _attn_case(7, nh=4, nkv=2, dqk=64, dv=64, plen=[12400, 12400], tlen=[3, 0, 9, 5])
+    c["kpre"][1, 0, 30, 3] = np.nan
+    call = Call(c, dev)
+    call()
+    got, ref = call.out.cpu().numpy().reshape(4, 4, 64), np.array(_reference(c)[0])
+    assert np.isnan(got[2:, :2]).all()
+    assert_close(got[:2], ref[:2], "other prompt", ATTN_TOL)
+    assert_close(got[2:, 2:], ref[2:, 2:], "other KV head", ATTN_TOL)
+
+
+def test_long_prompts_offsets_past_32_bits(dev):  # noqa: F811
+    """The second KV head's rows start 2^31 values behind the first's, in a prompt of three launches."""
+    import torch
+    call = Call(_attn_case(12, nh=4, nkv=2, dqk=32, dv=32, plen=[12400], tlen=[90]), dev)
+    cap = 1 << 26
+    for name in ("kpre", "vpre"):
+        big, small = torch.empty(1, 2, cap, 32, device=dev), getattr(call, name)
+        big[:, :, :small.shape[2]] = small
+        setattr(call, name, big)
+    call()
+    call.check()
+
+
+def test_lengths_outside_their_range_behind_long_prompts(dev):  # noqa: F811
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    c = _attn_case(22, nh=4, nkv=2, dqk=64, dv=64, plen=[12300], tlen=[10, 5])
+    call = Call(c, dev)
+    call.plen.fill_(12301)
+    call.tlen.copy_(torch.tensor([2 ** 31 - 1, 5], dtype=torch.int32))
+    call()
+    torch.cuda.synchronize()
+    assert M.mtp_workspace_status(call.ws) == 7
+    assert_close(call.out.cpu().numpy().reshape(2, 4, 64), np.array(_reference(c)[0]), "nearest lengths", ATTN_TOL)
+
+
+def test_counters_and_joins_of_a_shared_workspace(dev):  # noqa: F811
+    """Calls whose parts are counted, between rules of 1024 rows, whose joins lie beside the counters; captured and
+    replayed in turn as well."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    calls = [Call(_attn_case(31, nh=8, nkv=8, dqk=64, dv=64, plen=[0], tlen=[3000, 2, -1, 1700], sinks=True), dev),
+             Call(_attn_case(32, nh=16, nkv=2, dqk=256, dv=256, plen=[900], tlen=[9, 700, 2]), dev),
+             Call(_attn_case(33, nh=8, nkv=2, dqk=64, dv=64, plen=[12400], tlen=[900, 3]), dev)]
+    x = np.random.default_rng(4).standard_normal((1024, 5001)).astype(np.float32)
+    logits, want = _t(x, dev), [t for t, _ in T.greedy(x)]
+    tok, val = torch.empty(1024, dtype=torch.int32, device=dev), torch.empty(1024, device=dev)
+    ws = M.workspace(max([c.ws.numel() for c in calls] + [M.logit_rules_argmax_workspace_bytes(1024)]))
+    rules = M.logit_rules(5001)
+
+    def all_of_them():
+        for c in calls:
+            c.ws = ws
+            c()
+            M.logit_rules_argmax(rules, logits, tok, val, None, ws)
+
+    all_of_them()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        all_of_them()
+    for _ in range(3):
+        tok.fill_(-9)
+        for c in calls:
+            c.out.fill_(7.0)
+        g.replay()
+        all_of_them()
+        for i, c in enumerate(calls):
+            c.check(f"call {i}")
+        assert tok.tolist() == want
+
+
+def test_first_call_of_a_process_is_captured(dev):  # noqa: F811
+    """Each call's first launch in a process may be under capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import numpy as np, torch
+import test_gpu_beams as G
+import mtp_speculative_draft_gb300 as M
+from oracle import beam_oracle as B
+dev = torch.device("cuda:0")
+torch.zeros(1, device=dev)
+for kw in (dict(nh=8, nkv=2, dqk=64, dv=64, plen=[12300]), dict(nh=4, nkv=2, dqk=160, dv=128, plen=[300]),
+           dict(nh=5, nkv=1, dqk=64, dv=160, plen=[12300])):
+    call = G.Call(G._attn_case(3, tlen=[5, 90], norm=False, rot=0, **kw), dev)
+    sel = G.Select(G._beams(4, 2, 3, 9000), 3, dev)
+    k = np.random.default_rng(1).standard_normal((6, 2, 9, 32)).astype(np.float32)
+    tk, tv = G._t(k, dev), G._t(k, dev)
+    moves, parent = M.kv_tails([tk], [tv], 3), torch.tensor([1, 2, 0, 0, 0, 1], dtype=torch.int32, device=dev)
+    length, ws = torch.full((6,), 8, dtype=torch.int32, device=dev), M.workspace(M.kv_beam_workspace_bytes())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        sel()
+        M.kv_beam_reorder(moves, parent, length, 9, ws)
+    g.replay()
+    call.check()
+    sel.check()
+    assert (tk.cpu().numpy() == B.beam_reorder(k, [[1, 2, 0], [0, 0, 1]], [8] * 6, 3)).all() and torch.equal(tk, tv)
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = {**os.environ, "PYTHONPATH": os.pathsep.join([here, os.path.dirname(here)])}
+    done = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_calls_on_two_streams_at_once(dev):  # noqa: F811
+    """Selections and moves of their own workspaces, interleaved on two streams."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sel = [Select(_beams(60 + i, 4 - i, 5, 30000 + i, done=True, alpha=0.7), 7, dev, shift=i) for i in range(2)]
+    rng = np.random.default_rng(3)
+    k = [rng.standard_normal((4, 2, 50, 64)).astype(np.float32) for _ in side]
+    t = [_t(x, dev) for x in k]
+    tails = [M.kv_tails([x], [x.clone()], 2) for x in t]
+    swap, length = torch.tensor([1, 0, 1, 0], dtype=torch.int32, device=dev), torch.full((4,), 41, dtype=torch.int32, device=dev)
+    ws = [M.workspace(M.kv_beam_workspace_bytes()) for _ in side]
+    torch.cuda.synchronize()
+    for _ in range(25):  # an odd number of swaps
+        for i, s in enumerate(side):
+            sel[i](s)
+            M.kv_beam_reorder(tails[i], swap, length, 50, ws[i], s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        sel[i].check(f"stream {i}")
+        np.testing.assert_array_equal(t[i].cpu().numpy(), B.beam_reorder(k[i], [[1, 0], [1, 0]], [41] * 4, 2))
+
+
+def test_beams_of_a_length_above_their_tails(dev):  # noqa: F811
+    """A tail that is full: prefix and tail at their bounds, the last row of the cache written."""
+    c = _attn_case(41, nh=4, nkv=2, dqk=64, dv=64, plen=[100], tlen=[20, 20], m=3)
+    c["kt"], c["vt"] = c["kt"][:, :, :23].copy(), c["vt"][:, :, :23].copy()
+    call = Call(c, dev)
+    call()
+    call.check()
+
+
+@pytest.mark.parametrize("vocab,k", [(40000, 128), (152577, 64)])
+def test_values_of_few_bits(dev, vocab, k):  # noqa: F811
+    """Logits as a bfloat16 head leaves them: many equal ones around every border."""
+    import torch
+    c = _beams(51, 2, 4, vocab, done=True, alpha=0.6)
+    c["x"] = torch.from_numpy(c["x"]).bfloat16().float().numpy()
+    call = Select(c, k, dev)
+    call()
+    call.check()
