@@ -34,15 +34,15 @@ constexpr int kMergeList = 1024;                    // candidates that are put i
 struct SelArgs {
   const float* x;
   long long ld;
-  int beams, V, k, chunks, cap, eos;
+  int beams, V, k, chunks, cap, eos, resident;  // resident: CTAs of the rows launch at once
   unsigned long long magic;   // 2^64 / (chunks * cap), rounded up: an index' row by a product
   float alpha;
   const float* score;
   const int *len, *done;
   int *parent, *token, *len_out, *done_out;
   float* score_out;
-  double* sum;                // [rows][chunks] sum of exponentials, of which
-  float* top;                 // [rows][chunks] is the largest logit
+  unsigned long long* sum;    // [rows][chunks] sum of exponentials relative to the largest logit, in 2^-40
+  float* top;                 // [rows][chunks] (below 2^53; all ones: NaN), the largest logit
   unsigned long long* cand;   // [rows][chunks][cap] logit key, ~token; 0: none
   unsigned long long* ranks;  // [rows][chunks][cap] their ranks, where many are equal
   int* err;
@@ -110,7 +110,19 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   pdl_wait();
   pdl_launch_dependents();
   const size_t slot = (size_t)r * a.chunks + c;
+  if (tid == kSelThreads - 1) {
+    // the chunk that takes this one's place goes to L2 while this one is worked on
+    const unsigned next = blockIdx.y * gridDim.x + blockIdx.x + a.resident;
+    if (next < gridDim.x * gridDim.y) {
+      const float* row = a.x + (size_t)(next / gridDim.x) * a.ld;
+      const int skew = (int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3), c0 = (int)(next % gridDim.x) * kSelChunk - skew;
+      const int from = c0 < 0 ? (c0 + 4) & 3 : c0, to = min(c0 + kSelChunk, (a.V + skew) / 4 * 4 - skew);  // 16-byte words of the row
+      if (to > from) l2_prefetch(row + from, (uint32_t)(to - from) * 4);
+    }
+  }
   if (!beam_live(a, r)) return;  // the row is not read
+  unsigned long long* const out = a.cand + slot * a.cap;
+  for (int i = tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate, until one is written below
   const float* x = a.x + (size_t)r * a.ld;
   // chunks start at 16-byte boundaries: logit e of the row is number e + skew
   const int skew = (int)((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
@@ -168,7 +180,6 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   }
   __syncthreads();
   const float low = key_float(max(sh.low, kNoKey + 1));
-  unsigned long long* out = a.cand + slot * a.cap;
   if (mx >= low) {
     uint32_t mask = 0;
 #pragma unroll
@@ -181,25 +192,22 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
     }
   }
   if (warp == kWarps - 1) {
-    double t = 0.0;
+    unsigned long long t = 0;
     bool nan = false;
     if (lane < kWarps) {
       nan = sh.sum[lane][0] == 0xFFFFFFFFu;
-      t = (double)sh.sum[lane][0] * 0x1p-20 + (double)sh.sum[lane][1] * 0x1p-40;
+      t = ((unsigned long long)sh.sum[lane][0] << 20) + sh.sum[lane][1];
     }
 #pragma unroll
     for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     nan = __any_sync(0xffffffffu, nan);
     if (lane == 0) {
       a.top[slot] = M;
-      a.sum[slot] = nan ? __longlong_as_double(0x7FF8000000000000ll) : t;
+      a.sum[slot] = nan ? ~0ull : t;
     }
   }
   __syncthreads();
-  const int total = sh.n;
-  if (total <= a.cap) {
-    for (int i = total + tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate
-  } else {
+  if (sh.n > a.cap) {
     // the k-th largest key, then how many of that key are wanted, and up to which token
     uint32_t kth = 0;
 #pragma unroll 1
@@ -390,9 +398,15 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     const size_t at = (size_t)(row0 + b) * a.chunks;
     float m = -INFINITY;
     double s = 0.0;
+    bool nan = false;
+    auto part = [&](int c) {
+      const unsigned long long w = a.sum[at + c];
+      nan |= w == ~0ull;
+      return (double)w * 0x1p-40;
+    };
     if (lane < a.chunks) {
       m = a.top[at + lane];
-      s = a.sum[at + lane];
+      s = part(lane);
     }
     float M = m;
     for (int c = lane + 32; c < a.chunks; c += 32) M = fmaxf(M, a.top[at + c]);
@@ -400,11 +414,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     s = m == -INFINITY ? 0.0 : s * (double)expf(m - M);
     for (int c = lane + 32; c < a.chunks; c += 32) {
       m = a.top[at + c];
-      if (m != -INFINITY) s += a.sum[at + c] * (double)expf(m - M);
+      if (m != -INFINITY) s += part(c) * (double)expf(m - M);
     }
+    nan = __any_sync(0xffffffffu, nan);
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
-      if (fabsf(M) < INFINITY && s == s) {
+      if (fabsf(M) < INFINITY && !nan) {
         const double lse = (double)M + table_log(sh.math, s);
         sh.lse[b] = lse;
         sh.base[b] = (float)(sh.score[b] - lse);
@@ -573,6 +588,7 @@ struct MoveArgs {
   float* v[kMoveLayers];
   const int *parent, *len;
   int seqs, beams, nkv, dqk, dv, most, rows, tiles;  // rows a tile
+  int shift;                                         // of a beam's 2^shift 16-byte words of a tile
   long long cap;
   int* err;
 };
@@ -581,7 +597,8 @@ struct MoveArgs {
 // its rows of every beam that changes into registers before it writes any of
 // them, so beams may exchange places, or several take one beam's tail.
 __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_constant__ MoveArgs a) {
-  __shared__ int to[kBeamsMost], from[kBeamsMost], words[kBeamsMost];
+  __shared__ float *to[kBeamsMost], *from[kBeamsMost];
+  __shared__ int words[kBeamsMost];
   __shared__ int n;
   const int tid = threadIdx.x;
   const int seq = blockIdx.x / a.tiles, r0 = blockIdx.x % a.tiles * a.rows;
@@ -610,8 +627,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_cons
       const unsigned m = __ballot_sync(0xffffffffu, moves);
       if (moves) {
         const int i = have + __popc(m & ((1u << tid) - 1));
-        to[i] = b;
-        from[i] = p;
+        to[i] = base + b * beam_step;
+        from[i] = base + p * beam_step;
         words[i] = rows * d / 4;
       }
       have += __popc(m);
@@ -619,24 +636,25 @@ __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_cons
     if (tid == 0) n = have;
   }
   __syncthreads();
-  const int seg = a.rows * d / 4, all = n * seg;
+  // word w of the j-th beam that changes is number j 2^shift + w
+  const int all = n << a.shift, mask = (1 << a.shift) - 1;
   float4 x[kMoveWords];
 #pragma unroll
   for (int i = 0; i < kMoveWords; ++i) {
-    const int e = tid + i * kMoveThreads, j = e / seg, w = e - j * seg;
-    if (e < all && w < words[j]) x[i] = *reinterpret_cast<const float4*>(base + from[j] * beam_step + 4 * w);
+    const int e = tid + i * kMoveThreads, j = e >> a.shift, w = e & mask;
+    if (e < all && w < words[j]) x[i] = *reinterpret_cast<const float4*>(from[j] + 4 * w);
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMoveWords; ++i) {
-    const int e = tid + i * kMoveThreads, j = e / seg, w = e - j * seg;
-    if (e < all && w < words[j]) *reinterpret_cast<float4*>(base + to[j] * beam_step + 4 * w) = x[i];
+    const int e = tid + i * kMoveThreads, j = e >> a.shift, w = e & mask;
+    if (e < all && w < words[j]) *reinterpret_cast<float4*>(to[j] + 4 * w) = x[i];
   }
 }
 
 // ------------------------------------------------------------------ host
 struct SelWs {
-  double* sum;
+  unsigned long long* sum;
   unsigned long long* cand;
   unsigned long long* ranks;
   float* top;
@@ -660,7 +678,7 @@ static SelWs sel_ws(void* ws, int rows, int V, int k) {
     return p;
   };
   const size_t slots = (size_t)rows * sel_chunks(V);
-  w.sum = reinterpret_cast<double*>(take(8 * slots));
+  w.sum = reinterpret_cast<unsigned long long*>(take(8 * slots));
   w.cand = reinterpret_cast<unsigned long long*>(take(8 * slots * sel_cap(k)));
   w.ranks = reinterpret_cast<unsigned long long*>(take(8 * slots * sel_cap(k)));
   w.top = reinterpret_cast<float*>(take(4 * slots));
@@ -734,6 +752,7 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.k = k;
   a.chunks = sel_chunks(B->vocab);
   a.cap = sel_cap(k);
+  a.resident = 4 * sm_count();
   a.magic = ~0ull / ((unsigned long long)a.chunks * a.cap) + 1;
   a.eos = B->eos;
   a.alpha = B->length_penalty;
@@ -789,8 +808,11 @@ mtp_status kv_beam_reorder(const mtp_kv_caches* C, const int32_t* d_parent, int3
   a.dqk = C->head_dim_qk;
   a.dv = C->head_dim_v;
   a.most = max_len;
-  // a tile of every beam fits the CTA's registers: 64 KB, or a row each of 64 beams of 256 dims
-  a.rows = std::min(max_len, kMoveThreads * kMoveWords / (beams * std::max(a.dqk, a.dv) / 4));
+  // a tile of every beam fits the CTA's registers: 64 KB, a power of two a beam (a row each of 64 beams of 256 dims)
+  a.shift = 12;
+  static_assert(kMoveThreads * kMoveWords == 1 << 12, "16-byte words of a CTA");
+  while ((beams << a.shift) > 1 << 12) --a.shift;
+  a.rows = std::min(max_len, (4 << a.shift) / std::max(a.dqk, a.dv));
   a.tiles = (max_len + a.rows - 1) / a.rows;
   if ((int64_t)a.tiles * n_seqs > 0x7FFFFFFF)
     return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: more than 2^31 tiles of rows");

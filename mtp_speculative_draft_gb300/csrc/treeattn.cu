@@ -234,9 +234,6 @@ __device__ __forceinline__ void split_f16x2(uint64_t v, uint32_t& hi, uint32_t& 
   lo = half2_bits(__floats2half2_rn(d.x, d.y));
 }
 
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ float max16(const float (&v)[16]) {
   float t[8];
 #pragma unroll
