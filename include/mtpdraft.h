@@ -55,7 +55,7 @@
 extern "C" {
 #endif
 
-#define MTPDRAFT_VERSION 3
+#define MTPDRAFT_VERSION 4
 
 typedef enum {
     MTP_OK = 0,

@@ -8,13 +8,16 @@
 //   ranked by s / length^alpha; a finished beam's only candidate is itself.
 // Two launches for the selection:
 //   1. rows:   a CTA a chunk of a row: its largest logit, the sum of
-//              exponentials, and at most 2 k logits among which are its k largest;
+//              exponentials, and a few logits among which are its k largest;
 //   2. merge:  a CTA a prompt: the rows' normalisers, the candidates' ranks, the
 //              best k in order.
 // Within a row candidates go by their logits, between rows by ranks in 64 bits:
 // float32 scores of about -30 are 2e-6 apart, and candidates that close are
 // common among 150k tokens.  Sums of exponentials: 32 terms in float32 a thread,
-// the rest in 64 bits.
+// a row's 2e-8 from the exact one on ordinary logits.
+//
+// Measured (graph): 4 x 4096, 4 candidates 9 us; 8 x 151936, 16 candidates 13 us;
+// 16 prompts of 4 x 152577, 8 candidates 17.5 us (39 MB: 2.2 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -34,7 +37,7 @@ constexpr int kMergeList = 1024;                    // candidates that are put i
 struct SelArgs {
   const float* x;
   long long ld;
-  int beams, V, k, chunks, cap, eos, resident;  // resident: CTAs of the rows launch at once
+  int beams, V, k, chunks, cap, eos;
   unsigned long long magic;   // 2^64 / (chunks * cap), rounded up: an index' row by a product
   float alpha;
   const float* score;
@@ -100,8 +103,11 @@ struct RowsSmem {
 // above it hold the chunk's k largest; where equal logits make them more than
 // `cap`, the k largest are found exactly (lower tokens first among equals).
 // A thread's sum of exponentials has 6 roundings a term; the threads' are added
-// exactly, in integers of 2^-20 and 2^-40 (a 64-bit addition costs a warp 16 cycles
-// of an SM: 64 rows of 152577 took 16 us with them, 9 without).
+// exactly, in integers of 2^-20 and 2^-40 (a 64-bit floating addition costs a warp 16
+// cycles of an SM).
+// 64 rows of 152577: 11 us, two waves of CTAs, each 3 us of reads at HBM's rate and
+// 2.5 us of work behind them (the second wave's reads sent to L2 ahead: no change;
+// 512 threads of 16 logits 20 us in all, not 17.5; chunks of 4096 19.5).
 __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_constant__ SelArgs a) {
   __shared__ RowsSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -110,16 +116,6 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   pdl_wait();
   pdl_launch_dependents();
   const size_t slot = (size_t)r * a.chunks + c;
-  if (tid == kSelThreads - 1) {
-    // the chunk that takes this one's place goes to L2 while this one is worked on
-    const unsigned next = blockIdx.y * gridDim.x + blockIdx.x + a.resident;
-    if (next < gridDim.x * gridDim.y) {
-      const float* row = a.x + (size_t)(next / gridDim.x) * a.ld;
-      const int skew = (int)((reinterpret_cast<uintptr_t>(row) >> 2) & 3), c0 = (int)(next % gridDim.x) * kSelChunk - skew;
-      const int from = c0 < 0 ? (c0 + 4) & 3 : c0, to = min(c0 + kSelChunk, (a.V + skew) / 4 * 4 - skew);  // 16-byte words of the row
-      if (to > from) l2_prefetch(row + from, (uint32_t)(to - from) * 4);
-    }
-  }
   if (!beam_live(a, r)) return;  // the row is not read
   unsigned long long* const out = a.cand + slot * a.cap;
   for (int i = tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate, until one is written below
@@ -334,7 +330,9 @@ __device__ __forceinline__ double table_exp(const MathTables& t, double x) {
 // so candidates are first compared by float32 ranks with a bound of their error;
 // only those that may be among the k best get a rank in 64 bits.  What depends on
 // the beams alone is worked out while the rows are still being read.  Bound by the
-// latency of its steps and of fetching its instructions, which are few for that.
+// latency of its steps and of fetching its instructions, which are few for that: 8
+// rows of 151936 take 7 us from the rows' end (all ranks, logarithms and powers in
+// 64 bits: 45 us).
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
   __shared__ MergeSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -595,7 +593,9 @@ struct MoveArgs {
 
 // grid (row tiles x prompts, KV heads x K or V, layers).  In place: a CTA reads
 // its rows of every beam that changes into registers before it writes any of
-// them, so beams may exchange places, or several take one beam's tail.
+// them, so beams may exchange places, or several take one beam's tail.  Bound by
+// HBM: 8 prompts of 4 beams, tails of 94 to 101 rows, 48 layers of 8 heads of 2 x 128:
+// 272 us, 1.59 GB at 5.9 TB/s (301 with a division a word instead of a shift).
 __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_constant__ MoveArgs a) {
   __shared__ float *to[kBeamsMost], *from[kBeamsMost];
   __shared__ int words[kBeamsMost];
@@ -752,7 +752,6 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.k = k;
   a.chunks = sel_chunks(B->vocab);
   a.cap = sel_cap(k);
-  a.resident = 4 * sm_count();
   a.magic = ~0ull / ((unsigned long long)a.chunks * a.cap) + 1;
   a.eos = B->eos;
   a.alpha = B->length_penalty;
