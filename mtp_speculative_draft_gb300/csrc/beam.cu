@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     const float score = a.score[r];
     const bool done = a.done && a.done[r] != 0;
     kind = fabsf(score) < INFINITY ? (done ? 2 : 1) : 0;
-    next = (a.len ? a.len[r] : 0) + (kind == 1);
+    next = a.len ? a.len[r] : 0;
+    if (kind == 1 && next < 0x7FFFFFFF) ++next;
     sh.score[tid] = (double)score;
     sh.base[tid] = score;  // of a finished beam
     sh.kind[tid] = kind;

@@ -228,3 +228,65 @@ def test_values_of_few_bits(dev, vocab, k):  # noqa: F811
     call = Select(c, k, dev)
     call()
     call.check()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(nh=6, nkv=2, dqk=64, dv=64, plen=[90, 40], tlen=[5, 9, 0, 3], m=5, axes=(12, 10, 10)),
+    dict(nh=6, nkv=2, dqk=64, dv=64, plen=[12300], tlen=[5, 9], m=9, axes=(8, 8), rot=32),
+    dict(nh=4096, nkv=64, dqk=32, dv=32, plen=[70], tlen=[5], norm=False),
+    dict(nh=64, nkv=64, dqk=32, dv=32, plen=[12289], tlen=[5], sinks=True),
+    dict(nh=9, nkv=1, dqk=96, dv=160, plen=[33], tlen=[64, 65, 63], m=16, window=70),
+])
+def test_attention_of_other_layouts(dev, kw):  # noqa: F811
+    call = Call(_attn_case(900, **kw), dev)
+    call()
+    call.check(str(kw))
+
+
+@pytest.mark.parametrize("plen", [90, 12300])
+def test_most_sequences_and_rows(dev, plen):  # noqa: F811
+    """1024 sequences of 16 new rows: a few of them against the reference, which takes them alone."""
+    c = _attn_case(50, nh=2, nkv=1, dqk=32, dv=32, plen=[plen], tlen=[(5 * i) % 40 - 1 for i in range(1024)], m=16)
+    call = Call(c, dev)
+    call()
+    got, m = call.out.cpu().numpy().reshape(1024, 16, 2, 32), 16
+    pick = [0, 1, 7, 511, 512, 777, 1023]
+    rows = np.concatenate([np.arange(b * m, b * m + m) for b in pick])
+    sub = {**c, "tlen": [c["tlen"][b] for b in pick], "kt": c["kt"][pick], "vt": c["vt"][pick],
+           **{n: c[n][rows] for n in ("qp", "kp", "vp")}}
+    ref, k, _ = _reference(sub)
+    kt = call.kt.cpu().numpy()
+    for x, b in enumerate(pick):
+        t = c["tlen"][b]
+        if t < 0:
+            assert (got[b] == 7).all() and np.isnan(kt[b]).all()
+        else:
+            assert_close(got[b], np.array(ref[x * m:x * m + m]), f"sequence {b}", ATTN_TOL)
+            assert_close(kt[b, :, t:t + m], k[x * m:x * m + m].transpose(1, 0, 2), f"keys of {b}", 2e-6)
+
+
+def test_finished_beams_without_lengths(dev):  # noqa: F811
+    """Flags and scores alone, and no new flags wanted."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    c = _beams(71, 3, 4, 700, done=True)
+    call = Select(c, 5, dev)
+    beams = M.beam_set(3, 4, 700, call.score, done=call.done, eos=c["eos"])
+    M.beam_select(beams, call.x, 5, call.parent, call.token, call.new_score, ws=call.ws)
+    ref = B.beam_select(c["x"], 3, 4, 5, c["score"], done=c["done"], eos=c["eos"])
+    torch.cuda.synchronize()
+    assert call.parent.tolist() == ref[0].tolist() and call.token.tolist() == ref[1].tolist()
+    assert (call.new_length == -9).all() and (call.new_done == -9).all()
+
+
+def test_lengths_at_the_end_of_their_range(dev):  # noqa: F811
+    """2^31 - 1 tokens, and one less: the length stays there."""
+    c = _beams(72, 1, 3, 500, alpha=0.5)
+    c["length"][:] = 2 ** 31 - 1, 2 ** 31 - 2, 5
+    call = Select(c, 3, dev)
+    call()
+    import torch
+    torch.cuda.synchronize()
+    want = B.beam_select(c["x"], 1, 3, 3, c["score"], c["length"], alpha=0.5)
+    assert call.token.tolist() == want[1].tolist() and call.parent.tolist() == want[0].tolist()
+    assert call.new_length[0].tolist() == [min(2 ** 31 - 1, int(c["length"][p]) + 1) for p in call.parent[0].tolist()]
