@@ -48,7 +48,6 @@ struct SelArgs {
   float* top;                 // [rows][chunks] (below 2^53; all ones: NaN), the largest logit
   unsigned long long* cand;   // [rows][chunks][cap] logit key, ~token; 0: none
   unsigned long long* ranks;  // [rows][chunks][cap] their ranks, where many are equal
-  int* err;
 };
 
 // Floats as unsigned integers in the same order (-0 and 0 alike; NaN below all
@@ -102,9 +101,9 @@ struct RowsSmem {
 // threads bounds the chunk's k-th largest from below, so the few logits at or
 // above it hold the chunk's k largest; where equal logits make them more than
 // `cap`, the k largest are found exactly (lower tokens first among equals).
-// A thread's sum of exponentials has 6 roundings a term; the threads' are added
-// exactly, in integers of 2^-20 and 2^-40 (a 64-bit floating addition costs a warp 16
-// cycles of an SM).
+// A thread's sum of exponentials has 6 roundings a term; the threads' are cut off at
+// 2^-40 of the chunk's largest and added exactly, in integers of 2^-20 and 2^-40 (a
+// 64-bit floating addition costs a warp 16 cycles of an SM).
 // 64 rows of 152577: 11 us, two waves of CTAs, each 3 us of reads at HBM's rate and
 // 2.5 us of work behind them (the second wave's reads sent to L2 ahead: no change;
 // 512 threads of 16 logits 20 us in all, not 17.5; chunks of 4096 19.5).
@@ -220,8 +219,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
       __syncthreads();
       if (sh.n >= a.k) kth = t;
     }
-    // of the tokens with that key, the lowest below `end` are taken: the least
-    // end at which k tokens are there
+    // of the tokens with that key, those up to `end` are taken: the least end at
+    // which k tokens are there
     int end = 0;
 #pragma unroll 1
     for (int bit = 30; bit >= 0; --bit) {
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
             hik[i] = hi == hi ? float_key(hi) : 0xFFFFFFFFu;
           }
         }
-        if (hik[i] >= low) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], key_float((uint32_t)(w[i] >> 32)));
+        if (pass == 1 && hik[i] >= low) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], key_float((uint32_t)(w[i] >> 32)));
       }
     }
     if (pass == 0) {
@@ -768,7 +767,6 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.top = w.top;
   a.ranks = w.ranks;
   a.cand = w.cand;
-  a.err = &static_cast<WsHeader*>(d_ws)->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(beam_rows_kernel, dim3(a.chunks, rows), kSelThreads, 0, st, a);
   if (e == cudaSuccess) e = launch_pdl(beam_merge_kernel, dim3(B->n_seqs), kMergeThreads, 0, st, a);

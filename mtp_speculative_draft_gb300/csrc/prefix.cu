@@ -619,8 +619,8 @@ static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
 
 // Parts of a sequence's keys, for `units` (sequence, KV head, new row, block of
 // heads): as many as the SMs hold at once (`ctas`), of kPartBytes of keys and values
-// or more; tails that differ in length get a third more (24 of up to 2048 rows: 69
-// us, not 75).  One warp joins them.
+// or more; tails that differ in length get a third more (24 of up to 2048 rows: 60
+// us, 66 without, 68 with twice as many).  One warp joins them.
 constexpr int kTailCtas = 6, kPartBytes = 64 * 1024;  // CTAs a SM at most
 
 // CTAs of the tail launch that an SM holds.

@@ -290,3 +290,22 @@ def test_lengths_at_the_end_of_their_range(dev):  # noqa: F811
     want = B.beam_select(c["x"], 1, 3, 3, c["score"], c["length"], alpha=0.5)
     assert call.token.tolist() == want[1].tolist() and call.parent.tolist() == want[0].tolist()
     assert call.new_length[0].tolist() == [min(2 ** 31 - 1, int(c["length"][p]) + 1) for p in call.parent[0].tolist()]
+
+
+@pytest.mark.parametrize("vocab,k", [(12, 24), (9000, 128)])
+def test_logits_at_the_ends_of_their_range(dev, vocab, k):  # noqa: F811
+    """Scores below the lowest float: each candidate once, in order, its score -infinity."""
+    import torch
+    c = _beams(73, 1, 2, vocab)
+    if vocab > 100:
+        c["x"][0] = -3e38
+    c["x"][0, :8] = 3e38, -3e38, 0, 1e30, -1e38, -3.2e38, 2.9e38, 3.1e38
+    c["x"][1, 12:] = -np.inf
+    call = Select(c, k, dev)
+    call()
+    torch.cuda.synchronize()
+    want = B.beam_select(c["x"], 1, 2, k, c["score"], c["length"])
+    assert call.parent.tolist() == want[0].tolist() and call.token.tolist() == want[1].tolist()
+    with np.errstate(over="ignore"):
+        np.testing.assert_allclose(call.new_score.cpu().numpy(), want[2].astype(np.float32), rtol=2.0 ** -23)
+    assert call.new_length.tolist() == want[3].tolist()
