@@ -33,12 +33,15 @@ constexpr int kBeamRows = 1024;                     // beams of a call
 constexpr int kSelVocab = 1 << 30;                  // tokens
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeList = 1024;                    // candidates that are put in order at once
+constexpr int kMergeSort = 192;                     // and without a closer look first
+constexpr int kMergeChunks = 1024;                  // chunks in a list
 
 struct SelArgs {
   const float* x;
   long long ld;
   int beams, V, k, chunks, cap, eos;
-  unsigned long long magic;   // 2^64 / (chunks * cap), rounded up: an index' row by a product
+  int units;                  // warps' loads of a chunk's candidates
+  unsigned long long magic_chunks, magic_units;  // 2^64 / chunks and 2^32 / units, rounded up: quotients by products
   float alpha;
   const float* score;
   const int *len, *done;
@@ -86,6 +89,38 @@ __device__ __forceinline__ void kth_largest(const uint32_t* keys, int n, int k, 
               (x.z > mine || (x.z == mine && i + 2 < tid)) + (x.w > mine || (x.w == mine && i + 3 < tid));
   }
   if (before == k - 1) *found = mine;
+}
+
+// About the k-th largest of 32 P keys in shared memory, from below (between k and
+// k + k / 16 are at or above it, or it is exact): one warp, bit by bit behind those
+// that all have in common.
+template <int P>
+__device__ __forceinline__ void near_kth_largest(const uint32_t* keys, int k, uint32_t* found) {
+  const int lane = threadIdx.x & 31;
+  uint32_t mine[P], least = ~0u, most = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    mine[i] = keys[lane + 32 * i];
+    least = min(least, mine[i]);
+    most = max(most, mine[i]);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  uint32_t t = most;
+  if (least != most) {
+    uint32_t bit = 0x80000000u >> __clz(least ^ most);
+    t &= ~(2 * bit - 1);
+#pragma unroll 1
+    for (; bit; bit >>= 1) {
+      int m = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) m += mine[i] >= (t | bit);
+      m = __reduce_add_sync(0xffffffffu, m);
+      if (m >= k) t |= bit;
+      if (m >= k && m <= k + k / 16) break;
+    }
+  }
+  if (lane == 0) *found = t;
 }
 
 struct RowsSmem {
@@ -146,21 +181,26 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   for (int j = 0; j < kSelPer; ++j) mx = fmaxf(mx, v[j]);
   const uint32_t top = float_key(mx), wtop = __reduce_max_sync(0xffffffffu, top);
   // groups of 4 threads do for few candidates (64 groups, 18 logits at or above
-  // the 16th's), single threads for many
+  // the 16th's), of 2 for up to 32 (128; 39 at or above the 32nd's), single threads for
+  // more (64 rows, 64 candidates: 19 us; with 2 the chunks that keep more than `cap`
+  // make it 83).  Those by bits: counting 256 keys for each took 34 us, not 19.
   uint32_t gtop = top;
-  const bool quads = a.k <= 16;
-  if (quads) {
-    gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 1));
-    gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 2));
-  }
-  if (!quads || (lane & 3) == 0) sh.group[quads ? tid >> 2 : tid] = gtop;
+  const int group = a.k <= 16 ? 2 : a.k <= 32 ? 1 : 0;  // log2 of a group's threads
+  if (group > 0) gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 1));
+  if (group > 1) gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 2));
+  if ((lane & ((1 << group) - 1)) == 0) sh.group[tid >> group] = gtop;
   if (lane == 0) sh.wmax[warp] = wtop;
   __syncthreads();
   uint32_t mtop = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) mtop = max(mtop, sh.wmax[w]);
   const float M = key_float(mtop), ref = M == -INFINITY ? 0.f : M;  // the chunk's largest logit
-  kth_largest(sh.group, quads ? kSelThreads / 4 : kSelThreads, a.k, &sh.low);
+  if (group == 2)
+    kth_largest(sh.group, kSelThreads / 4, a.k, &sh.low);
+  else if (warp == 0 && group == 1)
+    near_kth_largest<kSelThreads / 64>(sh.group, a.k, &sh.low);
+  else if (warp == 0)
+    near_kth_largest<kSelThreads / 32>(sh.group, a.k, &sh.low);
   float s8[8] = {};
 #pragma unroll
   for (int j = 0; j < kSelPer; ++j) s8[j & 7] += ex2((v[j] - ref) * kLog2e);
@@ -302,7 +342,9 @@ struct MergeSmem {
   unsigned long long best_key[kMergeThreads / 32];
   unsigned long long best_id[kMergeThreads / 32];
   unsigned long long last_key, last_id;
-  int n;
+  uint32_t slot[kMergeChunks];                   // chunks that may hold one of the k best, and their beams
+  uint8_t slot_beam[kMergeChunks];
+  int n, slots;
 };
 
 // log of a finite s >= 2^-1022 after P. T. P. Tang's table-driven method (1990):
@@ -331,13 +373,14 @@ __device__ __forceinline__ double table_exp(const MathTables& t, double x) {
 // the beams alone is worked out while the rows are still being read.  Bound by the
 // latency of its steps and of fetching its instructions, which are few for that: 8
 // rows of 151936 take 7 us from the rows' end (all ranks, logarithms and powers in
-// 64 bits: 45 us).
+// 64 bits: 45 us).  Candidates are read a chunk by a warp: chunk and beam are then
+// known without a division a candidate.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
   __shared__ MergeSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = blockIdx.x, row0 = seq * a.beams;
   constexpr int kWarps = kMergeThreads / 32;
-  if (tid == 0) sh.n = 0;
+  if (tid == 0) sh.n = sh.slots = 0;
   if (tid < (int)(sizeof(MathTables) / 8)) reinterpret_cast<double*>(&sh.math)[tid] = reinterpret_cast<const double*>(&kTables)[tid];
   // scores, lengths and flags were final before the call's first launch
   int next = 1, kind = 0;
@@ -372,24 +415,41 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
     most = fmax(sh.least[0], sh.least[1]);
     if (tid < a.beams && kind) sh.inv[tid] = (float)(inverse / most);
   }
-  // Candidate `e` of the prompt's lists; 0: none.  (64 beams of 2^30 tokens: just
-  // above 2^31 candidates.)
-  const uint32_t per_row = (uint32_t)a.chunks * a.cap, all = a.beams * per_row;
-  const unsigned long long* cand = a.cand + (size_t)row0 * per_row;
-  auto beam_of = [&](uint32_t e) { return (int)__umul64hi((unsigned long long)e, a.magic); };
-  constexpr int kRound = 4;  // candidates a thread at once
-  const uint32_t rounds = (all + kRound * kMergeThreads - 1) / (kRound * kMergeThreads);
+  // A warp reads 32 candidates of one chunk at a time, a unit of all chunks or of the
+  // listed ones: unit u's beam, and where this lane's candidate is; ~0: none.  (64
+  // beams of 2^30 tokens: just below 2^31 candidates, 2^26 units.)
+  const uint32_t all_slots = (uint32_t)a.beams * a.chunks;
+  const unsigned long long* cand = a.cand + (size_t)row0 * a.chunks * a.cap;
+  uint32_t n_units = all_slots * a.units;
+  bool listed = false;
+  auto beam_of = [&](uint32_t slot) {
+    return a.chunks > 1 ? (int)__umul64hi((unsigned long long)slot, a.magic_chunks) : (int)slot;
+  };
+  auto locate = [&](uint32_t u, int& b) {
+    const uint32_t i = (uint32_t)((unsigned long long)u * a.magic_units >> 32), slot = listed ? sh.slot[i] : i;
+    const int j = (int)(u - i * a.units) * 32 + lane;
+    b = listed ? (int)sh.slot_beam[i] : beam_of(slot);
+    return j < a.cap ? slot * (uint32_t)a.cap + j : ~0u;
+  };
+  constexpr int kRound = 4;  // units of a warp at once
+  uint32_t rounds = (n_units + kRound * kWarps - 1) / (kRound * kWarps);
   unsigned long long w[kRound];
+  int beam[kRound];
   auto load_round = [&](uint32_t q) {
 #pragma unroll
     for (int i = 0; i < kRound; ++i) {
-      const uint32_t e = (q * kRound + i) * kMergeThreads + tid;
-      w[i] = e < all ? cand[e] : 0ull;  // anything where a row was not read
+      const uint32_t u = (q * kRound + i) * kWarps + warp;
+      w[i] = 0;  // also 0: no candidate; anything where a row was not read
+      beam[i] = 0;
+      if (u < n_units) {
+        const uint32_t at = locate(u, beam[i]);
+        if (at != ~0u) w[i] = cand[at];
+      }
     }
   };
   pdl_wait();
   pdl_launch_dependents();
-  load_round(0);  // on their way while the rows' normalisers are worked out
+  if (rounds == 1) load_round(0);  // on their way while the rows' normalisers are worked out
 #pragma unroll 1
   for (int b = warp; b < a.beams; b += kWarps) {
     if (sh.kind[b] != 1) continue;
@@ -451,27 +511,69 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   // first the threads' best from below, of which the k-th largest bounds the k best;
   // then every candidate that may reach it
   const bool itself = tid < a.beams && sh.kind[tid] == 2;  // a finished beam
-  float best = -INFINITY, self_hi = -INFINITY;
-  if (itself) bounds(tid, 0.f, best, self_hi);
-  uint32_t low = 0xFFFFFFFFu, hik[kRound];
+  float self_lo = -INFINITY, self_hi = -INFINITY;
+  if (itself) bounds(tid, 0.f, self_lo, self_hi);
+  uint32_t low = 0;
+  bool direct = false;
+  if (rounds > 1 && all_slots > (uint32_t)a.k) {
+    // many candidates: first the chunks whose largest logit may be among the k best,
+    // by the k-th largest of theirs and of the finished beams (16 rows of 151936, 32
+    // candidates: 17 us in all, 27 without; 64 rows, 64 candidates: 41 and 119)
+    const float* tops = a.top + (size_t)row0 * a.chunks;
+    if (tid < 256) sh.group[tid] = 0;
+    __syncthreads();
+    auto chunk_bounds = [&](uint32_t c, float& lo, float& hi) {
+      const int b = beam_of(c);
+      if (sh.kind[b] != 1) return false;
+      const float t = tops[c];
+      bounds(b, t, lo, hi);
+      return t != -INFINITY;
+    };
+    if (itself && self_lo == self_lo) atomicMax(&sh.group[255 - tid], float_key(self_lo));
+    for (uint32_t c = tid; c < all_slots; c += kMergeThreads) {
+      float lo, hi;
+      if (chunk_bounds(c, lo, hi) && lo == lo) atomicMax(&sh.group[c & 255], float_key(lo));
+    }
+    __syncthreads();
+    kth_largest(sh.group, 256, a.k, &sh.low);
+    __syncthreads();
+    low = sh.low;  // 0: fewer than k
+    direct = low != 0 && a.k <= 64;
+    for (uint32_t c = tid; c < all_slots; c += kMergeThreads) {
+      float lo, hi;
+      if (!chunk_bounds(c, lo, hi) || (hi == hi && float_key(hi) < low)) continue;
+      const int i = atomicAdd(&sh.slots, 1);
+      if (i < kMergeChunks) {
+        sh.slot[i] = c;
+        sh.slot_beam[i] = beam_of(c);
+      }
+    }
+    __syncthreads();
+    if (sh.slots <= kMergeChunks) {  // else all of them
+      listed = true;
+      n_units = sh.slots * a.units;
+      rounds = (n_units + kRound * kWarps - 1) / (kRound * kWarps);
+      load_round(0);
+    }
+  }
+  // the candidates that reach `low`; without one, or if they are too many, first the
+  // threads' best from below, of which the k-th largest is a (better) `low`.  (For
+  // more than 64 they often are: 8 rows, 128 candidates 41 us, not 53; 16 rows, 32
+  // candidates 17 us with one pass, 20 with two.)
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = direct ? 1 : 0; pass < 2; ++pass) {
+    float best = self_lo;
 #pragma unroll 1
     for (uint32_t q = 0; q < rounds; ++q) {
-      if (rounds > 1 && q + pass > 0) load_round(q);
+      if (rounds > 1) load_round(q);
 #pragma unroll
       for (int i = 0; i < kRound; ++i) {
-        const int b = min(beam_of((q * kRound + i) * kMergeThreads + tid), a.beams - 1);
-        if (pass == 0 || rounds > 1) {
-          hik[i] = 0;
-          if (w[i] != 0 && sh.kind[b] == 1) {
-            float lo, hi;
-            bounds(b, key_float((uint32_t)(w[i] >> 32)), lo, hi);
-            best = fmaxf(best, lo);  // NaN takes no part
-            hik[i] = hi == hi ? float_key(hi) : 0xFFFFFFFFu;
-          }
-        }
-        if (pass == 1 && hik[i] >= low) collect(b, 0xFFFFFFFFu - (uint32_t)w[i], key_float((uint32_t)(w[i] >> 32)));
+        if (w[i] == 0 || sh.kind[beam[i]] != 1) continue;
+        const float logit = key_float((uint32_t)(w[i] >> 32));
+        float lo, hi;
+        bounds(beam[i], logit, lo, hi);
+        best = fmaxf(best, lo);  // NaN takes no part
+        if (pass == 1 && (hi != hi || float_key(hi) >= low)) collect(beam[i], 0xFFFFFFFFu - (uint32_t)w[i], logit);
       }
     }
     if (pass == 0) {
@@ -482,13 +584,46 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       __syncthreads();
       kth_largest(sh.group, kMergeThreads / share, a.k, &sh.low);
       __syncthreads();
-      low = max(sh.low, 1u);  // 0: no candidate
-    } else if (itself && (self_hi != self_hi || float_key(self_hi) >= low)) {
-      collect(tid, (uint32_t)a.eos, 0.f);
+      low = max(sh.low, 1u);
+      direct = false;
+    } else {
+      if (itself && (self_hi != self_hi || float_key(self_hi) >= low)) collect(tid, (uint32_t)a.eos, 0.f);
+      __syncthreads();
+      if (sh.n > kMergeList && direct) {
+        __syncthreads();
+        if (tid == 0) sh.n = 0;
+        pass = -1;
+      }
     }
   }
   __syncthreads();
-  const int n = sh.n;
+  int n = sh.n;
+  if (n > kMergeSort && n <= kMergeList) {
+    // of many, only those that reach the k-th largest from below, found bit by bit:
+    // their order takes n^2 comparisons
+    float lo = -INFINITY, hi = -INFINITY;
+    uint32_t b = 0, t = 0;
+    float logit = 0.f;
+    if (tid < n) {
+      b = sh.beam[tid];
+      t = sh.tok[tid];
+      logit = sh.logit[tid];
+      bounds(b, logit, lo, hi);
+    }
+    const uint32_t mine = tid < n ? float_key(lo) : 0u;
+    uint32_t kth = 0;
+#pragma unroll 1
+    for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+      const int m = __syncthreads_count(mine >= (kth | bit));
+      if (m >= a.k) kth |= bit;
+      if (m >= a.k && m <= a.k + a.k / 8) break;
+    }
+    if (tid == 0) sh.n = 0;
+    __syncthreads();
+    if (tid < n && (hi != hi || float_key(hi) >= kth)) collect(b, t, logit);
+    __syncthreads();
+    n = sh.n;
+  }
   auto put = [&](int at, uint32_t b, uint32_t tok, unsigned long long key) {
     const size_t o = (size_t)seq * a.k + at;
     const bool none = b == 0xFFFFFFFFu;
@@ -521,11 +656,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   }
   // many (nearly) equal ranks: all of them in 64 bits, then one candidate after
   // another, each the best behind the last
-  unsigned long long* ranks = a.ranks + (size_t)row0 * per_row;
-  for (uint32_t e = tid; e < all; e += kMergeThreads) {
-    const int b = beam_of(e);
-    const unsigned long long x = sh.kind[b] == 1 ? cand[e] : 0ull;
-    ranks[e] = x ? rank(b, key_float((uint32_t)(x >> 32))) : 0ull;
+  unsigned long long* ranks = a.ranks + (size_t)row0 * a.chunks * a.cap;
+  for (uint32_t u = warp; u < n_units; u += kWarps) {
+    int b;
+    const uint32_t at = locate(u, b);
+    if (at == ~0u) continue;
+    const unsigned long long x = sh.kind[b] == 1 ? cand[at] : 0ull;
+    ranks[at] = x ? rank(b, key_float((uint32_t)(x >> 32))) : 0ull;
   }
   const unsigned long long self_key = itself ? rank(tid, 0.f) : 0ull;
   if (tid == 0) {
@@ -543,10 +680,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
         bi = id;
       }
     };
-    for (uint32_t e = tid; e < all; e += kMergeThreads) {
-      const unsigned long long key = ranks[e];
-      if (key >= bk && key != 0)
-        see(key, (unsigned long long)beam_of(e) << 32 | (0xFFFFFFFFu - (uint32_t)cand[e]));
+    for (uint32_t u = warp; u < n_units; u += kWarps) {
+      int b;
+      const uint32_t at = locate(u, b);
+      const unsigned long long key = at != ~0u ? ranks[at] : 0ull;
+      if (key >= bk && key != 0) see(key, (unsigned long long)b << 32 | (0xFFFFFFFFu - (uint32_t)cand[at]));
     }
     see(self_key, (unsigned long long)tid << 32 | (uint32_t)a.eos);
 #pragma unroll
@@ -752,7 +890,9 @@ mtp_status beam_select(const mtp_beam_set* B, const float* d_logits, int64_t ld,
   a.k = k;
   a.chunks = sel_chunks(B->vocab);
   a.cap = sel_cap(k);
-  a.magic = ~0ull / ((unsigned long long)a.chunks * a.cap) + 1;
+  a.units = (a.cap + 31) / 32;
+  a.magic_chunks = a.chunks > 1 ? ~0ull / (unsigned long long)a.chunks + 1 : 0;
+  a.magic_units = ((1ull << 32) + a.units - 1) / a.units;
   a.eos = B->eos;
   a.alpha = B->length_penalty;
   a.score = B->d_score;

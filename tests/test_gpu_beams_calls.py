@@ -309,3 +309,48 @@ def test_logits_at_the_ends_of_their_range(dev, vocab, k):  # noqa: F811
     with np.errstate(over="ignore"):
         np.testing.assert_allclose(call.new_score.cpu().numpy(), want[2].astype(np.float32), rtol=2.0 ** -23)
     assert call.new_length.tolist() == want[3].tolist()
+
+
+@pytest.mark.parametrize("beams,vocab,k,spread", [
+    (16, 60000, 32, 1.0), (16, 60001, 17, 40.0), (64, 17000, 64, 3.0), (12, 100000, 128, 1.0), (5, 151936, 33, 1.0)])
+@pytest.mark.parametrize("alpha,done", [(0.0, False), (0.7, True)])
+def test_selections_of_many_candidates(dev, beams, vocab, k, spread, alpha, done):  # noqa: F811
+    """More than a CTA holds at once: chunks by their largest logits first; beams alike and far apart."""
+    call = Select(_beams(74, 1, beams, vocab, done, alpha, spread), k, dev)
+    call()
+    call.check()
+
+
+def test_most_of_the_chunks_above_the_bound(dev):  # noqa: F811
+    """Three good beams of 19 chunks and a bad one: the 64th of the chunks' largest is one of the bad beam's."""
+    c = _beams(75, 1, 4, 151936)
+    c["score"][3] -= 30
+    call = Select(c, 64, dev)
+    call()
+    call.check()
+
+
+@pytest.mark.parametrize("k", [1, 16, 33, 128])
+def test_equal_logits_in_more_chunks_than_are_listed(dev, k):  # noqa: F811
+    """64 equal rows of 19 chunks: the first beam's first tokens."""
+    import torch
+    c = dict(x=np.zeros((64, 151936), np.float32), seqs=1, beams=64, score=np.full(64, -7, np.float32),
+             length=np.full(64, 9, np.int32), done=None, eos=2, alpha=0.5)
+    call = Select(c, k, dev)
+    call()
+    torch.cuda.synchronize()
+    assert call.parent[0].tolist() == [0] * k and call.token[0].tolist() == list(range(k))
+    np.testing.assert_allclose(call.new_score.cpu().numpy(), -7 - np.log(151936), rtol=2.0 ** -23)
+
+
+def test_scores_without_bounds_among_many_candidates(dev):  # noqa: F811
+    """Logits of +-3e38 in some of many chunks, a row of NaN, one of infinity, one without a token."""
+    c = _beams(76, 1, 16, 60000)
+    c["x"][0, [0, 9000, 59999]] = 3e38, -3e38, 2.9e38
+    c["x"][1] = np.nan
+    c["x"][2, 5] = np.inf
+    c["x"][3] = -np.inf
+    c["x"][4, 8192:] = -np.inf
+    call = Select(c, 32, dev)
+    call()
+    call.check()
