@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_cons
           len = min(len, a.most);
         }
       }
-      const int rows = min(a.rows, len - r0);
+      const int rows = min(a.rows, max(len, 0) - r0);
       const bool moves = p >= 0 && p != b && rows > 0;
       const unsigned m = __ballot_sync(0xffffffffu, moves);
       if (moves) {

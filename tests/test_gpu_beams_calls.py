@@ -354,3 +354,18 @@ def test_scores_without_bounds_among_many_candidates(dev):  # noqa: F811
     call = Select(c, 32, dev)
     call()
     call.check()
+
+
+def test_lowest_length_of_a_tail_of_several_tiles(dev):  # noqa: F811
+    """A length of -2^31 moves nothing, at any row."""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    k = np.random.default_rng(77).standard_normal((4, 1, 100, 256)).astype(np.float32)
+    tk = _t(k, dev)
+    tv = tk.clone()
+    length = np.array([100, -2 ** 31, 7, -1], np.int32)
+    ws = M.kv_beam_reorder(M.kv_tails([tk], [tv], 4), _t(np.array([1, 0, 3, 2], np.int32), dev), _t(length, dev), 100)
+    torch.cuda.synchronize()
+    assert M.mtp_workspace_status(ws) == 0
+    np.testing.assert_array_equal(tk.cpu().numpy(), B.beam_reorder(k, [1, 0, 3, 2], np.maximum(length, 0), 4))
+    assert torch.equal(tk, tv)
