@@ -733,8 +733,9 @@ struct MoveArgs {
 // its rows of every beam that changes into registers before it writes any of
 // them, so beams may exchange places, or several take one beam's tail.  Bound by
 // HBM: 8 prompts of 4 beams, tails of 94 to 101 rows, 48 layers of 8 heads of 2 x 128:
-// 272 us, 1.59 GB at 5.9 TB/s (301 with a division a word instead of a shift).
-__global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_constant__ MoveArgs a) {
+// 239 us, 1.59 GB at 6.6 TB/s with three CTAs an SM; 257 with CTAs of 512 threads of 8
+// words, 273 with two of this one, 275 with four, which spill.
+__global__ void __launch_bounds__(kMoveThreads, 3) kv_beam_kernel(const __grid_constant__ MoveArgs a) {
   __shared__ float *to[kBeamsMost], *from[kBeamsMost];
   __shared__ int words[kBeamsMost];
   __shared__ int n;
@@ -779,12 +780,14 @@ __global__ void __launch_bounds__(kMoveThreads) kv_beam_kernel(const __grid_cons
   float4 x[kMoveWords];
 #pragma unroll
   for (int i = 0; i < kMoveWords; ++i) {
+    if (i * kMoveThreads >= all) break;
     const int e = tid + i * kMoveThreads, j = e >> a.shift, w = e & mask;
     if (e < all && w < words[j]) x[i] = *reinterpret_cast<const float4*>(from[j] + 4 * w);
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kMoveWords; ++i) {
+    if (i * kMoveThreads >= all) break;
     const int e = tid + i * kMoveThreads, j = e >> a.shift, w = e & mask;
     if (e < all && w < words[j]) *reinterpret_cast<float4*>(to[j] + 4 * w) = x[i];
   }
@@ -950,8 +953,14 @@ mtp_status kv_beam_reorder(const mtp_kv_caches* C, const int32_t* d_parent, int3
   a.shift = 12;
   static_assert(kMoveThreads * kMoveWords == 1 << 12, "16-byte words of a CTA");
   while ((beams << a.shift) > 1 << 12) --a.shift;
-  a.rows = std::min(max_len, (4 << a.shift) / std::max(a.dqk, a.dv));
-  a.tiles = (max_len + a.rows - 1) / a.rows;
+  const int wide = std::max(a.dqk, a.dv);
+  auto tiles = [&](int rows) { return (max_len + rows - 1) / rows; };
+  // smaller tiles where there is not a CTA an SM: 5 beams' 17 rows of 64 dims in one
+  // layer 2.1 us, not 3.1
+  const int64_t lists = (int64_t)n_seqs * 2 * a.nkv * C->n_layers;
+  while (4 << (a.shift - 1) >= wide && lists * tiles((4 << a.shift) / wide) < sm_count()) --a.shift;
+  a.rows = std::min(max_len, (4 << a.shift) / wide);
+  a.tiles = tiles(a.rows);
   if ((int64_t)a.tiles * n_seqs > 0x7FFFFFFF)
     return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: more than 2^31 tiles of rows");
   a.cap = C->cache_cap;
