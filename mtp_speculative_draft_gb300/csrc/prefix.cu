@@ -85,7 +85,10 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 // exponential is taken twice.  The weights go through shared memory; for p.v a
 // lane has dims 4 l .. and 128 + 4 l .. of every key, so the output takes few
 // registers, many warps share an SM and hide each other's waits.  All query rows
-// of a CTA are heads of one new row: they see the same keys, and no mask is needed.
+// of a CTA are heads of one new row, which see the same keys; MANY: of several new
+// rows, whose masks differ in a few steps at the ends of what they see, and a
+// sequence's keys are read once for them (8/8 heads of 128, 8 sequences of 8 new rows,
+// tails of 512: 32 us, one row a CTA 46).
 // RG: query rows (heads) a CTA; H: 128-dim halves of the wider head size; ALONE:
 // without a split launch.
 //
@@ -121,7 +124,7 @@ __host__ __device__ constexpr int tail_padded(int rg) { return rg <= 2 ? 2 : rg 
 // CTAs a SM that the registers allow.
 __host__ __device__ constexpr int tail_ctas(int rg, int h) { return h == 1 || rg <= 4 ? 4 : 3; }
 
-template <int RG, int H, bool ALONE>
+template <int RG, int H, bool ALONE, bool MANY>
 __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     prefix_tail_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
@@ -129,8 +132,12 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   constexpr int PR = tail_padded(RG);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ks = lane >> 3, l8 = lane & 7;
   const int b = blockIdx.z, kv = blockIdx.y, part = blockIdx.x / a.items, item = blockIdx.x % a.items;
-  const int blocks = (a.G + RG - 1) / RG, i = item / blocks, g0 = item % blocks * RG;
-  const int p = b / a.per, head = p * a.nkv + kv, nr = min(RG, a.G - g0);
+  const int blocks = (a.G + RG - 1) / RG, g0 = item % blocks * RG;
+  const int i = item / blocks * (MANY ? a.mrows : 1), last = MANY ? min(i + a.mrows, a.m) - 1 : i;  // new rows i .. last
+  const int p = b / a.per, head = p * a.nkv + kv, nr = MANY ? (last + 1 - i) * a.G : min(RG, a.G - g0);
+  // query row r of the CTA: head g0 + head_of(r) of the KV head's, new row i + row_of(r)
+  auto row_of = [&](int r) { return MANY ? r / a.G : 0; };
+  auto head_of = [&](int r) { return MANY ? r % a.G : r; };
   const int cq = a.dqk / 32;
   const int r0 = ((b - p * a.per) * a.m + i) * a.G + g0;  // first query row
   float* qs = reinterpret_cast<float*>(sm);               // [RG][dqk]
@@ -157,13 +164,13 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     return;
   }
   const int first = ALONE ? P : first_shared_key(a, p, P);
-  // Keys: without a split launch the new rows j0 .. i, which are prepared below; the
+  // Keys: without a split launch the new rows j0 .. last, which are prepared below; the
   // prompt's e0 .. e1; the tail's t0 .. t2; in steps of their own.
   const int sees = a.window > 0 ? (int)max(0ll, (long long)P + t + i + 1 - a.window) : 0;  // lowest position
   const int e0 = min(sees, P), e1 = ALONE ? P : max(first, e0);
-  const int t2 = ALONE ? t : t + i + 1, t0 = min(max(0, sees - P), t2), j0 = max(0, sees - P - t);
+  const int t2 = ALONE ? t : t + last + 1, t0 = min(max(0, sees - P), t2), j0 = max(0, sees - P - t);
   auto steps_of = [](int n) { return (n + kTailKeys - 1) / kTailKeys; };
-  const int nn = ALONE ? steps_of(i + 1 - j0) : 0, ne = nn + steps_of(e1 - e0), nt = ne + steps_of(t2 - t0);
+  const int nn = ALONE ? steps_of(last + 1 - j0) : 0, ne = nn + steps_of(e1 - e0), nt = ne + steps_of(t2 - t0);
   // the sequence's parts: as many as its keys need, each with every parts-th of
   // the steps and of the splits' partials
   const int parts = max(1, min(a.parts, (nt * kTailKeys + a.part_keys - 1) / a.part_keys));
@@ -176,7 +183,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   const float* const vown = a.vt + (own_row + t0) * a.dv;
   Waiter wait{a.err, false};
   auto step_size = [&](int s) {
-    return min(kTailKeys, s < nn ? i + 1 - j0 - s * kTailKeys : s < ne ? e1 - e0 - (s - nn) * kTailKeys : t2 - t0 - (s - ne) * kTailKeys);
+    return min(kTailKeys, s < nn ? last + 1 - j0 - s * kTailKeys : s < ne ? e1 - e0 - (s - nn) * kTailKeys : t2 - t0 - (s - ne) * kTailKeys);
   };
   auto fetch_k = [&](int s) {
     if (lane != 0) return;
@@ -210,32 +217,32 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       const int r = rq + x * kTailWarps;
       hv[x] = HeadVals{};
       if (r < nr)
-        head_load(hv[x], a.qp + (size_t)(b * a.m + i) * a.ldq + (size_t)(kv * a.G + g0 + r) * a.dqk * (a.gated ? 2 : 1), a.dqk, half, lane);
+        head_load(hv[x], a.qp + (size_t)(b * a.m + i + row_of(r)) * a.ldq + (size_t)(kv * a.G + g0 + head_of(r)) * a.dqk * (a.gated ? 2 : 1), a.dqk, half, lane);
     }
     head_load(hw, a.qn, a.dqk, half, lane);
 #pragma unroll
     for (int x = 0; x < (RG + kTailWarps - 1) / kTailWarps; ++x) {
       const int r = rq + x * kTailWarps;
-      if (r < nr) head_norm_rope(hv[x], hw, a.qn != nullptr, a.dqk, a.eps, a.rope, b * a.m + i, a.err, lane, P + t + i);
+      if (r < nr) head_norm_rope(hv[x], hw, a.qn != nullptr, a.dqk, a.eps, a.rope, b * a.m + i + row_of(r), a.err, lane, P + t + i + row_of(r));
       if (r < RG) head_store(hv[x], qs + r * a.dqk, a.dqk, half, a.qscale, lane);
     }
     // A step of new rows, which is a warp's first, is written into its buffers; the
-    // CTA of a row's first heads appends it to the tail.
+    // CTA that has a row's first heads appends it to the tail.
     if (w0 < nn) {
 #pragma unroll 1
-      for (int j = j0 + w0 * kTailKeys, y = 0; j <= i && y < kTailKeys; ++j, ++y) {
+      for (int j = j0 + w0 * kTailKeys, y = 0; j <= last && y < kTailKeys; ++j, ++y) {
         const size_t row = (size_t)b * a.m + j;
         head_load(hv[0], a.kp + row * a.ldk + (size_t)kv * a.dqk, a.dqk, half, lane);
         head_load(hw, a.kn, a.dqk, half, lane);
         head_norm_rope(hv[0], hw, a.kn != nullptr, a.dqk, a.eps, a.rope, (int)row, a.err, lane, P + t + j);
         head_store(hv[0], kb + y * a.dqk, a.dqk, half, 1.f, lane);
-        const bool append = j == i && g0 == 0;
-        if (append) head_store(hv[0], a.kt + (own_row + t + i) * a.dqk, a.dqk, half, 1.f, lane);
+        const bool append = j >= i && g0 == 0;
+        if (append) head_store(hv[0], a.kt + (own_row + t + j) * a.dqk, a.dqk, half, 1.f, lane);
         const float* src = a.vp + row * a.ldv + (size_t)kv * a.dv;
         for (int c = 4 * lane; c < a.dv; c += 128) {
           const float4 x = *reinterpret_cast<const float4*>(src + c);
           *reinterpret_cast<float4*>(vb + y * a.dv + c) = x;
-          if (append) *reinterpret_cast<float4*>(a.vt + (own_row + t + i) * a.dv + c) = x;
+          if (append) *reinterpret_cast<float4*>(a.vt + (own_row + t + j) * a.dv + c) = x;
         }
       }
       fence_proxy_async_shared_cta();  // before a later copy into the buffers
@@ -261,11 +268,15 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   int vcol[H];  // this lane's dims of a value (past the last one: any, and not stored)
 #pragma unroll
   for (int h = 0; h < H; ++h) vcol[h] = min(128 * h + 4 * lane, a.dv - 4);
+  const int own_pos = P + t + min(i + row_of(row), last);  // position of this lane's row
   float ref = -INFINITY, l = 0.f;
   uint32_t phase = 0;
 #pragma unroll 1
   for (int s = w0; s < nt; s += stride) {
     const int n = step_size(s);
+    const int pos = s < nn ? P + t + j0 + s * kTailKeys : s < ne ? e0 + (s - nn) * kTailKeys : P + t0 + (s - ne) * kTailKeys;
+    auto hidden = [&](int key) { return MANY && (unsigned)(own_pos - pos - key) >= (a.window > 0 ? (unsigned)a.window : 0x80000000u); };
+    const bool edge = MANY && __any_sync(0xffffffffu, hidden(0) || hidden(n - 1));  // some row does not see some key
     wait(&sh.kfull[warp], phase);
     uint64_t acc[RG][2];
 #pragma unroll
@@ -325,9 +336,9 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       }
     }
     float mx;
-    if (mine >= n) x[0] = -INFINITY;
+    if (mine >= n || hidden(mine)) x[0] = -INFINITY;
     if (PR == 8) {
-      if (mine + 4 >= n) x[PL - 1] = -INFINITY;
+      if (mine + 4 >= n || hidden(mine + 4)) x[PL - 1] = -INFINITY;
       mx = fmaxf(x[0], x[PL - 1]);
     } else {
       mx = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], PR == 4 ? 1 : 2));
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
     for (int k = 0; k < PL; ++k) {
       const float w = ex2(x[k] - nref);
       l += w;
-      sh.p[warp][mine + 4 * k][row] = make_float2(w, w);
+      sh.p[warp][mine + 4 * k][row] = edge && hidden(mine + 4 * k) ? make_float2(-1.f, -1.f) : make_float2(w, w);
     }
     wait(&sh.vfull[warp], phase);
     phase ^= 1u;
@@ -366,6 +377,24 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       fence_proxy_async_shared_cta();  // before a later copy into the buffer
     }
     __syncwarp();
+    if (edge) {  // a weight of -1: the row does not see the key, whose value may be anything
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(vb + k * a.dv + vcol[h]);
+#pragma unroll
+          for (int r = 0; r < RG; ++r) {
+            const float f = sh.p[warp][k][r].x;
+            if (f != -1.f) {
+              const uint64_t f2 = pack2(f, f);
+              o[r][h][0] = fma2(f2, v.x, o[r][h][0]);
+              o[r][h][1] = fma2(f2, v.y, o[r][h][1]);
+            }
+          }
+        }
+      }
+    } else {
 #pragma unroll
     for (int k = 0; k < kTailKeys; ++k) {
       uint64_t w[8];
@@ -384,6 +413,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
           o[r][h][1] = fma2(w[r], v.y, o[r][h][1]);
         }
       }
+    }
     }
     __syncwarp();  // every lane has read the values
     if (s + stride < nt) fetch_v(s + stride);
@@ -473,7 +503,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
   auto weight = [](float m, float sum, float top) { return m == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2(m - top); };
   float4 y[H];
   auto finish = [&](int r, float M, float den) {
-    const int h = kv * a.G + g0 + r;
+    const int h = kv * a.G + g0 + head_of(r);
     if (a.sinks) {
       const float sink = a.sinks[h] * kLog2e, to = fmaxf(M, sink);
       if (to != M) {  // M may be -infinity: then nothing was summed
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
       if (sink != -INFINITY) den += ex2(sink - to);
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    const size_t at = (size_t)(b * a.m + i);
+    const size_t at = (size_t)(b * a.m + i + row_of(r));
 #pragma unroll
     for (int x = 0; x < H; ++x) {
       const int c = 128 * x + 4 * lane;
@@ -577,15 +607,25 @@ __global__ void __launch_bounds__(kTailWarps * 32, tail_ctas(RG, H))
 }
 
 // ------------------------------------------------------------------ host
-// Heads a CTA of the tail launch: a KV head's in as few CTAs as 8 a CTA allow, as
-// even as they go.
-static int tail_rows(int G) {
-  const int blocks = (G + 7) / 8, each = (G + blocks - 1) / blocks;
+// Query rows a CTA of the tail launch: a KV head's heads in as few CTAs as 8 a CTA
+// allow, as even as they go, of `mrows` new rows (more than one: at most 4 in all).
+static int tail_rows(int G, int mrows) {
+  const int blocks = (G + 7) / 8, each = mrows * ((G + blocks - 1) / blocks);
   return each <= 2 ? 2 : each <= 4 ? 4 : each == 7 ? 8 : each;
+}
+// New rows a CTA, where reading a sequence's keys once for several pays: with one or
+// two heads a KV head, up to 4 query rows (up to 8: 34 us, not 32, in the case above;
+// 32/8 heads, 2 new rows a CTA 55 us, one 47).  Not where the keys of all rows are few:
+// then more CTAs read them sooner (16 MB: 8/8 heads of 64, 4 x 8 rows 16 us, not 18).
+constexpr long long kManyBytes = 64 << 20;
+static int tail_new_rows(int G, int m) {
+  if (G > 2) return 1;
+  const int most = 4 / G, groups = (m + most - 1) / most;
+  return (m + groups - 1) / groups;
 }
 static size_t tail_smem(int rg, int dqk, int dv) { return (size_t)rg * dqk * 4 + (size_t)kTailWarps * kTailKeys * (dqk + dv) * 4; }
 
-template <int RG, int H, bool ALONE>
+template <int RG, int H, bool ALONE, bool MANY = false>
 static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
   static_assert(RG <= kTailKeys, "a warp's state fits one buffer of values");
   static std::atomic<bool> attr[64];  // per device
@@ -593,17 +633,19 @@ static cudaError_t launch_tail_as(const PrefixArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H, ALONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
+    e = cudaFuncSetAttribute(prefix_tail_kernel<RG, H, ALONE, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 * 1024);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
-  return launch_pdl(prefix_tail_kernel<RG, H, ALONE>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
+  return launch_pdl(prefix_tail_kernel<RG, H, ALONE, MANY>, dim3(a.parts * a.items, a.nkv, a.groups * a.per), kTailWarps * 32,
                     tail_smem(RG, a.dqk, a.dv), st, a);
 }
 
 template <int H, bool ALONE>
 static cudaError_t launch_tail_h(const PrefixArgs& a, cudaStream_t st) {
-  switch (tail_rows(a.G)) {
+  const int rg = tail_rows(a.G, a.mrows);
+  if (a.mrows > 1) return rg == 2 ? launch_tail_as<2, H, ALONE, true>(a, st) : launch_tail_as<4, H, ALONE, true>(a, st);
+  switch (rg) {
     case 2: return launch_tail_as<2, H, ALONE>(a, st);
     case 4: return launch_tail_as<4, H, ALONE>(a, st);
     case 5: return launch_tail_as<5, H, ALONE>(a, st);
@@ -844,16 +886,21 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
   a.mt = (a.R + 127) / 128;  // 1 where rows are repeated
   const int sms = sm_count(), heads = a.groups * a.nkv;
   const int keys = shared_keys(g, m, pmax);
-  const int rg = tail_rows(a.G);
-  a.items = m * ((a.G + rg - 1) / rg);
-  const long long units = (long long)B->n_seqs * a.nkv * a.items;
   const long long common = a.window > 0 ? std::min<long long>(pmax, std::max<long long>(0, (long long)a.window - m - tmax)) : pmax;
-  const bool alone = tail_alone(units, heads, common, a.dqk + a.dv, rg);
-  a.ns = alone ? 0 : prefix_splits(heads * a.mt, keys, sms);
-  // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
-  const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
-  long long own = (long long)edge + tmax + m;
-  if (a.window > 0) own = std::min<long long>(own, a.window);
+  int rg;
+  long long units, own;
+  for (a.mrows = tail_new_rows(a.G, m);; a.mrows = 1) {
+    rg = tail_rows(a.G, a.mrows);
+    a.items = (m + a.mrows - 1) / a.mrows * ((a.G + rg - 1) / rg);
+    units = (long long)B->n_seqs * a.nkv * a.items;
+    const bool alone = tail_alone(units, heads, common, a.dqk + a.dv, rg);
+    a.ns = alone ? 0 : prefix_splits(heads * a.mt, keys, sms);
+    // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
+    const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
+    own = (long long)edge + tmax + m;
+    if (a.window > 0) own = std::min<long long>(own, a.window);
+    if (a.mrows == 1 || (long long)B->n_seqs * a.nkv * m * own * (a.dqk + a.dv) * 4 >= kManyBytes) break;
+  }
   const TailPlan tp = tail_plan(units, own, a.dqk + a.dv, (long long)tail_resident(rg, a.dqk, a.dv) * sms, a.ns == 0);
   a.parts = tp.parts;
   a.part_keys = tp.keys;

@@ -24,7 +24,8 @@ struct PrefixArgs : SplitArgs {
   const int *plen, *tlen;
   float* out;
   float* qf;                     // [groups * nkv][R][dqk] scaled queries
-  int items;                     // CTAs of a sequence's KV head: new rows times blocks of query heads
+  int mrows;                     // new rows of a CTA of the tail launch
+  int items;                     // CTAs of a sequence's KV head: groups of new rows times blocks of query heads
   int parts, part_keys;          // parts of a sequence's own keys at most, keys of a part
   unsigned* tail_count;          // [seqs][nkv][items] parts that have arrived, zero at rest
   float2* tail_ml;               // [seqs][nkv][items][parts][rows] their states

@@ -369,3 +369,60 @@ def test_lowest_length_of_a_tail_of_several_tiles(dev):  # noqa: F811
     assert M.mtp_workspace_status(ws) == 0
     np.testing.assert_array_equal(tk.cpu().numpy(), B.beam_reorder(k, [1, 0, 3, 2], np.maximum(length, 0), 4))
     assert torch.equal(tk, tv)
+
+
+# Sequences whose keys are many enough that a CTA takes several new rows of them.
+def _many_rows(seed, nh, plen, m, window=0, per=160, **kw):
+    rng = np.random.default_rng(seed)
+    return _attn_case(seed, nh=nh, nkv=1, dqk=64, dv=32, plen=plen, window=window, m=m, sinks=True,
+                      tlen=[int(t) for t in rng.integers(-1, 500, per - 3)] + [0, 500, 7], **kw)
+
+
+@pytest.mark.parametrize("nh,m", [(1, 16), (2, 16), (1, 7), (2, 5)])
+@pytest.mark.parametrize("plen,window,kw", [([40], 0, {}), ([300, 123], 200, {}), ([12400], 0, {}), ([12400], 12200, {}),
+                                            ([0], 9, dict(per=600)), ([90], 0, dict(axes=(12, 10, 10)))])
+def test_several_new_rows_of_few_heads(dev, nh, m, plen, window, kw):  # noqa: F811
+    per = kw.get("per", 160) // len(plen) * len(plen)
+    call = Call(_many_rows(80 + m, nh, plen, m, window, **{**kw, "per": per}), dev)
+    call()
+    call.check()
+
+
+@pytest.mark.parametrize("plen,window,where", [
+    (50, 0, "new"), (50, 300, "new"), (50, 300, "tail"), (300, 300, "prompt"), (12500, 0, "new"), (12500, 12400, "new"),
+    (12500, 12400, "prompt")])
+@pytest.mark.parametrize("nh", [1, 2])
+def test_hidden_values_among_several_new_rows(dev, nh, plen, window, where):  # noqa: F811
+    """NaN in a later new row's key and value, or below the window of some of the rows: who does not see it gives the
+    same result to the bit."""
+    m, dv = 8, 32
+    c = _many_rows(90, nh, [plen], m, window)
+    c["tlen"] = [max(t, 0) for t in c["tlen"]]
+    for n in ("kt", "vt"):
+        c[n] = np.nan_to_num(c[n])
+    clean = Call(c, dev)
+    clean()
+    clean = clean.out.cpu().numpy().reshape(-1, m, nh, dv)
+    bad = []  # positions
+    for b, t in enumerate(c["tlen"]):
+        at = plen + t + 5 if where == "new" else plen + t + 3 - window if where == "tail" else plen + 250 - window
+        if where == "new":
+            c["kp"][b * m + 5], c["vp"][b * m + 5] = np.inf, np.nan
+        elif where == "tail" and at >= plen:
+            c["vt"][b, :, at - plen] = np.nan
+        elif where == "prompt":
+            c["vpre"][0, :, at] = np.nan
+        bad.append(at)
+    call = Call(c, dev)
+    call()
+    got = call.out.cpu().numpy().reshape(-1, m, nh, dv)
+    seen = 0
+    for b, t in enumerate(c["tlen"]):
+        for i in range(m):
+            low = max(0, plen + t + i + 1 - window) if window else 0
+            if low <= bad[b] <= plen + t + i and (where != "tail" or bad[b] >= plen):
+                assert np.isnan(got[b, i]).all(), (b, i)
+                seen += 1
+            else:
+                np.testing.assert_array_equal(got[b, i], clean[b, i])
+    assert 0 < seen < len(c["tlen"]) * m and not np.isnan(clean).any()
