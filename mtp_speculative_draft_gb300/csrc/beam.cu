@@ -16,7 +16,7 @@
 // common among 150k tokens.  Sums of exponentials: 32 terms in float32 a thread,
 // a row's 2e-8 from the exact one on ordinary logits.
 //
-// Measured (graph): 4 x 4096, 4 candidates 9 us; 8 x 151936, 16 candidates 13 us;
+// Measured (graph): 4 x 4096, 4 candidates 9 us; 8 x 151936, 16 candidates 12 us;
 // 16 prompts of 4 x 152577, 8 candidates 17.5 us (39 MB: 2.2 TB/s).
 #include <algorithm>
 #include <cmath>
@@ -74,26 +74,11 @@ __device__ __forceinline__ bool beam_live(const SelArgs& a, int r) {
   return (!a.done || a.done[r] == 0) && fabsf(a.score[r]) < INFINITY;
 }
 
-// The k-th largest of n keys in shared memory (n a multiple of 4, above or equal
-// to k), by counting for each the ones before it: threads below n, one of which
-// finds it.
-__device__ __forceinline__ void kth_largest(const uint32_t* keys, int n, int k, uint32_t* found) {
-  const int tid = threadIdx.x;
-  if (tid >= n) return;
-  const uint32_t mine = keys[tid];
-  int before = 0;
-#pragma unroll 4
-  for (int i = 0; i < n; i += 4) {
-    const uint4 x = *reinterpret_cast<const uint4*>(keys + i);
-    before += (x.x > mine || (x.x == mine && i < tid)) + (x.y > mine || (x.y == mine && i + 1 < tid)) +
-              (x.z > mine || (x.z == mine && i + 2 < tid)) + (x.w > mine || (x.w == mine && i + 3 < tid));
-  }
-  if (before == k - 1) *found = mine;
-}
-
 // About the k-th largest of 32 P keys in shared memory, from below (between k and
 // k + k / 16 are at or above it, or it is exact): one warp, bit by bit behind those
-// that all have in common.
+// that all have in common.  (Each key's place by counting the larger ones: 8 rows of
+// 151936, 16 candidates 12.8 us, not 11.8; 64 rows, 64 candidates 34 us for the rows
+// kernel, not 19.)
 template <int P>
 __device__ __forceinline__ void near_kth_largest(const uint32_t* keys, int k, uint32_t* found) {
   const int lane = threadIdx.x & 31;
@@ -124,8 +109,8 @@ __device__ __forceinline__ void near_kth_largest(const uint32_t* keys, int k, ui
 }
 
 struct RowsSmem {
-  alignas(16) uint32_t group[kSelThreads];        // largest keys of groups of threads
-  alignas(16) uint32_t wmax[kSelThreads / 32];    // and of warps
+  uint32_t group[kSelThreads];        // largest keys of groups of threads
+  uint32_t wmax[kSelThreads / 32];    // and of warps
   uint32_t sum[kSelThreads / 32][2];              // a warp's sum, in 2^-20 and 2^-40
   uint32_t low;
   int n;
@@ -183,7 +168,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   // groups of 4 threads do for few candidates (64 groups, 18 logits at or above
   // the 16th's), of 2 for up to 32 (128; 39 at or above the 32nd's), single threads for
   // more (64 rows, 64 candidates: 19 us; with 2 the chunks that keep more than `cap`
-  // make it 83).  Those by bits: counting 256 keys for each took 34 us, not 19.
+  // make it 83)
   uint32_t gtop = top;
   const int group = a.k <= 16 ? 2 : a.k <= 32 ? 1 : 0;  // log2 of a group's threads
   if (group > 0) gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 1));
@@ -195,8 +180,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) mtop = max(mtop, sh.wmax[w]);
   const float M = key_float(mtop), ref = M == -INFINITY ? 0.f : M;  // the chunk's largest logit
-  if (group == 2)
-    kth_largest(sh.group, kSelThreads / 4, a.k, &sh.low);
+  if (warp == 0 && group == 2)
+    near_kth_largest<kSelThreads / 128>(sh.group, a.k, &sh.low);
   else if (warp == 0 && group == 1)
     near_kth_largest<kSelThreads / 64>(sh.group, a.k, &sh.low);
   else if (warp == 0)
@@ -334,7 +319,7 @@ struct MergeSmem {
   double least[2];
   float base[kBeamsMost], inv[kBeamsMost];       // score - lse, and inverse / the largest inverse
   int len[kBeamsMost], kind[kBeamsMost];         // 0 nothing, 1 tokens, 2 itself
-  alignas(16) uint32_t group[256];
+  uint32_t group[256];
   uint32_t low;
   unsigned long long key[kMergeList];            // ranks
   uint32_t beam[kMergeList], tok[kMergeList];
@@ -372,7 +357,7 @@ __device__ __forceinline__ double table_exp(const MathTables& t, double x) {
 // only those that may be among the k best get a rank in 64 bits.  What depends on
 // the beams alone is worked out while the rows are still being read.  Bound by the
 // latency of its steps and of fetching its instructions, which are few for that: 8
-// rows of 151936 take 7 us from the rows' end (all ranks, logarithms and powers in
+// rows of 151936 take 6 us from the rows' end (all ranks, logarithms and powers in
 // 64 bits: 45 us).  Candidates are read a chunk by a warp: chunk and beam are then
 // known without a division a candidate.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
@@ -535,7 +520,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       if (chunk_bounds(c, lo, hi) && lo == lo) atomicMax(&sh.group[c & 255], float_key(lo));
     }
     __syncthreads();
-    kth_largest(sh.group, 256, a.k, &sh.low);
+    if (warp == 0) near_kth_largest<8>(sh.group, a.k, &sh.low);
     __syncthreads();
     low = sh.low;  // 0: fewer than k
     direct = low != 0 && a.k <= 64;
@@ -582,7 +567,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
       for (int o = 1; o < share; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (tid % share == 0) sh.group[tid / share] = top;
       __syncthreads();
-      kth_largest(sh.group, kMergeThreads / share, a.k, &sh.low);
+      if (warp == 0 && a.k <= 16)
+        near_kth_largest<2>(sh.group, a.k, &sh.low);
+      else if (warp == 0)
+        near_kth_largest<8>(sh.group, a.k, &sh.low);
       __syncthreads();
       low = max(sh.low, 1u);
       direct = false;
