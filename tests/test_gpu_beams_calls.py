@@ -426,3 +426,23 @@ def test_hidden_values_among_several_new_rows(dev, nh, plen, window, where):  # 
             else:
                 np.testing.assert_array_equal(got[b, i], clean[b, i])
     assert 0 < seen < len(c["tlen"]) * m and not np.isnan(clean).any()
+
+
+@pytest.mark.parametrize("kw", [dict(gated=True, rot=20), dict(gated=True, norm=False, pos_base=11), dict(loose=(70, 90))])
+@pytest.mark.parametrize("nh,nkv,dim", [(4, 2, 64), (3, 3, 160)])
+def test_several_new_rows_gated_and_strided(dev, nh, nkv, dim, kw):  # noqa: F811
+    """Gates, some rotated dims, rows with gaps, bounds above the lengths; captured and replayed."""
+    import torch
+    rng = np.random.default_rng(95)
+    c = _attn_case(95, nh=nh, nkv=nkv, dqk=dim, dv=dim, plen=[120, 60], tlen=[int(t) for t in rng.integers(-1, 300, 48)], m=6, **kw)
+    call = Call(c, dev, pad=8)
+    call()
+    call.check()
+    first = call.out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    call.out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(call.out, first)
