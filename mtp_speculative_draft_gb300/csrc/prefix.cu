@@ -726,6 +726,9 @@ static int shared_keys(const mtp_attn_geom* g, int m, int pmax) {
 // keys 13, 14, 32768 keys 32, 23.
 constexpr long long kAloneBytes = 52 << 20, kAloneBytesFew = 72 << 20;
 constexpr int kAloneKeys = 12288;
+// A split launch has prompts times KV heads along a grid's third axis, which ends at
+// 65535: 1024 prompts of 64 KV heads are one more.
+constexpr int kSplitHeads = 65535;
 static bool tail_alone(long long units, long long heads, long long keys, int dims, int rg) {
   return keys <= kAloneKeys && (units - heads) * keys * dims * 4 <= (rg <= 4 ? kAloneBytesFew : kAloneBytes);
 }
@@ -893,7 +896,7 @@ mtp_status attn_prefix_sink(const mtp_attn_geom* g, const mtp_prefix_batch* B, c
     rg = tail_rows(a.G, a.mrows);
     a.items = (m + a.mrows - 1) / a.mrows * ((a.G + rg - 1) / rg);
     units = (long long)B->n_seqs * a.nkv * a.items;
-    const bool alone = tail_alone(units, heads, common, a.dqk + a.dv, rg);
+    const bool alone = heads > kSplitHeads || tail_alone(units, heads, common, a.dqk + a.dv, rg);
     a.ns = alone ? 0 : prefix_splits(heads * a.mt, keys, sms);
     // a sequence's own keys: its tail, a window's edge in the prompt, or all of the prompt
     const int edge = a.ns > 0 ? (a.window > 0 ? (int)std::min<long long>(pmax, (long long)tmax + m) : 0) : pmax;
