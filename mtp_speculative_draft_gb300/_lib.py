@@ -100,6 +100,7 @@ class LogitRules(C.Structure):
 
 class KvCaches(C.Structure):
     device = None  # of the tensors, where a wrapper made the descriptor
+    seqs = beams = 0  # prompts and beams of one, where the arrays are beams' tails
     _fields_ = [("h_k", C.POINTER(vp)), ("h_v", C.POINTER(vp)), ("n_layers", i32),
                 ("n_kv_heads", i32), ("head_dim_qk", i32), ("head_dim_v", i32), ("cache_cap", i32)]
 

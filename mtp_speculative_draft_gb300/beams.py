@@ -149,6 +149,8 @@ def kv_beam_reorder(tails: KvCaches, parent, length, max_len, ws=None, stream=No
     dev = _device()
     if tails.device != dev:
         _here(tails, dev)
+    if not tails.beams:
+        raise ValueError("kv_beam_reorder: tails [n_seqs * beams, n_kv, cap, dim] are required (kv_tails)")
     lib = L.load()
     if ws is None:
         ws = workspace(lib.kv_beam_workspace_bytes(), stream=stream)

@@ -328,6 +328,8 @@ def kv_tree_commit(caches: KvCaches, path, cache_len, ws=None, stream=None):
     dev = _device()
     if caches.device != dev:
         _here(caches, dev)
+    if caches.beams:
+        raise ValueError("kv_tree_commit: caches [n_kv, cap, dim] are required (kv_caches), not beams' tails")
     if ws is None:
         ws = workspace(mtp_tree_workspace_bytes(), stream=stream)
     n = path.numel()

@@ -230,3 +230,38 @@ def test_reorder_refuses(lib):
         assert _reorder(lib, **kw) == want, kw
     assert _reorder(lib, most=0) == 0  # no row moves: nothing is launched
     assert lib.kv_beam_workspace_bytes() == 1024
+
+
+def test_caches_of_one_layout_are_refused_where_the_other_is_taken(monkeypatch):
+    """Caches [n_kv, cap, dim] and beams' tails [rows, n_kv, cap, dim] have one descriptor: each call takes its own."""
+    import torch
+    from mtp_speculative_draft_gb300 import _lib, beams as W, tree as T_
+    from test_tree_calls_host import _Lib, _Tensor
+    lib, at = _Lib(), iter(range(0x100000, 0x900000, 0x100000))
+    for m in (W, T_):
+        monkeypatch.setattr(m, "_device", lambda: 0)
+        monkeypatch.setattr(m, "_on", lambda stream, device: None)
+    monkeypatch.setattr(_lib, "load", lambda: lib)
+
+    def cache(*shape):
+        t = _Tensor(0, torch.float32, *shape)
+        p = next(at)
+        t.data_ptr = lambda: p
+        return t
+
+    n, ws = _Tensor(0, torch.int32, 4), _Tensor(0, torch.uint8, 4096)
+    caches = T_.kv_caches([cache(2, 20, 64)], [cache(2, 20, 64)])
+    tails = W.kv_tails([cache(4, 2, 20, 64)], [cache(4, 2, 20, 64)], 2)
+    T_.kv_tree_commit(caches, n, 5, ws)
+    W.kv_beam_reorder(tails, n, n, 5, ws)
+    assert lib.calls == 2
+    for call in (lambda: T_.kv_tree_commit(tails, n, 5, ws), lambda: W.kv_beam_reorder(caches, n, n, 5, ws)):
+        with pytest.raises(ValueError):
+            call()
+    assert lib.calls == 2
+    # a descriptor that a program filled in by itself goes to the call it was made for
+    own = _lib.KvCaches(caches.h_k, caches.h_v, 1, 2, 64, 64, 20)
+    T_.kv_tree_commit(own, n, 5, ws)
+    own.seqs, own.beams = 2, 2
+    W.kv_beam_reorder(own, n, n, 5, ws)
+    assert lib.calls == 4
