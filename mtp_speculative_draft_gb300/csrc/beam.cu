@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "move.h"
 #include "prefix.cuh"
 
 namespace mtp {
@@ -704,8 +705,6 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
 
 // ------------------------------------------------------------------ reorder
 constexpr int kMoveLayers = 64;  // layers of one launch
-constexpr int kMoveThreads = 256;
-constexpr int kMoveWords = 16;   // 16-byte words a thread
 
 struct MoveArgs {
   float* k[kMoveLayers];
@@ -937,18 +936,10 @@ mtp_status kv_beam_reorder(const mtp_kv_caches* C, const int32_t* d_parent, int3
   a.dqk = C->head_dim_qk;
   a.dv = C->head_dim_v;
   a.most = max_len;
-  // a tile of every beam fits the CTA's registers: 64 KB, a power of two a beam (a row each of 64 beams of 256 dims)
-  a.shift = 12;
-  static_assert(kMoveThreads * kMoveWords == 1 << 12, "16-byte words of a CTA");
-  while ((beams << a.shift) > 1 << 12) --a.shift;
-  const int wide = std::max(a.dqk, a.dv);
-  auto tiles = [&](int rows) { return (max_len + rows - 1) / rows; };
-  // smaller tiles where there is not a CTA an SM: 5 beams' 17 rows of 64 dims in one
-  // layer 2.1 us, not 3.1
-  const int64_t lists = (int64_t)n_seqs * 2 * a.nkv * C->n_layers;
-  while (4 << (a.shift - 1) >= wide && lists * tiles((4 << a.shift) / wide) < sm_count()) --a.shift;
-  a.rows = std::min(max_len, (4 << a.shift) / wide);
-  a.tiles = tiles(a.rows);
+  const MovePlan plan = move_plan(beams, std::max(a.dqk, a.dv), (int64_t)n_seqs * 2 * a.nkv * C->n_layers, max_len, sm_count());
+  a.shift = plan.shift;
+  a.rows = plan.rows;
+  a.tiles = plan.tiles;
   if ((int64_t)a.tiles * n_seqs > 0x7FFFFFFF)
     return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: more than 2^31 tiles of rows");
   a.cap = C->cache_cap;

@@ -265,3 +265,45 @@ def test_caches_of_one_layout_are_refused_where_the_other_is_taken(monkeypatch):
     own.seqs, own.beams = 2, 2
     W.kv_beam_reorder(own, n, n, 5, ws)
     assert lib.calls == 4
+
+
+@pytest.fixture(scope="module")
+def move_plan(tmp_path_factory):
+    """The tiles of kv_beam_reorder, compiled so that undefined arithmetic ends the program: (shift, rows, tiles) of
+    lines "beams wide lists max_len sms"."""
+    import os
+    import shutil
+    import subprocess
+    if shutil.which("g++") is None:
+        pytest.skip("no g++")
+    at = tmp_path_factory.mktemp("move")
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mtp_speculative_draft_gb300", "csrc")
+    (at / "plan.cpp").write_text('#include <cstdio>\n#include "move.h"\n'
+                                 "int main() {\n  int b, w, m, s;\n  long long l;\n"
+                                 '  while (scanf("%d %d %lld %d %d", &b, &w, &l, &m, &s) == 5) {\n'
+                                 "    const mtp::MovePlan p = mtp::move_plan(b, w, l, m, s);\n"
+                                 '    printf("%d %d %lld\\n", p.shift, p.rows, (long long)p.tiles);\n  }\n}\n')
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", csrc,
+                    str(at / "plan.cpp"), "-o", str(at / "plan")], check=True)
+
+    def run(cases):
+        done = subprocess.run([str(at / "plan")], input="".join("%d %d %d %d %d\n" % c for c in cases), capture_output=True,
+                              text=True)
+        assert done.returncode == 0, done.stderr
+        plans = [tuple(map(int, line.split())) for line in done.stdout.splitlines()]
+        assert len(plans) == len(cases)
+        for (beams, wide, _, most, _), (shift, rows, tiles) in zip(cases, plans):
+            # the beams' tiles fit the CTA's registers, and the tiles cover the rows, each with some
+            assert shift >= 0 and beams << shift <= 4096 and 1 <= rows and rows * wide <= 4 << shift
+            assert (tiles - 1) * rows < most <= tiles * rows
+        return plans
+
+    return run
+
+
+def test_tiles_of_the_narrowest_rows(move_plan):
+    """Rows of 4 dims and few lists: tiles shrink to one 16-byte word a beam, and no further."""
+    cases = [(b, w, n, most, 152) for b in (1, 2, 3, 5, 17, 64) for w in (4, 8, 12, 64, 256) for n in (1, 2, 16, 4096)
+             for most in (1, 2, 17, 100, 4096)]
+    plans = move_plan(cases)
+    assert plans[cases.index((1, 4, 1, 1, 152))] == (0, 1, 1)
