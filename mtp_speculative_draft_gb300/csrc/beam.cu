@@ -939,9 +939,9 @@ mtp_status kv_beam_reorder(const mtp_kv_caches* C, const int32_t* d_parent, int3
   const MovePlan plan = move_plan(beams, std::max(a.dqk, a.dv), (int64_t)n_seqs * 2 * a.nkv * C->n_layers, max_len, sm_count());
   a.shift = plan.shift;
   a.rows = plan.rows;
-  a.tiles = plan.tiles;
-  if ((int64_t)a.tiles * n_seqs > 0x7FFFFFFF)
+  if (plan.tiles * n_seqs > 0x7FFFFFFF)
     return fail(MTP_ERR_UNSUPPORTED, "kv_beam_reorder: more than 2^31 tiles of rows");
+  a.tiles = (int)plan.tiles;
   a.cap = C->cache_cap;
   a.err = &static_cast<WsHeader*>(d_ws)->err;
   for (int l0 = 0; l0 < C->n_layers; l0 += kMoveLayers) {

@@ -10,9 +10,9 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveWords = 16;  // 16-byte words a thread
 
 struct MovePlan {
-  int shift;  // a tile has 2^shift 16-byte words of a beam
-  int rows;   // rows a tile
-  int tiles;  // tiles of max_len rows
+  int shift;      // a tile has 2^shift 16-byte words of a beam
+  int rows;       // rows a tile
+  int64_t tiles;  // tiles of max_len rows
 };
 
 // `wide`: the wider head size; `lists`: prompts times KV heads times K or V times
@@ -23,7 +23,7 @@ inline MovePlan move_plan(int beams, int wide, int64_t lists, int max_len, int s
   p.shift = 12;
   static_assert(kMoveThreads * kMoveWords == 1 << 12, "16-byte words of a CTA");
   while ((beams << p.shift) > 1 << 12) --p.shift;
-  auto tiles = [&](int rows) { return (max_len + rows - 1) / rows; };
+  auto tiles = [&](int rows) { return ((int64_t)max_len + rows - 1) / rows; };
   // smaller tiles where there is not a CTA an SM: 5 beams' 17 rows of 64 dims in one
   // layer 2.1 us, not 3.1
   while (p.shift > 0 && 4 << (p.shift - 1) >= wide && lists * tiles((4 << p.shift) / wide) < sms) --p.shift;

@@ -307,3 +307,10 @@ def test_tiles_of_the_narrowest_rows(move_plan):
              for most in (1, 2, 17, 100, 4096)]
     plans = move_plan(cases)
     assert plans[cases.index((1, 4, 1, 1, 152))] == (0, 1, 1)
+
+
+def test_tiles_of_tails_near_the_longest_length(move_plan):
+    """Bounds up to 2^31 - 1 rows: the rounding up to whole tiles passes 32 bits."""
+    most = 2 ** 31 - 1
+    plans = move_plan([(b, w, n, m, 152) for b in (1, 2, 64) for w in (4, 64, 256) for n in (1, 4096) for m in (most, most - 1, 2 ** 30 + 1)])
+    assert plans[0] == (12, 4096, 2 ** 19)
