@@ -118,7 +118,10 @@ struct RowsSmem {
 };
 
 // grid (chunks, rows).  Bound by HBM on many rows; a row's logits are read once
-// and stay in registers.  The k-th largest of the largest logits of groups of
+// and stay in registers.  Which thread has a token does not depend on where the row
+// lies, so equal rows get equal sums to the bit, and equal ranks go to the lower beam
+// (16-byte reads from the row's first aligned word on did not have that, and took 17.4
+// us, not 15.9, for all of 64 rows of 152577).  The k-th largest of the largest logits of groups of
 // threads bounds the chunk's k-th largest from below, so the few logits at or
 // above it hold the chunk's k largest; where equal logits make them more than
 // `cap`, the k largest are found exactly (lower tokens first among equals).
@@ -139,28 +142,18 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   if (!beam_live(a, r)) return;  // the row is not read
   unsigned long long* const out = a.cand + slot * a.cap;
   for (int i = tid; i < a.cap; i += kSelThreads) out[i] = 0;  // no candidate, until one is written below
-  const float* x = a.x + (size_t)r * a.ld;
-  // chunks start at 16-byte boundaries: logit e of the row is number e + skew
-  const int skew = (int)((reinterpret_cast<uintptr_t>(x) >> 2) & 3);
-  const int e0 = c * kSelChunk - skew + 4 * tid;
+  const float* x = a.x + (size_t)r * a.ld + (size_t)c * kSelChunk;
+  const int e0 = c * kSelChunk + tid, left = a.V - c * kSelChunk;  // this thread has logits e0 + j kSelThreads
   float v[kSelPer];
+  if (left >= kSelChunk) {
 #pragma unroll
-  for (int j = 0; j < kSelPer / 4; ++j) {
-    const int e = e0 + j * 4 * kSelThreads;
-    float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (e >= 0 && e <= a.V - 4) {
-      f = __ldcs(reinterpret_cast<const float4*>(x + e));
-    } else {
-      if (e >= 0 && e < a.V) f.x = x[e];
-      if (e + 1 >= 0 && e + 1 < a.V) f.y = x[e + 1];
-      if (e + 2 >= 0 && e + 2 < a.V) f.z = x[e + 2];
-      if (e + 3 >= 0 && e + 3 < a.V) f.w = x[e + 3];
-    }
-    v[4 * j] = fmaxf(f.x, -INFINITY);  // NaN counts as -infinity
-    v[4 * j + 1] = fmaxf(f.y, -INFINITY);
-    v[4 * j + 2] = fmaxf(f.z, -INFINITY);
-    v[4 * j + 3] = fmaxf(f.w, -INFINITY);
+    for (int j = 0; j < kSelPer; ++j) v[j] = __ldcs(x + tid + j * kSelThreads);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kSelPer; ++j) v[j] = tid + j * kSelThreads < left ? __ldcs(x + tid + j * kSelThreads) : -INFINITY;
   }
+#pragma unroll
+  for (int j = 0; j < kSelPer; ++j) v[j] = fmaxf(v[j], -INFINITY);  // NaN counts as -infinity
   if (tid == 0) sh.n = 0;
   float mx = -INFINITY;
 #pragma unroll
@@ -208,8 +201,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
     int at = atomicAdd(&sh.n, __popc(mask));
 #pragma unroll 1
     for (; mask; mask &= mask - 1, ++at) {
-      const int j = __ffs(mask) - 1, tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
-      if (at < a.cap) out[at] = (unsigned long long)float_key(x[tok]) << 32 | (0xFFFFFFFFu - (uint32_t)tok);
+      const int j = __ffs(mask) - 1, tok = e0 + j * kSelThreads;
+      if (at < a.cap) out[at] = (unsigned long long)float_key(x[tid + j * kSelThreads]) << 32 | (0xFFFFFFFFu - (uint32_t)tok);
     }
   }
   if (warp == kWarps - 1) {
@@ -254,7 +247,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
       int m = 0;
 #pragma unroll
       for (int j = 0; j < kSelPer; ++j) {
-        const int tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
+        const int tok = e0 + j * kSelThreads;
         const uint32_t key = float_key(v[j]);
         m += key > kth || (key == kth && tok < t);
       }
@@ -275,7 +268,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < kSelPer; ++i)
         if (i == j) f = v[i];
-      const int tok = e0 + (j >> 2) * 4 * kSelThreads + (j & 3);
+      const int tok = e0 + j * kSelThreads;
       const uint32_t key = float_key(f);
       if (key > kth || (key == kth && tok <= end))
         out[atomicAdd(&sh.n, 1)] = (unsigned long long)key << 32 | (0xFFFFFFFFu - (uint32_t)tok);
@@ -793,8 +786,8 @@ struct SelWs {
 // the groups' largest (18 for 16 candidates, 73 for 64, 176 for 128), and some.
 static int sel_cap(int k) { return k + k / 4 + k * k / 256 + 8; }
 
-// Chunks of a row of V logits at any alignment.
-static int sel_chunks(int V) { return (int)(((int64_t)V + 3 + kSelChunk - 1) / kSelChunk); }
+// Chunks of a row of V logits.
+static int sel_chunks(int V) { return (V + kSelChunk - 1) / kSelChunk; }
 
 static SelWs sel_ws(void* ws, int rows, int V, int k) {
   SelWs w = {};

@@ -446,3 +446,17 @@ def test_several_new_rows_gated_and_strided(dev, nh, nkv, dim, kw):  # noqa: F81
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(call.out, first)
+
+
+@pytest.mark.parametrize("vocab,pad", [(9001, 0), (9002, 0), (20003, 0), (9000, 1), (152577, 0)])
+def test_equal_beams_at_every_alignment(dev, vocab, pad):  # noqa: F811
+    """Beams of equal rows, scores and lengths whose rows start at different places of a 16-byte word: the lower beam
+    first, token by token."""
+    c = _beams(78, 2, 4, vocab)
+    c["x"][:] = c["x"][0]
+    c["score"][:], c["length"][:] = -20.5, 9
+    for shift in range(4):
+        call = Select(c, 12, dev, shift=shift, pad=pad)
+        call()
+        call.check(f"shift {shift}")
+        assert call.parent.tolist() == [[0, 1, 2, 3] * 3] * 2
