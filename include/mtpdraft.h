@@ -779,9 +779,14 @@ typedef struct {
  * a finished beam offers itself alone, with token eos and its own score and
  * length; its row is not read.  A row with +infinity, or with nothing above
  * -infinity, offers nothing.  Candidates go by rank; equal ranks by the lower
- * beam, then the lower token.  Ranks are compared in 64 bits, tokens of one beam
- * by their float32 logits (of several logits whose scores round to one 64-bit
- * rank, equal ranks' order takes effect among the k largest of each beam).
+ * beam, then the lower token.  A row's log sum is taken once, from float32
+ * exponentials: off by 2^-18.7 at most, 1e-7 on ordinary logits.  Scores and ranks
+ * on top of it are computed and compared in 64 bits, tokens of one beam by their
+ * float32 logits (of several logits whose scores round to one 64-bit rank, equal
+ * ranks' order takes effect among the k largest of each beam).  So tokens of one
+ * beam, and beams of equal rows, scores and lengths, keep the formula's order;
+ * candidates of different beams whose scores differ by less than the two rows' log
+ * sums are off may change places.
  *   d_parent [n_seqs][k]: the beam extended (within its prompt), d_token its
  *   token, d_score_out its score; -1, -1 and -inf where there are fewer than k.
  *   d_len_out (needs d_len), d_done_out [n_seqs][k] or NULL: the new beam's

@@ -460,3 +460,35 @@ def test_equal_beams_at_every_alignment(dev, vocab, pad):  # noqa: F811
         call()
         call.check(f"shift {shift}")
         assert call.parent.tolist() == [[0, 1, 2, 3] * 3] * 2
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.5])
+@pytest.mark.parametrize("depth", [1.0, 4.0, 7.5, 9.0])
+@pytest.mark.parametrize("top", [0.0, 3.1])
+def test_normaliser_of_tokens_far_below_the_best(dev, depth, spread, top):  # noqa: F811
+    """One token at `top` and 7999 about `depth` below it, alike or spread; the beam's score is the normaliser in
+    float32, so what is written is their difference.
+
+    In units of 2^-24: a term d below the best is off by d for the rounding of the difference, d for that of the product
+    with log2(e), 0.225 d for log2(e) in float32, 4 for the exponential (2^-22), and takes 6 float32 additions; so the
+    sum is off by 10 + 2.225 times the mean of d under the softmax.  (8191 tokens of a chunk have a mean of 6.2 at most;
+    2^30 tokens 17, of which what lies between the largest logits of chunks takes one rounding more, and a chunk's
+    weight 4: 39 units, 2^-18.7.)"""
+    import torch
+    import mtp_speculative_draft_gb300 as M
+    rows, V = 8, 8000
+    rng = np.random.default_rng(int(10 * depth))
+    x = (top - depth * (1 + 0.01 * np.arange(rows)[:, None]) + rng.uniform(-spread, spread, (rows, V))).astype(np.float32)
+    x[:, 77] = top
+    d = x[:, 77:78].astype(np.float64) - x
+    p = np.exp(-d)
+    lse = x[:, 77] + np.log(p.sum(-1))
+    score = lse.astype(np.float32)
+    i = lambda: torch.empty(rows, 1, dtype=torch.int32, device=dev)  # noqa: E731
+    parent, token, out = i(), i(), torch.empty(rows, 1, device=dev)
+    M.beam_select(M.beam_set(rows, 1, V, _t(score, dev)), _t(x, dev), 1, parent, token, out)
+    assert (token == 77).all()
+    want = score + (x[:, 77] - lse)  # the output's own rounding, of a value of 2^-18 or so, is 2^-24 of it
+    off = np.abs(out.cpu().numpy()[:, 0] - want)
+    bound = (10 + 2.225 * (p * d).sum(-1) / p.sum(-1)) * 2.0 ** -24 + np.abs(want) * 2.0 ** -24
+    assert (off <= bound).all(), (off, bound)
