@@ -610,7 +610,8 @@ typedef struct {
  *   others leaves them 15 bits); a weight's absolute error is 2^-33 of the
  *   largest weight.  New rows and the keys at a window's edge are read as float32.
  *   NaN in a K or V row that a node sees gives NaN.  Infinity gives NaN in a
- *   cached row that all nodes see, and what the formula gives in the others.
+ *   cached row that all nodes see, and what the formula gives in the others (but
+ *   NaN for infinity in a V row whose weight is below about 2^-126 of the largest).
  * ------------------------------------------------------------------------ */
 /* Enough for every call of up to n nodes and cache_len cached keys. */
 size_t attn_tree_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n, int32_t cache_len);
@@ -742,9 +743,13 @@ typedef struct {
  *   The lengths are the caller's to advance.
  *   Accuracy: prompt rows that all of a prompt's sequences see may enter as 22-bit
  *   operands, as attn_tree_sink's cached keys do (its statement holds, with the
- *   prompt's sequences for a tree's nodes); other rows are read as float32.  NaN
- *   in a K or V row that a row sees gives NaN there.  Infinity gives NaN in a prompt
- *   row that entered as above, and what the formula gives in the others.
+ *   prompt's sequences for a tree's nodes); other rows are read as float32.  Whether
+ *   they do depends on the sizes of the call (geometry, n_groups, n_seqs, m, the
+ *   bounds prefix_max and tail_max), not on what the arrays hold: a repeated call
+ *   gives the same bits, a looser bound may give other roundings.  NaN in a K or V
+ *   row that a row sees gives NaN there.  Infinity gives NaN in a prompt
+ *   row that entered as above, and what the formula gives in the others (but NaN for
+ *   infinity in a V row whose weight is below about 2^-126 of the largest).
  * ------------------------------------------------------------------------ */
 /* Enough for every call of up to these sizes (and any lengths of tails). */
 size_t attn_prefix_sink_workspace_bytes(const mtp_attn_geom *g, int32_t n_groups, int32_t n_seqs,

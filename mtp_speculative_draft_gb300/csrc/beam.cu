@@ -22,8 +22,9 @@
 // (log2 e is 1.3e-8 short and 2^x errs by -5e-8 in the mean: they work against each
 // other); 1e-7 where a few tokens have the most (deviation 6).
 //
-// Measured (graph): 4 x 4096, 4 candidates 9 us; 8 x 151936, 16 candidates 12 us;
-// 16 prompts of 4 x 152577, 8 candidates 17.5 us (39 MB: 2.2 TB/s).
+// Measured (graph): 4 x 4096, 4 candidates 8.2 us; 8 x 151936, 16 candidates 10.8 us;
+// 16 prompts of 4 x 152577, 8 candidates 15.9 us (33 MB, without the finished beams'
+// rows: 2.1 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -83,9 +84,8 @@ __device__ __forceinline__ bool beam_live(const SelArgs& a, int r) {
 
 // About the k-th largest of 32 P keys in shared memory, from below (between k and
 // k + k / 16 are at or above it, or it is exact): one warp, bit by bit behind those
-// that all have in common.  (Each key's place by counting the larger ones: 8 rows of
-// 151936, 16 candidates 12.8 us, not 11.8; 64 rows, 64 candidates 34 us for the rows
-// kernel, not 19.)
+// that all have in common.  (Each key's place by counting the larger ones took 1 us
+// more for 8 rows of 151936 and 16 candidates, 15 us more for 64 rows and 64.)
 template <int P>
 __device__ __forceinline__ void near_kth_largest(const uint32_t* keys, int k, uint32_t* found) {
   const int lane = threadIdx.x & 31;
@@ -127,16 +127,18 @@ struct RowsSmem {
 // and stay in registers.  Which thread has a token does not depend on where the row
 // lies, so equal rows get equal sums to the bit, and equal ranks go to the lower beam
 // (16-byte reads from the row's first aligned word on did not have that, and took 17.4
-// us, not 15.9, for all of 64 rows of 152577).  The k-th largest of the largest logits of groups of
-// threads bounds the chunk's k-th largest from below, so the few logits at or
-// above it hold the chunk's k largest; where equal logits make them more than
+// us, not 15.9, for all of 64 rows of 152577).  The k-th largest of the largest logits
+// of groups of threads bounds the chunk's k-th largest from below, so the few logits
+// at or above it hold the chunk's k largest; where equal logits make them more than
 // `cap`, the k largest are found exactly (lower tokens first among equals).
 // A thread's sum of exponentials has 6 roundings a term; the threads' are cut off at
 // 2^-40 of the chunk's largest and added exactly, in integers of 2^-20 and 2^-40 (a
 // 64-bit floating addition costs a warp 16 cycles of an SM).
-// 64 rows of 152577: 11 us, two waves of CTAs, each 3 us of reads at HBM's rate and
-// 2.5 us of work behind them (the second wave's reads sent to L2 ahead: no change;
-// 512 threads of 16 logits 20 us in all, not 17.5; chunks of 4096 19.5).
+// 64 rows of 152577: two waves of CTAs, 3 us apart, each 1.3 us until its logits are
+// there and 1 to 1.7 us of work behind them.  (With 16-byte reads the second wave's
+// sent to L2 ahead changed nothing; 512 threads of 16 logits took 20 us in all, not
+// 17.5, chunks of 4096 19.5.)  64 registers, four CTAs an SM: 40 bytes a thread are
+// spilled.
 __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_constant__ SelArgs a) {
   __shared__ RowsSmem sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) beam_rows_kernel(const __grid_
   const uint32_t top = float_key(mx), wtop = __reduce_max_sync(0xffffffffu, top);
   // groups of 4 threads do for few candidates (64 groups, 18 logits at or above
   // the 16th's), of 2 for up to 32 (128; 39 at or above the 32nd's), single threads for
-  // more (64 rows, 64 candidates: 19 us; with 2 the chunks that keep more than `cap`
-  // make it 83)
+  // more (64 rows, 64 candidates: with 2 the chunks that keep more than `cap` took 64 us
+  // more)
   uint32_t gtop = top;
   const int group = a.k <= 16 ? 2 : a.k <= 32 ? 1 : 0;  // log2 of a group's threads
   if (group > 0) gtop = max(gtop, __shfl_xor_sync(0xffffffffu, gtop, 1));
@@ -358,7 +360,7 @@ __device__ __forceinline__ double table_exp(const MathTables& t, double x) {
 // the beams alone is worked out while the rows are still being read.  Bound by the
 // latency of its steps and of fetching its instructions, which are few for that: 8
 // rows of 151936 take 6 us from the rows' end (all ranks, logarithms and powers in
-// 64 bits: 45 us).  Candidates are read a chunk by a warp: chunk and beam are then
+// 64 bits took 45).  Candidates are read a chunk by a warp: chunk and beam are then
 // known without a division a candidate.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_constant__ SelArgs a) {
   __shared__ MergeSmem sh;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   if (rounds > 1 && all_slots > (uint32_t)a.k) {
     // many candidates: first the chunks whose largest logit may be among the k best,
     // by the k-th largest of theirs and of the finished beams (16 rows of 151936, 32
-    // candidates: 17 us in all, 27 without; 64 rows, 64 candidates: 41 and 119)
+    // candidates: 15 us in all, 10 more without; 64 rows, 64 candidates: 38, 78 more)
     const float* tops = a.top + (size_t)row0 * a.chunks;
     if (tid < 256) sh.group[tid] = 0;
     __syncthreads();
@@ -543,8 +545,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const __grid_
   }
   // the candidates that reach `low`; without one, or if they are too many, first the
   // threads' best from below, of which the k-th largest is a (better) `low`.  (For
-  // more than 64 they often are: 8 rows, 128 candidates 41 us, not 53; 16 rows, 32
-  // candidates 17 us with one pass, 20 with two.)
+  // more than 64 they often are: 8 rows, 128 candidates took 12 us more in one pass at
+  // first; 16 rows, 32 candidates 3 us less.)
 #pragma unroll 1
   for (int pass = direct ? 1 : 0; pass < 2; ++pass) {
     float best = self_lo;

@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kPrefixPrepThreads) prefix_prep_kernel(const _
 // 40/8 heads of 128, take 44 us (219 MB at 5 TB/s; shared memory's pipe 49 % busy, issue
 // slots 34 %), 64 of up to 256 take 22 (two waves; 79 MB).  Outputs by key groups
 // (half as many warps) took 76 and 35 us, clusters over long tails 53 and 28.  One
-// buffer of keys and one of values a warp do as well as two of each.
+// buffer of keys and one of values a warp do as well as two of each.  At 128 (168)
+// registers for four (three) CTAs an SM, 19 of the 28 forms spill 4 to 28 bytes a thread.
 constexpr int kTailWarps = 4;
 constexpr int kTailKeys = 8;
 constexpr float kTailMove = 8.f;
@@ -662,7 +663,10 @@ static cudaError_t launch_tail(const PrefixArgs& a, cudaStream_t st) {
 // Parts of a sequence's keys, for `units` (sequence, KV head, new row, block of
 // heads): as many as the SMs hold at once (`ctas`), of kPartBytes of keys and values
 // or more; tails that differ in length get a third more (24 of up to 2048 rows: 60
-// us, 66 without, 68 with twice as many).  One warp joins them.
+// us, 66 without, 68 with twice as many).  One warp joins them.  us with parts of 32,
+// 64 and 128 KB at least: 40/8 heads of 128, 8 beams, 4096 keys 28.3, 27.3, 27.3; 32
+// samples, 1024 keys 25.6, 24.0, 24.0; 16/2 heads of 256, 3 x 5 samples 32.0, 32.1,
+// 35.1; alone, 8/2 heads of 64, 4 sequences, 3000 keys 11.1, 11.6, 13.9.
 constexpr int kTailCtas = 6, kPartBytes = 64 * 1024;  // CTAs a SM at most
 
 // CTAs of the tail launch that an SM holds.
@@ -685,7 +689,13 @@ static TailPlan tail_plan(long long units, long long own, int dims, long long ct
 }
 
 // Splits of a prompt's keys: the fewest waves of CTAs (one a SM) times the keys
-// of a split and a CTA's fixed cost, about 192 keys.
+// of a split and a CTA's fixed cost, about 192 keys (48: 64 samples of 32768 keys 200
+// us, not 190, 64/8 heads, 64 x 4096 62, not 53; 512: no change there).  A split has 64
+// keys at least: with 32 and 128, 16/2 heads of 256, 3 x 5 samples 32.1 and 33.2 us, 32.1
+// with 64; 8 x 4096 32.8 and 30.3, 31.3; 40/8 heads of 128, 8 x 2048 23.5 and 20.9, 23.1.
+// Up to three waves: 32/8 heads of 128, 13 x 4 sequences, 4096 keys 113 us, 117 with up to
+// one or two; 12 x 4, 8192 keys 160, 212 with one; 16/2 heads of 256, 50 x 4, 2048 keys
+// 130, 194 with one; up to six: 20 x 4, 2048 keys 110, not 107.
 constexpr int kSplitCost = 192;
 constexpr int kSplitKeys = 64;   // of a split at least
 constexpr int kSplitWaves = 3;   // CTAs a SM at most, where a prompt has several splits
